@@ -17,7 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libw4a16.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "w4a16.h")
 HEADERS = [HEADER, os.path.join(os.path.dirname(HERE), "include", "w4a8.h"),
-           os.path.join(os.path.dirname(HERE), "include", "mxfp.h")]
+           os.path.join(os.path.dirname(HERE), "include", "mxfp.h"),
+           os.path.join(os.path.dirname(HERE), "include", "decode.h")]
 
 W4A16_OK = 0
 W4A16_ERR_INVALID_ARG = -1
@@ -42,6 +43,18 @@ W4A16_GEMM_NO_WEIGHT_PREFETCH = 2
 W4A16_GEMM_DEQUANT_LUT = 4
 W4A16_GEMM_DEQUANT_INT = 8
 
+DEC_KV_FP16 = 0
+DEC_KV_BF16 = 1
+DEC_KV_E4M3 = 2
+
+DEC_ROPE_HALF = 0
+DEC_ROPE_INTERLEAVED = 1
+
+DEC_ROPE_SCALE_NONE = 0
+DEC_ROPE_SCALE_LINEAR = 1
+DEC_ROPE_SCALE_BASE = 2
+DEC_ROPE_SCALE_RAMP = 3
+
 _lock = threading.Lock()
 _lib = None
 
@@ -56,6 +69,42 @@ class GemmConfig(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("split_k", ctypes.c_int), ("tile_m", ctypes.c_int),
                 ("stages", ctypes.c_int), ("flags", ctypes.c_int),
                 ("reserved", ctypes.c_int * 3)]
+
+
+class KvCache(ctypes.Structure):
+    """dec_kv_cache: where a paged cache lies (kv_cache() fills it from tensors)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_slot_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_slot_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class RopeScaling(ctypes.Structure):
+    """dec_rope_scaling."""
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_float), ("low", ctypes.c_float),
+                ("high", ctypes.c_float), ("original_len", ctypes.c_float),
+                ("magnitude", ctypes.c_float)]
+
+
+class RopeConfig(ctypes.Structure):
+    """dec_rope_config (rope_config() fills it)."""
+    _fields_ = [("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("layout", ctypes.c_int), ("table_len", ctypes.c_int),
+                ("reserved", ctypes.c_int), ("table", ctypes.c_void_p),
+                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64),
+                ("ldqo", ctypes.c_int64), ("ldko", ctypes.c_int64)]
+
+
+class AttnConfig(ctypes.Structure):
+    """dec_attn_config (attn_config() fills it)."""
+    _fields_ = [("q_heads", ctypes.c_int), ("dtype", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("window", ctypes.c_int), ("scale", ctypes.c_float), ("reserved", ctypes.c_int),
+                ("ldq", ctypes.c_int64), ("ldo", ctypes.c_int64), ("ld_table", ctypes.c_int64)]
 
 
 def lib() -> ctypes.CDLL:
@@ -109,16 +158,35 @@ def lib() -> ctypes.CDLL:
             L.mx_repack.restype = I
             L.mx_gemm.argtypes = [P, P, P, I, I, I, I, P, P]
             L.mx_gemm.restype = I
+            J, F, D = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+            L.dec_rms_norm.argtypes = [P, J, P, J, P, I, I, I, F, P, P, J, P]
+            L.dec_rms_norm.restype = I
+            L.dec_rms_norm_i8.argtypes = [P, J, P, J, P, I, I, I, F, P, P, P, P]
+            L.dec_rms_norm_i8.restype = I
+            L.dec_rms_norm_mx.argtypes = [P, J, P, J, P, I, I, I, F, P, P, P, P]
+            L.dec_rms_norm_mx.restype = I
+            L.dec_rope_table.argtypes = [I, D, ctypes.POINTER(RopeScaling), P, I, P]
+            L.dec_rope_table.restype = I
+            L.dec_rope_append.argtypes = [ctypes.POINTER(RopeConfig), ctypes.POINTER(KvCache),
+                                          P, P, P, I, P, P, P, P, P]
+            L.dec_rope_append.restype = I
+            L.dec_attn_workspace_bytes.argtypes = [ctypes.POINTER(AttnConfig),
+                                                   ctypes.POINTER(KvCache)]
+            L.dec_attn_workspace_bytes.restype = Z
+            L.dec_attn_paged.argtypes = [ctypes.POINTER(AttnConfig), ctypes.POINTER(KvCache),
+                                         P, P, P, I, P, P, P, Z, P]
+            L.dec_attn_paged.restype = I
             _lib = L
     return _lib
 
 
 def header_functions() -> list[str]:
-    """Names of the functions the public headers (include/w4a16.h, w4a8.h, mxfp.h) declare."""
+    """Names of the functions the public headers (include/w4a16.h, w4a8.h, mxfp.h, decode.h)
+    declare."""
     names = set()
     for h in HEADERS:
         src = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
-        names.update(re.findall(r"\b((?:w4a16|w4a8|mx)_[a-z_0-9]+)\s*\(", src))
+        names.update(re.findall(r"\b((?:w4a16|w4a8|mx|dec)_[a-z_0-9]+)\s*\(", src))
     return sorted(names)
 
 
@@ -273,6 +341,52 @@ def mx_gemm(a_codes, a_scales, packed, M: int, N: int, K: int, dtype: int, Y,
                          _stream(stream)), "mx_gemm")
 
 
+def dec_rms_norm(x, residual, weight, M: int, H: int, dtype: int, eps: float, residual_out, y, *,
+                 ldx: int = 0, ldr: int = 0, ldy: int = 0, stream=None) -> None:
+    _check(lib().dec_rms_norm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), M, H, dtype, eps,
+                              _ptr(residual_out), _ptr(y), ldy, _stream(stream)), "dec_rms_norm")
+
+
+def dec_rms_norm_i8(x, residual, weight, M: int, H: int, dtype: int, eps: float, residual_out,
+                    y_i8, s_y, *, ldx: int = 0, ldr: int = 0, stream=None) -> None:
+    _check(lib().dec_rms_norm_i8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), M, H, dtype,
+                                 eps, _ptr(residual_out), _ptr(y_i8), _ptr(s_y),
+                                 _stream(stream)), "dec_rms_norm_i8")
+
+
+def dec_rms_norm_mx(x, residual, weight, M: int, H: int, dtype: int, eps: float, residual_out,
+                    y_codes, y_scales, *, ldx: int = 0, ldr: int = 0, stream=None) -> None:
+    _check(lib().dec_rms_norm_mx(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), M, H, dtype,
+                                 eps, _ptr(residual_out), _ptr(y_codes), _ptr(y_scales),
+                                 _stream(stream)), "dec_rms_norm_mx")
+
+
+def dec_rope_table(rot_dim: int, base: float, scaling: RopeScaling | None, table,
+                   table_len: int, stream=None) -> None:
+    _check(lib().dec_rope_table(rot_dim, base, scaling, _ptr(table), table_len,
+                                _stream(stream)), "dec_rope_table")
+
+
+def dec_rope_append(cfg: RopeConfig, cache: KvCache | None, q, k, v, T: int, positions, slots,
+                    q_out, k_out=None, stream=None) -> None:
+    _check(lib().dec_rope_append(cfg, cache, _ptr(q), _ptr(k), _ptr(v), T, _ptr(positions),
+                                 _ptr(slots), _ptr(q_out), _ptr(k_out), _stream(stream)),
+           "dec_rope_append")
+
+
+def dec_attn_workspace_bytes(cfg: AttnConfig, cache: KvCache) -> int:
+    return int(lib().dec_attn_workspace_bytes(cfg, cache))
+
+
+def dec_attn_paged(cfg: AttnConfig, cache: KvCache, q, block_table, lens, B: int, out, lse,
+                   workspace, ws_bytes: int | None = None, stream=None) -> None:
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().dec_attn_paged(cfg, cache, _ptr(q), _ptr(block_table), _ptr(lens), B, _ptr(out),
+                                _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)),
+           "dec_attn_paged")
+
+
 # ---- torch-friendly helpers (allocation + the calls above) ---------------------------
 
 def repack(qweight, scales, qzeros, N: int, K: int, group: int, dtype: int,
@@ -298,3 +412,50 @@ def gemm(A, packed, N: int, K: int, group: int, dtype: int, out=None, stream=Non
     else:
         w4a16_gemm(A, packed, M, N, K, group, dtype, Y, stream)
     return Y
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
+    """The paged cache in tensors k and v of shape [pages, page_size, kv_heads, head_dim], in
+    any order of strides as long as head_dim is contiguous (pass a permuted view of a cache
+    stored as [pages, kv_heads, page_size, head_dim]).  float16, bfloat16 or float8_e4m3fn,
+    the last with optional float32 scales [kv_heads].  The struct keeps addresses, not the
+    tensors: they have to outlive it."""
+    import torch
+    kinds = {torch.float16: DEC_KV_FP16, torch.bfloat16: DEC_KV_BF16,
+             torch.float8_e4m3fn: DEC_KV_E4M3}
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in kinds \
+            or k.stride(3) != 1 or v.stride(3) != 1:
+        raise W4A16Error(W4A16_ERR_UNSUPPORTED, "kv_cache")
+    pages, size, heads, dim = k.shape
+    for s in (k_scale, v_scale):
+        if s is not None and (k.dtype != torch.float8_e4m3fn or s.dtype != torch.float32
+                              or s.shape != (heads,) or not s.is_contiguous()):
+            raise W4A16Error(W4A16_ERR_UNSUPPORTED, "kv_cache")
+    return KvCache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                   k.stride(0), k.stride(1), k.stride(2), v.stride(0), v.stride(1), v.stride(2),
+                   pages, size, heads, dim, kinds[k.dtype], 0)
+
+
+def rope_config(q_heads: int, kv_heads: int, head_dim: int, dtype: int, table, rot_dim: int,
+                layout: int = DEC_ROPE_HALF, *, ldq: int = 0, ldk: int = 0, ldv: int = 0,
+                ldqo: int = 0, ldko: int = 0) -> RopeConfig:
+    """dec_rope_append's settings; table: float32 [positions, rot_dim] (it has to outlive the
+    struct), or None with rot_dim 0 and no rotation (any non-negative position)."""
+    n = table.shape[0] if table is not None else 0x7FFFFFFF
+    return RopeConfig(q_heads, kv_heads, head_dim, dtype, rot_dim, layout, n, 0, _ptr(table),
+                      ldq, ldk, ldv, ldqo, ldko)
+
+
+def attn_config(q_heads: int, dtype: int, scale: float, max_pages: int, *, window: int = 0,
+                ldq: int = 0, ldo: int = 0, ld_table: int = 0) -> AttnConfig:
+    """dec_attn_paged's settings."""
+    return AttnConfig(q_heads, dtype, max_pages, window, scale, 0, ldq, ldo, ld_table)
+
+
+def attn_workspace(cfg: AttnConfig, cache: KvCache, device="cuda"):
+    """A zero-filled workspace for dec_attn_paged (a uint8 tensor)."""
+    import torch
+    nbytes = dec_attn_workspace_bytes(cfg, cache)
+    if nbytes == 0:
+        raise W4A16Error(W4A16_ERR_UNSUPPORTED, "dec_attn_workspace_bytes")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)

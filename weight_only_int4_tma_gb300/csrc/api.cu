@@ -2,12 +2,14 @@
 // selection and the device status word.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdlib>
 #include <mutex>
 
 #include "w4a16.h"
 #include "w4a8.h"
 #include "mxfp.h"
+#include "decode.h"
 #include "format.cuh"
 #include "launch.h"
 
@@ -524,6 +526,261 @@ int mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const void* packed,
     if (rc != W4A16_OK) return rc;
     return launch_mx_gemm(*ctx, a_codes, a_scales, packed, M, N, K, dtype, Y,
                           static_cast<cudaStream_t>(stream));
+}
+
+// ---- decoder-layer operators (include/decode.h) -----------------------------------------
+
+namespace {
+bool dtype_ok(int dtype) { return dtype == W4A16_FP16 || dtype == W4A16_BF16; }
+
+int norm_common(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                const void* weight, int M, int H, int dtype, float eps, void* residual_out,
+                void* y, int64_t ldy, void* scales, int out, void* stream) {
+    if (M < 0 || H < 1 || !(eps >= 0.0f) || !std::isfinite(eps)) return W4A16_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || H > (1 << 20)) return W4A16_ERR_UNSUPPORTED;
+    if (out == kNormI8 && (H % 8 != 0 || H > 32768)) return W4A16_ERR_UNSUPPORTED;
+    if (out == kNormMx && (H % 32 != 0 || H > 32768)) return W4A16_ERR_UNSUPPORTED;
+    if (M == 0) return W4A16_OK;
+    if (ldx == 0) ldx = H;
+    if (ldr == 0) ldr = H;
+    if (ldy == 0) ldy = H;
+    if (!x || !y || ldx < H || ldr < H || ldy < H) return W4A16_ERR_INVALID_ARG;
+    if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(weight, 2) || !aligned(residual_out, 2))
+        return W4A16_ERR_INVALID_ARG;
+    if (out == kNormSame) {
+        if (!aligned(y, 2)) return W4A16_ERR_INVALID_ARG;
+    } else {
+        if (!scales || !aligned(y, 8) || (out == kNormI8 && !aligned(scales, 4)))
+            return W4A16_ERR_INVALID_ARG;
+        if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+            !aligned(residual_out, 16) || ldx % 8 != 0 || ldr % 8 != 0)
+            return W4A16_ERR_INVALID_ARG;
+    }
+    const DeviceCtx* ctx = nullptr;
+    const int rc = get_ctx(&ctx);
+    if (rc != W4A16_OK) return rc;
+    const NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual),
+                     static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(residual_out),
+                     y, scales, ldx, ldr, ldy, H, eps};
+    return launch_norm(*ctx, a, M, dtype, out, static_cast<cudaStream_t>(stream));
+}
+
+// A cache's struct by itself: W4A16_OK, or the error of a call that takes it.
+int check_cache(const dec_kv_cache* c) {
+    if (!c->k || !c->v || c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 ||
+        c->head_dim < 1 || c->reserved != 0)
+        return W4A16_ERR_INVALID_ARG;
+    if (c->dtype != DEC_KV_FP16 && c->dtype != DEC_KV_BF16 && c->dtype != DEC_KV_E4M3)
+        return W4A16_ERR_UNSUPPORTED;
+    const int per16 = c->dtype == DEC_KV_E4M3 ? 16 : 8;  // elements in 16 bytes
+    if (c->head_dim % per16 != 0 || c->head_dim > 256) return W4A16_ERR_UNSUPPORTED;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+        !aligned(c->v_scale, 4))
+        return W4A16_ERR_INVALID_ARG;
+    const int64_t st[6] = {c->k_page_stride, c->k_slot_stride, c->k_head_stride,
+                           c->v_page_stride, c->v_slot_stride, c->v_head_stride};
+    for (int i = 0; i < 6; ++i)
+        if (st[i] < 0 || st[i] % per16 != 0) return W4A16_ERR_INVALID_ARG;
+    return W4A16_OK;
+}
+
+KvView key_view(const dec_kv_cache& c) {
+    return {c.k, c.k_scale, c.k_page_stride, c.k_slot_stride, c.k_head_stride};
+}
+KvView value_view(const dec_kv_cache& c) {
+    return {c.v, c.v_scale, c.v_page_stride, c.v_slot_stride, c.v_head_stride};
+}
+
+// A row stride: 0 stands for packed rows of n elements.
+int resolve_ld(int64_t* ld, int64_t n) {
+    if (*ld == 0) *ld = n;
+    if (*ld < n) return W4A16_ERR_INVALID_ARG;
+    return *ld % 8 == 0 ? W4A16_OK : W4A16_ERR_UNSUPPORTED;
+}
+
+int check_attn(const dec_attn_config* cfg, const dec_kv_cache* cache) {
+    if (!cfg || !cache || cfg->reserved != 0) return W4A16_ERR_INVALID_ARG;
+    int rc = check_cache(cache);
+    if (rc != W4A16_OK) return rc;
+    if (!dtype_ok(cfg->dtype) || (cache->dtype != DEC_KV_E4M3 && cache->dtype != cfg->dtype))
+        return W4A16_ERR_UNSUPPORTED;
+    if (cfg->q_heads < 1 || cfg->q_heads % cache->kv_heads != 0 || cfg->max_pages < 1 ||
+        cfg->window < 0 || !std::isfinite(cfg->scale))
+        return W4A16_ERR_INVALID_ARG;
+    // token numbers are 32-bit
+    if (static_cast<int64_t>(cfg->max_pages) * cache->page_size > 0x7FFFFF00LL)
+        return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+}  // namespace
+
+int dec_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                 const void* weight, int M, int H, int dtype, float eps, void* residual_out,
+                 void* y, int64_t ldy, void* stream) {
+    return norm_common(x, ldx, residual, ldr, weight, M, H, dtype, eps, residual_out, y, ldy,
+                       nullptr, kNormSame, stream);
+}
+
+int dec_rms_norm_i8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                    const void* weight, int M, int H, int dtype, float eps,
+                    void* residual_out, int8_t* y_i8, float* s_y, void* stream) {
+    return norm_common(x, ldx, residual, ldr, weight, M, H, dtype, eps, residual_out, y_i8, 0,
+                       s_y, kNormI8, stream);
+}
+
+int dec_rms_norm_mx(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                    const void* weight, int M, int H, int dtype, float eps,
+                    void* residual_out, uint8_t* y_codes, uint8_t* y_scales, void* stream) {
+    return norm_common(x, ldx, residual, ldr, weight, M, H, dtype, eps, residual_out, y_codes, 0,
+                       y_scales, kNormMx, stream);
+}
+
+int dec_rope_table(int rot_dim, double base, const dec_rope_scaling* scaling, float* table,
+                   int table_len, void* stream) {
+    if (table_len < 0 || !(base > 1.0) || !std::isfinite(base)) return W4A16_ERR_INVALID_ARG;
+    if (rot_dim < 2 || rot_dim > 256 || rot_dim % 2 != 0) return W4A16_ERR_UNSUPPORTED;
+    RopeTableArgs a{base, 1.0, 0.0, 1.0, 1.0, 1.0, DEC_ROPE_SCALE_NONE, rot_dim, table_len, table};
+    if (scaling) {
+        if (scaling->kind < DEC_ROPE_SCALE_NONE || scaling->kind > DEC_ROPE_SCALE_RAMP ||
+            !(scaling->magnitude >= 0.0f) || !std::isfinite(scaling->magnitude))
+            return W4A16_ERR_INVALID_ARG;
+        if (scaling->kind != DEC_ROPE_SCALE_NONE &&
+            (!(scaling->factor > 0.0f) || !std::isfinite(scaling->factor)))
+            return W4A16_ERR_INVALID_ARG;
+        if (scaling->kind == DEC_ROPE_SCALE_BASE && rot_dim < 4) return W4A16_ERR_UNSUPPORTED;
+        if (scaling->kind == DEC_ROPE_SCALE_RAMP &&
+            (!(scaling->low < scaling->high) || !std::isfinite(scaling->low) ||
+             !std::isfinite(scaling->high) || !(scaling->original_len > 0.0f) ||
+             !std::isfinite(scaling->original_len)))
+            return W4A16_ERR_INVALID_ARG;
+        a.kind = scaling->kind;
+        a.factor = scaling->factor;
+        a.low = scaling->low;
+        a.high = scaling->high;
+        a.original_len = scaling->original_len;
+        if (scaling->magnitude != 0.0f) a.magnitude = scaling->magnitude;
+    }
+    if (table_len == 0) return W4A16_OK;
+    if (!table || !aligned(table, 16)) return W4A16_ERR_INVALID_ARG;
+    return launch_rope_table(a, static_cast<cudaStream_t>(stream));
+}
+
+int dec_rope_append(const dec_rope_config* cfg, const dec_kv_cache* cache, const void* q,
+                    const void* k, const void* v, int T, const int32_t* positions,
+                    const int64_t* slots, void* q_out, void* k_out, void* stream) {
+    if (!cfg || T < 0 || cfg->reserved != 0 || cfg->q_heads < 0 || cfg->kv_heads < 0 ||
+        cfg->head_dim < 1 || cfg->rot_dim < 0 || cfg->table_len < 0 ||
+        (cfg->layout != DEC_ROPE_HALF && cfg->layout != DEC_ROPE_INTERLEAVED))
+        return W4A16_ERR_INVALID_ARG;
+    if (!dtype_ok(cfg->dtype) || cfg->head_dim % 8 != 0 || cfg->head_dim > 256 ||
+        cfg->rot_dim % 2 != 0)
+        return W4A16_ERR_UNSUPPORTED;
+    if (cfg->rot_dim > cfg->head_dim) return W4A16_ERR_INVALID_ARG;
+    // head and pair numbers of a token are 32-bit
+    if (cfg->q_heads > (1 << 20) || cfg->kv_heads > (1 << 20)) return W4A16_ERR_UNSUPPORTED;
+    if (cache) {
+        const int rc = check_cache(cache);
+        if (rc != W4A16_OK) return rc;
+        if (cache->kv_heads != cfg->kv_heads || cache->head_dim != cfg->head_dim)
+            return W4A16_ERR_INVALID_ARG;
+        if (cache->dtype != DEC_KV_E4M3 && cache->dtype != cfg->dtype)
+            return W4A16_ERR_UNSUPPORTED;
+    }
+    RopeArgs a{};
+    const int64_t nq = static_cast<int64_t>(cfg->q_heads) * cfg->head_dim;
+    const int64_t nk = static_cast<int64_t>(cfg->kv_heads) * cfg->head_dim;
+    a.ldq = cfg->ldq, a.ldk = cfg->ldk, a.ldv = cfg->ldv, a.ldqo = cfg->ldqo, a.ldko = cfg->ldko;
+    int rc = 0;
+    if ((rc = resolve_ld(&a.ldq, nq)) || (rc = resolve_ld(&a.ldk, nk)) ||
+        (rc = resolve_ld(&a.ldv, nk)) || (rc = resolve_ld(&a.ldqo, nq)) ||
+        (rc = resolve_ld(&a.ldko, nk)))
+        return rc;
+    if (T == 0 || (nq == 0 && nk == 0)) return W4A16_OK;
+    if ((nq && (!q || !q_out)) || (nk && !k) || (nk && cache && !v) || !positions ||
+        (cache && !slots) || (cfg->rot_dim && !cfg->table))
+        return W4A16_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+        !aligned(k_out, 16) || !aligned(cfg->table, 16) || !aligned(positions, 4) ||
+        !aligned(slots, 8))
+        return W4A16_ERR_INVALID_ARG;
+    const DeviceCtx* ctx = nullptr;
+    if ((rc = get_ctx(&ctx)) != W4A16_OK) return rc;
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.k_out = static_cast<uint16_t*>(k_out);
+    a.table = cfg->table;
+    a.positions = positions;
+    a.slots = slots;
+    a.page_size = 1;
+    if (cache) {
+        a.kc = key_view(*cache);
+        a.vc = value_view(*cache);
+        a.num_slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
+        a.page_size = cache->page_size;
+    }
+    a.T = T;
+    a.q_heads = cfg->q_heads;
+    a.kv_heads = cfg->kv_heads;
+    a.head_dim = cfg->head_dim;
+    a.rot_dim = cfg->rot_dim;
+    a.layout = cfg->layout;
+    a.table_len = cfg->table_len;
+    a.status = ctx->status;
+    return launch_rope(*ctx, a, cfg->dtype, cache && cache->dtype == DEC_KV_E4M3,
+                       static_cast<cudaStream_t>(stream));
+}
+
+size_t dec_attn_workspace_bytes(const dec_attn_config* cfg, const dec_kv_cache* cache) {
+    if (check_attn(cfg, cache) != W4A16_OK) return 0;
+    const DeviceCtx* ctx = nullptr;
+    if (get_ctx(&ctx) != W4A16_OK) return 0;
+    return attn_workspace_bytes(*ctx, cfg->q_heads, cache->kv_heads, cache->head_dim,
+                                cache->dtype == DEC_KV_E4M3);
+}
+
+int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const void* q,
+                   const int32_t* block_table, const int32_t* lens, int B, void* out,
+                   float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    int rc = check_attn(cfg, cache);
+    if (rc != W4A16_OK) return rc;
+    if (B < 0) return W4A16_ERR_INVALID_ARG;
+    AttnArgs a{};
+    const int64_t nq = static_cast<int64_t>(cfg->q_heads) * cache->head_dim;
+    a.ldq = cfg->ldq, a.ldo = cfg->ldo;
+    if ((rc = resolve_ld(&a.ldq, nq)) || (rc = resolve_ld(&a.ldo, nq))) return rc;
+    a.ld_table = cfg->ld_table ? cfg->ld_table : cfg->max_pages;
+    if (a.ld_table < cfg->max_pages) return W4A16_ERR_INVALID_ARG;
+    if (B == 0) return W4A16_OK;
+    if (!q || !block_table || !lens || !out || !workspace) return W4A16_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
+        !aligned(lse, 4) || !aligned(workspace, 16))
+        return W4A16_ERR_INVALID_ARG;
+    const DeviceCtx* ctx = nullptr;
+    if ((rc = get_ctx(&ctx)) != W4A16_OK) return rc;
+    const bool e4m3 = cache->dtype == DEC_KV_E4M3;
+    if (ws_bytes < attn_workspace_bytes(*ctx, cfg->q_heads, cache->kv_heads, cache->head_dim, e4m3))
+        return W4A16_ERR_INVALID_ARG;
+    a.q = static_cast<const uint16_t*>(q);
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.block_table = block_table;
+    a.lens = lens;
+    a.kc = key_view(*cache);
+    a.vc = value_view(*cache);
+    a.scale = cfg->scale;
+    a.B = B;
+    a.q_heads = cfg->q_heads;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.page_size = cache->page_size;
+    a.num_pages = cache->num_pages;
+    a.max_pages = cfg->max_pages;
+    a.window = cfg->window;
+    a.workspace = workspace;
+    a.status = ctx->status;
+    return launch_attn(*ctx, a, cfg->dtype, e4m3, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -78,6 +78,68 @@ int launch_mx_gemm(const DeviceCtx& ctx, const uint8_t* a_codes, const uint8_t* 
                    const void* packed, int M, int N, int K, int dtype, void* Y,
                    cudaStream_t stream);
 
+// Decoder-layer operators (norm.cu, rope.cu, attn.cu); arguments as in include/decode.h,
+// checked by the C entries, strides resolved.
+constexpr int kNormSame = 0, kNormI8 = 1, kNormMx = 2;  // output form
+struct NormArgs {
+    const uint16_t* x;
+    const uint16_t* residual;  // or null
+    const uint16_t* weight;    // or null
+    uint16_t* residual_out;    // or null
+    void* y;
+    void* scales;              // float [M] (i8), uint8 [M][H/32] (mx)
+    int64_t ldx, ldr, ldy;
+    int H;
+    float eps;
+};
+int launch_norm(const DeviceCtx& ctx, const NormArgs& a, int M, int dtype, int out,
+                cudaStream_t stream);
+
+struct RopeTableArgs {
+    double base, factor, low, high, original_len, magnitude;
+    int kind, rot_dim, table_len;
+    float* table;
+};
+int launch_rope_table(const RopeTableArgs& a, cudaStream_t stream);
+
+struct KvView {  // one side (keys or values) of a paged cache; strides in elements
+    void* p;
+    const float* scale;  // or null
+    int64_t page_stride, slot_stride, head_stride;
+};
+struct RopeArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *k_out;  // or null
+    int64_t ldq, ldk, ldv, ldqo, ldko;
+    const float* table;
+    const int32_t* positions;
+    const int64_t* slots;
+    KvView kc, vc;            // kc.p null: no cache
+    int64_t num_slots;
+    int T, q_heads, kv_heads, head_dim, rot_dim, layout, table_len, page_size;
+    int* status;
+};
+int launch_rope(const DeviceCtx& ctx, const RopeArgs& a, int dtype, bool e4m3,
+                cudaStream_t stream);
+
+struct AttnArgs {
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;  // or null
+    const int32_t* block_table;
+    const int32_t* lens;
+    KvView kc, vc;
+    int64_t ldq, ldo, ld_table;
+    float scale;
+    int B, q_heads, kv_heads, head_dim, page_size, num_pages, max_pages, window;
+    void* workspace;
+    int* status;
+};
+size_t attn_workspace_bytes(const DeviceCtx& ctx, int q_heads, int kv_heads, int head_dim,
+                            bool e4m3);
+int launch_attn(const DeviceCtx& ctx, const AttnArgs& a, int dtype, bool e4m3,
+                cudaStream_t stream);
+
 // Rows of A staged per 64-K chunk (8 or 16 for decode tiles, else the tile height).
 int tc_a_rows(int tile_m, int M);
 // 128-K weight blocks per ring stage (one bulk copy each stage).
