@@ -110,6 +110,8 @@ class AttnConfig(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """Loads libw4a16.so (built by weight_only_int4_tma_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -202,10 +204,20 @@ def _ptr(x):
     return x.data_ptr()
 
 
+def _current_stream() -> int:
+    """The current torch stream's handle.  The first call binds torch's raw accessors: the
+    Stream object of torch.cuda.current_stream() costs 3 us, most of a small launch."""
+    global _current_stream
+    import torch
+    torch.cuda.current_stream()  # initialises CUDA
+    device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

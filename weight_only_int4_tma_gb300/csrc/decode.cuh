@@ -25,6 +25,15 @@ __device__ __forceinline__ uint16_t dec_from_f32(float v) {
     else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Two values rounded and packed, lo in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t dec_pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (DT == 0) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Two fp32 values to E4M3, round to nearest even, saturated to +-448 (lo in the low byte).
 __device__ __forceinline__ uint32_t dec_e4m3x2(float lo, float hi) {
     uint16_t r;

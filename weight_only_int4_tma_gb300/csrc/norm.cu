@@ -3,12 +3,14 @@
 // written in the input's type, as int8 with one scale per row (max |y| / 127), or as E4M3
 // with one power-of-two scale per 32 values.  Everything between the loads and the stores
 // is fp32; h is rounded only for residual_out.
+//
+// A row is read once: its threads hold it in registers, in 16-byte pieces of 8 values, from
+// the loads over the reductions to the stores.  Bound by HBM for many rows, by the latency
+// of one load, two block reductions and one store for few.
 #include "decode.cuh"
 
 namespace w4g {
 namespace {
-
-constexpr int kNormThreads = 256;
 
 // E8M0 exponent of a block whose largest magnitude is `most`: floor(log2(most)) - 8 (8 is
 // the exponent of E4M3's largest value), at least -127; -127 for a zero block.  Below the
@@ -22,34 +24,165 @@ __device__ __forceinline__ float norm_pow2(int e) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-__device__ __forceinline__ float norm_block_sum(float v, float* red) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.0f;
-    for (int w = 0; w < kNormThreads / 32; ++w) s += red[w];
-    __syncthreads();
-    return s;
+template <int DT>
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = dec_to_f32<DT>(static_cast<uint16_t>(w[j] & 0xFFFFu));
+        f[2 * j + 1] = dec_to_f32<DT>(static_cast<uint16_t>(w[j] >> 16));
+    }
 }
-__device__ __forceinline__ float norm_block_max(float v, float* red) {
-    v = warp_max(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.0f;
-    for (int w = 0; w < kNormThreads / 32; ++w) s = fmaxf(s, red[w]);
-    __syncthreads();
-    return s;
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(dec_pack2<DT>(f[0], f[1]), dec_pack2<DT>(f[2], f[3]),
+                      dec_pack2<DT>(f[4], f[5]), dec_pack2<DT>(f[6], f[7]));
 }
 
-// One CTA per row, one value per thread and step.
-template <int DT, int OUT>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
+// Reduction over the warps of one row (warps row_warp0 .. + row_warps - 1 of the CTA); every
+// thread of the CTA takes part, `red` holds one value per warp.
+template <bool kMax>
+__device__ __forceinline__ float row_reduce(float v, float* red, int row_warp0, int row_warps) {
+    v = kMax ? warp_max(v) : warp_sum(v);
+    if (row_warps == 1) return v;
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < row_warps ? red[row_warp0 + lane] : 0.0f;  // sums and magnitudes: 0 is neutral
+    return kMax ? warp_max(v) : warp_sum(v);
+}
+
+// `row_threads` (a multiple of 32) threads per row, rows_per_cta rows per CTA, V pieces per
+// thread: piece p of a row is held by thread p % row_threads.
+template <int DT, int OUT, int V>
+__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int M, int row_threads) {
+    __shared__ float red[2][32];
+    const int in_cta = static_cast<int>(threadIdx.x) / row_threads;
+    const int t = static_cast<int>(threadIdx.x) - in_cta * row_threads;
+    const int rows_per_cta = static_cast<int>(blockDim.x) / row_threads;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * rows_per_cta + in_cta;
+    const int row_warps = row_threads >> 5, row_warp0 = in_cta * row_warps;
+    const int pieces = a.H >> 3;
+    const bool live = m < M;
+    float h[V][8];
+    uint4 xv[V], rv[V], wv[V];
+    grid_dep_wait();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int p = t + j * row_threads;
+        const bool in = live && p < pieces;
+        xv[j] = rv[j] = wv[j] = make_uint4(0, 0, 0, 0);
+        if (in) {
+            xv[j] = reinterpret_cast<const uint4*>(a.x + m * a.ldx)[p];
+            if (a.residual) rv[j] = reinterpret_cast<const uint4*>(a.residual + m * a.ldr)[p];
+        }
+    }
+    if (a.weight) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int p = t + j * row_threads;
+            if (p < pieces) wv[j] = reinterpret_cast<const uint4*>(a.weight)[p];
+        }
+    }
+    grid_dep_launch();
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float r8[8];
+        unpack8<DT>(xv[j], h[j]);
+        unpack8<DT>(rv[j], r8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[j][e] += r8[e];
+            ss = fmaf(h[j][e], h[j][e], ss);
+        }
+    }
+    ss = row_reduce<false>(ss, red[0], row_warp0, row_warps);
+    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
+    if (a.residual_out) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int p = t + j * row_threads;
+            if (live && p < pieces)
+                reinterpret_cast<uint4*>(a.residual_out + m * a.ldr)[p] = pack8<DT>(h[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float w8[8];
+        unpack8<DT>(wv[j], w8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] = a.weight ? h[j][e] * r * w8[e] : h[j][e] * r;
+    }
+    if constexpr (OUT == kNormSame) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int p = t + j * row_threads;
+            if (live && p < pieces)
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + m * a.ldy)[p] =
+                    pack8<DT>(h[j]);
+        }
+    } else if constexpr (OUT == kNormI8) {
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(h[j][e]));
+        most = row_reduce<true>(most, red[1], row_warp0, row_warps);
+        const float s = most > 0.0f ? __fdiv_rn(most, 127.0f) : 1.0f;
+        uint2* y = reinterpret_cast<uint2*>(static_cast<int8_t*>(a.y) + m * a.H);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int p = t + j * row_threads;
+            uint32_t o[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                int q = __float2int_rn(__fdiv_rn(h[j][e], s));
+                q = max(-127, min(127, q));
+                o[e >> 2] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (e & 3));
+            }
+            if (live && p < pieces) y[p] = make_uint2(o[0], o[1]);
+        }
+        if (live && t == 0) static_cast<float*>(a.scales)[m] = s;
+    } else {
+        uint2* y = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + m * a.H);
+        uint8_t* sc = static_cast<uint8_t*>(a.scales) + m * (a.H / 32);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int p = t + j * row_threads;
+            float most = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(h[j][e]));
+            // a block of 32 is the pieces of four neighbouring lanes
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            const int e2 = norm_mx_exponent(most);
+            const float f = norm_pow2(-e2);
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = dec_e4m3x2(h[j][2 * e] * f, h[j][2 * e + 1] * f);
+            if (live && p < pieces) {
+                y[p] = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+                if ((p & 3) == 0) sc[p >> 2] = static_cast<uint8_t>(e2 + 127);
+            }
+        }
+    }
+}
+
+constexpr int kNormThreads = 256;
+
+// Rows that are not 16-byte aligned, of a length that is no multiple of 8, or longer than
+// 32768: one CTA per row, one value per thread and step, the row read twice (the second time
+// from L1 or L2).
+template <int DT>
+__global__ void __launch_bounds__(kNormThreads) norm_any_kernel(NormArgs a) {
     __shared__ float red[kNormThreads / 32];
     grid_dep_wait();
-    const int m = static_cast<int>(blockIdx.x);
+    const int64_t m = blockIdx.x;
     const uint16_t* x = a.x + m * a.ldx;
     const uint16_t* res = a.residual ? a.residual + m * a.ldr : nullptr;
     uint16_t* res_out = a.residual_out ? a.residual_out + m * a.ldr : nullptr;
+    uint16_t* y = static_cast<uint16_t*>(a.y) + m * a.ldy;
     auto value = [&](int i) {
         float h = dec_to_f32<DT>(x[i]);
         if (res) h += dec_to_f32<DT>(res[i]);
@@ -60,65 +193,57 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
         const float h = value(i);
         ss += h * h;
     }
-    ss = norm_block_sum(ss, red);
+    ss = row_reduce<false>(ss, red, 0, kNormThreads / 32);
     const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
-    auto normed = [&](int i, float h) {
+    for (int i = threadIdx.x; i < a.H; i += kNormThreads) {
+        const float h = value(i);
         const float w = a.weight ? dec_to_f32<DT>(a.weight[i]) : 1.0f;
-        return h * r * w;
-    };
-    if constexpr (OUT == kNormSame) {
-        uint16_t* y = static_cast<uint16_t*>(a.y) + m * a.ldy;
-        for (int i = threadIdx.x; i < a.H; i += kNormThreads) {
-            const float h = value(i);
-            const uint16_t out = dec_from_f32<DT>(normed(i, h));
-            if (res_out) res_out[i] = dec_from_f32<DT>(h);
-            y[i] = out;
-        }
-    } else if constexpr (OUT == kNormI8) {
-        float most = 0.0f;
-        for (int i = threadIdx.x; i < a.H; i += kNormThreads)
-            most = fmaxf(most, fabsf(normed(i, value(i))));
-        most = norm_block_max(most, red);
-        const float s = most > 0.0f ? __fdiv_rn(most, 127.0f) : 1.0f;
-        int8_t* y = static_cast<int8_t*>(a.y) + static_cast<int64_t>(m) * a.H;
-        for (int i = threadIdx.x; i < a.H; i += kNormThreads) {
-            const float h = value(i);
-            const int q = __float2int_rn(__fdiv_rn(normed(i, h), s));
-            if (res_out) res_out[i] = dec_from_f32<DT>(h);
-            y[i] = static_cast<int8_t>(max(-127, min(127, q)));
-        }
-        if (threadIdx.x == 0) static_cast<float*>(a.scales)[m] = s;
-    } else {
-        uint8_t* y = static_cast<uint8_t*>(a.y) + static_cast<int64_t>(m) * a.H;
-        uint8_t* sc = static_cast<uint8_t*>(a.scales) + static_cast<int64_t>(m) * (a.H / 32);
-        for (int i = threadIdx.x; i < a.H; i += kNormThreads) {  // H % 32 == 0: whole warps
-            const float h = value(i);
-            const float v = normed(i, h);
-            const float most = warp_max(fabsf(v));
-            const int e = norm_mx_exponent(most);
-            if (res_out) res_out[i] = dec_from_f32<DT>(h);
-            y[i] = static_cast<uint8_t>(dec_e4m3x2(v * norm_pow2(-e), 0.0f));
-            if ((i & 31) == 0) sc[i / 32] = static_cast<uint8_t>(e + 127);
-        }
+        if (res_out) res_out[i] = dec_from_f32<DT>(h);
+        y[i] = dec_from_f32<DT>(h * r * w);
     }
 }
 
+template <int DT, int OUT, int V>
+int launch_norm_v(const NormArgs& a, int M, int row_threads, cudaStream_t stream) {
+    // several short rows share a CTA
+    const int rows = row_threads >= 256 ? 1 : 256 / row_threads;
+    return launch_dependent(norm_kernel<DT, OUT, V>, dim3(static_cast<unsigned>((M + rows - 1) / rows)),
+                            rows * row_threads, 0, stream, a, M, row_threads);
+}
+
+template <int DT, int OUT>
+int launch_norm_out(const DeviceCtx& ctx, const NormArgs& a, int M, cudaStream_t stream) {
+    const int pieces = a.H / 8;
+    // Few rows: one piece per thread where 1024 threads suffice (latency).  Rows for every
+    // SM: four pieces per thread, so that several CTAs of independent loads share an SM.
+    int V = M <= ctx.num_sms ? (pieces + 1023) / 1024 : (pieces >= 128 ? 4 : 1);
+    V = V <= 1 ? 1 : V <= 2 ? 2 : 4;
+    const int row_threads = ((pieces + V - 1) / V + 31) / 32 * 32;
+    if (V == 1) return launch_norm_v<DT, OUT, 1>(a, M, row_threads, stream);
+    if (V == 2) return launch_norm_v<DT, OUT, 2>(a, M, row_threads, stream);
+    return launch_norm_v<DT, OUT, 4>(a, M, row_threads, stream);
+}
+
 template <int DT>
-int launch_norm_dt(const NormArgs& a, int M, int out, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(M));
-    if (out == kNormSame)
-        return launch_dependent(norm_kernel<DT, kNormSame>, grid, kNormThreads, 0, stream, a);
-    if (out == kNormI8)
-        return launch_dependent(norm_kernel<DT, kNormI8>, grid, kNormThreads, 0, stream, a);
-    return launch_dependent(norm_kernel<DT, kNormMx>, grid, kNormThreads, 0, stream, a);
+int launch_norm_dt(const DeviceCtx& ctx, const NormArgs& a, int M, int out, cudaStream_t stream) {
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
+                            reinterpret_cast<uintptr_t>(a.weight) |
+                            reinterpret_cast<uintptr_t>(a.residual_out);
+    if (out == kNormI8) return launch_norm_out<DT, kNormI8>(ctx, a, M, stream);
+    if (out == kNormMx) return launch_norm_out<DT, kNormMx>(ctx, a, M, stream);
+    const bool pieces = a.H % 8 == 0 && a.H <= 32768 && a.ldx % 8 == 0 && a.ldr % 8 == 0 &&
+                        a.ldy % 8 == 0 && (bases | reinterpret_cast<uintptr_t>(a.y)) % 16 == 0;
+    if (pieces) return launch_norm_out<DT, kNormSame>(ctx, a, M, stream);
+    return launch_dependent(norm_any_kernel<DT>, dim3(static_cast<unsigned>(M)), kNormThreads, 0,
+                            stream, a);
 }
 
 }  // namespace
 
 int launch_norm(const DeviceCtx& ctx, const NormArgs& a, int M, int dtype, int out,
                 cudaStream_t stream) {
-    (void)ctx;
-    return dtype == 0 ? launch_norm_dt<0>(a, M, out, stream) : launch_norm_dt<1>(a, M, out, stream);
+    return dtype == 0 ? launch_norm_dt<0>(ctx, a, M, out, stream)
+                      : launch_norm_dt<1>(ctx, a, M, out, stream);
 }
 
 }  // namespace w4g
