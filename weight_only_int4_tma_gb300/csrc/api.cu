@@ -607,8 +607,8 @@ int check_attn(const dec_attn_config* cfg, const dec_kv_cache* cache) {
     if (cfg->q_heads < 1 || cfg->q_heads % cache->kv_heads != 0 || cfg->max_pages < 1 ||
         cfg->window < 0 || !std::isfinite(cfg->scale))
         return W4A16_ERR_INVALID_ARG;
-    // token numbers are 32-bit
-    if (static_cast<int64_t>(cfg->max_pages) * cache->page_size > 0x7FFFFF00LL)
+    // token numbers are 32-bit, with room for steps past the end
+    if (static_cast<int64_t>(cfg->max_pages) * cache->page_size > 0x7FFF0000LL)
         return W4A16_ERR_UNSUPPORTED;
     return W4A16_OK;
 }

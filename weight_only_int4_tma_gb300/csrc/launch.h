@@ -133,6 +133,7 @@ struct AttnArgs {
     float scale;
     int B, q_heads, kv_heads, head_dim, page_size, num_pages, max_pages, window;
     void* workspace;
+    int max_ctas;  // of any instance: where the workspace's parts begin (set by launch_attn)
     int* status;
 };
 size_t attn_workspace_bytes(const DeviceCtx& ctx, int q_heads, int kv_heads, int head_dim,
