@@ -100,10 +100,12 @@ struct AttnShape {
     static constexpr int Q_BYTES = NT * MS * 32 * 8;
     static constexpr int O_FLOATS = kAttnWarps * ROWS * DP;
     static constexpr int SMEM = Q_BYTES + 4 * O_FLOATS;
+    // a join keeps one factor per part and row where the warps' sums stood before
+    static_assert(kAttnWarps * DP >= 64, "at most 57 parts in one round");
 };
 
-// Where the parts of one CTA stand in the workspace: counters first (as many as any instance
-// has CTAs, so that calls of different instances may share a workspace), then for each CTA two
+// Where the parts of one CTA stand in the workspace: counters first (three times as many
+// as any instance has CTAs, so that calls of different instances may share a workspace), then for each CTA two
 // parts (its first item if that began in an earlier CTA, its last if that ends in a later
 // one) of m[ROWS], l[ROWS], O[ROWS][DP].
 __host__ __device__ constexpr size_t part_floats(int rows, int dp) {
@@ -129,6 +131,13 @@ __device__ __forceinline__ Span visible(const AttnArgs& a, int b, bool report) {
 template <int STEP>
 __device__ __forceinline__ int span_steps(Span s) {
     return s.len == 0 ? 0 : (s.len + STEP - 1) / STEP - s.first / STEP;
+}
+
+// a / b; the long division only where 32 bits do not hold the numbers.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0)
+        return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
 }
 
 template <class S>
@@ -174,8 +183,7 @@ __global__ void __launch_bounds__(kAttnThreads, S::OCC) attn_kernel(AttnArgs a, 
         total += scan[w];
     }
     // whole rounds of the warps: a share of fewer steps would take as long
-    const long long rounds = (total + static_cast<long long>(ctas) * kAttnWarps - 1) /
-                             (static_cast<long long>(ctas) * kAttnWarps);
+    const long long rounds = quotient(total + ctas * kAttnWarps - 1, ctas * kAttnWarps);
     const long long share = max(rounds, 1ll) * kAttnWarps;
     long long u = share * cta;
     const long long u_end = min(total, u + share);
@@ -205,11 +213,11 @@ __global__ void __launch_bounds__(kAttnThreads, S::OCC) attn_kernel(AttnArgs a, 
     int b = find_b;
     Span span = visible(a, b, false);
     int n_steps = span_steps<STEP>(span);
-    int item = static_cast<int>(find_u / n_steps);
+    int item = static_cast<int>(quotient(find_u, n_steps));
     int step = static_cast<int>(find_u - static_cast<long long>(item) * n_steps);
 
     int* counters = static_cast<int*>(a.workspace);
-    float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counter_bytes(a.max_ctas));
+    float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counter_bytes(3 * a.max_ctas));
     const uint32_t row_bytes = static_cast<uint32_t>(a.head_dim) * S::ES;
 
     while (u < u_end) {
@@ -561,50 +569,84 @@ __global__ void __launch_bounds__(kAttnThreads, S::OCC) attn_kernel(AttnArgs a, 
         if (whole) {
             if (tid < rows) store_lse(tid, row_m[tid], row_l[tid]);
         } else {
-            // ---- join the CTAs: the last one to arrive reads every part, in order ----
-            const int c0 = static_cast<int>((u - step) / share);
-            const int c1 = static_cast<int>((u - step + n_steps - 1) / share);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                is_last = atomicAdd(counters + c0, 1) == c1 - c0;
-                if (is_last) counters[c0] = 0;  // ready for the next call
+            // ---- join the CTAs: the last one to arrive reads the others' parts, in order ----
+            // Many parts are joined in two rounds, runs of `fan` first: one CTA reads about
+            // 0.1 TB/s, and 456 parts of 8 rows and 128 dimensions are 1.9 MB.
+            const int c0 = static_cast<int>(quotient(u - step, share));
+            const int n = static_cast<int>(quotient(u - step + n_steps - 1, share)) - c0 + 1;
+            const int fan = n <= 16 ? n : n <= 256 ? 16 : 32;
+            auto part_of = [&](int k) {  // part k of the item
+                return parts + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * part_floats(ROWS, DP);
+            };
+            // true in every thread of the CTA that completes the counter's `want` arrivals
+            auto arrive = [&](int* counter, int want) {
                 __threadfence();
-            }
-            __syncthreads();
-            if (is_last) {
-                auto part_of = [&](int c) {
-                    return parts + (2 * c + (c == c0 ? 1 : 0)) * part_floats(ROWS, DP);
-                };
-                for (int row = warp; row < rows; row += kAttnWarps) {
-                    float top = -INFINITY, sum = 0.0f;
-                    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(part_of(c) + row));
-                    top = warp_max(top);
-                    for (int c = c0 + lane; c <= c1; c += 32) {
-                        const float f = top == -INFINITY ? 0.0f : exp2_fast(__ldcg(part_of(c) + row) - top);
-                        sum += f * __ldcg(part_of(c) + ROWS + row);
-                    }
-                    sum = warp_sum(sum);
-                    if (lane == 0) {
-                        row_m[row] = top, row_l[row] = sum;
-                        store_lse(row, top, sum);
-                    }
+                __syncthreads();
+                if (tid == 0) {
+                    is_last = atomicAdd(counter, 1) == want - 1;
+                    if (is_last) *counter = 0;  // ready for the next call
+                    __threadfence();
                 }
                 __syncthreads();
-                for (int e = tid; e < rows * words; e += kAttnThreads) {
-                    const int row = e / words, d = 2 * (e - row * words);
-                    const float top = row_m[row];
-                    float2 v = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* p = part_of(c);
-                        const float2 x = __ldcg(reinterpret_cast<const float2*>(p + 2 * ROWS + row * DP + d));
+                return is_last != 0;
+            };
+            // parts k0, k0 + stride, ... (count of them) into one: written over part k0, or
+            // stored as the result
+            auto join = [&](int k0, int stride, int count, bool final) {
+                for (int row = warp; row < rows; row += kAttnWarps) {
+                    float top = -INFINITY;
+                    for (int k = lane; k < count; k += 32)
+                        top = fmaxf(top, __ldcg(part_of(k0 + k * stride) + row));
+                    top = warp_max(top);
+                    float sum = 0.0f;
+                    for (int k = lane; k < count; k += 32) {
+                        const float* p = part_of(k0 + k * stride);
                         const float f = top == -INFINITY ? 0.0f : exp2_fast(__ldcg(p + row) - top);
-                        v.x += x.x * f;
-                        v.y += x.y * f;
+                        sum += f * __ldcg(p + ROWS + row);
+                        so[k * ROWS + row] = f;  // count <= kMaxFan of them
                     }
-                    store(row, d, v.x, v.y, row_l[row]);
+                    sum = warp_sum(sum);
+                    if (lane == 0) row_m[row] = top, row_l[row] = sum;
                 }
+                __syncthreads();
+                float* to = part_of(k0);
+                for (int e = tid; e < rows * (DP / 4); e += kAttnThreads) {
+                    const int row = e / (DP / 4), d = 4 * (e % (DP / 4));
+                    if (d >= a.head_dim) continue;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int k = 0; k < count; k += 8) {
+                        float4 x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            x[j] = k + j < count ? __ldcg(reinterpret_cast<const float4*>(
+                                                       part_of(k0 + (k + j) * stride) + 2 * ROWS + row * DP + d))
+                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float f = k + j < count ? so[(k + j) * ROWS + row] : 0.0f;
+                            v.x += x[j].x * f, v.y += x[j].y * f;
+                            v.z += x[j].z * f, v.w += x[j].w * f;
+                        }
+                    }
+                    if (final) {
+                        store(row, d, v.x, v.y, row_l[row]);
+                        store(row, d + 2, v.z, v.w, row_l[row]);
+                    } else {
+                        *reinterpret_cast<float4*>(to + 2 * ROWS + row * DP + d) = v;
+                    }
+                }
+                if (tid < rows) {
+                    if (final) store_lse(tid, row_m[tid], row_l[tid]);
+                    else to[tid] = row_m[tid], to[ROWS + tid] = row_l[tid];
+                }
+            };
+            const int mine_k = cta - c0, run = mine_k / fan, runs = (n + fan - 1) / fan;
+            // counters by the CTA of the run's first part.  That CTA may end one item and
+            // begin another, so first runs, later runs and second rounds count apart.
+            int* first = counters + (run == 0 ? 0 : a.max_ctas) + c0 + run * fan;
+            if (arrive(first, min(fan, n - run * fan))) {
+                join(run * fan, 1, min(fan, n - run * fan), runs == 1);
+                if (runs > 1 && arrive(counters + 2 * a.max_ctas + c0, runs)) join(0, fan, runs, true);
             }
         }
         // ---- the next item ----
@@ -667,7 +709,7 @@ size_t attn_workspace_bytes(const DeviceCtx& ctx, int q_heads, int kv_heads, int
     const int ctas = ctx.num_sms * kMaxCtasPerSm;
     const int rows = q_heads / kv_heads <= 8 ? 8 : 16;
     const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    return counter_bytes(ctas) + 2ull * ctas * part_floats(rows, dp) * 4;
+    return counter_bytes(3 * ctas) + 2ull * ctas * part_floats(rows, dp) * 4;
 }
 
 int launch_attn(const DeviceCtx& ctx, const AttnArgs& args, int dtype, bool e4m3,
