@@ -736,8 +736,7 @@ size_t dec_attn_workspace_bytes(const dec_attn_config* cfg, const dec_kv_cache* 
     if (check_attn(cfg, cache) != W4A16_OK) return 0;
     const DeviceCtx* ctx = nullptr;
     if (get_ctx(&ctx) != W4A16_OK) return 0;
-    return attn_workspace_bytes(*ctx, cfg->q_heads, cache->kv_heads, cache->head_dim,
-                                cache->dtype == DEC_KV_E4M3);
+    return attn_workspace_bytes(*ctx, cfg->q_heads, cache->kv_heads, cache->head_dim);
 }
 
 int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const void* q,
@@ -760,7 +759,7 @@ int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const 
     const DeviceCtx* ctx = nullptr;
     if ((rc = get_ctx(&ctx)) != W4A16_OK) return rc;
     const bool e4m3 = cache->dtype == DEC_KV_E4M3;
-    if (ws_bytes < attn_workspace_bytes(*ctx, cfg->q_heads, cache->kv_heads, cache->head_dim, e4m3))
+    if (ws_bytes < attn_workspace_bytes(*ctx, cfg->q_heads, cache->kv_heads, cache->head_dim))
         return W4A16_ERR_INVALID_ARG;
     a.q = static_cast<const uint16_t*>(q);
     a.out = static_cast<uint16_t*>(out);
@@ -779,6 +778,7 @@ int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const 
     a.max_pages = cfg->max_pages;
     a.window = cfg->window;
     a.workspace = workspace;
+    a.timeout_ns = ctx->timeout_ns;
     a.status = ctx->status;
     return launch_attn(*ctx, a, cfg->dtype, e4m3, static_cast<cudaStream_t>(stream));
 }

@@ -1,0 +1,934 @@
+// Attention of one new token per sequence over a paged key-value cache (include/decode.h):
+//   s_j = scale q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j)  over the visible tokens.
+//
+// The keys and values are read once and nothing else of size is: with G query heads per
+// key-value head the work is 2 G operations per cached 16-bit value, far below what the
+// tensor cores do in the time of the read, so the kernel is built to keep loads in flight.
+//
+// Data path.  Steps of 16 R tokens go through a ring in shared memory of about 190 KB (one CTA
+// per SM): four producer warps fill it with asynchronous copies, eight consumer warps take its
+// steps in turn, each working alone.  ldmatrix turns a step into mma.sync operands:
+//   S^T = K Q^T   tokens are the MMA's 16 rows, query heads its 8 columns (with 8 heads or
+//                 fewer per key-value head half of a 16-row query tile would be padding);
+//   O^T = V^T P^T head dimensions are the rows; ldmatrix's transposed form reads V^T.
+// 8-bit caches are converted to fp16 between ldmatrix and MMA (exact), two values at a time.
+// The probabilities leave S^T with tokens in rows and are wanted with tokens as the K index:
+// one 8 x 8 transpose of 16-bit pairs (movmatrix).  They are split in a high and a low
+// 16-bit part, each multiplied with V: a single 16-bit rounding of P (2^-9 for bf16) would
+// show in the result as much as the result's own.
+//
+// Softmax.  One pass with a running reference m per query head: weights are exp2(s - m), and
+// when a score passes m by more than 2^8 the sums so far are scaled to the new reference
+// (a warp vote finds out; exact in the end, since numerator and denominator share it).
+//
+// Work split.  The steps of all (sequence, head, row tile) items stand in one line that is
+// cut into equal shares, one per CTA, whatever the lengths; every CTA finds its share from
+// the lengths on the device.  The producers run on into the next item while the consumers
+// finish one.  An item inside one CTA is finished there; one that is cut leaves (m, l, O) in fp32 in the
+// workspace, and the CTA that arrives last joins the parts in their order.
+#pragma once
+#include "decode.cuh"
+
+namespace w4g {
+
+constexpr float kLag = 8.0f;       // scores may pass the reference by 2^8
+constexpr int kMaxJoin = 16;       // parts that one CTA joins at once
+
+// Parts of cut items in the workspace: three counters per CTA first, then for each CTA two
+// parts (its first item if that began in an earlier CTA, its last if that ends in a later
+// one) of m[rows], l[rows], O[rows][dp].
+__host__ __device__ constexpr size_t attn_part_floats(int rows, int dp) {
+    return static_cast<size_t>(rows) * (dp + 2);
+}
+__host__ __device__ constexpr size_t attn_counter_bytes(int ctas) {
+    return (static_cast<size_t>(ctas) * 12 + 127) / 128 * 128;
+}
+
+namespace {
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 bytes global -> shared, asynchronously; zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+// Arrives on the barrier once this thread's copies so far are there.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Barrier of the consumer warps alone.
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+// D += A B, 16 x 8 x 16, fp32 accumulate; BF: bf16 operands, else fp16.
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// DT: 0 fp16, 1 bf16 (queries, output).  E4M3: 8-bit cache.  DP: head dimension rounded up
+// to 64, 128 or 256.  NT: tiles of 8 query heads that a CTA takes at once.  P16: the page
+// size is a multiple of 16, so 16 tokens that begin at a multiple of 16 lie in one page.
+template <int DT_, bool E4M3_, int DP_, int NT_, bool P16_>
+struct AttnShape {
+    static constexpr int DT = DT_, DP = DP_, NT = NT_;
+    static constexpr bool E4M3 = E4M3_, P16 = P16_;
+    static constexpr bool BF = DT == 1 && !E4M3;  // type of the MMA's operands
+    static constexpr int ES = E4M3 ? 1 : 2;
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int PITCH = DP * ES;         // bytes of a token's row in the ring
+    static constexpr int CH = PITCH / 16;         // 16-byte chunks of it
+    // 16 R tokens per step: 4 KB of keys where that is at most 64 tokens; 32 where every
+    // lane looks up the page of one token
+    static constexpr int R = PITCH >= 256 ? 1 : PITCH == 128 ? 2 : (P16 ? 4 : 2);
+    static constexpr int STEP = 16 * R;
+    static constexpr int SLOT = STEP * PITCH;     // bytes of a step's keys, or values
+    static constexpr int W = 8;                   // consumer warps
+    static constexpr int PW = 4;                  // producer warps
+    static constexpr int NST = 196608 / (2 * SLOT);            // steps of the ring
+    static constexpr int MS = DP / 16;            // MMA steps over the head dimension
+    static constexpr int OP = DP + 4;             // row of the warps' sums, in floats
+    static constexpr int SOE = NT == 1 ? (DP == 256 ? 2 : 4) : DP == 256 ? 1 : 2;  // warps' sums
+                                                               // in shared memory at once
+    static constexpr int THREADS = 32 * (W + PW);
+    static constexpr int RING = NST * 2 * SLOT;
+    static constexpr int SMEM = RING + SOE * ROWS * OP * 4 + NST * (4 + 3 * 8);
+    static_assert(NST >= W && SMEM <= 224 * 1024 && W % SOE == 0, "the ring fits");
+    static_assert(SOE * OP >= 2 * kMaxJoin, "a join's numbers fit where the sums stood");
+};
+
+// Byte offset of chunk c of token row r in a slot: the chunks of eight rows that ldmatrix
+// reads together stand in different 16-byte columns of 128.
+template <int CH>
+__device__ __forceinline__ constexpr uint32_t ring_at(int r, int c) {
+    return static_cast<uint32_t>(r * CH * 16 + ((CH >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Visible tokens [first, len) of sequence b.
+struct Span {
+    int first, len;
+};
+__device__ __forceinline__ Span visible(const AttnArgs& a, int b, bool report) {
+    int len = a.lens[b];
+    const int most = a.max_pages * a.page_size;
+    if (len < 0 || len > most) {
+        if (report) record_status(a.status, kDecInvalidArg);
+        len = len < 0 ? 0 : most;
+    }
+    return {a.window > 0 && len > a.window ? len - a.window : 0, len};
+}
+template <int STEP>
+__device__ __forceinline__ int span_steps(Span s) {
+    return s.len == 0 ? 0 : (s.len + STEP - 1) / STEP - s.first / STEP;
+}
+
+// a / b; the long division only where 32 bits do not hold the numbers.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0)
+        return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
+
+// One item's steps [step, step_end) of n_steps, as one CTA takes them.
+struct Segment {
+    int b, item, step, step_end, n_steps;
+    Span span;
+};
+
+// An item cut over several CTAs: parts of the CTAs c0 .. c0 + n - 1, and where its rows go.
+struct Cut {
+    int c0, n, b, head0, rows, last;  // last: this CTA's arrival completed its run of parts
+    float vs;
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int page_shift) {
+    constexpr int NT = S::NT, R = S::R, DP = S::DP, ROWS = S::ROWS, STEP = S::STEP, W = S::W;
+    constexpr int NST = S::NST, MS = S::MS, CH = S::CH;
+    constexpr int T = S::BF ? 1 : 0;                  // type of the weights
+    constexpr float kShift = S::BF ? 0.0f : 7.0f;     // see the weights below
+    extern __shared__ __align__(1024) unsigned char smem[];
+    float* so = reinterpret_cast<float*>(smem + S::RING);        // [SOE][ROWS][OP]
+    // per step of the ring: its keys are there, its values are there, it may be refilled
+    uint64_t* bars = reinterpret_cast<uint64_t*>(so + S::SOE * ROWS * S::OP);
+    uint32_t* metas = reinterpret_cast<uint32_t*>(bars + 3 * NST);   // which tokens have a page
+    __shared__ int abort_flag;
+    __shared__ float sm_m[W][ROWS], sm_l[W][ROWS];
+    __shared__ float row_m[ROWS], row_l[ROWS];
+    __shared__ long long scan[2][W + S::PW];
+    __shared__ int find_b;
+    __shared__ long long find_u;
+    __shared__ Segment segs[2];      // the current one and the one after it, in turn
+    __shared__ Cut cuts[2];          // an item that began in an earlier CTA, one that ends in a later
+    __shared__ int is_last;
+
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, i = lane & 3;
+    const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+    const int G = a.q_heads / a.kv_heads;
+    const int row_tiles = (G + ROWS - 1) / ROWS;
+    const int items_per_seq = a.kv_heads * row_tiles;
+    const int row_bytes = a.head_dim * S::ES;
+    int* counters = static_cast<int*>(a.workspace);
+    float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + attn_counter_bytes(ctas));
+
+    if (row_bytes < S::PITCH) {  // columns past the head dimension are never copied: zero
+        for (int e = tid; e < S::RING / 16; e += S::THREADS)
+            reinterpret_cast<uint4*>(smem)[e] = make_uint4(0, 0, 0, 0);
+    }
+    const uint32_t full_k = smem_addr(bars), full_v = full_k + 8 * NST, empty = full_v + 8 * NST;
+    if (tid < NST) {
+        mbar_init(full_k + 8 * tid, 33);  // 32 lanes' copies, and the word of `metas`
+        mbar_init(full_v + 8 * tid, 32);
+        mbar_init(empty + 8 * tid, 1);
+    }
+    if (tid == 0) abort_flag = 0;
+    grid_dep_wait();
+    // ---- this CTA's share ----
+    const int per_thread = (a.B + S::THREADS - 1) / S::THREADS;
+    const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
+    // exclusive sum over the threads' sequences, and the total
+    auto block_scan = [&](long long mine, int slot, long long& total) {
+        long long incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) scan[slot][warp] = incl;
+        __syncthreads();
+        long long before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < W + S::PW; ++w) {
+            if (w < warp) before += scan[slot][w];
+            total += scan[slot][w];
+        }
+        return before + incl - mine;
+    };
+    // steps in the low bits, sequences that have any above them
+    constexpr int kSeqBit = 40;
+    long long mine = 0, total = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int n = span_steps<STEP>(visible(a, b, cta == 0));
+        mine += n + (n ? 1ll << kSeqBit : 0);
+    }
+    long long excl = block_scan(mine, 0, total);
+    const long long seqs = total >> kSeqBit, items = seqs * items_per_seq;
+    constexpr long long kLow = (1ll << kSeqBit) - 1;
+    total = (total & kLow) * items_per_seq;
+    // Whole rounds of the warps: a share of fewer steps would take as long.  Where a share is
+    // cut from one item alone (no CTA has two partial items to write and join one after the
+    // other) it takes up to `items` shares more; that is worth one round.
+    const int slots = ctas * W;
+    const long long rounds = max(quotient(total + slots - 1, slots), 1ll);
+    bool apart = false;
+    long long share = rounds * W;
+    if (2 * items <= ctas) {
+        const int left = static_cast<int>(ctas - items) * W;
+        const long long r = max(quotient(total + left - 1, left), 1ll);
+        apart = r <= rounds + 1;
+        if (apart) share = r * W;
+    }
+    // u: position in the line of steps, or (apart) in the line of parts
+    long long u = apart ? cta : share * cta, u_end = min(total, u + share);
+    mine = (mine & kLow) * items_per_seq;
+    excl = (excl & kLow) * items_per_seq;
+    auto parts_of = [&](int n_steps) { return static_cast<int>(quotient(n_steps + share - 1, share)); };
+    if (apart) {
+        mine = 0;
+        for (int b = b_lo; b < b_hi; ++b)
+            mine += static_cast<long long>(parts_of(span_steps<STEP>(visible(a, b, false)))) * items_per_seq;
+        excl = block_scan(mine, 1, total);
+        u_end = min(total, u + 1);
+    }
+    if (u < u_end && excl <= u && u < excl + mine) {  // one thread at most
+        long long at = excl;
+        int b = b_lo;
+        for (; b + 1 < b_hi; ++b) {
+            const int n_steps = span_steps<STEP>(visible(a, b, false));
+            const long long n = static_cast<long long>(apart ? parts_of(n_steps) : n_steps) * items_per_seq;
+            if (u < at + n) break;
+            at += n;
+        }
+        find_b = b;
+        find_u = u - at;
+    }
+    // rows with nothing to attend to
+    for (int b = cta; b < a.B; b += ctas) {
+        if (visible(a, b, false).len != 0) continue;
+        uint16_t* o = a.out + b * a.ldo;
+        for (int e = tid; e < a.q_heads * a.head_dim; e += S::THREADS) o[e] = 0;
+        if (a.lse)
+            for (int h = tid; h < a.q_heads; h += S::THREADS)
+                a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
+    }
+    __syncthreads();
+    if (u >= u_end) return;
+
+    // the segment after `s`: the next item's first steps, at most `left`
+    auto after = [&](const Segment& s, int left) {
+        Segment n = s;
+        if (++n.item == items_per_seq) {
+            n.item = 0;
+            do {
+                ++n.b;
+                n.span = visible(a, n.b, false);
+                n.n_steps = span_steps<STEP>(n.span);
+            } while (n.n_steps == 0 && n.b + 1 < a.B);
+        }
+        n.step = 0;
+        n.step_end = min(n.n_steps, left);
+        return n;
+    };
+    int left = static_cast<int>(u_end - u);  // steps of this CTA not yet begun
+    Segment ld;
+    ld.b = find_b;
+    ld.span = visible(a, ld.b, false);
+    ld.n_steps = span_steps<STEP>(ld.span);
+    {
+        const int per_item = apart ? parts_of(ld.n_steps) : ld.n_steps;
+        ld.item = static_cast<int>(quotient(find_u, per_item));
+        ld.step = static_cast<int>(find_u - static_cast<long long>(ld.item) * per_item);
+        if (apart) ld.step *= static_cast<int>(share);
+        ld.step_end = static_cast<int>(min(static_cast<long long>(ld.n_steps), ld.step + (apart ? share : left)));
+    }
+    if (apart) left = ld.step_end - ld.step;
+    if (tid == 0) {
+        segs[0] = ld;
+        cuts[0].last = cuts[1].last = 0;
+    }
+    __syncthreads();  // segs, the barriers, and the zeroed ring
+
+    const uint32_t ring = smem_addr(smem);
+    if (warp >= W) {
+        // ---- producers: steps pw, pw + PW, ... of the CTA's share ----
+        const int pw = warp - W;
+        constexpr int RPI = 32 / CH;   // token rows that one instruction of the warp copies
+        static_assert(CH <= 32, "a row is one instruction at most");
+        const int lrow = lane / CH, lchunk = lane % CH;
+        const bool column = 16 * lchunk < row_bytes;    // this lane's chunk is within the head
+        const int64_t kss = a.kc.slot_stride * S::ES, vss = a.vc.slot_stride * S::ES;
+        const int64_t kps = a.kc.page_stride * S::ES, vps = a.vc.page_stride * S::ES;
+        const uint32_t lane_at = ring_at<CH>(lrow, lchunk);
+        auto page_of = [&](int tok) { return page_shift >= 0 ? tok >> page_shift : tok / a.page_size; };
+        auto wanted = [&](int tok) {
+            return tok < ld.span.len && (S::P16 ? tok + 16 > ld.span.first : tok >= ld.span.first);
+        };
+        // Page numbers.  P16: lane n R + r has that of group r of the warp's n-th step from the
+        // batch's first on, 32 / R steps at a time and the next ones under way; else lane t
+        // has that of token t of the next step.
+        constexpr int PB = S::P16 ? 32 / R : 1;
+        const int32_t* table;
+        const char* kbase;
+        const char* vbase;
+        int first_st, pid = 0, pid_next = 0, in_batch = 0;
+        auto fetch_pages = [&](int st) {
+            const int s_ = S::P16 ? st + lane / R * S::PW : st;
+            const int tok = s_ * STEP + (S::P16 ? 16 * (lane % R) : lane);
+            int p = 0;
+            if (s_ < first_st + ld.step_end && (S::P16 || lane < STEP) && wanted(tok)) p = table[page_of(tok)];
+            return p;
+        };
+        auto open = [&](int st) {  // begins segment ld at token step ld's first + st
+            const int head = ld.item / row_tiles;
+            first_st = ld.span.first / STEP;
+            table = a.block_table + ld.b * a.ld_table;
+            kbase = static_cast<const char*>(a.kc.p) + head * a.kc.head_stride * S::ES + lrow * kss + 16 * lchunk;
+            vbase = static_cast<const char*>(a.vc.p) + head * a.vc.head_stride * S::ES + lrow * vss + 16 * lchunk;
+            pid = fetch_pages(first_st + st);
+            pid_next = fetch_pages(first_st + st + PB * S::PW);
+            in_batch = 0;
+        };
+        constexpr int NP = S::P16 ? R : 1;
+        // one side's copies of a step: rows of `at` (bytes from base: of each group's first row,
+        // or of the lane's token), `lo` <= token < `hi`
+        auto copy = [&](uint32_t dst, const char* base, const int64_t (&at)[NP], int64_t stride,
+                        uint32_t there, int lo, int hi, bool partial) {
+            if (S::P16 && !partial) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const char* p = base + at[r];
+#pragma unroll
+                    for (int j = 0; j < 16 / RPI; ++j) {
+                        const uint32_t to = (dst ^ (CH >= 8 ? ((RPI * j) & 7) << 4 : 0)) + (16 * r + RPI * j) * S::PITCH;
+                        if (column) copy16(to, p, 16);
+                        p += RPI * stride;
+                    }
+                }
+                return;
+            }
+#pragma unroll 1
+            for (int t0 = 0; t0 < STEP; t0 += RPI) {
+                const int t = t0 + lrow;
+                const char* p;
+                bool ok;
+                if constexpr (S::P16) {
+                    int64_t from = at[0];
+#pragma unroll
+                    for (int r = 1; r < R; ++r) from = t0 / 16 == r ? at[r] : from;
+                    p = base + from + (t0 % 16) * stride;
+                    ok = (there >> (t0 / 16)) & 1u;
+                } else {
+                    p = base - lrow * stride + __shfl_sync(0xFFFFFFFFu, at[0], t);
+                    ok = (there >> t) & 1u;
+                }
+                ok = ok && t >= lo && t < hi;
+                const uint32_t to = (dst ^ (CH >= 8 ? (t0 & 7) << 4 : 0)) + t0 * S::PITCH;
+                if (column) copy16(to, ok ? p : base, ok ? 16 : 0);
+            }
+        };
+        int seg0 = 0;                                   // steps of the share before segment ld
+        int seg_n = ld.step_end - ld.step;
+        open(ld.step + pw);
+        int stage = pw;
+        uint32_t phase = 0;
+        const int n_all = left;
+#pragma unroll 1
+        for (int x = pw; x < n_all; x += S::PW) {
+            if (x >= seg0 + seg_n) {
+                do {
+                    seg0 += seg_n;
+                    ld = after(ld, n_all - seg0);
+                    seg_n = ld.step_end - ld.step;
+                } while (x >= seg0 + seg_n);
+                open(ld.step + x - seg0);
+            }
+            const int st = first_st + ld.step + x - seg0;
+            int64_t kat[NP], vat[NP];
+            uint32_t there = 0;  // groups (P16) or tokens whose page is there
+#pragma unroll
+            for (int r = 0; r < NP; ++r) {
+                const int tok = st * STEP + (S::P16 ? 16 * r : lane);
+                const int page = S::P16 ? __shfl_sync(0xFFFFFFFFu, pid, in_batch * R + r) : pid;
+                const bool in = wanted(tok) && (S::P16 || lane < STEP);
+                const bool ok = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages);
+                if (in && !ok) record_status(a.status, kDecInvalidArg);
+                const int slot = tok - page_of(tok) * a.page_size;
+                kat[r] = ok ? page * kps + slot * kss : 0;
+                vat[r] = ok ? page * vps + slot * vss : 0;
+                if constexpr (S::P16) there |= static_cast<uint32_t>(ok) << r;
+                else there = __ballot_sync(0xFFFFFFFFu, ok);
+            }
+            const int lo = ld.span.first - st * STEP, hi = ld.span.len - st * STEP;
+            const bool partial = there != (1u << R) - 1 || lo > 0 || hi < STEP;
+            mbar_wait_warp(empty + 8 * stage, phase ^ 1u, &abort_flag, a.status, a.timeout_ns);
+            const uint32_t dst = ring + stage * 2 * S::SLOT + lane_at;
+            if (lane == 0) {
+                metas[stage] = there;
+                mbar_arrive(full_k + 8 * stage);
+            }
+            copy(dst, kbase, kat, kss, there, lo, hi, partial);
+            copies_arrive(full_k + 8 * stage);
+            copy(dst + S::SLOT, vbase, vat, vss, there, lo, hi, partial);
+            copies_arrive(full_v + 8 * stage);
+            if (++in_batch == PB) {
+                in_batch = 0;
+                pid = pid_next;
+                pid_next = fetch_pages(st + (PB + 1) * S::PW);  // the batch after the one from st + PW on
+            }
+            stage += S::PW;
+            if (stage >= NST) stage -= NST, phase ^= 1u;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
+
+    // ---- consumers ----
+    constexpr int CT = 32 * W;  // their threads
+    // ---- parts of an item that several CTAs took ----
+    auto part_of = [&](const Cut& c, int k) {  // part k of the item
+        return parts + (2 * (c.c0 + k) + (k == 0 ? 1 : 0)) * attn_part_floats(ROWS, DP);
+    };
+    // After the CTA's part is written: counts it; thread 0 learns whether it was the last.
+    auto arrive = [&](int* counter, int want, int* last) {
+        __threadfence();
+        consumers_sync<CT>();
+        if (tid == 0) {
+            *last = atomicAdd(counter, 1) == want - 1;
+            if (*last) *counter = 0;  // ready for the next call
+            __threadfence();
+        }
+    };
+    auto store = [&](const Cut& c, int row, int d, float4 v, float sum) {
+        const float f = sum > 0.0f ? c.vs / sum : 0.0f;
+        uint16_t* dst = a.out + c.b * a.ldo + static_cast<int64_t>(c.head0 + row) * a.head_dim + d;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(dec_pack2<S::DT>(v.x * f, v.y * f), dec_pack2<S::DT>(v.z * f, v.w * f));
+    };
+    auto store_lse = [&](const Cut& c, int row, float top, float sum) {
+        if (a.lse)
+            a.lse[static_cast<int64_t>(c.b) * a.q_heads + c.head0 + row] =
+                sum > 0.0f ? (top - kShift) * 0.69314718055994531f + logf(sum) : -INFINITY;
+    };
+    constexpr int E = (ROWS * DP / 4 + CT - 1) / CT;  // 16-byte pieces per thread
+    // Parts k0, k0 + stride, ... (count of them, at most kMaxJoin) into one: written over part
+    // k0, or stored as the result.
+    auto join = [&](const Cut& c, int k0, int stride, int count, bool final) {
+        constexpr int KB = E >= 8 ? 2 : 16 / E;     // parts in flight
+        float* jm = so;                             // [part][row]: m, then its factor
+        float* jl = so + kMaxJoin * ROWS;           // [part][row]
+        for (int e = tid; e < count * ROWS; e += CT) {
+            const float* p = part_of(c, k0 + e / ROWS * stride) + e % ROWS;
+            const bool in = e % ROWS < c.rows;
+            jm[e] = in ? __ldcg(p) : -INFINITY;
+            jl[e] = in ? __ldcg(p + ROWS) : 0.0f;
+        }
+        float4 acc[E], x[KB][E];
+        auto fetch = [&](int k) {
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+                    x[j][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (k + j < count && row < c.rows && d < a.head_dim)
+                        x[j][e] = __ldcg(reinterpret_cast<const float4*>(
+                            part_of(c, k0 + (k + j) * stride) + 2 * ROWS + row * DP + d));
+                }
+        };
+        fetch(0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        consumers_sync<CT>();
+        for (int row = warp; row < ROWS; row += W) {
+            const float m = lane < count ? jm[lane * ROWS + row] : -INFINITY;
+            const float top = warp_max(m);
+            const float f = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+            const float sum = warp_sum(lane < count ? f * jl[lane * ROWS + row] : 0.0f);
+            if (lane < count) jm[lane * ROWS + row] = f;
+            if (lane == 0) row_m[row] = top, row_l[row] = sum;
+        }
+        consumers_sync<CT>();
+        for (int k = 0; k < count; k += KB) {
+            if (k) fetch(k);
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int row = (tid + e * CT) / (DP / 4);
+                    const float f = k + j < count && row < ROWS ? jm[(k + j) * ROWS + row] : 0.0f;
+                    acc[e].x = fmaf(x[j][e].x, f, acc[e].x), acc[e].y = fmaf(x[j][e].y, f, acc[e].y);
+                    acc[e].z = fmaf(x[j][e].z, f, acc[e].z), acc[e].w = fmaf(x[j][e].w, f, acc[e].w);
+                }
+        }
+        float* to = part_of(c, k0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+            if (row >= c.rows || d >= a.head_dim) continue;
+            if (final) store(c, row, d, acc[e], row_l[row]);
+            else *reinterpret_cast<float4*>(to + 2 * ROWS + row * DP + d) = acc[e];
+        }
+        if (tid < c.rows) {
+            if (final) store_lse(c, tid, row_m[tid], row_l[tid]);
+            else to[tid] = row_m[tid], to[ROWS + tid] = row_l[tid];
+        }
+    };
+    // Joins what this CTA's arrival completed.  More than kMaxJoin parts are joined in two
+    // rounds, runs of kMaxJoin first: one CTA reads about 0.1 TB/s, and the 152 parts of one
+    // item of 8 rows and 128 dimensions are 0.6 MB.
+    auto settle = [&](const Cut& c) {
+        if (!c.last) return;
+        const int run = (cta - c.c0) / kMaxJoin, runs = (c.n + kMaxJoin - 1) / kMaxJoin;
+        join(c, run * kMaxJoin, 1, min(kMaxJoin, c.n - run * kMaxJoin), runs == 1);
+        if (runs > 1) {
+            arrive(counters + 2 * ctas + c.c0, runs, &is_last);
+            consumers_sync<CT>();
+            if (is_last) join(c, 0, kMaxJoin, runs, true);
+        }
+        consumers_sync<CT>();
+    };
+
+    // ---- addresses of ldmatrix's rows in a slot, for this lane ----
+    const int mi = lane >> 3, l7 = lane & 7;
+    const uint32_t kfrag = ring_at<CH>((mi & 1) * 8 + l7, mi >> 1);
+    const uint32_t vfrag = S::E4M3 ? kfrag : ring_at<CH>((mi >> 1) * 8 + l7, mi & 1);
+    // chunk pair c, c + 1 (c even) of group r, from the address of chunk pair 0
+    auto pair_at = [](int r, int c) {
+        return static_cast<uint32_t>(r * 16 * S::PITCH + (CH >= 8 ? (c & ~7) << 4 : 0));
+    };
+
+    int stage = warp;          // of this warp's next step
+    uint32_t phase = 0;
+    int taken = 0;             // steps of the share before the segment
+    for (int turn = 0;; turn ^= 1) {
+        const Segment& cur = segs[turn];
+        left -= cur.step_end - cur.step;
+        if (left > 0 && tid == 0) segs[turn ^ 1] = after(cur, left);
+        const int kvh = cur.item / row_tiles, row0 = (cur.item - kvh * row_tiles) * ROWS;
+        const int rows = min(ROWS, G - row0), head0 = kvh * G + row0;
+        const Span span = cur.span;
+
+        // queries as B fragments: lane (g, i) has four values of row 8 nt + g per MMA step.
+        // With an 8-bit cache the MMA is fp16: bf16 queries are scaled there by a power of
+        // two per row that brings the largest to 2^8..2^9, undone in the row's factor.
+        uint32_t qf[NT][MS][2];
+        float fct[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g;
+            const uint16_t* q = a.q + cur.b * a.ldq + static_cast<int64_t>(head0 + r) * a.head_dim;
+#pragma unroll
+            for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = S::E4M3 ? 16 * ms + 4 * i + 2 * h : 16 * ms + 8 * h + 2 * i;
+                    qf[nt][ms][h] = r < rows && col < a.head_dim ? *reinterpret_cast<const uint32_t*>(q + col) : 0;
+                }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f = a.scale * 1.4426950408889634f;
+            if (S::E4M3 && a.kc.scale) f *= a.kc.scale[kvh];
+            if constexpr (S::E4M3 && S::DT == 1) {
+                uint32_t top = 0;  // of the magnitudes, as numbers of 15 bits
+#pragma unroll
+                for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        top = max(top, max(qf[nt][ms][h] & 0x7FFFu, (qf[nt][ms][h] >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const int e = static_cast<int>(top >> 7) - 127;
+                float up = 1.0f;
+                if (e > -119 && e < 128) {
+                    up = __uint_as_float(static_cast<uint32_t>(8 - e + 127) << 23);
+                    f *= __uint_as_float(static_cast<uint32_t>(e - 8 + 127) << 23);
+                }
+#pragma unroll
+                for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t v = qf[nt][ms][h];
+                        qf[nt][ms][h] = dec_pack2<0>(__uint_as_float(v << 16) * up,
+                                                     __uint_as_float(v & 0xFFFF0000u) * up);
+                    }
+            }
+            fct[nt][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * i);      // of rows 2i and 2i + 1
+            fct[nt][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * i + 4);
+        }
+
+        // ---- the warp's steps ----
+        float m[NT][2], ref[NT][2], l[NT][2], o[NT][MS][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) m[nt][c] = -INFINITY, ref[nt][c] = 0.0f, l[nt][c] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < MS; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
+        }
+        const int st1 = span.first / STEP + cur.step_end;
+        // step x of the share is warp x % W's
+        int st = span.first / STEP + cur.step + ((warp - taken) & (W - 1));
+        taken += cur.step_end - cur.step;
+#pragma unroll 1
+        for (; st < st1; st += W) {
+            const uint32_t kslot = ring + stage * 2 * S::SLOT, vslot = kslot + S::SLOT;
+            mbar_wait_warp(full_k + 8 * stage, phase, &abort_flag, a.status, a.timeout_ns);
+            const uint32_t there = metas[stage];
+            float s[R][NT][4];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float s2[NT][4];  // two sums at a time: half the MMA's latency
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[r][nt][e] = s2[nt][e] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
+                    uint32_t k[4];
+                    ldmatrix4<false>(k, kslot + (kfrag ^ ((c & 7) << 4)) + pair_at(r, c));
+                    if constexpr (S::E4M3) {  // chunks c and c + 1 are a step each
+                        const uint32_t a0 = dec_e4m3x2_to_f16x2(k[0]), a1 = dec_e4m3x2_to_f16x2(k[1]);
+                        const uint32_t a2 = dec_e4m3x2_to_f16x2(k[0] >> 16), a3 = dec_e4m3x2_to_f16x2(k[1] >> 16);
+                        const uint32_t b0 = dec_e4m3x2_to_f16x2(k[2]), b1 = dec_e4m3x2_to_f16x2(k[3]);
+                        const uint32_t b2 = dec_e4m3x2_to_f16x2(k[2] >> 16), b3 = dec_e4m3x2_to_f16x2(k[3] >> 16);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<S::BF>(s[r][nt], a0, a1, a2, a3, qf[nt][c][0], qf[nt][c][1]);
+                            mma16816<S::BF>(s2[nt], b0, b1, b2, b3, qf[nt][c + 1][0], qf[nt][c + 1][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float(&to)[4] = (c & 2) ? s2[nt] : s[r][nt];
+                            mma16816<S::BF>(to, k[0], k[1], k[2], k[3], qf[nt][c / 2][0], qf[nt][c / 2][1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[r][nt][e] += s2[nt][e];
+            }
+            // scores in units of log 2; those of tokens that do not count are -inf
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[r][nt][e] *= fct[nt][e & 1];
+            if (!S::P16 || there != (1u << R) - 1 || st * STEP < span.first || st * STEP + STEP > span.len) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = 16 * r + g + 8 * h, tok = st * STEP + t;
+                        const bool ok = ((there >> (S::P16 ? r : t)) & 1u) && tok >= span.first && tok < span.len;
+                        if (!ok) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) s[r][nt][2 * h] = s[r][nt][2 * h + 1] = -INFINITY;
+                        }
+                    }
+            }
+            bool passed = false;
+            float tops[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < R; ++r) top = fmaxf(top, fmaxf(s[r][nt][c], s[r][nt][c + 2]));
+                    tops[nt][c] = top;
+                    passed |= top > m[nt][c] + kLag;
+                }
+            if (__any_sync(0xFFFFFFFFu, passed)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float top = fmaxf(m[nt][c], tops[nt][c]);
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                        const float f = top == m[nt][c] ? 1.0f : exp2_fast(m[nt][c] - top);
+                        m[nt][c] = top;
+                        ref[nt][c] = top == -INFINITY ? 0.0f : top - kShift;
+                        l[nt][c] *= f;
+#pragma unroll
+                        for (int ms = 0; ms < MS; ++ms) {
+                            o[nt][ms][c] *= f;
+                            o[nt][ms][c + 2] *= f;
+                        }
+                    }
+            }
+            // weights, split in 16-bit parts, as B fragments.  fp16 keeps 2^-14 as its
+            // smallest full number: its weights are scaled by 2^7 (at most 2^15 with the lag).
+            uint32_t ph[R][NT][2], pl[R][NT][2];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float p[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            p[c] = exp2_fast(s[r][nt][2 * h + c] - ref[nt][c]);
+                            l[nt][c] += p[c];
+                        }
+                        const uint32_t hi = dec_pack2<T>(p[0], p[1]);
+                        const float low0 = p[0] - dec_to_f32<T>(static_cast<uint16_t>(hi & 0xFFFFu));
+                        const float low1 = p[1] - dec_to_f32<T>(static_cast<uint16_t>(hi >> 16));
+                        ph[r][nt][h] = transpose8x8(hi);
+                        pl[r][nt][h] = transpose8x8(dec_pack2<T>(low0, low1));
+                    }
+            mbar_wait_warp(full_v + 8 * stage, phase, &abort_flag, a.status, a.timeout_ns);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int c = 0; c < CH; c += 2) {
+                    uint32_t v[4];
+                    ldmatrix4<true>(v, vslot + (vfrag ^ ((c & 7) << 4)) + pair_at(r, c));
+                    auto accumulate = [&](int ms, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<S::BF>(o[nt][ms], a0, a1, a2, a3, ph[r][nt][0], ph[r][nt][1]);
+                            mma16816<S::BF>(o[nt][ms], a0, a1, a2, a3, pl[r][nt][0], pl[r][nt][1]);
+                        }
+                    };
+                    if constexpr (S::E4M3) {
+                        // a pair of bytes per token: (d, d + 1) of tokens 2i, 2i + 1 to pairs of tokens
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = __byte_perm(v[2 * h], 0, 0x3120);
+                            const uint32_t y = __byte_perm(v[2 * h + 1], 0, 0x3120);
+                            accumulate(c + h, dec_e4m3x2_to_f16x2(x), dec_e4m3x2_to_f16x2(x >> 16),
+                                       dec_e4m3x2_to_f16x2(y), dec_e4m3x2_to_f16x2(y >> 16));
+                        }
+                    } else {
+                        accumulate(c / 2, v[0], v[1], v[2], v[3]);
+                    }
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * stage);
+            stage += W;
+            if (stage >= NST) stage -= NST, phase ^= 1u;
+        }
+
+        // ---- join the warps, SOE of them at a time ----
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float v = l[nt][c];
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+                const int row = 8 * nt + 2 * i + c;
+                if (g == 0) sm_m[warp][row] = m[nt][c], sm_l[warp][row] = v;
+            }
+        float4 acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w0 = 0; w0 < W; w0 += S::SOE) {
+            if (w0) consumers_sync<CT>();
+            if (warp >= w0 && warp < w0 + S::SOE) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int row = 8 * nt + 2 * i + c;
+                        if (row >= rows) continue;
+                        float* dst = so + ((warp - w0) * ROWS + row) * S::OP;
+#pragma unroll
+                        for (int ms = 0; ms < MS; ++ms) {
+                            dst[16 * ms + (S::E4M3 ? 2 * g : g)] = o[nt][ms][c];
+                            dst[16 * ms + (S::E4M3 ? 2 * g + 1 : g + 8)] = o[nt][ms][c + 2];
+                        }
+                    }
+            }
+            consumers_sync<CT>();
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+                if (row >= rows) continue;
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w][row]);
+#pragma unroll
+                for (int w = 0; w < S::SOE; ++w) {
+                    const float mw = sm_m[w0 + w][row];
+                    const float f = mw == -INFINITY ? 0.0f : exp2_fast(mw - top);
+                    const float4 x = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * S::OP + d);
+                    acc[e].x = fmaf(x.x, f, acc[e].x), acc[e].y = fmaf(x.y, f, acc[e].y);
+                    acc[e].z = fmaf(x.z, f, acc[e].z), acc[e].w = fmaf(x.w, f, acc[e].w);
+                }
+            }
+        }
+        auto row_sum = [&](int row, float& top) {
+            top = -INFINITY;
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w][row]);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float mw = sm_m[w][row];
+                sum += mw == -INFINITY ? 0.0f : sm_l[w][row] * exp2_fast(mw - top);
+            }
+            return sum;
+        };
+        const bool begins = cur.step == 0, ends = cur.step_end == cur.n_steps;
+        const bool whole = begins && ends;
+        Cut here{0, 0, cur.b, head0, rows, 0, S::E4M3 && a.vc.scale ? a.vc.scale[kvh] : 1.0f};
+        float* part = parts + (2 * cta + (begins ? 1 : 0)) * attn_part_floats(ROWS, DP);
+        float top;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+            if (row >= rows || d >= a.head_dim) continue;
+            if (whole) store(here, row, d, acc[e], row_sum(row, top));
+            else *reinterpret_cast<float4*>(part + 2 * ROWS + row * DP + d) = acc[e];
+        }
+        if (tid < rows) {
+            const float sum = row_sum(tid, top);
+            if (whole) store_lse(here, tid, top, sum);
+            else part[tid] = top, part[ROWS + tid] = sum;
+        }
+        if (!whole) {
+            if (apart) {
+                here.c0 = cta - static_cast<int>(quotient(cur.step, share));
+                here.n = parts_of(cur.n_steps);
+            } else {
+                here.c0 = static_cast<int>(quotient(u - cur.step, share));
+                here.n = static_cast<int>(quotient(u - cur.step + cur.n_steps - 1, share)) - here.c0 + 1;
+            }
+            // counters by the CTA of the run's first part.  That CTA may end one item and
+            // begin another, so first runs, later runs and second rounds count apart.
+            const int run = (cta - here.c0) / kMaxJoin;
+            if (tid == 0) cuts[begins] = here;
+            arrive(counters + (run == 0 ? 0 : ctas) + here.c0 + run * kMaxJoin,
+                   min(kMaxJoin, here.n - run * kMaxJoin), &cuts[begins].last);
+        }
+        if (left <= 0) break;
+        u += cur.step_end - cur.step;
+        consumers_sync<CT>();
+    }
+    consumers_sync<CT>();
+    settle(cuts[0]);
+    settle(cuts[1]);
+}
+
+template <class S>
+int launch_attn_shape(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(attn_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) !=
+        cudaSuccess)
+        return -3;
+    int shift = -1;
+    if ((a.page_size & (a.page_size - 1)) == 0)
+        for (shift = 0; (1 << shift) < a.page_size;) ++shift;
+    return launch_dependent(attn_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), S::THREADS,
+                            S::SMEM, stream, a, shift);
+}
+
+template <int DT, bool E4M3, int DP>
+int launch_attn_dp(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stream) {
+    const bool p16 = a.page_size % 16 == 0;
+    if (a.q_heads / a.kv_heads <= 8)
+        return p16 ? launch_attn_shape<AttnShape<DT, E4M3, DP, 1, true>>(ctx, a, stream)
+                   : launch_attn_shape<AttnShape<DT, E4M3, DP, 1, false>>(ctx, a, stream);
+    return p16 ? launch_attn_shape<AttnShape<DT, E4M3, DP, 2, true>>(ctx, a, stream)
+               : launch_attn_shape<AttnShape<DT, E4M3, DP, 2, false>>(ctx, a, stream);
+}
+
+}  // namespace
+
+// One instance per translation unit (attn_*.cu), which compile in parallel.
+template <int DT, bool E4M3>
+int launch_attn_typed(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stream);
+
+}  // namespace w4g

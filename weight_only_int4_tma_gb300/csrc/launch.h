@@ -133,11 +133,10 @@ struct AttnArgs {
     float scale;
     int B, q_heads, kv_heads, head_dim, page_size, num_pages, max_pages, window;
     void* workspace;
-    int max_ctas;  // of any instance: where the workspace's parts begin (set by launch_attn)
     int* status;
+    uint64_t timeout_ns;    // limit of every bounded wait
 };
-size_t attn_workspace_bytes(const DeviceCtx& ctx, int q_heads, int kv_heads, int head_dim,
-                            bool e4m3);
+size_t attn_workspace_bytes(const DeviceCtx& ctx, int q_heads, int kv_heads, int head_dim);
 int launch_attn(const DeviceCtx& ctx, const AttnArgs& a, int dtype, bool e4m3,
                 cudaStream_t stream);
 
