@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(RopeTableArgs a) {
 
 constexpr int kRopeThreads = 256;
 
-// One value per thread: heads 0..q_heads-1 are queries, then keys, then values.
+// Any rot_dim: one pair per thread; heads 0..q_heads-1 are queries, then keys, then values.
 template <int DT, bool E4M3>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
     grid_dep_wait();
@@ -97,6 +97,127 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
     }
 }
 
+// Eight neighbouring values of a head.
+template <int DT>
+__device__ __forceinline__ void rope_load8(const uint16_t* p, float (&f)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = dec_to_f32<DT>(static_cast<uint16_t>(w[j] & 0xFFFFu));
+        f[2 * j + 1] = dec_to_f32<DT>(static_cast<uint16_t>(w[j] >> 16));
+    }
+}
+template <int DT>
+__device__ __forceinline__ uint4 rope_pack8(const float (&f)[8]) {
+    return make_uint4(dec_pack2<DT>(f[0], f[1]), dec_pack2<DT>(f[2], f[3]),
+                      dec_pack2<DT>(f[4], f[5]), dec_pack2<DT>(f[6], f[7]));
+}
+
+// How a token's work is cut: a unit is two 16-byte chunks of one head (one, where their number
+// is odd), the two that a rotation in the half layout needs, or neighbours.
+struct RopeUnits {
+    int per_head;         // units of a head
+    int rot_units;        // of those, the first ones, pairs (c, c + rot/16) of the half layout
+    int chunks;           // chunks of a head
+    int heads;            // queries, keys and, with a cache, values (without one v may be null)
+    int threads;          // threads per token, a multiple of 32
+    int tokens;           // tokens per CTA
+    int blocks;           // CTAs per group of tokens
+};
+
+// One unit per thread, loaded and stored in 16-byte pieces; a token's position, slot and table
+// row come through L1, which its threads share.  Bound by HBM for many tokens (2 + 2 bytes per
+// value), by the chain position -> table row -> store for few.
+template <int DT, bool E4M3>
+__global__ void __launch_bounds__(256) rope_units_kernel(RopeArgs a, RopeUnits n) {
+    const int in_cta = static_cast<int>(threadIdx.x) / n.threads;
+    const int lane = static_cast<int>(threadIdx.x) - in_cta * n.threads;
+    const int64_t group = blockIdx.x / static_cast<unsigned>(n.blocks);
+    const int part = static_cast<int>(blockIdx.x - group * n.blocks);
+    const int64_t t = group * n.tokens + in_cta;
+    const int unit = part * n.threads + lane;
+    const int head = unit / n.per_head, u = unit - head * n.per_head;
+    grid_dep_wait();
+    if (t >= a.T || head >= n.heads) return;
+    const bool is_q = head < a.q_heads, is_v = head >= a.q_heads + a.kv_heads;
+    const int h = is_q ? head : is_v ? head - a.q_heads - a.kv_heads : head - a.q_heads;
+    const int D = a.head_dim, half = a.rot_dim / 2;
+    // the unit's chunks c0, c1 (c1 < 0: none) and whether each turns
+    const bool paired = !is_v && u < n.rot_units;
+    int c0 = paired ? u : 2 * u, c1 = paired ? u + n.rot_units : 2 * u + 1;
+    if (c1 >= n.chunks) c1 = -1;
+    const uint16_t* src = (is_q ? a.q + t * a.ldq : is_v ? a.v + t * a.ldv : a.k + t * a.ldk) +
+                          static_cast<int64_t>(h) * D;
+    float x0[8], x1[8];
+    rope_load8<DT>(src + 8 * c0, x0);
+    if (c1 >= 0) rope_load8<DT>(src + 8 * c1, x1);
+    const int pos = a.positions[t];
+    const int64_t wanted = a.kc.p && !is_q ? a.slots[t] : -1;
+    if (pos < 0 || pos >= a.table_len) {
+        record_status(a.status, kDecInvalidArg);
+        return;
+    }
+    if (wanted >= a.num_slots && a.kc.p) record_status(a.status, kDecInvalidArg);
+    const int64_t slot = wanted < a.num_slots ? wanted : -1;
+    const float* cs = a.table + static_cast<int64_t>(pos) * a.rot_dim;
+    if (paired) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float4 c = *reinterpret_cast<const float4*>(cs + 8 * u + 4 * q);
+            const float4 s = *reinterpret_cast<const float4*>(cs + half + 8 * u + 4 * q);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = x0[4 * q + e], r = x1[4 * q + e];
+                x0[4 * q + e] = p * cc[e] - r * ss[e];
+                x1[4 * q + e] = r * cc[e] + p * ss[e];
+            }
+        }
+    } else if (!is_v && a.layout == 1) {
+        auto turn = [&](float (&x)[8], int chunk) {
+            if (8 * chunk >= a.rot_dim) return;
+            const float4 c = *reinterpret_cast<const float4*>(cs + 4 * chunk);
+            const float4 s = *reinterpret_cast<const float4*>(cs + half + 4 * chunk);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p = x[2 * e], r = x[2 * e + 1];
+                x[2 * e] = p * cc[e] - r * ss[e];
+                x[2 * e + 1] = r * cc[e] + p * ss[e];
+            }
+        };
+        turn(x0, c0);
+        if (c1 >= 0) turn(x1, c1);
+    }
+    if (is_q || (!is_v && a.k_out)) {
+        uint16_t* dst = (is_q ? a.q_out + t * a.ldqo : a.k_out + t * a.ldko) + static_cast<int64_t>(h) * D;
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = rope_pack8<DT>(x0);
+        if (c1 >= 0) *reinterpret_cast<uint4*>(dst + 8 * c1) = rope_pack8<DT>(x1);
+    }
+    if (slot < 0) return;
+    const KvView& kv = is_v ? a.vc : a.kc;
+    const int64_t page = (slot >> 32) == 0 ? static_cast<unsigned>(slot) / static_cast<unsigned>(a.page_size)
+                                           : slot / a.page_size;
+    const int64_t off = page * kv.page_stride + (slot - page * a.page_size) * kv.slot_stride + h * kv.head_stride;
+    if constexpr (E4M3) {
+        const float s = kv.scale ? kv.scale[h] : 1.0f;
+        auto pack = [&](const float (&x)[8]) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = dec_e4m3x2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
+            return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+        };
+        uint8_t* dst = static_cast<uint8_t*>(kv.p) + off;
+        *reinterpret_cast<uint2*>(dst + 8 * c0) = pack(x0);
+        if (c1 >= 0) *reinterpret_cast<uint2*>(dst + 8 * c1) = pack(x1);
+    } else {
+        uint16_t* dst = static_cast<uint16_t*>(kv.p) + off;
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = rope_pack8<DT>(x0);
+        if (c1 >= 0) *reinterpret_cast<uint4*>(dst + 8 * c1) = rope_pack8<DT>(x1);
+    }
+}
+
 }  // namespace
 
 int launch_rope_table(const RopeTableArgs& a, cudaStream_t stream) {
@@ -108,6 +229,26 @@ int launch_rope_table(const RopeTableArgs& a, cudaStream_t stream) {
 int launch_rope(const DeviceCtx& ctx, const RopeArgs& a, int dtype, bool e4m3,
                 cudaStream_t stream) {
     (void)ctx;
+    // Whole chunks turn: rot_dim / 2 of whole chunks in the half layout, rot_dim in the other.
+    const bool whole = a.layout == 0 ? a.rot_dim % 16 == 0 : a.rot_dim % 8 == 0;
+    if (whole) {
+        RopeUnits n{};
+        n.chunks = a.head_dim / 8;
+        n.rot_units = a.layout == 0 ? a.rot_dim / 16 : 0;
+        n.per_head = (n.chunks + 1) / 2;
+        n.heads = a.q_heads + a.kv_heads * (a.kc.p ? 2 : 1);
+        const int units = n.per_head * n.heads;
+        n.blocks = (units + 255) / 256;
+        n.threads = ((units + n.blocks - 1) / n.blocks + 31) / 32 * 32;
+        n.tokens = n.blocks > 1 ? 1 : 256 / n.threads;
+        const int64_t groups = (static_cast<int64_t>(a.T) + n.tokens - 1) / n.tokens;
+        if (groups * n.blocks <= 0x7FFFFFFFLL) {
+            auto kern = dtype == 0 ? (e4m3 ? rope_units_kernel<0, true> : rope_units_kernel<0, false>)
+                                   : (e4m3 ? rope_units_kernel<1, true> : rope_units_kernel<1, false>);
+            return launch_dependent(kern, dim3(static_cast<unsigned>(groups * n.blocks)),
+                                    n.threads * n.tokens, 0, stream, a, n);
+        }
+    }
     const dim3 grid(static_cast<unsigned>(a.T));
     auto kern = dtype == 0 ? (e4m3 ? rope_kernel<0, true> : rope_kernel<0, false>)
                            : (e4m3 ? rope_kernel<1, true> : rope_kernel<1, false>);
