@@ -61,11 +61,11 @@ __device__ __forceinline__ float warp_max(float v) {
 // Launch that may begin while the stream's previous kernel still runs (every kernel here
 // calls grid_dep_wait() before its first access to memory).  Returns a w4a16_status.
 template <typename... KArgs, typename... Args>
-int launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem,
+int launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                      cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
