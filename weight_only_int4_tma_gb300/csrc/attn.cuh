@@ -21,27 +21,45 @@
 // when a score passes m by more than 2^8 the sums so far are scaled to the new reference
 // (a warp vote finds out; exact in the end, since numerator and denominator share it).
 //
-// Work split.  The steps of all (sequence, head, row tile) items stand in one line that is
-// cut into equal shares, one per CTA, whatever the lengths; every CTA finds its share from
-// the lengths on the device.  The producers run on into the next item while the consumers
-// finish one.  An item inside one CTA is finished there; one that is cut leaves (m, l, O) in fp32 in the
-// workspace, and the CTA that arrives last joins the parts in their order.
+// Work split.  The steps of all (sequence, head, row tile) items stand in one line, which is cut
+// in chunks whatever the lengths; the cut follows from the lengths on the device alone.  Every
+// CTA has one chunk to begin with, of 9/16 of its share; the rest is cut in ever smaller chunks
+// that CTAs claim as they become free, because SMs do not get equal shares of the bandwidth
+// (measured with equal shares: the first of 152 done after 49 us, the last after 86).  The
+// producers run on into the next item and the next chunk while the consumers finish one.  An
+// item inside one chunk is finished there; one that is cut leaves (m, l, O) of each part in
+// fp32 in the workspace.  A CTA counts its parts once its chunks are done, and whoever completes
+// an item's count joins its parts, in their order.  Which CTA takes a chunk changes no result.
+// (Counting and joining at once, while copies run, costs the consumers 4 to 7 us a part; a
+// second kernel for the joins costs 6 to 10 us a call.)
 #pragma once
+#include <type_traits>
+
 #include "decode.cuh"
 
 namespace w4g {
 
 constexpr float kLag = 8.0f;       // scores may pass the reference by 2^8
-constexpr int kMaxJoin = 16;       // parts that one CTA joins at once
+constexpr int kMaxJoin = 32;       // parts that one CTA joins at once
+constexpr int kFewParts = 8;       // parts that one warp joins
+constexpr int kMaxCuts = 32;       // parts that a CTA writes before it counts them
+constexpr int kTierRounds = 24;    // rounds of the warps from which on chunks come in tiers
+constexpr int kManyRounds = 128;   // the same for few items
+constexpr int kLeastRounds = 4;    // of the smallest chunks: 4 us at a CTA's share of the bandwidth
 
-// Parts of cut items in the workspace: three counters per CTA first, then for each CTA two
-// parts (its first item if that began in an earlier CTA, its last if that ends in a later
-// one) of m[rows], l[rows], O[rows][dp].
+// The workspace: the ticket of the next chunk to claim, three counters per chunk, then for each
+// chunk two parts (its first item if that began in an earlier chunk, its last if that ends in
+// a later one) of m[rows], l[rows], O[rows][dp].
+constexpr int kTiers = 6;          // chunk sizes; one chunk of each size per CTA
+// One CTA per SM; two rounds of joins hold the parts of at most kMaxJoin^2 chunks.
+constexpr int attn_ctas(int num_sms) {
+    return num_sms * kTiers <= kMaxJoin * kMaxJoin ? num_sms : kMaxJoin * kMaxJoin / kTiers;
+}
 __host__ __device__ constexpr size_t attn_part_floats(int rows, int dp) {
     return static_cast<size_t>(rows) * (dp + 2);
 }
 __host__ __device__ constexpr size_t attn_counter_bytes(int ctas) {
-    return (static_cast<size_t>(ctas) * 12 + 127) / 128 * 128;
+    return (static_cast<size_t>(ctas) * kTiers * 12 + 4 + 127) / 128 * 128;
 }
 
 namespace {
@@ -122,8 +140,8 @@ struct AttnShape {
     static constexpr int THREADS = 32 * (W + PW);
     static constexpr int RING = NST * 2 * SLOT;
     static constexpr int SMEM = RING + SOE * ROWS * OP * 4 + NST * (4 + 3 * 8);
+    static_assert(SOE * OP >= 2 * kMaxJoin, "a join's numbers fit where the sums stand");
     static_assert(NST >= W && SMEM <= 224 * 1024 && W % SOE == 0, "the ring fits");
-    static_assert(SOE * OP >= 2 * kMaxJoin, "a join's numbers fit where the sums stood");
 };
 
 // Byte offset of chunk c of token row r in a slot: the chunks of eight rows that ldmatrix
@@ -164,11 +182,124 @@ struct Segment {
     Span span;
 };
 
-// An item cut over several CTAs: parts of the CTAs c0 .. c0 + n - 1, and where its rows go.
+// A chunk of the line: its number, where it begins, its steps (0: no more chunks) and the first
+// item's part of it.
+struct Chunk {
+    long long u;
+    int number, n;
+    Segment first;
+};
+constexpr int kChunkRing = 8;  // chunks announced inside a CTA
+
+// A part of an item that several chunks hold: the item's are those of chunks c0 .. c0 + n - 1.
 struct Cut {
-    int c0, n, b, head0, rows, last;  // last: this CTA's arrival completed its run of parts
+    int c0, n, at, b, head0, rows, last;  // at: the part written here; last: it completes its run
     float vs;
 };
+
+// The line of steps and its chunks, the same in every CTA.
+struct Line {
+    long long tier_base[kTiers], tier_size[kTiers], end;
+    bool apart;   // chunks are parts of one item each
+    bool tiers;   // chunks of several sizes, all but the first of each CTA claimed
+};
+// chunk of step u of the line (not `apart`)
+__device__ __forceinline__ int chunk_of(const Line& line, int ctas, long long u) {
+    int k = 0;
+    if (line.tiers)
+        while (k < kTiers - 1 && u >= line.tier_base[k + 1]) ++k;
+    return k * ctas + static_cast<int>(quotient(u - line.tier_base[k], line.tier_size[k]));
+}
+// first step of a chunk (not `apart`)
+__device__ __forceinline__ long long chunk_begin(const Line& line, int ctas, int c) {
+    const int k = line.tiers ? min(c / ctas, kTiers - 1) : 0;
+    return min(line.end, line.tier_base[k] + line.tier_size[k] * (c - k * ctas));
+}
+// parts that an item of n_steps is cut in (`apart`)
+__device__ __forceinline__ int parts_of(const Line& line, int n_steps) {
+    return static_cast<int>(quotient(n_steps + line.tier_size[0] - 1, line.tier_size[0]));
+}
+
+// Fills `line` and prefix[thread], the steps before each thread's sequences (thread t has
+// sequences t * per_thread ...); by all threads of a CTA, which then meet at a barrier.
+template <int STEP, int THREADS, int WARPS>
+__device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, int ctas, bool report,
+                                         Line& line, long long* prefix, long long* scan) {
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int per_thread = (a.B + THREADS - 1) / THREADS;
+    const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
+    // steps in the low bits, sequences that have any above them
+    constexpr int kSeqBit = 40;
+    constexpr long long kLow = (1ll << kSeqBit) - 1;
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int n = span_steps<STEP>(visible(a, b, report));
+        mine += n + (n ? 1ll << kSeqBit : 0);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) incl += scan[w];
+        total += scan[w];
+    }
+    prefix[tid] = ((incl - mine) & kLow) * items_per_seq;
+    if (tid == 0) {
+        const long long items = (total >> kSeqBit) * items_per_seq;
+        total = (total & kLow) * items_per_seq;
+        line.end = total;
+        // Whole rounds of the warps: a chunk of fewer steps would take as long.
+        const int slots = ctas * WARPS;
+        const long long rounds = max(quotient(total + slots - 1, slots), 1ll);
+        // Few items: equal chunks until there are many rounds (many small chunks of few items
+        // are many parts to join).
+        const bool few = 2 * items <= ctas;
+        line.tiers = rounds >= (few ? kManyRounds : kTierRounds);
+        line.apart = false;
+        line.tier_base[0] = 0;
+        line.tier_size[0] = rounds * WARPS;
+        if (line.tiers) {
+            // Each size 5/8 of what is left, down to kLeastRounds; few items: at most three.
+            long long base = 0, togo = rounds;
+            for (int k = 0; k < kTiers; ++k) {
+                long long r = max((togo * 5) >> 3, static_cast<long long>(kLeastRounds));
+                const bool rest = k == kTiers - 1 || togo - r < kLeastRounds || (few && k == 2);
+                const long long size = rest ? max(quotient(max(total - base, 0ll) + ctas - 1, ctas), 1ll) : r * WARPS;
+                line.tier_base[k] = base;
+                line.tier_size[k] = size;
+                if (base < total) base += size * ctas;
+                togo = rest ? 0 : togo - r;
+            }
+        } else if (few) {
+            // Chunks cut from one item each, so that no CTA has two partial items to write and
+            // join; at most one round more, and one chunk per CTA.
+            const int left = static_cast<int>(ctas - items) * WARPS;
+            const long long r = max(quotient(total + left - 1, left), 1ll);
+            line.apart = r <= rounds + 1;
+            if (line.apart) line.tier_size[0] = r * WARPS;
+        }
+    }
+}
+
+// One row of a finished item, four of its values.
+template <int DT>
+__device__ __forceinline__ void store_out(const AttnArgs& a, int b, int head, int d, float4 v, float f) {
+    uint16_t* dst = a.out + b * a.ldo + static_cast<int64_t>(head) * a.head_dim + d;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(dec_pack2<DT>(v.x * f, v.y * f), dec_pack2<DT>(v.z * f, v.w * f));
+}
+// m and l of a row to its log-sum-exp; `shift`: see the weights in attn_kernel.
+__device__ __forceinline__ void store_lse(const AttnArgs& a, int b, int head, float m, float l, float shift) {
+    if (a.lse)
+        a.lse[static_cast<int64_t>(b) * a.q_heads + head] =
+            l > 0.0f ? (m - shift) * 0.69314718055994531f + logf(l) : -INFINITY;
+}
 
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int page_shift) {
@@ -183,13 +314,15 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     uint32_t* metas = reinterpret_cast<uint32_t*>(bars + 3 * NST);   // which tokens have a page
     __shared__ int abort_flag;
     __shared__ float sm_m[W][ROWS], sm_l[W][ROWS];
+    __shared__ Line line;
+    __shared__ long long scan[W + S::PW];
+    __shared__ long long prefix[S::THREADS];
+    __shared__ Chunk chunks[kChunkRing];
+    __shared__ uint64_t chunk_bars[kChunkRing];
+    __shared__ Segment segs[2];                // the segment after the chunk's first, in turn
+    __shared__ Cut cuts[kMaxCuts];             // parts written, not yet counted
     __shared__ float row_m[ROWS], row_l[ROWS];
-    __shared__ long long scan[2][W + S::PW];
-    __shared__ int find_b;
-    __shared__ long long find_u;
-    __shared__ Segment segs[2];      // the current one and the one after it, in turn
-    __shared__ Cut cuts[2];          // an item that began in an earlier CTA, one that ends in a later
-    __shared__ int is_last;
+    __shared__ int chunk_n, is_last;
 
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, i = lane & 3;
@@ -198,7 +331,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     const int row_tiles = (G + ROWS - 1) / ROWS;
     const int items_per_seq = a.kv_heads * row_tiles;
     const int row_bytes = a.head_dim * S::ES;
-    int* counters = static_cast<int*>(a.workspace);
+    int* ticket = static_cast<int*>(a.workspace);
+    int* counters = ticket + 1;
     float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + attn_counter_bytes(ctas));
 
     if (row_bytes < S::PITCH) {  // columns past the head dimension are never copied: zero
@@ -211,78 +345,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         mbar_init(full_v + 8 * tid, 32);
         mbar_init(empty + 8 * tid, 1);
     }
+    const uint32_t announced = smem_addr(chunk_bars);
+    if (tid < kChunkRing) mbar_init(announced + 8 * tid, 1);
     if (tid == 0) abort_flag = 0;
     grid_dep_wait();
-    // ---- this CTA's share ----
+    lay_line<STEP, S::THREADS, W>(a, items_per_seq, ctas, cta == 0, line, prefix, scan);
     const int per_thread = (a.B + S::THREADS - 1) / S::THREADS;
-    const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
-    // exclusive sum over the threads' sequences, and the total
-    auto block_scan = [&](long long mine, int slot, long long& total) {
-        long long incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-            if (lane >= d) incl += o;
-        }
-        if (lane == 31) scan[slot][warp] = incl;
-        __syncthreads();
-        long long before = 0;
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < W + S::PW; ++w) {
-            if (w < warp) before += scan[slot][w];
-            total += scan[slot][w];
-        }
-        return before + incl - mine;
-    };
-    // steps in the low bits, sequences that have any above them
-    constexpr int kSeqBit = 40;
-    long long mine = 0, total = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-        const int n = span_steps<STEP>(visible(a, b, cta == 0));
-        mine += n + (n ? 1ll << kSeqBit : 0);
-    }
-    long long excl = block_scan(mine, 0, total);
-    const long long seqs = total >> kSeqBit, items = seqs * items_per_seq;
-    constexpr long long kLow = (1ll << kSeqBit) - 1;
-    total = (total & kLow) * items_per_seq;
-    // Whole rounds of the warps: a share of fewer steps would take as long.  Where a share is
-    // cut from one item alone (no CTA has two partial items to write and join one after the
-    // other) it takes up to `items` shares more; that is worth one round.
-    const int slots = ctas * W;
-    const long long rounds = max(quotient(total + slots - 1, slots), 1ll);
-    bool apart = false;
-    long long share = rounds * W;
-    if (2 * items <= ctas) {
-        const int left = static_cast<int>(ctas - items) * W;
-        const long long r = max(quotient(total + left - 1, left), 1ll);
-        apart = r <= rounds + 1;
-        if (apart) share = r * W;
-    }
-    // u: position in the line of steps, or (apart) in the line of parts
-    long long u = apart ? cta : share * cta, u_end = min(total, u + share);
-    mine = (mine & kLow) * items_per_seq;
-    excl = (excl & kLow) * items_per_seq;
-    auto parts_of = [&](int n_steps) { return static_cast<int>(quotient(n_steps + share - 1, share)); };
-    if (apart) {
-        mine = 0;
-        for (int b = b_lo; b < b_hi; ++b)
-            mine += static_cast<long long>(parts_of(span_steps<STEP>(visible(a, b, false)))) * items_per_seq;
-        excl = block_scan(mine, 1, total);
-        u_end = min(total, u + 1);
-    }
-    if (u < u_end && excl <= u && u < excl + mine) {  // one thread at most
-        long long at = excl;
-        int b = b_lo;
-        for (; b + 1 < b_hi; ++b) {
-            const int n_steps = span_steps<STEP>(visible(a, b, false));
-            const long long n = static_cast<long long>(apart ? parts_of(n_steps) : n_steps) * items_per_seq;
-            if (u < at + n) break;
-            at += n;
-        }
-        find_b = b;
-        find_u = u - at;
-    }
     // rows with nothing to attend to
     for (int b = cta; b < a.B; b += ctas) {
         if (visible(a, b, false).len != 0) continue;
@@ -292,8 +360,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             for (int h = tid; h < a.q_heads; h += S::THREADS)
                 a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
     }
-    __syncthreads();
-    if (u >= u_end) return;
+    __syncthreads();  // prefix, the barriers, and the zeroed ring
 
     // the segment after `s`: the next item's first steps, at most `left`
     auto after = [&](const Segment& s, int left) {
@@ -310,29 +377,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         n.step_end = min(n.n_steps, left);
         return n;
     };
-    int left = static_cast<int>(u_end - u);  // steps of this CTA not yet begun
-    Segment ld;
-    ld.b = find_b;
-    ld.span = visible(a, ld.b, false);
-    ld.n_steps = span_steps<STEP>(ld.span);
-    {
-        const int per_item = apart ? parts_of(ld.n_steps) : ld.n_steps;
-        ld.item = static_cast<int>(quotient(find_u, per_item));
-        ld.step = static_cast<int>(find_u - static_cast<long long>(ld.item) * per_item);
-        if (apart) ld.step *= static_cast<int>(share);
-        ld.step_end = static_cast<int>(min(static_cast<long long>(ld.n_steps), ld.step + (apart ? share : left)));
-    }
-    if (apart) left = ld.step_end - ld.step;
-    if (tid == 0) {
-        segs[0] = ld;
-        cuts[0].last = cuts[1].last = 0;
-    }
-    __syncthreads();  // segs, the barriers, and the zeroed ring
 
     const uint32_t ring = smem_addr(smem);
     if (warp >= W) {
-        // ---- producers: steps pw, pw + PW, ... of the CTA's share ----
+        // ---- producers: steps pw, pw + PW, ... of the CTA's chunks ----
         const int pw = warp - W;
+        Segment ld{};
         constexpr int RPI = 32 / CH;   // token rows that one instruction of the warp copies
         static_assert(CH <= 32, "a row is one instruction at most");
         const int lrow = lane / CH, lchunk = lane % CH;
@@ -351,7 +401,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         const int32_t* table;
         const char* kbase;
         const char* vbase;
-        int first_st, pid = 0, pid_next = 0, in_batch = 0;
+        int first_st = 0, pid = 0, pid_next = 0, in_batch = 0;
         auto fetch_pages = [&](int st) {
             const int s_ = S::P16 ? st + lane / R * S::PW : st;
             const int tok = s_ * STEP + (S::P16 ? 16 * (lane % R) : lane);
@@ -407,22 +457,117 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                 if (column) copy16(to, ok ? p : base, ok ? 16 : 0);
             }
         };
-        int seg0 = 0;                                   // steps of the share before segment ld
-        int seg_n = ld.step_end - ld.step;
-        open(ld.step + pw);
+        // Warp 0 finds the chunks: the CTA's own first, then claims, one chunk ahead of use.
+        auto locate = [&](int number) {  // by all lanes; lane 0's result counts
+            Chunk c{};
+            c.number = number;
+            if (line.apart) {  // the number-th part of all items
+                int done = 0;
+                for (int b0 = 0; b0 < a.B && c.n == 0; b0 += 32) {
+                    const int b = b0 + lane, size0 = static_cast<int>(line.tier_size[0]);
+                    const Span span = b < a.B ? visible(a, b, false) : Span{0, 0};
+                    const int n_steps = span_steps<STEP>(span), per = parts_of(line, n_steps);
+                    int incl = per * items_per_seq;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                        if (lane >= d) incl += o;
+                    }
+                    const int at = number - done - (incl - per * items_per_seq);
+                    const bool here = at >= 0 && at < per * items_per_seq;
+                    if (here) {
+                        const int step = at % per * size0;
+                        c.first = Segment{b, at / per, step, min(n_steps, step + size0), n_steps, span};
+                        c.n = c.first.step_end - step;
+                    }
+                    const unsigned who = __ballot_sync(0xFFFFFFFFu, here);
+                    if (who) {  // to lane 0, word by word
+                        int* w = reinterpret_cast<int*>(&c);
+#pragma unroll
+                        for (int e = 0; e < static_cast<int>(sizeof(Chunk) / 4); ++e)
+                            w[e] = __shfl_sync(0xFFFFFFFFu, w[e], __ffs(who) - 1);
+                    }
+                    done += __shfl_sync(0xFFFFFFFFu, incl, 31);
+                }
+                return c;
+            }
+            c.u = chunk_begin(line, ctas, number);
+            if (c.u >= line.end) return c;
+            c.n = static_cast<int>(chunk_begin(line, ctas, number + 1) - c.u);
+            // the thread whose sequences hold step u, then the sequence
+            int t = 0;
+            for (int t0 = 0; t0 < S::THREADS && t0 * per_thread < a.B; t0 += 32)
+                t += __popc(__ballot_sync(0xFFFFFFFFu, prefix[t0 + lane] <= c.u));
+            --t;
+            long long at = prefix[t];
+            int b = t * per_thread;
+            Span span = visible(a, b, false);
+            int n_steps = span_steps<STEP>(span);
+            while (at + static_cast<long long>(n_steps) * items_per_seq <= c.u && b + 1 < a.B) {
+                at += static_cast<long long>(n_steps) * items_per_seq;
+                span = visible(a, ++b, false);
+                n_steps = span_steps<STEP>(span);
+            }
+            const int item = static_cast<int>(quotient(c.u - at, n_steps));
+            const int step = static_cast<int>(c.u - at - static_cast<long long>(item) * n_steps);
+            c.first = Segment{b, item, step, min(n_steps, step + c.n), n_steps, span};
+            return c;
+        };
+        auto announce = [&](int k, int number) {  // the CTA's k-th chunk
+            const Chunk c = number < 0 ? Chunk{} : locate(number);
+            if (lane == 0) {
+                chunks[k % kChunkRing] = c;
+                mbar_arrive(announced + 8 * (k % kChunkRing));
+            }
+            return c.n > 0;
+        };
+        // The ticket of the next chunk, drawn early and looked at later; -1: there is no more.
+        // Every CTA fails once; the one that does so last readies the ticket for the next call.
+        const int claimable = line.tiers ? chunk_of(line, ctas, line.end - 1) + 1 - ctas : 0;
+        int drawn = 0;
+        auto draw = [&]() {
+            if (line.tiers && lane == 0) drawn = atomicAdd(ticket, 1);
+        };
+        auto claim = [&]() {
+            if (!line.tiers) return -1;
+            if (lane == 0 && drawn == claimable + ctas - 1) *ticket = 0;
+            const int v = __shfl_sync(0xFFFFFFFFu, drawn, 0);
+            return v < claimable ? ctas + v : -1;
+        };
+        bool more = true;
+        if (pw == 0) more = announce(0, cta);
+        int x = pw;                    // this warp's next step of the CTA
+        int seg0 = 0;                  // the CTA's steps before segment ld
         int stage = pw;
         uint32_t phase = 0;
-        const int n_all = left;
 #pragma unroll 1
-        for (int x = pw; x < n_all; x += S::PW) {
-            if (x >= seg0 + seg_n) {
-                do {
-                    seg0 += seg_n;
-                    ld = after(ld, n_all - seg0);
-                    seg_n = ld.step_end - ld.step;
-                } while (x >= seg0 + seg_n);
-                open(ld.step + x - seg0);
+        for (int k = 0;; ++k) {
+            bool may_draw = pw == 0 && more, drew = false;
+            const bool there_is = mbar_wait_warp(announced + 8 * (k % kChunkRing), (k / kChunkRing) & 1,
+                                                 &abort_flag, a.status, a.timeout_ns);
+            const Chunk& chunk = chunks[k % kChunkRing];
+            const int n_all = seg0 + chunk.n;
+            if (!there_is) {  // given up: the ticket has to end as it began
+                while (line.tiers && may_draw) {
+                    draw();
+                    may_draw = claim() >= 0;
+                }
+                break;
             }
+            if (chunk.n == 0) break;
+            ld = chunk.first;
+            int seg_n = ld.step_end - ld.step;
+            bool opened = false;
+#pragma unroll 1
+            for (; x < n_all; x += S::PW) {
+            while (x >= seg0 + seg_n) {
+                seg0 += seg_n;
+                ld = after(ld, n_all - seg0);
+                seg_n = ld.step_end - ld.step;
+                opened = false;
+            }
+            if (!opened) open(ld.step + x - seg0);
+            opened = true;
             const int st = first_st + ld.step + x - seg0;
             int64_t kat[NP], vat[NP];
             uint32_t there = 0;  // groups (P16) or tokens whose page is there
@@ -458,6 +603,20 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             }
             stage += S::PW;
             if (stage >= NST) stage -= NST, phase ^= 1u;
+            // the next chunk: drawn some 4 us before this one ends, looked at 2 us later
+            if (may_draw && n_all - x <= 10 * S::PW) {
+                draw();
+                drew = true;
+                may_draw = false;
+            }
+            if (drew && n_all - x <= 5 * S::PW) {
+                more = announce(k + 1, claim());
+                drew = false;
+            }
+            }
+            if (may_draw) draw();
+            if (may_draw || drew) more = announce(k + 1, claim());
+            seg0 = n_all;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
@@ -465,32 +624,15 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
 
     // ---- consumers ----
     constexpr int CT = 32 * W;  // their threads
-    // ---- parts of an item that several CTAs took ----
+    constexpr int E = (ROWS * DP / 4 + CT - 1) / CT;  // 16-byte pieces of a result per thread
+    // ---- parts of an item that several chunks hold ----
+    auto fan_of = [](int n) { return n > kMaxJoin && n <= 256 ? 16 : kMaxJoin; };  // parts of a run
     auto part_of = [&](const Cut& c, int k) {  // part k of the item
         return parts + (2 * (c.c0 + k) + (k == 0 ? 1 : 0)) * attn_part_floats(ROWS, DP);
     };
-    // After the CTA's part is written: counts it; thread 0 learns whether it was the last.
-    auto arrive = [&](int* counter, int want, int* last) {
-        __threadfence();
-        consumers_sync<CT>();
-        if (tid == 0) {
-            *last = atomicAdd(counter, 1) == want - 1;
-            if (*last) *counter = 0;  // ready for the next call
-            __threadfence();
-        }
+    auto give = [&](const Cut& c, int row, int d, float4 v, float sum) {
+        if (d < a.head_dim) store_out<S::DT>(a, c.b, c.head0 + row, d, v, sum > 0.0f ? c.vs / sum : 0.0f);
     };
-    auto store = [&](const Cut& c, int row, int d, float4 v, float sum) {
-        const float f = sum > 0.0f ? c.vs / sum : 0.0f;
-        uint16_t* dst = a.out + c.b * a.ldo + static_cast<int64_t>(c.head0 + row) * a.head_dim + d;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(dec_pack2<S::DT>(v.x * f, v.y * f), dec_pack2<S::DT>(v.z * f, v.w * f));
-    };
-    auto store_lse = [&](const Cut& c, int row, float top, float sum) {
-        if (a.lse)
-            a.lse[static_cast<int64_t>(c.b) * a.q_heads + c.head0 + row] =
-                sum > 0.0f ? (top - kShift) * 0.69314718055994531f + logf(sum) : -INFINITY;
-    };
-    constexpr int E = (ROWS * DP / 4 + CT - 1) / CT;  // 16-byte pieces per thread
     // Parts k0, k0 + stride, ... (count of them, at most kMaxJoin) into one: written over part
     // k0, or stored as the result.
     auto join = [&](const Cut& c, int k0, int stride, int count, bool final) {
@@ -545,27 +687,102 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
-            if (row >= c.rows || d >= a.head_dim) continue;
-            if (final) store(c, row, d, acc[e], row_l[row]);
+            if (row >= c.rows) continue;
+            if (final) give(c, row, d, acc[e], row_l[row]);
             else *reinterpret_cast<float4*>(to + 2 * ROWS + row * DP + d) = acc[e];
         }
         if (tid < c.rows) {
-            if (final) store_lse(c, tid, row_m[tid], row_l[tid]);
+            if (final) store_lse(a, c.b, c.head0 + tid, row_m[tid], row_l[tid], kShift);
             else to[tid] = row_m[tid], to[ROWS + tid] = row_l[tid];
         }
     };
-    // Joins what this CTA's arrival completed.  More than kMaxJoin parts are joined in two
-    // rounds, runs of kMaxJoin first: one CTA reads about 0.1 TB/s, and the 152 parts of one
-    // item of 8 rows and 128 dimensions are 0.6 MB.
+    // The parts of an item, or of a run of `fan` where they are many: one CTA reads about
+    // 0.1 TB/s, and 152 parts of one item of 8 rows and 128 dimensions are 0.6 MB.  The runs'
+    // results are parts again, joined by the CTA that completes the last run.
     auto settle = [&](const Cut& c) {
-        if (!c.last) return;
-        const int run = (cta - c.c0) / kMaxJoin, runs = (c.n + kMaxJoin - 1) / kMaxJoin;
-        join(c, run * kMaxJoin, 1, min(kMaxJoin, c.n - run * kMaxJoin), runs == 1);
+        const int fan = fan_of(c.n), run = c.at / fan, runs = (c.n + fan - 1) / fan;
+        consumers_sync<CT>();
+        join(c, run * fan, 1, min(fan, c.n - run * fan), runs == 1);
         if (runs > 1) {
-            arrive(counters + 2 * ctas + c.c0, runs, &is_last);
+            __threadfence();
             consumers_sync<CT>();
-            if (is_last) join(c, 0, kMaxJoin, runs, true);
+            if (tid == 0) {
+                int* counter = counters + 2 * ctas * kTiers + c.c0;
+                is_last = atomicAdd(counter, 1) == runs - 1;
+                if (is_last) *counter = 0;
+                __threadfence();
+            }
+            consumers_sync<CT>();
+            if (is_last) join(c, 0, fan, runs, true);
         }
+    };
+    // The same for up to kFewParts parts, by one warp: a CTA that claims chunks completes several
+    // small items.  N parts of 16 / N pieces are read at a time.
+    auto join_few = [&](const Cut& c, auto parts_at_once) {
+        constexpr int N = decltype(parts_at_once)::value, U = 16 / N;
+#pragma unroll 1
+        for (int at0 = lane; at0 < c.rows * (DP / 4); at0 += 32 * U) {
+            float pm[U][N], pl[U][N];
+            float4 x[U][N];
+#pragma unroll
+            for (int o = 0; o < U; ++o)
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int at = at0 + 32 * o, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+                    const float* p = part_of(c, k);
+                    const bool in = k < c.n && row < c.rows;
+                    pm[o][k] = in ? __ldcg(p + row) : -INFINITY;
+                    pl[o][k] = in ? __ldcg(p + ROWS + row) : 0.0f;
+                    x[o][k] = in && d < a.head_dim ? __ldcg(reinterpret_cast<const float4*>(p + 2 * ROWS + row * DP + d))
+                                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+            for (int o = 0; o < U; ++o) {
+                const int at = at0 + 32 * o, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+                if (row >= c.rows) continue;
+                float top = -INFINITY, sum = 0.0f;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < N; ++k) top = fmaxf(top, pm[o][k]);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const float f = pm[o][k] == -INFINITY ? 0.0f : exp2_fast(pm[o][k] - top);
+                    sum = fmaf(pl[o][k], f, sum);
+                    v.x = fmaf(x[o][k].x, f, v.x), v.y = fmaf(x[o][k].y, f, v.y);
+                    v.z = fmaf(x[o][k].z, f, v.z), v.w = fmaf(x[o][k].w, f, v.w);
+                }
+                give(c, row, d, v, sum);
+                if (d == 0) store_lse(a, c.b, c.head0 + row, top, sum, kShift);
+            }
+        }
+    };
+    // Counts the parts written since the last time, and joins the items (or runs) they complete.
+    auto flush = [&](int n_cuts) {
+        __threadfence();
+        consumers_sync<CT>();
+        if (tid < n_cuts) {
+            Cut& c = cuts[tid];
+            // counters by the chunk of the run's first part.  That chunk may end one item and
+            // begin another, so first runs, later runs and second rounds count apart.
+            const int fan = fan_of(c.n), run = c.at / fan;
+            int* counter = counters + (run == 0 ? 0 : ctas * kTiers) + c.c0 + run * fan;
+            c.last = atomicAdd(counter, 1) == min(fan, c.n - run * fan) - 1;
+            if (c.last) *counter = 0;  // ready for the next call
+            __threadfence();
+        }
+        consumers_sync<CT>();
+        // the choice follows from the line and the item: equal inputs give equal bits
+        auto by_warp = [&](const Cut& c) { return line.tiers && c.n <= kFewParts; };
+        int nth = 0;
+        for (int j = 0; j < n_cuts; ++j)
+            if (cuts[j].last && by_warp(cuts[j]) && nth++ % W == warp) {
+                const Cut c = cuts[j];
+                if (c.n <= 2) join_few(c, std::integral_constant<int, 2>{});
+                else if (c.n <= 4) join_few(c, std::integral_constant<int, 4>{});
+                else join_few(c, std::integral_constant<int, kFewParts>{});
+            }
+        for (int j = 0; j < n_cuts; ++j)
+            if (cuts[j].last && !by_warp(cuts[j])) settle(cuts[j]);
         consumers_sync<CT>();
     };
 
@@ -578,13 +795,23 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         return static_cast<uint32_t>(r * 16 * S::PITCH + (CH >= 8 ? (c & ~7) << 4 : 0));
     };
 
-    int stage = warp;          // of this warp's next step
-    uint32_t phase = 0;
-    int taken = 0;             // steps of the share before the segment
-    for (int turn = 0;; turn ^= 1) {
-        const Segment& cur = segs[turn];
+    int taken = 0;             // the CTA's steps before the segment
+    int turn = 0, n_cuts = 0;
+    for (int k = 0;; ++k) {
+    if (tid == 0) {
+        mbar_wait_bounded(announced + 8 * (k % kChunkRing), (k / kChunkRing) & 1, &abort_flag, a.status, a.timeout_ns);
+        chunk_n = abort_flag ? 0 : chunks[k % kChunkRing].n;
+    }
+    consumers_sync<CT>();
+    int left = chunk_n;        // steps of the chunk not yet begun
+    if (left == 0) break;
+    const int number = chunks[k % kChunkRing].number;
+    long long u = chunks[k % kChunkRing].u;
+    const Segment* seg = &chunks[k % kChunkRing].first;
+    for (;; turn ^= 1) {
+        const Segment& cur = *seg;
         left -= cur.step_end - cur.step;
-        if (left > 0 && tid == 0) segs[turn ^ 1] = after(cur, left);
+        if (left > 0 && tid == 0) segs[turn] = after(cur, left);
         const int kvh = cur.item / row_tiles, row0 = (cur.item - kvh * row_tiles) * ROWS;
         const int rows = min(ROWS, G - row0), head0 = kvh * G + row0;
         const Span span = cur.span;
@@ -650,8 +877,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                 for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
         }
         const int st1 = span.first / STEP + cur.step_end;
-        // step x of the share is warp x % W's
-        int st = span.first / STEP + cur.step + ((warp - taken) & (W - 1));
+        // A step's warp follows from its place in the item alone: the sums of a part then do
+        // not depend on what the CTA did before.
+        int st = span.first / STEP + cur.step + ((warp - cur.step - cur.item) & (W - 1));
+        int x = taken + st - span.first / STEP - cur.step;
+        int stage = x % NST;
+        uint32_t phase = (x / NST) & 1;
         taken += cur.step_end - cur.step;
 #pragma unroll 1
         for (; st < st1; st += W) {
@@ -864,43 +1095,46 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         };
         const bool begins = cur.step == 0, ends = cur.step_end == cur.n_steps;
         const bool whole = begins && ends;
-        Cut here{0, 0, cur.b, head0, rows, 0, S::E4M3 && a.vc.scale ? a.vc.scale[kvh] : 1.0f};
-        float* part = parts + (2 * cta + (begins ? 1 : 0)) * attn_part_floats(ROWS, DP);
+        const float vs = S::E4M3 && a.vc.scale ? a.vc.scale[kvh] : 1.0f;
+        float* part = parts + (2 * number + (begins ? 1 : 0)) * attn_part_floats(ROWS, DP);
         float top;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
             if (row >= rows || d >= a.head_dim) continue;
-            if (whole) store(here, row, d, acc[e], row_sum(row, top));
-            else *reinterpret_cast<float4*>(part + 2 * ROWS + row * DP + d) = acc[e];
+            if (whole) {
+                const float sum = row_sum(row, top);
+                store_out<S::DT>(a, cur.b, head0 + row, d, acc[e], sum > 0.0f ? vs / sum : 0.0f);
+            } else {
+                *reinterpret_cast<float4*>(part + 2 * ROWS + row * DP + d) = acc[e];
+            }
         }
         if (tid < rows) {
             const float sum = row_sum(tid, top);
-            if (whole) store_lse(here, tid, top, sum);
+            if (whole) store_lse(a, cur.b, head0 + tid, top, sum, kShift);
             else part[tid] = top, part[ROWS + tid] = sum;
         }
         if (!whole) {
-            if (apart) {
-                here.c0 = cta - static_cast<int>(quotient(cur.step, share));
-                here.n = parts_of(cur.n_steps);
+            Cut c{0, 0, 0, cur.b, head0, rows, 0, vs};
+            if (line.apart) {
+                c.at = static_cast<int>(quotient(cur.step, line.tier_size[0]));
+                c.c0 = number - c.at;
+                c.n = parts_of(line, cur.n_steps);
             } else {
-                here.c0 = static_cast<int>(quotient(u - cur.step, share));
-                here.n = static_cast<int>(quotient(u - cur.step + cur.n_steps - 1, share)) - here.c0 + 1;
+                c.c0 = chunk_of(line, ctas, u - cur.step);
+                c.at = number - c.c0;
+                c.n = chunk_of(line, ctas, u - cur.step + cur.n_steps - 1) - c.c0 + 1;
             }
-            // counters by the CTA of the run's first part.  That CTA may end one item and
-            // begin another, so first runs, later runs and second rounds count apart.
-            const int run = (cta - here.c0) / kMaxJoin;
-            if (tid == 0) cuts[begins] = here;
-            arrive(counters + (run == 0 ? 0 : ctas) + here.c0 + run * kMaxJoin,
-                   min(kMaxJoin, here.n - run * kMaxJoin), &cuts[begins].last);
+            if (tid == 0) cuts[n_cuts] = c;
+            if (++n_cuts == kMaxCuts) flush(n_cuts), n_cuts = 0;
         }
         if (left <= 0) break;
         u += cur.step_end - cur.step;
         consumers_sync<CT>();
+        seg = &segs[turn];
     }
-    consumers_sync<CT>();
-    settle(cuts[0]);
-    settle(cuts[1]);
+    }
+    if (n_cuts) flush(n_cuts);
 }
 
 template <class S>
@@ -911,8 +1145,8 @@ int launch_attn_shape(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stre
     int shift = -1;
     if ((a.page_size & (a.page_size - 1)) == 0)
         for (shift = 0; (1 << shift) < a.page_size;) ++shift;
-    return launch_dependent(attn_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), S::THREADS,
-                            S::SMEM, stream, a, shift);
+    return launch_dependent(attn_kernel<S>, dim3(static_cast<unsigned>(attn_ctas(ctx.num_sms))),
+                            dim3(S::THREADS), S::SMEM, stream, a, shift);
 }
 
 template <int DT, bool E4M3, int DP>
