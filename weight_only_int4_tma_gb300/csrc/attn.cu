@@ -9,10 +9,10 @@ template <> int launch_attn_typed<1, false>(const DeviceCtx&, const AttnArgs&, c
 template <> int launch_attn_typed<1, true>(const DeviceCtx&, const AttnArgs&, cudaStream_t);
 
 size_t attn_workspace_bytes(const DeviceCtx& ctx, int q_heads, int kv_heads, int head_dim) {
-    const int ctas = attn_ctas(ctx.num_sms);
+    const int ctas = ctx.num_sms;
     const int rows = q_heads / kv_heads <= 8 ? 8 : 16;
     const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    return attn_counter_bytes(ctas) + 2ull * ctas * kTiers * attn_part_floats(rows, dp) * 4;
+    return attn_counter_bytes(ctas) + 2ull * ctas * attn_part_floats(rows, dp) * 4;
 }
 
 int launch_attn(const DeviceCtx& ctx, const AttnArgs& a, int dtype, bool e4m3, cudaStream_t stream) {

@@ -22,44 +22,27 @@
 // (a warp vote finds out; exact in the end, since numerator and denominator share it).
 //
 // Work split.  The steps of all (sequence, head, row tile) items stand in one line, which is cut
-// in chunks whatever the lengths; the cut follows from the lengths on the device alone.  Every
-// CTA has one chunk to begin with, of 9/16 of its share; the rest is cut in ever smaller chunks
-// that CTAs claim as they become free, because SMs do not get equal shares of the bandwidth
-// (measured with equal shares: the first of 152 done after 49 us, the last after 86).  The
-// producers run on into the next item and the next chunk while the consumers finish one.  An
-// item inside one chunk is finished there; one that is cut leaves (m, l, O) of each part in
-// fp32 in the workspace.  A CTA counts its parts once its chunks are done, and whoever completes
-// an item's count joins its parts, in their order.  Which CTA takes a chunk changes no result.
-// (Counting and joining at once, while copies run, costs the consumers 4 to 7 us a part; a
-// second kernel for the joins costs 6 to 10 us a call.)
+// in equal shares, one per CTA, whatever the lengths; every CTA finds its own from the lengths
+// on the device.  The producers run on into the next item while the consumers finish one.  An
+// item inside one share is finished there; one that is cut leaves (m, l, O) of each part in
+// fp32 in the workspace, and the CTA that completes an item's count of parts joins them, in
+// their order.  (SMs do not get equal bandwidth, so shares of falling size claimed by whoever
+// is free end more evenly; but each more part costs more than that gives: 24 sequences of 8192
+// tokens, 4 heads of 128 with 16 rows: 77 us with equal shares, 87 to 92 with claimed ones; 64
+// sequences up to 16384 tokens: 355 and 349 us.)
 #pragma once
-#include <type_traits>
-
 #include "decode.cuh"
 
 namespace w4g {
 
 constexpr float kLag = 8.0f;       // scores may pass the reference by 2^8
-constexpr int kMaxJoin = 32;       // parts that one CTA joins at once
-constexpr int kFewParts = 8;       // parts that one warp joins
-constexpr int kMaxCuts = 32;       // parts that a CTA writes before it counts them
-constexpr int kTierRounds = 24;    // rounds of the warps from which on chunks come in tiers
-constexpr int kManyRounds = 128;   // the same for few items
-constexpr int kLeastRounds = 4;    // of the smallest chunks: 4 us at a CTA's share of the bandwidth
-
-// The workspace: the ticket of the next chunk to claim, three counters per chunk, then for each
-// chunk two parts (its first item if that began in an earlier chunk, its last if that ends in
-// a later one) of m[rows], l[rows], O[rows][dp].
-constexpr int kTiers = 6;          // chunk sizes; one chunk of each size per CTA
-// One CTA per SM; two rounds of joins hold the parts of at most kMaxJoin^2 chunks.
-constexpr int attn_ctas(int num_sms) {
-    return num_sms * kTiers <= kMaxJoin * kMaxJoin ? num_sms : kMaxJoin * kMaxJoin / kTiers;
-}
+// The workspace: a counter per CTA, then for each CTA two parts (its first item if that began in
+// an earlier share, its last if that ends in a later one) of m[rows], l[rows], O[rows][dp].
 __host__ __device__ constexpr size_t attn_part_floats(int rows, int dp) {
     return static_cast<size_t>(rows) * (dp + 2);
 }
 __host__ __device__ constexpr size_t attn_counter_bytes(int ctas) {
-    return (static_cast<size_t>(ctas) * kTiers * 12 + 4 + 127) / 128 * 128;
+    return (static_cast<size_t>(ctas) * 4 + 127) / 128 * 128;
 }
 
 namespace {
@@ -140,7 +123,6 @@ struct AttnShape {
     static constexpr int THREADS = 32 * (W + PW);
     static constexpr int RING = NST * 2 * SLOT;
     static constexpr int SMEM = RING + SOE * ROWS * OP * 4 + NST * (4 + 3 * 8);
-    static_assert(SOE * OP >= 2 * kMaxJoin, "a join's numbers fit where the sums stand");
     static_assert(NST >= W && SMEM <= 224 * 1024 && W % SOE == 0, "the ring fits");
 };
 
@@ -182,42 +164,20 @@ struct Segment {
     Span span;
 };
 
-// A chunk of the line: its number, where it begins, its steps (0: no more chunks) and the first
-// item's part of it.
-struct Chunk {
-    long long u;
-    int number, n;
-    Segment first;
-};
-constexpr int kChunkRing = 8;  // chunks announced inside a CTA
-
-// A part of an item that several chunks hold: the item's are those of chunks c0 .. c0 + n - 1.
+// A part of an item that several CTAs hold: the item's are those of CTAs c0 .. c0 + n - 1.
 struct Cut {
-    int c0, n, at, b, head0, rows, last;  // at: the part written here; last: it completes its run
+    int c0, n, b, head0, rows, last;  // last: the part counted here completes the item
     float vs;
 };
 
-// The line of steps and its chunks, the same in every CTA.
+// The line of steps and its shares, the same in every CTA.
 struct Line {
-    long long tier_base[kTiers], tier_size[kTiers], end;
-    bool apart;   // chunks are parts of one item each
-    bool tiers;   // chunks of several sizes, all but the first of each CTA claimed
+    long long end, share;
+    bool apart;   // a share is a part of one item
 };
-// chunk of step u of the line (not `apart`)
-__device__ __forceinline__ int chunk_of(const Line& line, int ctas, long long u) {
-    int k = 0;
-    if (line.tiers)
-        while (k < kTiers - 1 && u >= line.tier_base[k + 1]) ++k;
-    return k * ctas + static_cast<int>(quotient(u - line.tier_base[k], line.tier_size[k]));
-}
-// first step of a chunk (not `apart`)
-__device__ __forceinline__ long long chunk_begin(const Line& line, int ctas, int c) {
-    const int k = line.tiers ? min(c / ctas, kTiers - 1) : 0;
-    return min(line.end, line.tier_base[k] + line.tier_size[k] * (c - k * ctas));
-}
 // parts that an item of n_steps is cut in (`apart`)
 __device__ __forceinline__ int parts_of(const Line& line, int n_steps) {
-    return static_cast<int>(quotient(n_steps + line.tier_size[0] - 1, line.tier_size[0]));
+    return static_cast<int>(quotient(n_steps + line.share - 1, line.share));
 }
 
 // Fills `line` and prefix[thread], the steps before each thread's sequences (thread t has
@@ -255,35 +215,18 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
         const long long items = (total >> kSeqBit) * items_per_seq;
         total = (total & kLow) * items_per_seq;
         line.end = total;
-        // Whole rounds of the warps: a chunk of fewer steps would take as long.
+        // Whole rounds of the warps: a share of fewer steps would take as long.
         const int slots = ctas * WARPS;
         const long long rounds = max(quotient(total + slots - 1, slots), 1ll);
-        // Few items: equal chunks until there are many rounds (many small chunks of few items
-        // are many parts to join).
-        const bool few = 2 * items <= ctas;
-        line.tiers = rounds >= (few ? kManyRounds : kTierRounds);
+        line.share = rounds * WARPS;
+        // Few items: shares cut from one item each, so that no CTA has two partial items to write
+        // and join, if that takes at most one round more.
         line.apart = false;
-        line.tier_base[0] = 0;
-        line.tier_size[0] = rounds * WARPS;
-        if (line.tiers) {
-            // Each size 5/8 of what is left, down to kLeastRounds; few items: at most three.
-            long long base = 0, togo = rounds;
-            for (int k = 0; k < kTiers; ++k) {
-                long long r = max((togo * 5) >> 3, static_cast<long long>(kLeastRounds));
-                const bool rest = k == kTiers - 1 || togo - r < kLeastRounds || (few && k == 2);
-                const long long size = rest ? max(quotient(max(total - base, 0ll) + ctas - 1, ctas), 1ll) : r * WARPS;
-                line.tier_base[k] = base;
-                line.tier_size[k] = size;
-                if (base < total) base += size * ctas;
-                togo = rest ? 0 : togo - r;
-            }
-        } else if (few) {
-            // Chunks cut from one item each, so that no CTA has two partial items to write and
-            // join; at most one round more, and one chunk per CTA.
+        if (2 * items <= ctas) {
             const int left = static_cast<int>(ctas - items) * WARPS;
             const long long r = max(quotient(total + left - 1, left), 1ll);
             line.apart = r <= rounds + 1;
-            if (line.apart) line.tier_size[0] = r * WARPS;
+            if (line.apart) line.share = r * WARPS;
         }
     }
 }
@@ -317,12 +260,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     __shared__ Line line;
     __shared__ long long scan[W + S::PW];
     __shared__ long long prefix[S::THREADS];
-    __shared__ Chunk chunks[kChunkRing];
-    __shared__ uint64_t chunk_bars[kChunkRing];
-    __shared__ Segment segs[2];                // the segment after the chunk's first, in turn
-    __shared__ Cut cuts[kMaxCuts];             // parts written, not yet counted
-    __shared__ float row_m[ROWS], row_l[ROWS];
-    __shared__ int chunk_n, is_last;
+    __shared__ Segment segs[2];                // the current one and the one after it, in turn
+    __shared__ int share_n;
+    __shared__ Cut cuts[2];                    // an item begun by an earlier CTA, one left to a later
 
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, i = lane & 3;
@@ -331,8 +271,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     const int row_tiles = (G + ROWS - 1) / ROWS;
     const int items_per_seq = a.kv_heads * row_tiles;
     const int row_bytes = a.head_dim * S::ES;
-    int* ticket = static_cast<int*>(a.workspace);
-    int* counters = ticket + 1;
+    int* counters = static_cast<int*>(a.workspace);
     float* parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + attn_counter_bytes(ctas));
 
     if (row_bytes < S::PITCH) {  // columns past the head dimension are never copied: zero
@@ -345,8 +284,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         mbar_init(full_v + 8 * tid, 32);
         mbar_init(empty + 8 * tid, 1);
     }
-    const uint32_t announced = smem_addr(chunk_bars);
-    if (tid < kChunkRing) mbar_init(announced + 8 * tid, 1);
     if (tid == 0) abort_flag = 0;
     grid_dep_wait();
     lay_line<STEP, S::THREADS, W>(a, items_per_seq, ctas, cta == 0, line, prefix, scan);
@@ -360,7 +297,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             for (int h = tid; h < a.q_heads; h += S::THREADS)
                 a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
     }
-    __syncthreads();  // prefix, the barriers, and the zeroed ring
+    __syncthreads();  // line, prefix, the barriers, and the zeroed ring
 
     // the segment after `s`: the next item's first steps, at most `left`
     auto after = [&](const Segment& s, int left) {
@@ -378,9 +315,62 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         return n;
     };
 
+    // The CTA's share: its steps (0: none), and the first item's part of it.  By all lanes of a warp.
+    long long u = 0;   // its first step in the line (not `apart`)
+    auto locate = [&](Segment& first) {
+        if (line.apart) {  // the cta-th part of all items
+            int done = 0, n = 0;
+            for (int b0 = 0; b0 < a.B && n == 0; b0 += 32) {
+                const int b = b0 + lane, share = static_cast<int>(line.share);
+                const Span span = b < a.B ? visible(a, b, false) : Span{0, 0};
+                const int n_steps = span_steps<STEP>(span), per = parts_of(line, n_steps);
+                int incl = per * items_per_seq;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+                    if (lane >= d) incl += o;
+                }
+                const int at = cta - done - (incl - per * items_per_seq);
+                const bool here = at >= 0 && at < per * items_per_seq;
+                const int step = here ? at % per * share : 0;
+                const unsigned who = __ballot_sync(0xFFFFFFFFu, here);
+                if (who) {
+                    const int from = __ffs(who) - 1;
+                    auto get = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
+                    first = Segment{get(b), get(here ? at / per : 0), get(step), get(min(n_steps, step + share)),
+                                    get(n_steps), Span{get(span.first), get(span.len)}};
+                    n = first.step_end - first.step;
+                }
+                done += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
+            return n;
+        }
+        u = line.share * cta;
+        if (u >= line.end) return 0;
+        const int n = static_cast<int>(min(line.end - u, line.share));
+        // the thread whose sequences hold step u, then the sequence
+        int t = 0;
+        for (int t0 = 0; t0 < S::THREADS && t0 * per_thread < a.B; t0 += 32)
+            t += __popc(__ballot_sync(0xFFFFFFFFu, prefix[t0 + lane] <= u));
+        --t;
+        long long at = prefix[t];
+        int b = t * per_thread;
+        Span span = visible(a, b, false);
+        int n_steps = span_steps<STEP>(span);
+        while (at + static_cast<long long>(n_steps) * items_per_seq <= u && b + 1 < a.B) {
+            at += static_cast<long long>(n_steps) * items_per_seq;
+            span = visible(a, ++b, false);
+            n_steps = span_steps<STEP>(span);
+        }
+        const int item = static_cast<int>(quotient(u - at, n_steps));
+        const int step = static_cast<int>(u - at - static_cast<long long>(item) * n_steps);
+        first = Segment{b, item, step, min(n_steps, step + n), n_steps, span};
+        return n;
+    };
+
     const uint32_t ring = smem_addr(smem);
     if (warp >= W) {
-        // ---- producers: steps pw, pw + PW, ... of the CTA's chunks ----
+        // ---- producers: steps pw, pw + PW, ... of the share ----
         const int pw = warp - W;
         Segment ld{};
         constexpr int RPI = 32 / CH;   // token rows that one instruction of the warp copies
@@ -457,109 +447,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                 if (column) copy16(to, ok ? p : base, ok ? 16 : 0);
             }
         };
-        // Warp 0 finds the chunks: the CTA's own first, then claims, one chunk ahead of use.
-        auto locate = [&](int number) {  // by all lanes; lane 0's result counts
-            Chunk c{};
-            c.number = number;
-            if (line.apart) {  // the number-th part of all items
-                int done = 0;
-                for (int b0 = 0; b0 < a.B && c.n == 0; b0 += 32) {
-                    const int b = b0 + lane, size0 = static_cast<int>(line.tier_size[0]);
-                    const Span span = b < a.B ? visible(a, b, false) : Span{0, 0};
-                    const int n_steps = span_steps<STEP>(span), per = parts_of(line, n_steps);
-                    int incl = per * items_per_seq;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-                        if (lane >= d) incl += o;
-                    }
-                    const int at = number - done - (incl - per * items_per_seq);
-                    const bool here = at >= 0 && at < per * items_per_seq;
-                    if (here) {
-                        const int step = at % per * size0;
-                        c.first = Segment{b, at / per, step, min(n_steps, step + size0), n_steps, span};
-                        c.n = c.first.step_end - step;
-                    }
-                    const unsigned who = __ballot_sync(0xFFFFFFFFu, here);
-                    if (who) {  // to lane 0, word by word
-                        int* w = reinterpret_cast<int*>(&c);
-#pragma unroll
-                        for (int e = 0; e < static_cast<int>(sizeof(Chunk) / 4); ++e)
-                            w[e] = __shfl_sync(0xFFFFFFFFu, w[e], __ffs(who) - 1);
-                    }
-                    done += __shfl_sync(0xFFFFFFFFu, incl, 31);
-                }
-                return c;
-            }
-            c.u = chunk_begin(line, ctas, number);
-            if (c.u >= line.end) return c;
-            c.n = static_cast<int>(chunk_begin(line, ctas, number + 1) - c.u);
-            // the thread whose sequences hold step u, then the sequence
-            int t = 0;
-            for (int t0 = 0; t0 < S::THREADS && t0 * per_thread < a.B; t0 += 32)
-                t += __popc(__ballot_sync(0xFFFFFFFFu, prefix[t0 + lane] <= c.u));
-            --t;
-            long long at = prefix[t];
-            int b = t * per_thread;
-            Span span = visible(a, b, false);
-            int n_steps = span_steps<STEP>(span);
-            while (at + static_cast<long long>(n_steps) * items_per_seq <= c.u && b + 1 < a.B) {
-                at += static_cast<long long>(n_steps) * items_per_seq;
-                span = visible(a, ++b, false);
-                n_steps = span_steps<STEP>(span);
-            }
-            const int item = static_cast<int>(quotient(c.u - at, n_steps));
-            const int step = static_cast<int>(c.u - at - static_cast<long long>(item) * n_steps);
-            c.first = Segment{b, item, step, min(n_steps, step + c.n), n_steps, span};
-            return c;
-        };
-        auto announce = [&](int k, int number) {  // the CTA's k-th chunk
-            const Chunk c = number < 0 ? Chunk{} : locate(number);
-            if (lane == 0) {
-                chunks[k % kChunkRing] = c;
-                mbar_arrive(announced + 8 * (k % kChunkRing));
-            }
-            return c.n > 0;
-        };
-        // The ticket of the next chunk, drawn early and looked at later; -1: there is no more.
-        // Every CTA fails once; the one that does so last readies the ticket for the next call.
-        const int claimable = line.tiers ? chunk_of(line, ctas, line.end - 1) + 1 - ctas : 0;
-        int drawn = 0;
-        auto draw = [&]() {
-            if (line.tiers && lane == 0) drawn = atomicAdd(ticket, 1);
-        };
-        auto claim = [&]() {
-            if (!line.tiers) return -1;
-            if (lane == 0 && drawn == claimable + ctas - 1) *ticket = 0;
-            const int v = __shfl_sync(0xFFFFFFFFu, drawn, 0);
-            return v < claimable ? ctas + v : -1;
-        };
-        bool more = true;
-        if (pw == 0) more = announce(0, cta);
-        int x = pw;                    // this warp's next step of the CTA
-        int seg0 = 0;                  // the CTA's steps before segment ld
+        const int n_all = locate(ld);
+        int seg0 = 0, seg_n = ld.step_end - ld.step;   // the share's steps before segment ld, and its own
         int stage = pw;
         uint32_t phase = 0;
+        bool opened = false;
 #pragma unroll 1
-        for (int k = 0;; ++k) {
-            bool may_draw = pw == 0 && more, drew = false;
-            const bool there_is = mbar_wait_warp(announced + 8 * (k % kChunkRing), (k / kChunkRing) & 1,
-                                                 &abort_flag, a.status, a.timeout_ns);
-            const Chunk& chunk = chunks[k % kChunkRing];
-            const int n_all = seg0 + chunk.n;
-            if (!there_is) {  // given up: the ticket has to end as it began
-                while (line.tiers && may_draw) {
-                    draw();
-                    may_draw = claim() >= 0;
-                }
-                break;
-            }
-            if (chunk.n == 0) break;
-            ld = chunk.first;
-            int seg_n = ld.step_end - ld.step;
-            bool opened = false;
-#pragma unroll 1
-            for (; x < n_all; x += S::PW) {
+        for (int x = pw; x < n_all; x += S::PW) {
             while (x >= seg0 + seg_n) {
                 seg0 += seg_n;
                 ld = after(ld, n_all - seg0);
@@ -603,20 +497,6 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             }
             stage += S::PW;
             if (stage >= NST) stage -= NST, phase ^= 1u;
-            // the next chunk: drawn some 4 us before this one ends, looked at 2 us later
-            if (may_draw && n_all - x <= 10 * S::PW) {
-                draw();
-                drew = true;
-                may_draw = false;
-            }
-            if (drew && n_all - x <= 5 * S::PW) {
-                more = announce(k + 1, claim());
-                drew = false;
-            }
-            }
-            if (may_draw) draw();
-            if (may_draw || drew) more = announce(k + 1, claim());
-            seg0 = n_all;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
@@ -625,165 +505,87 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     // ---- consumers ----
     constexpr int CT = 32 * W;  // their threads
     constexpr int E = (ROWS * DP / 4 + CT - 1) / CT;  // 16-byte pieces of a result per thread
-    // ---- parts of an item that several chunks hold ----
-    auto fan_of = [](int n) { return n > kMaxJoin && n <= 256 ? 16 : kMaxJoin; };  // parts of a run
+    // ---- parts of an item that several CTAs hold ----
     auto part_of = [&](const Cut& c, int k) {  // part k of the item
         return parts + (2 * (c.c0 + k) + (k == 0 ? 1 : 0)) * attn_part_floats(ROWS, DP);
     };
-    auto give = [&](const Cut& c, int row, int d, float4 v, float sum) {
-        if (d < a.head_dim) store_out<S::DT>(a, c.b, c.head0 + row, d, v, sum > 0.0f ? c.vs / sum : 0.0f);
-    };
-    // Parts k0, k0 + stride, ... (count of them, at most kMaxJoin) into one: written over part
-    // k0, or stored as the result.
-    auto join = [&](const Cut& c, int k0, int stride, int count, bool final) {
-        constexpr int KB = E >= 8 ? 2 : 16 / E;     // parts in flight
-        float* jm = so;                             // [part][row]: m, then its factor
-        float* jl = so + kMaxJoin * ROWS;           // [part][row]
-        for (int e = tid; e < count * ROWS; e += CT) {
-            const float* p = part_of(c, k0 + e / ROWS * stride) + e % ROWS;
-            const bool in = e % ROWS < c.rows;
-            jm[e] = in ? __ldcg(p) : -INFINITY;
-            jl[e] = in ? __ldcg(p + ROWS) : 0.0f;
-        }
-        float4 acc[E], x[KB][E];
-        auto fetch = [&](int k) {
+    // One row of an item from its parts, by one warp: lane k has part k's m and l (of 32 parts at
+    // a time), kAtOnce parts' values are under way together.
+    constexpr int JV = DP > 128 ? DP / 128 : 1;      // 16-byte pieces of a row per lane
+    constexpr int JS = DP < 128 ? 128 / DP : 1;      // parts that a warp reads side by side
+    constexpr int kAtOnce = 16 / JV;
+    auto join_row = [&](const Cut& c, int row) {
+        const int sub = lane / (32 / JS), l4 = 4 * (lane % (32 / JS));
+        float top = -INFINITY, sum = 0.0f;
+        float4 acc[JV];
 #pragma unroll
-            for (int j = 0; j < KB; ++j)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
-                    x[j][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (k + j < count && row < c.rows && d < a.head_dim)
-                        x[j][e] = __ldcg(reinterpret_cast<const float4*>(
-                            part_of(c, k0 + (k + j) * stride) + 2 * ROWS + row * DP + d));
-                }
-        };
-        fetch(0);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        consumers_sync<CT>();
-        for (int row = warp; row < ROWS; row += W) {
-            const float m = lane < count ? jm[lane * ROWS + row] : -INFINITY;
-            const float top = warp_max(m);
-            const float f = m == -INFINITY ? 0.0f : exp2_fast(m - top);
-            const float sum = warp_sum(lane < count ? f * jl[lane * ROWS + row] : 0.0f);
-            if (lane < count) jm[lane * ROWS + row] = f;
-            if (lane == 0) row_m[row] = top, row_l[row] = sum;
-        }
-        consumers_sync<CT>();
-        for (int k = 0; k < count; k += KB) {
-            if (k) fetch(k);
-#pragma unroll
-            for (int j = 0; j < KB; ++j)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int row = (tid + e * CT) / (DP / 4);
-                    const float f = k + j < count && row < ROWS ? jm[(k + j) * ROWS + row] : 0.0f;
-                    acc[e].x = fmaf(x[j][e].x, f, acc[e].x), acc[e].y = fmaf(x[j][e].y, f, acc[e].y);
-                    acc[e].z = fmaf(x[j][e].z, f, acc[e].z), acc[e].w = fmaf(x[j][e].w, f, acc[e].w);
-                }
-        }
-        float* to = part_of(c, k0);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
-            if (row >= c.rows) continue;
-            if (final) give(c, row, d, acc[e], row_l[row]);
-            else *reinterpret_cast<float4*>(to + 2 * ROWS + row * DP + d) = acc[e];
-        }
-        if (tid < c.rows) {
-            if (final) store_lse(a, c.b, c.head0 + tid, row_m[tid], row_l[tid], kShift);
-            else to[tid] = row_m[tid], to[ROWS + tid] = row_l[tid];
-        }
-    };
-    // The parts of an item, or of a run of `fan` where they are many: one CTA reads about
-    // 0.1 TB/s, and 152 parts of one item of 8 rows and 128 dimensions are 0.6 MB.  The runs'
-    // results are parts again, joined by the CTA that completes the last run.
-    auto settle = [&](const Cut& c) {
-        const int fan = fan_of(c.n), run = c.at / fan, runs = (c.n + fan - 1) / fan;
-        consumers_sync<CT>();
-        join(c, run * fan, 1, min(fan, c.n - run * fan), runs == 1);
-        if (runs > 1) {
-            __threadfence();
-            consumers_sync<CT>();
-            if (tid == 0) {
-                int* counter = counters + 2 * ctas * kTiers + c.c0;
-                is_last = atomicAdd(counter, 1) == runs - 1;
-                if (is_last) *counter = 0;
-                __threadfence();
-            }
-            consumers_sync<CT>();
-            if (is_last) join(c, 0, fan, runs, true);
-        }
-    };
-    // The same for up to kFewParts parts, by one warp: a CTA that claims chunks completes several
-    // small items.  N parts of 16 / N pieces are read at a time.
-    auto join_few = [&](const Cut& c, auto parts_at_once) {
-        constexpr int N = decltype(parts_at_once)::value, U = 16 / N;
+        for (int v = 0; v < JV; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-        for (int at0 = lane; at0 < c.rows * (DP / 4); at0 += 32 * U) {
-            float pm[U][N], pl[U][N];
-            float4 x[U][N];
+        for (int k32 = 0; k32 < c.n; k32 += 32) {
+            const int mine = k32 + lane;
+            const float pm = mine < c.n ? __ldcg(part_of(c, mine) + row) : -INFINITY;
+            const float pl = mine < c.n ? __ldcg(part_of(c, mine) + ROWS + row) : 0.0f;
+            float f = 0.0f;
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32 && k32 + k0 < c.n; k0 += kAtOnce * JS) {
+                float4 x[kAtOnce][JV];
 #pragma unroll
-            for (int o = 0; o < U; ++o)
+                for (int j = 0; j < kAtOnce; ++j)
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const int at = at0 + 32 * o, row = at / (DP / 4), d = 4 * (at % (DP / 4));
-                    const float* p = part_of(c, k);
-                    const bool in = k < c.n && row < c.rows;
-                    pm[o][k] = in ? __ldcg(p + row) : -INFINITY;
-                    pl[o][k] = in ? __ldcg(p + ROWS + row) : 0.0f;
-                    x[o][k] = in && d < a.head_dim ? __ldcg(reinterpret_cast<const float4*>(p + 2 * ROWS + row * DP + d))
-                                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int v = 0; v < JV; ++v) {
+                        const int k = k32 + k0 + j * JS + sub, d = l4 + 128 * v;
+                        x[j][v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (k < c.n && d < a.head_dim)
+                            x[j][v] = __ldcg(reinterpret_cast<const float4*>(part_of(c, k) + 2 * ROWS + row * DP + d));
+                    }
+                if (k0 == 0) {  // the new maximum, and what it makes of the sums so far
+                    const float now = fmaxf(top, warp_max(pm));
+                    const float old = top == -INFINITY ? 0.0f : exp2_fast(top - now);
+                    top = now;
+                    f = pm == -INFINITY ? 0.0f : exp2_fast(pm - now);
+                    sum = sum * old + warp_sum(pl * f);
+#pragma unroll
+                    for (int v = 0; v < JV; ++v) acc[v].x *= old, acc[v].y *= old, acc[v].z *= old, acc[v].w *= old;
                 }
 #pragma unroll
-            for (int o = 0; o < U; ++o) {
-                const int at = at0 + 32 * o, row = at / (DP / 4), d = 4 * (at % (DP / 4));
-                if (row >= c.rows) continue;
-                float top = -INFINITY, sum = 0.0f;
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const float fk = __shfl_sync(0xFFFFFFFFu, f, (k0 + j * JS + sub) & 31);
 #pragma unroll
-                for (int k = 0; k < N; ++k) top = fmaxf(top, pm[o][k]);
-#pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const float f = pm[o][k] == -INFINITY ? 0.0f : exp2_fast(pm[o][k] - top);
-                    sum = fmaf(pl[o][k], f, sum);
-                    v.x = fmaf(x[o][k].x, f, v.x), v.y = fmaf(x[o][k].y, f, v.y);
-                    v.z = fmaf(x[o][k].z, f, v.z), v.w = fmaf(x[o][k].w, f, v.w);
+                    for (int v = 0; v < JV; ++v) {
+                        acc[v].x = fmaf(x[j][v].x, fk, acc[v].x), acc[v].y = fmaf(x[j][v].y, fk, acc[v].y);
+                        acc[v].z = fmaf(x[j][v].z, fk, acc[v].z), acc[v].w = fmaf(x[j][v].w, fk, acc[v].w);
+                    }
                 }
-                give(c, row, d, v, sum);
-                if (d == 0) store_lse(a, c.b, c.head0 + row, top, sum, kShift);
             }
         }
+        if constexpr (JS == 2) {
+            acc[0].x += __shfl_xor_sync(0xFFFFFFFFu, acc[0].x, 16), acc[0].y += __shfl_xor_sync(0xFFFFFFFFu, acc[0].y, 16);
+            acc[0].z += __shfl_xor_sync(0xFFFFFFFFu, acc[0].z, 16), acc[0].w += __shfl_xor_sync(0xFFFFFFFFu, acc[0].w, 16);
+        }
+        const float f = sum > 0.0f ? c.vs / sum : 0.0f;
+#pragma unroll
+        for (int v = 0; v < JV; ++v)
+            if (sub == 0 && l4 + 128 * v < a.head_dim) store_out<S::DT>(a, c.b, c.head0 + row, l4 + 128 * v, acc[v], f);
+        if (lane == 0) store_lse(a, c.b, c.head0 + row, top, sum, kShift);
     };
-    // Counts the parts written since the last time, and joins the items (or runs) they complete.
-    auto flush = [&](int n_cuts) {
+    // Counts the parts written, and joins the items that they complete, a row per warp.
+    auto settle = [&](int n_cuts) {
         __threadfence();
         consumers_sync<CT>();
         if (tid < n_cuts) {
             Cut& c = cuts[tid];
-            // counters by the chunk of the run's first part.  That chunk may end one item and
-            // begin another, so first runs, later runs and second rounds count apart.
-            const int fan = fan_of(c.n), run = c.at / fan;
-            int* counter = counters + (run == 0 ? 0 : ctas * kTiers) + c.c0 + run * fan;
-            c.last = atomicAdd(counter, 1) == min(fan, c.n - run * fan) - 1;
-            if (c.last) *counter = 0;  // ready for the next call
+            c.last = atomicAdd(counters + c.c0, 1) == c.n - 1;
+            if (c.last) counters[c.c0] = 0;  // ready for the next call
             __threadfence();
         }
         consumers_sync<CT>();
-        // the choice follows from the line and the item: equal inputs give equal bits
-        auto by_warp = [&](const Cut& c) { return line.tiers && c.n <= kFewParts; };
         int nth = 0;
-        for (int j = 0; j < n_cuts; ++j)
-            if (cuts[j].last && by_warp(cuts[j]) && nth++ % W == warp) {
-                const Cut c = cuts[j];
-                if (c.n <= 2) join_few(c, std::integral_constant<int, 2>{});
-                else if (c.n <= 4) join_few(c, std::integral_constant<int, 4>{});
-                else join_few(c, std::integral_constant<int, kFewParts>{});
-            }
-        for (int j = 0; j < n_cuts; ++j)
-            if (cuts[j].last && !by_warp(cuts[j])) settle(cuts[j]);
-        consumers_sync<CT>();
+        for (int j = 0; j < n_cuts; ++j) {
+            if (!cuts[j].last) continue;
+            const Cut c = cuts[j];
+            for (int row = 0; row < c.rows; ++row)
+                if (nth++ % W == warp) join_row(c, row);
+        }
     };
 
     // ---- addresses of ldmatrix's rows in a slot, for this lane ----
@@ -795,23 +597,21 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         return static_cast<uint32_t>(r * 16 * S::PITCH + (CH >= 8 ? (c & ~7) << 4 : 0));
     };
 
-    int taken = 0;             // the CTA's steps before the segment
-    int turn = 0, n_cuts = 0;
-    for (int k = 0;; ++k) {
-    if (tid == 0) {
-        mbar_wait_bounded(announced + 8 * (k % kChunkRing), (k / kChunkRing) & 1, &abort_flag, a.status, a.timeout_ns);
-        chunk_n = abort_flag ? 0 : chunks[k % kChunkRing].n;
+    if (warp == 0) {
+        Segment first{};
+        const int n = locate(first);
+        if (lane == 0) segs[0] = first, share_n = n;
     }
     consumers_sync<CT>();
-    int left = chunk_n;        // steps of the chunk not yet begun
-    if (left == 0) break;
-    const int number = chunks[k % kChunkRing].number;
-    long long u = chunks[k % kChunkRing].u;
-    const Segment* seg = &chunks[k % kChunkRing].first;
-    for (;; turn ^= 1) {
-        const Segment& cur = *seg;
+    int left = share_n;        // steps of the share not yet begun
+    if (left == 0) return;
+    u = line.share * cta;
+    int taken = 0;             // the share's steps before the segment
+    int n_cuts = 0;
+    for (int turn = 0;; turn ^= 1) {
+        const Segment& cur = segs[turn];
         left -= cur.step_end - cur.step;
-        if (left > 0 && tid == 0) segs[turn] = after(cur, left);
+        if (left > 0 && tid == 0) segs[turn ^ 1] = after(cur, left);
         const int kvh = cur.item / row_tiles, row0 = (cur.item - kvh * row_tiles) * ROWS;
         const int rows = min(ROWS, G - row0), head0 = kvh * G + row0;
         const Span span = cur.span;
@@ -1096,7 +896,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         const bool begins = cur.step == 0, ends = cur.step_end == cur.n_steps;
         const bool whole = begins && ends;
         const float vs = S::E4M3 && a.vc.scale ? a.vc.scale[kvh] : 1.0f;
-        float* part = parts + (2 * number + (begins ? 1 : 0)) * attn_part_floats(ROWS, DP);
+        float* part = parts + (2 * cta + (begins ? 1 : 0)) * attn_part_floats(ROWS, DP);
         float top;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -1115,26 +915,22 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             else part[tid] = top, part[ROWS + tid] = sum;
         }
         if (!whole) {
-            Cut c{0, 0, 0, cur.b, head0, rows, 0, vs};
+            Cut c{0, 0, cur.b, head0, rows, 0, vs};
             if (line.apart) {
-                c.at = static_cast<int>(quotient(cur.step, line.tier_size[0]));
-                c.c0 = number - c.at;
+                c.c0 = cta - static_cast<int>(quotient(cur.step, line.share));
                 c.n = parts_of(line, cur.n_steps);
             } else {
-                c.c0 = chunk_of(line, ctas, u - cur.step);
-                c.at = number - c.c0;
-                c.n = chunk_of(line, ctas, u - cur.step + cur.n_steps - 1) - c.c0 + 1;
+                c.c0 = static_cast<int>(quotient(u - cur.step, line.share));
+                c.n = static_cast<int>(quotient(u - cur.step + cur.n_steps - 1, line.share)) - c.c0 + 1;
             }
             if (tid == 0) cuts[n_cuts] = c;
-            if (++n_cuts == kMaxCuts) flush(n_cuts), n_cuts = 0;
+            ++n_cuts;
         }
         if (left <= 0) break;
         u += cur.step_end - cur.step;
         consumers_sync<CT>();
-        seg = &segs[turn];
     }
-    }
-    if (n_cuts) flush(n_cuts);
+    if (n_cuts) settle(n_cuts);
 }
 
 template <class S>
@@ -1145,7 +941,7 @@ int launch_attn_shape(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stre
     int shift = -1;
     if ((a.page_size & (a.page_size - 1)) == 0)
         for (shift = 0; (1 << shift) < a.page_size;) ++shift;
-    return launch_dependent(attn_kernel<S>, dim3(static_cast<unsigned>(attn_ctas(ctx.num_sms))),
+    return launch_dependent(attn_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)),
                             dim3(S::THREADS), S::SMEM, stream, a, shift);
 }
 
