@@ -97,12 +97,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 // DT: 0 fp16, 1 bf16 (queries, output).  E4M3: 8-bit cache.  DP: head dimension rounded up
-// to 64, 128 or 256.  NT: tiles of 8 query heads that a CTA takes at once.  P16: the page
-// size is a multiple of 16, so 16 tokens that begin at a multiple of 16 lie in one page.
-template <int DT_, bool E4M3_, int DP_, int NT_, bool P16_>
+// to 64, 128 or 256.  NT: tiles of 8 query heads that a CTA takes at once.  PG: 16 or 8 where
+// the page size is a multiple of that, so that PG tokens that begin at a multiple of PG lie in
+// one page; else 1.
+template <int DT_, bool E4M3_, int DP_, int NT_, int PG_>
 struct AttnShape {
     static constexpr int DT = DT_, DP = DP_, NT = NT_;
-    static constexpr bool E4M3 = E4M3_, P16 = P16_;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr int PG = PG_;
+    static constexpr bool GROUPS = PG > 1;
     static constexpr bool BF = DT == 1 && !E4M3;  // type of the MMA's operands
     static constexpr int ES = E4M3 ? 1 : 2;
     static constexpr int ROWS = 8 * NT;
@@ -110,20 +113,27 @@ struct AttnShape {
     static constexpr int CH = PITCH / 16;         // 16-byte chunks of it
     // 16 R tokens per step: 4 KB of keys where that is at most 64 tokens; 32 where every
     // lane looks up the page of one token
-    static constexpr int R = PITCH >= 256 ? 1 : PITCH == 128 ? 2 : (P16 ? 4 : 2);
+    static constexpr int R = PITCH >= 256 ? 1 : PITCH == 128 ? 2 : (GROUPS ? 4 : 2);
+    static constexpr int NG = GROUPS ? 16 * R / PG : 1;   // groups of a step
     static constexpr int STEP = 16 * R;
     static constexpr int SLOT = STEP * PITCH;     // bytes of a step's keys, or values
     static constexpr int W = 8;                   // consumer warps
     static constexpr int PW = 4;                  // producer warps
-    static constexpr int NST = 196608 / (2 * SLOT);            // steps of the ring
     static constexpr int MS = DP / 16;            // MMA steps over the head dimension
     static constexpr int OP = DP + 4;             // row of the warps' sums, in floats
-    static constexpr int SOE = NT == 1 ? (DP == 256 ? 2 : 4) : DP == 256 ? 1 : 2;  // warps' sums
-                                                               // in shared memory at once
+    // warps' sums in shared memory at once
+    static constexpr int SOE = DP == 64 ? (NT == 1 ? 8 : 4) : DP == 256 && !E4M3 ? 4 : DP == 128 ? 4 / NT : 2 / NT;
+    static constexpr int SO_BYTES = SOE * ROWS * OP * 4;
+    // Steps of the ring: 192 KB of them (128 KB of those with 512-byte rows), in a multiple of W
+    // and of PW.  A stage then has the same producer in every round, and the same consumer
+    // within an item: nobody waits for a stage two rounds ahead of it, which the barriers' one
+    // bit of phase could not tell from the round at hand.
+    static constexpr int NST = 2 * SLOT == 16384 ? 8 : 24;
     static constexpr int THREADS = 32 * (W + PW);
     static constexpr int RING = NST * 2 * SLOT;
-    static constexpr int SMEM = RING + SOE * ROWS * OP * 4 + NST * (4 + 3 * 8);
-    static_assert(NST >= W && SMEM <= 224 * 1024 && W % SOE == 0, "the ring fits");
+    static constexpr int SMEM = RING + SO_BYTES + NST * (4 + 3 * 8);
+    static_assert(NST % W == 0 && NST % PW == 0, "a stage's producer and consumer are fixed");
+    static_assert(SMEM <= 219 * 1024 && W % SOE == 0, "the ring fits");
 };
 
 // Byte offset of chunk c of token row r in a slot: the chunks of eight rows that ldmatrix
@@ -382,21 +392,21 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         const uint32_t lane_at = ring_at<CH>(lrow, lchunk);
         auto page_of = [&](int tok) { return page_shift >= 0 ? tok >> page_shift : tok / a.page_size; };
         auto wanted = [&](int tok) {
-            return tok < ld.span.len && (S::P16 ? tok + 16 > ld.span.first : tok >= ld.span.first);
+            return tok < ld.span.len && tok + S::PG > ld.span.first;
         };
-        // Page numbers.  P16: lane n R + r has that of group r of the warp's n-th step from the
-        // batch's first on, 32 / R steps at a time and the next ones under way; else lane t
+        // Page numbers.  Groups: lane n NG + r has that of group r of the warp's n-th step from the
+        // batch's first on, 32 / NG steps at a time and the next ones under way; else lane t
         // has that of token t of the next step.
-        constexpr int PB = S::P16 ? 32 / R : 1;
+        constexpr int NG = S::NG, PB = S::GROUPS ? 32 / NG : 1;
         const int32_t* table;
         const char* kbase;
         const char* vbase;
         int first_st = 0, pid = 0, pid_next = 0, in_batch = 0;
         auto fetch_pages = [&](int st) {
-            const int s_ = S::P16 ? st + lane / R * S::PW : st;
-            const int tok = s_ * STEP + (S::P16 ? 16 * (lane % R) : lane);
+            const int s_ = S::GROUPS ? st + lane / NG * S::PW : st;
+            const int tok = s_ * STEP + (S::GROUPS ? S::PG * (lane % NG) : lane);
             int p = 0;
-            if (s_ < first_st + ld.step_end && (S::P16 || lane < STEP) && wanted(tok)) p = table[page_of(tok)];
+            if (s_ < first_st + ld.step_end && (S::GROUPS || lane < STEP) && wanted(tok)) p = table[page_of(tok)];
             return p;
         };
         auto open = [&](int st) {  // begins segment ld at token step ld's first + st
@@ -409,18 +419,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             pid_next = fetch_pages(first_st + st + PB * S::PW);
             in_batch = 0;
         };
-        constexpr int NP = S::P16 ? R : 1;
         // one side's copies of a step: rows of `at` (bytes from base: of each group's first row,
         // or of the lane's token), `lo` <= token < `hi`
-        auto copy = [&](uint32_t dst, const char* base, const int64_t (&at)[NP], int64_t stride,
+        auto copy = [&](uint32_t dst, const char* base, const int64_t (&at)[NG], int64_t stride,
                         uint32_t there, int lo, int hi, bool partial) {
-            if (S::P16 && !partial) {
+            if (S::GROUPS && !partial) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+                for (int r = 0; r < NG; ++r) {
                     const char* p = base + at[r];
 #pragma unroll
-                    for (int j = 0; j < 16 / RPI; ++j) {
-                        const uint32_t to = (dst ^ (CH >= 8 ? ((RPI * j) & 7) << 4 : 0)) + (16 * r + RPI * j) * S::PITCH;
+                    for (int j = 0; j < S::PG / RPI; ++j) {
+                        const uint32_t to = (dst ^ (CH >= 8 ? ((RPI * j) & 7) << 4 : 0)) + (S::PG * r + RPI * j) * S::PITCH;
                         if (column) copy16(to, p, 16);
                         p += RPI * stride;
                     }
@@ -432,12 +441,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                 const int t = t0 + lrow;
                 const char* p;
                 bool ok;
-                if constexpr (S::P16) {
+                if constexpr (S::GROUPS) {
                     int64_t from = at[0];
 #pragma unroll
-                    for (int r = 1; r < R; ++r) from = t0 / 16 == r ? at[r] : from;
-                    p = base + from + (t0 % 16) * stride;
-                    ok = (there >> (t0 / 16)) & 1u;
+                    for (int r = 1; r < NG; ++r) from = t0 / S::PG == r ? at[r] : from;
+                    p = base + from + (t0 % S::PG) * stride;
+                    ok = (there >> (t0 / S::PG)) & 1u;
                 } else {
                     p = base - lrow * stride + __shfl_sync(0xFFFFFFFFu, at[0], t);
                     ok = (there >> t) & 1u;
@@ -463,23 +472,23 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             if (!opened) open(ld.step + x - seg0);
             opened = true;
             const int st = first_st + ld.step + x - seg0;
-            int64_t kat[NP], vat[NP];
-            uint32_t there = 0;  // groups (P16) or tokens whose page is there
+            int64_t kat[NG], vat[NG];
+            uint32_t there = 0;  // groups, or tokens, whose page is there
 #pragma unroll
-            for (int r = 0; r < NP; ++r) {
-                const int tok = st * STEP + (S::P16 ? 16 * r : lane);
-                const int page = S::P16 ? __shfl_sync(0xFFFFFFFFu, pid, in_batch * R + r) : pid;
-                const bool in = wanted(tok) && (S::P16 || lane < STEP);
+            for (int r = 0; r < NG; ++r) {
+                const int tok = st * STEP + (S::GROUPS ? S::PG * r : lane);
+                const int page = S::GROUPS ? __shfl_sync(0xFFFFFFFFu, pid, in_batch * NG + r) : pid;
+                const bool in = wanted(tok) && (S::GROUPS || lane < STEP);
                 const bool ok = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages);
                 if (in && !ok) record_status(a.status, kDecInvalidArg);
                 const int slot = tok - page_of(tok) * a.page_size;
                 kat[r] = ok ? page * kps + slot * kss : 0;
                 vat[r] = ok ? page * vps + slot * vss : 0;
-                if constexpr (S::P16) there |= static_cast<uint32_t>(ok) << r;
+                if constexpr (S::GROUPS) there |= static_cast<uint32_t>(ok) << r;
                 else there = __ballot_sync(0xFFFFFFFFu, ok);
             }
             const int lo = ld.span.first - st * STEP, hi = ld.span.len - st * STEP;
-            const bool partial = there != (1u << R) - 1 || lo > 0 || hi < STEP;
+            const bool partial = there != (1u << NG) - 1 || lo > 0 || hi < STEP;
             mbar_wait_warp(empty + 8 * stage, phase ^ 1u, &abort_flag, a.status, a.timeout_ns);
             const uint32_t dst = ring + stage * 2 * S::SLOT + lane_at;
             if (lane == 0) {
@@ -608,23 +617,15 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     u = line.share * cta;
     int taken = 0;             // the share's steps before the segment
     int n_cuts = 0;
-    for (int turn = 0;; turn ^= 1) {
-        const Segment& cur = segs[turn];
-        left -= cur.step_end - cur.step;
-        if (left > 0 && tid == 0) segs[turn ^ 1] = after(cur, left);
-        const int kvh = cur.item / row_tiles, row0 = (cur.item - kvh * row_tiles) * ROWS;
+    // queries as B fragments: lane (g, i) has four values of row 8 nt + g per MMA step
+    uint32_t qf[NT][MS][2];
+    auto load_q = [&](const Segment& seg) {
+        const int kvh = seg.item / row_tiles, row0 = (seg.item - kvh * row_tiles) * ROWS;
         const int rows = min(ROWS, G - row0), head0 = kvh * G + row0;
-        const Span span = cur.span;
-
-        // queries as B fragments: lane (g, i) has four values of row 8 nt + g per MMA step.
-        // With an 8-bit cache the MMA is fp16: bf16 queries are scaled there by a power of
-        // two per row that brings the largest to 2^8..2^9, undone in the row's factor.
-        uint32_t qf[NT][MS][2];
-        float fct[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = 8 * nt + g;
-            const uint16_t* q = a.q + cur.b * a.ldq + static_cast<int64_t>(head0 + r) * a.head_dim;
+            const uint16_t* q = a.q + seg.b * a.ldq + static_cast<int64_t>(head0 + r) * a.head_dim;
 #pragma unroll
             for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
@@ -633,6 +634,21 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                     qf[nt][ms][h] = r < rows && col < a.head_dim ? *reinterpret_cast<const uint32_t*>(q + col) : 0;
                 }
         }
+    };
+    bool have_q = false;
+    for (int turn = 0;; turn ^= 1) {
+        const Segment& cur = segs[turn];
+        left -= cur.step_end - cur.step;
+        if (left > 0 && tid == 0) segs[turn ^ 1] = after(cur, left);
+        const int kvh = cur.item / row_tiles, row0 = (cur.item - kvh * row_tiles) * ROWS;
+        const int rows = min(ROWS, G - row0), head0 = kvh * G + row0;
+        const Span span = cur.span;
+
+        if (!have_q) load_q(cur);
+        have_q = false;
+        // With an 8-bit cache the MMA is fp16: bf16 queries are scaled there by a power of
+        // two per row that brings the largest to 2^8..2^9, undone in the row's factor.
+        float fct[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float f = a.scale * 1.4426950408889634f;
@@ -731,13 +747,13 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[r][nt][e] *= fct[nt][e & 1];
-            if (!S::P16 || there != (1u << R) - 1 || st * STEP < span.first || st * STEP + STEP > span.len) {
+            if (!S::GROUPS || there != (1u << S::NG) - 1 || st * STEP < span.first || st * STEP + STEP > span.len) {
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int t = 16 * r + g + 8 * h, tok = st * STEP + t;
-                        const bool ok = ((there >> (S::P16 ? r : t)) & 1u) && tok >= span.first && tok < span.len;
+                        const bool ok = ((there >> (S::GROUPS ? (16 * r + 8 * h) / S::PG : t)) & 1u) && tok >= span.first && tok < span.len;
                         if (!ok) {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) s[r][nt][2 * h] = s[r][nt][2 * h + 1] = -INFINITY;
@@ -864,6 +880,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                     }
             }
             consumers_sync<CT>();
+            if (w0 == 0 && left > 0) load_q(segs[turn ^ 1]), have_q = true;  // under way meanwhile
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
@@ -947,12 +964,15 @@ int launch_attn_shape(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stre
 
 template <int DT, bool E4M3, int DP>
 int launch_attn_dp(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stream) {
-    const bool p16 = a.page_size % 16 == 0;
-    if (a.q_heads / a.kv_heads <= 8)
-        return p16 ? launch_attn_shape<AttnShape<DT, E4M3, DP, 1, true>>(ctx, a, stream)
-                   : launch_attn_shape<AttnShape<DT, E4M3, DP, 1, false>>(ctx, a, stream);
-    return p16 ? launch_attn_shape<AttnShape<DT, E4M3, DP, 2, true>>(ctx, a, stream)
-               : launch_attn_shape<AttnShape<DT, E4M3, DP, 2, false>>(ctx, a, stream);
+    const bool narrow = a.q_heads / a.kv_heads <= 8;
+    if (a.page_size % 16 == 0)
+        return narrow ? launch_attn_shape<AttnShape<DT, E4M3, DP, 1, 16>>(ctx, a, stream)
+                      : launch_attn_shape<AttnShape<DT, E4M3, DP, 2, 16>>(ctx, a, stream);
+    if (a.page_size % 8 == 0)
+        return narrow ? launch_attn_shape<AttnShape<DT, E4M3, DP, 1, 8>>(ctx, a, stream)
+                      : launch_attn_shape<AttnShape<DT, E4M3, DP, 2, 8>>(ctx, a, stream);
+    return narrow ? launch_attn_shape<AttnShape<DT, E4M3, DP, 1, 1>>(ctx, a, stream)
+                  : launch_attn_shape<AttnShape<DT, E4M3, DP, 2, 1>>(ctx, a, stream);
 }
 
 }  // namespace
