@@ -36,13 +36,13 @@
 namespace w4g {
 
 constexpr float kLag = 8.0f;       // scores may pass the reference by 2^8
-// The workspace: a counter per CTA, then for each CTA two parts (its first item if that began in
+// The workspace: three counters per CTA, then for each CTA two parts (its first item if that began in
 // an earlier share, its last if that ends in a later one) of m[rows], l[rows], O[rows][dp].
 __host__ __device__ constexpr size_t attn_part_floats(int rows, int dp) {
     return static_cast<size_t>(rows) * (dp + 2);
 }
 __host__ __device__ constexpr size_t attn_counter_bytes(int ctas) {
-    return (static_cast<size_t>(ctas) * 4 + 127) / 128 * 128;
+    return (static_cast<size_t>(ctas) * 12 + 127) / 128 * 128;
 }
 
 namespace {
@@ -176,7 +176,7 @@ struct Segment {
 
 // A part of an item that several CTAs hold: the item's are those of CTAs c0 .. c0 + n - 1.
 struct Cut {
-    int c0, n, b, head0, rows, last;  // last: the part counted here completes the item
+    int c0, n, at, b, head0, rows, last;  // at: the part written here; last: it completes its run
     float vs;
 };
 
@@ -523,20 +523,20 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     constexpr int JV = DP > 128 ? DP / 128 : 1;      // 16-byte pieces of a row per lane
     constexpr int JS = DP < 128 ? 128 / DP : 1;      // parts that a warp reads side by side
     constexpr int kAtOnce = 16 / JV;
-    auto join_row = [&](const Cut& c, int row) {
+    auto join_row = [&](const Cut& c, int row, int k_first, int stride, int count, bool final) {
         const int sub = lane / (32 / JS), l4 = 4 * (lane % (32 / JS));
         float top = -INFINITY, sum = 0.0f;
         float4 acc[JV];
 #pragma unroll
         for (int v = 0; v < JV; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-        for (int k32 = 0; k32 < c.n; k32 += 32) {
+        for (int k32 = 0; k32 < count; k32 += 32) {
             const int mine = k32 + lane;
-            const float pm = mine < c.n ? __ldcg(part_of(c, mine) + row) : -INFINITY;
-            const float pl = mine < c.n ? __ldcg(part_of(c, mine) + ROWS + row) : 0.0f;
+            const float pm = mine < count ? __ldcg(part_of(c, k_first + mine * stride) + row) : -INFINITY;
+            const float pl = mine < count ? __ldcg(part_of(c, k_first + mine * stride) + ROWS + row) : 0.0f;
             float f = 0.0f;
 #pragma unroll 1
-            for (int k0 = 0; k0 < 32 && k32 + k0 < c.n; k0 += kAtOnce * JS) {
+            for (int k0 = 0; k0 < 32 && k32 + k0 < count; k0 += kAtOnce * JS) {
                 float4 x[kAtOnce][JV];
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j)
@@ -544,8 +544,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                     for (int v = 0; v < JV; ++v) {
                         const int k = k32 + k0 + j * JS + sub, d = l4 + 128 * v;
                         x[j][v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (k < c.n && d < a.head_dim)
-                            x[j][v] = __ldcg(reinterpret_cast<const float4*>(part_of(c, k) + 2 * ROWS + row * DP + d));
+                        if (k < count && d < a.head_dim)
+                            x[j][v] = __ldcg(reinterpret_cast<const float4*>(part_of(c, k_first + k * stride) + 2 * ROWS + row * DP + d));
                     }
                 if (k0 == 0) {  // the new maximum, and what it makes of the sums so far
                     const float now = fmaxf(top, warp_max(pm));
@@ -571,29 +571,64 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             acc[0].x += __shfl_xor_sync(0xFFFFFFFFu, acc[0].x, 16), acc[0].y += __shfl_xor_sync(0xFFFFFFFFu, acc[0].y, 16);
             acc[0].z += __shfl_xor_sync(0xFFFFFFFFu, acc[0].z, 16), acc[0].w += __shfl_xor_sync(0xFFFFFFFFu, acc[0].w, 16);
         }
+        if (!final) {  // a run's result stands where its first part did
+            float* to = part_of(c, k_first);
+#pragma unroll
+            for (int v = 0; v < JV; ++v)
+                if (sub == 0) *reinterpret_cast<float4*>(to + 2 * ROWS + row * DP + l4 + 128 * v) = acc[v];
+            if (lane == 0) to[row] = top, to[ROWS + row] = sum;
+            return;
+        }
         const float f = sum > 0.0f ? c.vs / sum : 0.0f;
 #pragma unroll
         for (int v = 0; v < JV; ++v)
             if (sub == 0 && l4 + 128 * v < a.head_dim) store_out<S::DT>(a, c.b, c.head0 + row, l4 + 128 * v, acc[v], f);
         if (lane == 0) store_lse(a, c.b, c.head0 + row, top, sum, kShift);
     };
-    // Counts the parts written, and joins the items that they complete, a row per warp.
+    // Counts the parts written, and joins what they complete, a row per warp.  Over 32 parts are
+    // joined in two rounds, runs of 16 first, so that several CTAs read them (one sequence of
+    // 131072 tokens with one head, 147 parts: @B@).
     auto settle = [&](int n_cuts) {
+        auto fan_of = [](const Cut& c) { return c.n <= 32 ? 32 : 16; };
         __threadfence();
         consumers_sync<CT>();
         if (tid < n_cuts) {
             Cut& c = cuts[tid];
-            c.last = atomicAdd(counters + c.c0, 1) == c.n - 1;
-            if (c.last) counters[c.c0] = 0;  // ready for the next call
+            // counters by the CTA of the run's first part.  That CTA may end one item and begin
+            // another, so first runs, later runs and second rounds count apart.
+            const int fan = fan_of(c), run = c.at / fan;
+            int* counter = counters + (run == 0 ? 0 : ctas) + c.c0 + run * fan;
+            c.last = atomicAdd(counter, 1) == min(fan, c.n - run * fan) - 1;
+            if (c.last) *counter = 0;  // ready for the next call
             __threadfence();
         }
         consumers_sync<CT>();
+        bool again = false;
         int nth = 0;
         for (int j = 0; j < n_cuts; ++j) {
             if (!cuts[j].last) continue;
             const Cut c = cuts[j];
+            const int fan = fan_of(c), run = c.at / fan;
+            again |= c.n > fan;
             for (int row = 0; row < c.rows; ++row)
-                if (nth++ % W == warp) join_row(c, row);
+                if (nth++ % W == warp) join_row(c, row, run * fan, 1, min(fan, c.n - run * fan), c.n <= fan);
+        }
+        if (!again) return;
+        __threadfence();
+        consumers_sync<CT>();
+        if (tid < n_cuts && cuts[tid].last) {
+            Cut& c = cuts[tid];
+            const int fan = fan_of(c), runs = (c.n + fan - 1) / fan;
+            int* counter = counters + 2 * ctas + c.c0;
+            c.last = runs > 1 && atomicAdd(counter, 1) == runs - 1;
+            if (c.last) *counter = 0;
+            __threadfence();
+        }
+        consumers_sync<CT>();
+        for (int j = 0; j < n_cuts; ++j) {
+            if (!cuts[j].last) continue;
+            const Cut c = cuts[j];
+            for (int row = warp; row < c.rows; row += W) join_row(c, row, 0, fan_of(c), (c.n + 15) / 16, true);
         }
     };
 
@@ -932,12 +967,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             else part[tid] = top, part[ROWS + tid] = sum;
         }
         if (!whole) {
-            Cut c{0, 0, cur.b, head0, rows, 0, vs};
+            Cut c{0, 0, 0, cur.b, head0, rows, 0, vs};
             if (line.apart) {
-                c.c0 = cta - static_cast<int>(quotient(cur.step, line.share));
+                c.at = static_cast<int>(quotient(cur.step, line.share));
+                c.c0 = cta - c.at;
                 c.n = parts_of(line, cur.n_steps);
             } else {
                 c.c0 = static_cast<int>(quotient(u - cur.step, line.share));
+                c.at = cta - c.c0;
                 c.n = static_cast<int>(quotient(u - cur.step + cur.n_steps - 1, line.share)) - c.c0 + 1;
             }
             if (tid == 0) cuts[n_cuts] = c;
