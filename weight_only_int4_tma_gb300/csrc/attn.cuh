@@ -21,20 +21,22 @@
 // when a score passes m by more than 2^8 the sums so far are scaled to the new reference
 // (a warp vote finds out; exact in the end, since numerator and denominator share it).
 //
-// Work split.  The steps of all (sequence, head, row tile) items stand in one line, which is cut
-// in equal shares, one per CTA, whatever the lengths; every CTA finds its own from the lengths
-// on the device.  The producers run on into the next item while the consumers finish one.  An
-// item inside one share is finished there; one that is cut leaves (m, l, O) of each part in
-// fp32 in the workspace, and the CTA that completes an item's count of parts joins them, in
-// their order.  (SMs do not get equal bandwidth, so shares of falling size claimed by whoever
-// is free end more evenly; but each more part costs more than that gives: 24 sequences of 8192
-// tokens, 4 heads of 128 with 16 rows: 77 us with equal shares, 87 to 92 with claimed ones; 64
-// sequences up to 16384 tokens: 355 and 349 us.)
+// Work split.  All (sequence, head, row tile) items stand in one line, each as long as its steps
+// and kItemCost more for what an item costs by itself.  The line is cut in equal shares, one per
+// CTA, whatever the lengths; every CTA finds its own from the lengths on the device.  The
+// producers run on into the next item while the consumers finish one.  An item whose steps lie
+// in one share is finished there; one that is cut leaves (m, l, O) of each part in fp32 in the
+// workspace, and the CTA that completes an item's count of parts joins them, in their order.
+// (SMs do not get equal bandwidth, so shares of falling size claimed by whoever is free end more
+// evenly; but each more part costs more than that gives: 24 sequences of 8192 tokens, 4 heads of
+// 128 with 16 rows: 77 us with equal shares, 87 to 92 with claimed ones; 64 sequences up to
+// 16384 tokens: 355 and 349 us.)
 #pragma once
 #include "decode.cuh"
 
 namespace w4g {
 
+constexpr int kItemCost = 8;       // of an item by itself, in steps: some 2 us
 constexpr float kLag = 8.0f;       // scores may pass the reference by 2^8
 // The workspace: three counters per CTA, then for each CTA two parts (its first item if that began in
 // an earlier share, its last if that ends in a later one) of m[rows], l[rows], O[rows][dp].
@@ -171,6 +173,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // One item's steps [step, step_end) of n_steps, as one CTA takes them.
 struct Segment {
     int b, item, step, step_end, n_steps;
+    int rest;   // what the CTA's share holds after this item; with more than kItemCost, more steps
     Span span;
 };
 
@@ -180,7 +183,7 @@ struct Cut {
     float vs;
 };
 
-// The line of steps and its shares, the same in every CTA.
+// The line and its shares, the same in every CTA.
 struct Line {
     long long end, share;
     bool apart;   // a share is a part of one item
@@ -190,7 +193,7 @@ __device__ __forceinline__ int parts_of(const Line& line, int n_steps) {
     return static_cast<int>(quotient(n_steps + line.share - 1, line.share));
 }
 
-// Fills `line` and prefix[thread], the steps before each thread's sequences (thread t has
+// Fills `line` and prefix[thread], what lies before each thread's sequences (thread t has
 // sequences t * per_thread ...); by all threads of a CTA, which then meet at a barrier.
 template <int STEP, int THREADS, int WARPS>
 __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, int ctas, bool report,
@@ -198,13 +201,13 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int per_thread = (a.B + THREADS - 1) / THREADS;
     const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
-    // steps in the low bits, sequences that have any above them
+    // their length in the line in the low bits, the number that have any steps above
     constexpr int kSeqBit = 40;
     constexpr long long kLow = (1ll << kSeqBit) - 1;
     long long mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const int n = span_steps<STEP>(visible(a, b, report));
-        mine += n + (n ? 1ll << kSeqBit : 0);
+        if (n) mine += n + kItemCost + (1ll << kSeqBit);
     }
     long long incl = mine;
 #pragma unroll
@@ -225,17 +228,15 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
         const long long items = (total >> kSeqBit) * items_per_seq;
         total = (total & kLow) * items_per_seq;
         line.end = total;
-        // Whole rounds of the warps: a share of fewer steps would take as long.
-        const int slots = ctas * WARPS;
-        const long long rounds = max(quotient(total + slots - 1, slots), 1ll);
-        line.share = rounds * WARPS;
-        // Few items: shares cut from one item each, so that no CTA has two partial items to write
-        // and join, if that takes at most one round more.
+        line.share = max(quotient(total + ctas - 1, ctas), 1ll);
+        // Few items: shares cut from one item each, in whole rounds of the warps, so that no CTA has
+        // two partial items to write and join, if that takes at most one round more.
         line.apart = false;
         if (2 * items <= ctas) {
-            const int left = static_cast<int>(ctas - items) * WARPS;
-            const long long r = max(quotient(total + left - 1, left), 1ll);
-            line.apart = r <= rounds + 1;
+            const long long steps = total - items * kItemCost;
+            const int slots = ctas * WARPS, left = static_cast<int>(ctas - items) * WARPS;
+            const long long r = max(quotient(steps + left - 1, left), 1ll);
+            line.apart = r <= max(quotient(steps + slots - 1, slots), 1ll) + 1;
             if (line.apart) line.share = r * WARPS;
         }
     }
@@ -309,8 +310,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     }
     __syncthreads();  // line, prefix, the barriers, and the zeroed ring
 
-    // the segment after `s`: the next item's first steps, at most `left`
-    auto after = [&](const Segment& s, int left) {
+    // the segment after `s`, where s.rest > kItemCost: the next item's first steps
+    auto after = [&](const Segment& s) {
         Segment n = s;
         if (++n.item == items_per_seq) {
             n.item = 0;
@@ -321,16 +322,18 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             } while (n.n_steps == 0 && n.b + 1 < a.B);
         }
         n.step = 0;
-        n.step_end = min(n.n_steps, left);
+        n.step_end = min(n.n_steps, s.rest - kItemCost);
+        n.rest = s.rest - kItemCost - n.n_steps;
         return n;
     };
 
-    // The CTA's share: its steps (0: none), and the first item's part of it.  By all lanes of a warp.
-    long long u = 0;   // its first step in the line (not `apart`)
+    // The first segment of the CTA's share; false: there is none.  By all lanes of a warp.
+    const long long share_end = min(line.end, line.share * (cta + 1));   // in the line (not `apart`)
     auto locate = [&](Segment& first) {
         if (line.apart) {  // the cta-th part of all items
-            int done = 0, n = 0;
-            for (int b0 = 0; b0 < a.B && n == 0; b0 += 32) {
+            int done = 0;
+            bool found = false;
+            for (int b0 = 0; b0 < a.B && !found; b0 += 32) {
                 const int b = b0 + lane, share = static_cast<int>(line.share);
                 const Span span = b < a.B ? visible(a, b, false) : Span{0, 0};
                 const int n_steps = span_steps<STEP>(span), per = parts_of(line, n_steps);
@@ -348,17 +351,16 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                     const int from = __ffs(who) - 1;
                     auto get = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
                     first = Segment{get(b), get(here ? at / per : 0), get(step), get(min(n_steps, step + share)),
-                                    get(n_steps), Span{get(span.first), get(span.len)}};
-                    n = first.step_end - first.step;
+                                    get(n_steps), 0, Span{get(span.first), get(span.len)}};
+                    found = true;
                 }
                 done += __shfl_sync(0xFFFFFFFFu, incl, 31);
             }
-            return n;
+            return found;
         }
-        u = line.share * cta;
-        if (u >= line.end) return 0;
-        const int n = static_cast<int>(min(line.end - u, line.share));
-        // the thread whose sequences hold step u, then the sequence
+        const long long u = line.share * cta;
+        if (u >= line.end) return false;
+        // the thread whose sequences hold place u, then the sequence
         int t = 0;
         for (int t0 = 0; t0 < S::THREADS && t0 * per_thread < a.B; t0 += 32)
             t += __popc(__ballot_sync(0xFFFFFFFFu, prefix[t0 + lane] <= u));
@@ -367,15 +369,21 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         int b = t * per_thread;
         Span span = visible(a, b, false);
         int n_steps = span_steps<STEP>(span);
-        while (at + static_cast<long long>(n_steps) * items_per_seq <= u && b + 1 < a.B) {
-            at += static_cast<long long>(n_steps) * items_per_seq;
+        auto length = [&]() { return n_steps ? static_cast<long long>(n_steps + kItemCost) * items_per_seq : 0ll; };
+        while (at + length() <= u && b + 1 < a.B) {
+            at += length();
             span = visible(a, ++b, false);
             n_steps = span_steps<STEP>(span);
         }
-        const int item = static_cast<int>(quotient(u - at, n_steps));
-        const int step = static_cast<int>(u - at - static_cast<long long>(item) * n_steps);
-        first = Segment{b, item, step, min(n_steps, step + n), n_steps, span};
-        return n;
+        const int item = static_cast<int>(quotient(u - at, n_steps + kItemCost));
+        const long long begin = at + static_cast<long long>(item) * (n_steps + kItemCost);
+        const int step = max(static_cast<int>(u - begin) - kItemCost, 0);
+        const int rest = static_cast<int>(share_end - begin) - kItemCost - n_steps;
+        first = Segment{b, item, step, min(n_steps, n_steps + rest), n_steps, rest, span};
+        if (first.step < first.step_end) return true;
+        if (rest <= kItemCost) return false;   // the share ends before any step
+        first = after(first);
+        return true;
     };
 
     const uint32_t ring = smem_addr(smem);
@@ -420,57 +428,46 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             in_batch = 0;
         };
         // one side's copies of a step: rows of `at` (bytes from base: of each group's first row,
-        // or of the lane's token), `lo` <= token < `hi`
+        // or of the lane's token); of a partial step those with `lo` <= token < `hi` and a page,
+        // zeros for the others
         auto copy = [&](uint32_t dst, const char* base, const int64_t (&at)[NG], int64_t stride,
                         uint32_t there, int lo, int hi, bool partial) {
-            if (S::GROUPS && !partial) {
+            if constexpr (S::GROUPS) {
+                auto all = [&](auto ok_of) {
 #pragma unroll
-                for (int r = 0; r < NG; ++r) {
-                    const char* p = base + at[r];
+                    for (int r = 0; r < NG; ++r) {
+                        const char* p = base + at[r];
 #pragma unroll
-                    for (int j = 0; j < S::PG / RPI; ++j) {
-                        const uint32_t to = (dst ^ (CH >= 8 ? ((RPI * j) & 7) << 4 : 0)) + (S::PG * r + RPI * j) * S::PITCH;
-                        if (column) copy16(to, p, 16);
-                        p += RPI * stride;
+                        for (int j = 0; j < S::PG / RPI; ++j) {
+                            const uint32_t to = (dst ^ (CH >= 8 ? ((RPI * j) & 7) << 4 : 0)) + (S::PG * r + RPI * j) * S::PITCH;
+                            const bool ok = ok_of(r, S::PG * r + RPI * j + lrow);
+                            if (column) copy16(to, ok ? p : base, ok ? 16 : 0);
+                            p += RPI * stride;
+                        }
                     }
-                }
-                return;
-            }
-#pragma unroll 1
-            for (int t0 = 0; t0 < STEP; t0 += RPI) {
-                const int t = t0 + lrow;
-                const char* p;
-                bool ok;
-                if constexpr (S::GROUPS) {
-                    int64_t from = at[0];
+                };
+                if (!partial) all([](int, int) { return true; });
+                else all([&](int r, int t) { return ((there >> r) & 1u) && t >= lo && t < hi; });
+            } else {
 #pragma unroll
-                    for (int r = 1; r < NG; ++r) from = t0 / S::PG == r ? at[r] : from;
-                    p = base + from + (t0 % S::PG) * stride;
-                    ok = (there >> (t0 / S::PG)) & 1u;
-                } else {
-                    p = base - lrow * stride + __shfl_sync(0xFFFFFFFFu, at[0], t);
-                    ok = (there >> t) & 1u;
+                for (int t0 = 0; t0 < STEP; t0 += RPI) {
+                    const int t = t0 + lrow;
+                    const char* p = base - lrow * stride + __shfl_sync(0xFFFFFFFFu, at[0], t);
+                    const bool ok = ((there >> t) & 1u) && t >= lo && t < hi;
+                    const uint32_t to = (dst ^ (CH >= 8 ? (t0 & 7) << 4 : 0)) + t0 * S::PITCH;
+                    if (column) copy16(to, ok ? p : base, ok ? 16 : 0);
                 }
-                ok = ok && t >= lo && t < hi;
-                const uint32_t to = (dst ^ (CH >= 8 ? (t0 & 7) << 4 : 0)) + t0 * S::PITCH;
-                if (column) copy16(to, ok ? p : base, ok ? 16 : 0);
             }
         };
-        const int n_all = locate(ld);
-        int seg0 = 0, seg_n = ld.step_end - ld.step;   // the share's steps before segment ld, and its own
-        int stage = pw;
+        int seg0 = 0;            // the share's steps before segment ld
+        int stage = pw, x = pw;  // of this warp's next step
         uint32_t phase = 0;
-        bool opened = false;
 #pragma unroll 1
-        for (int x = pw; x < n_all; x += S::PW) {
-            while (x >= seg0 + seg_n) {
-                seg0 += seg_n;
-                ld = after(ld, n_all - seg0);
-                seg_n = ld.step_end - ld.step;
-                opened = false;
-            }
-            if (!opened) open(ld.step + x - seg0);
-            opened = true;
+        for (bool more = locate(ld); more;) {
+        const int seg_end = seg0 + ld.step_end - ld.step;
+        if (x < seg_end) open(ld.step + x - seg0);
+#pragma unroll 1
+        for (; x < seg_end; x += S::PW) {
             const int st = first_st + ld.step + x - seg0;
             int64_t kat[NG], vat[NG];
             uint32_t there = 0;  // groups, or tokens, whose page is there
@@ -506,6 +503,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             }
             stage += S::PW;
             if (stage >= NST) stage -= NST, phase ^= 1u;
+        }
+        seg0 = seg_end;
+        more = ld.rest > kItemCost;
+        if (more) ld = after(ld);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
@@ -643,13 +644,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
 
     if (warp == 0) {
         Segment first{};
-        const int n = locate(first);
-        if (lane == 0) segs[0] = first, share_n = n;
+        const bool any = locate(first);
+        if (lane == 0) segs[0] = first, share_n = any;
     }
     consumers_sync<CT>();
-    int left = share_n;        // steps of the share not yet begun
-    if (left == 0) return;
-    u = line.share * cta;
+    if (!share_n) return;
+    long long begin = share_end - segs[0].rest - kItemCost - segs[0].n_steps;  // of the item in the line
     int taken = 0;             // the share's steps before the segment
     int n_cuts = 0;
     // queries as B fragments: lane (g, i) has four values of row 8 nt + g per MMA step
@@ -673,8 +673,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     bool have_q = false;
     for (int turn = 0;; turn ^= 1) {
         const Segment& cur = segs[turn];
-        left -= cur.step_end - cur.step;
-        if (left > 0 && tid == 0) segs[turn ^ 1] = after(cur, left);
+        const bool more = cur.rest > kItemCost;
+        if (more && tid == 0) segs[turn ^ 1] = after(cur);
         const int kvh = cur.item / row_tiles, row0 = (cur.item - kvh * row_tiles) * ROWS;
         const int rows = min(ROWS, G - row0), head0 = kvh * G + row0;
         const Span span = cur.span;
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                     }
             }
             consumers_sync<CT>();
-            if (w0 == 0 && left > 0) load_q(segs[turn ^ 1]), have_q = true;  // under way meanwhile
+            if (w0 == 0 && more) load_q(segs[turn ^ 1]), have_q = true;  // under way meanwhile
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
@@ -973,15 +973,15 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                 c.c0 = cta - c.at;
                 c.n = parts_of(line, cur.n_steps);
             } else {
-                c.c0 = static_cast<int>(quotient(u - cur.step, line.share));
+                c.c0 = static_cast<int>(quotient(begin + kItemCost, line.share));
                 c.at = cta - c.c0;
-                c.n = static_cast<int>(quotient(u - cur.step + cur.n_steps - 1, line.share)) - c.c0 + 1;
+                c.n = static_cast<int>(quotient(begin + kItemCost + cur.n_steps - 1, line.share)) - c.c0 + 1;
             }
             if (tid == 0) cuts[n_cuts] = c;
             ++n_cuts;
         }
-        if (left <= 0) break;
-        u += cur.step_end - cur.step;
+        if (!more) break;
+        begin += kItemCost + cur.n_steps;
         consumers_sync<CT>();
     }
     if (n_cuts) settle(n_cuts);
