@@ -39,24 +39,28 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       dec_pack2<DT>(f[4], f[5]), dec_pack2<DT>(f[6], f[7]));
 }
 
-// Reduction over the warps of one row (warps row_warp0 .. + row_warps - 1 of the CTA); every
-// thread of the CTA takes part, `red` holds one value per warp.
-template <bool kMax>
-__device__ __forceinline__ float row_reduce(float v, float* red, int row_warp0, int row_warps) {
-    v = kMax ? warp_max(v) : warp_sum(v);
-    if (row_warps == 1) return v;
+// The sum of `sum` and, with MAX, the largest `most` (magnitudes) over the warps of one row (warps
+// row_warp0 .. + row_warps - 1 of the CTA); every thread of the CTA takes part, `red` holds a
+// pair per warp.
+template <bool MAX>
+__device__ __forceinline__ void row_reduce(float& sum, float& most, float2* red, int row_warp0,
+                                           int row_warps) {
+    sum = warp_sum(sum);
+    if (MAX) most = warp_max(most);
+    if (row_warps == 1) return;
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    if (lane == 0) red[threadIdx.x >> 5] = v;
+    if (lane == 0) red[threadIdx.x >> 5] = make_float2(sum, most);
     __syncthreads();
-    v = lane < row_warps ? red[row_warp0 + lane] : 0.0f;  // sums and magnitudes: 0 is neutral
-    return kMax ? warp_max(v) : warp_sum(v);
+    const float2 v = lane < row_warps ? red[row_warp0 + lane] : make_float2(0.0f, 0.0f);
+    sum = warp_sum(v.x);
+    if (MAX) most = warp_max(v.y);
 }
 
 // `row_threads` (a multiple of 32) threads per row, rows_per_cta rows per CTA, V pieces per
 // thread: piece p of a row is held by thread p % row_threads.
 template <int DT, int OUT, int V>
 __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int M, int row_threads) {
-    __shared__ float red[2][32];
+    __shared__ float2 red[32];
     const int in_cta = static_cast<int>(threadIdx.x) / row_threads;
     const int t = static_cast<int>(threadIdx.x) - in_cta * row_threads;
     const int rows_per_cta = static_cast<int>(blockDim.x) / row_threads;
@@ -85,35 +89,36 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int M, int row_t
         }
     }
     grid_dep_launch();
-    float ss = 0.0f;
+    // h, and in its place h * weight once the sum has it: y = (h * weight) * r.  Rounding is
+    // monotone, so the row's largest |y| is (the largest |h * weight|) * r to the bit, and one
+    // reduction gives both the sum and what an int8 row's scale needs.
+    float ss = 0.0f, most = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        float r8[8];
+        float r8[8], w8[8];
+        const int p = t + j * row_threads;
         unpack8<DT>(xv[j], h[j]);
         unpack8<DT>(rv[j], r8);
+        unpack8<DT>(wv[j], w8);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             h[j][e] += r8[e];
             ss = fmaf(h[j][e], h[j][e], ss);
         }
-    }
-    ss = row_reduce<false>(ss, red[0], row_warp0, row_warps);
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
-    if (a.residual_out) {
+        if (a.residual_out && live && p < pieces)
+            reinterpret_cast<uint4*>(a.residual_out + m * a.ldr)[p] = pack8<DT>(h[j]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int p = t + j * row_threads;
-            if (live && p < pieces)
-                reinterpret_cast<uint4*>(a.residual_out + m * a.ldr)[p] = pack8<DT>(h[j]);
+        for (int e = 0; e < 8; ++e) {
+            if (a.weight) h[j][e] *= w8[e];
+            if (OUT == kNormI8) most = fmaxf(most, fabsf(h[j][e]));
         }
     }
+    row_reduce<OUT == kNormI8>(ss, most, red, row_warp0, row_warps);
+    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float w8[8];
-        unpack8<DT>(wv[j], w8);
+    for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[j][e] = a.weight ? h[j][e] * r * w8[e] : h[j][e] * r;
-    }
+        for (int e = 0; e < 8; ++e) h[j][e] *= r;
     if constexpr (OUT == kNormSame) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -123,25 +128,23 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int M, int row_t
                     pack8<DT>(h[j]);
         }
     } else if constexpr (OUT == kNormI8) {
-        float most = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(h[j][e]));
-        most = row_reduce<true>(most, red[1], row_warp0, row_warps);
+        most *= r;
         const float s = most > 0.0f ? __fdiv_rn(most, 127.0f) : 1.0f;
+        // y / s as y * (127 / most): 2^-23 off, like y itself; the division for each value took
+        // half of the kernel's time.  The sum with 1.5 * 2^23 rounds to the nearest integer
+        // (ties to even) and leaves it in the low byte.
+        const float up = most < 1e-30f ? 0x1p64f : 1.0f;  // keeps the factor finite
+        const float inv = most > 0.0f ? __fdiv_rn(127.0f, most * up) : 0.0f;
         uint2* y = reinterpret_cast<uint2*>(static_cast<int8_t*>(a.y) + m * a.H);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int p = t + j * row_threads;
-            uint32_t o[2] = {0, 0};
+            uint32_t q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                int q = __float2int_rn(__fdiv_rn(h[j][e], s));
-                q = max(-127, min(127, q));
-                o[e >> 2] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (e & 3));
-            }
-            if (live && p < pieces) y[p] = make_uint2(o[0], o[1]);
+            for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(fmaf(h[j][e] * up, inv, 12582912.0f));
+            const uint32_t lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+            const uint32_t hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+            if (live && p < pieces) y[p] = make_uint2(lo, hi);
         }
         if (live && t == 0) static_cast<float*>(a.scales)[m] = s;
     } else {
@@ -150,13 +153,13 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int M, int row_t
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int p = t + j * row_threads;
-            float most = 0.0f;
+            float top = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(h[j][e]));
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(h[j][e]));
             // a block of 32 is the pieces of four neighbouring lanes
-            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-            const int e2 = norm_mx_exponent(most);
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const int e2 = norm_mx_exponent(top);
             const float f = norm_pow2(-e2);
             uint32_t o[4];
 #pragma unroll
@@ -176,7 +179,7 @@ constexpr int kNormThreads = 256;
 // from L1 or L2).
 template <int DT>
 __global__ void __launch_bounds__(kNormThreads) norm_any_kernel(NormArgs a) {
-    __shared__ float red[kNormThreads / 32];
+    __shared__ float2 red[kNormThreads / 32];
     grid_dep_wait();
     const int64_t m = blockIdx.x;
     const uint16_t* x = a.x + m * a.ldx;
@@ -193,13 +196,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_any_kernel(NormArgs a) {
         const float h = value(i);
         ss += h * h;
     }
-    ss = row_reduce<false>(ss, red, 0, kNormThreads / 32);
+    float none = 0.0f;
+    row_reduce<false>(ss, none, red, 0, kNormThreads / 32);
     const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
     for (int i = threadIdx.x; i < a.H; i += kNormThreads) {
         const float h = value(i);
         const float w = a.weight ? dec_to_f32<DT>(a.weight[i]) : 1.0f;
         if (res_out) res_out[i] = dec_from_f32<DT>(h);
-        y[i] = dec_from_f32<DT>(h * r * w);
+        y[i] = dec_from_f32<DT>(h * w * r);
     }
 }
 
@@ -214,10 +218,12 @@ int launch_norm_v(const NormArgs& a, int M, int row_threads, cudaStream_t stream
 template <int DT, int OUT>
 int launch_norm_out(const DeviceCtx& ctx, const NormArgs& a, int M, cudaStream_t stream) {
     const int pieces = a.H / 8;
-    // Few rows: one piece per thread where 1024 threads suffice (latency).  Rows for every
-    // SM: four pieces per thread, so that several CTAs of independent loads share an SM.
-    int V = M <= ctx.num_sms ? (pieces + 1023) / 1024 : (pieces >= 128 ? 4 : 1);
-    V = V <= 1 ? 1 : V <= 2 ? 2 : 4;
+    // Few rows: one piece per thread where 1024 threads suffice (latency).  Rows for every SM: two
+    // (bf16 with residual, 800 x 4096: 4.6 us against 5.2 with one and 5.7 with four).  Long
+    // rows, many of them: four, the most loads under way (4096 x 8192: 41.3 us against 47.5 and
+    // 43.5; at 400 x 8192 5.7 against 5.8 and 4.9).
+    int V = M <= ctx.num_sms || pieces < 64 ? 1 : pieces > 512 && M > 8 * ctx.num_sms ? 4 : 2;
+    if (V * 1024 < pieces) V = pieces <= 2048 ? 2 : 4;
     const int row_threads = ((pieces + V - 1) / V + 31) / 32 * 32;
     if (V == 1) return launch_norm_v<DT, OUT, 1>(a, M, row_threads, stream);
     if (V == 2) return launch_norm_v<DT, OUT, 2>(a, M, row_threads, stream);
