@@ -36,10 +36,11 @@ extern "C" {
  *
  *   h[m, i] = x[m, i] + residual[m, i]                       (fp32; x alone without one)
  *   r[m]    = 1 / sqrt( sum_i h[m, i]^2 / H + eps )          (fp32)
- *   y[m, i] = h[m, i] * r[m] * weight[i]                     (fp32)
+ *   y[m, i] = (h[m, i] * weight[i]) * r[m]                   (fp32)
  *   residual_out[m, i] = RNE_dtype( h[m, i] )
  *
- * The sums take h before it is rounded: y does not depend on residual_out's rounding.
+ * The sums take h before it is rounded: y does not depend on residual_out's rounding.  The
+ * products are taken in that order, so h^2 and h weight have to stay within fp32's range.
  *   x         device, dtype [M] rows of H, ldx elements apart.
  *   residual  device, dtype [M] rows, ldr apart, or NULL.
  *   weight    device, dtype [H], or NULL (all ones).
@@ -64,7 +65,9 @@ int dec_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
  * y as int8 rows, the activations that w4a8_gemm takes, from the fp32 values (they are not
  * rounded to dtype in between, unlike dec_rms_norm followed by w4a8_quantize_act):
  *     s_y[m] = max_i |y[m, i]| / 127   (fp32; 1 for a zero row)
- *     y_i8[m, i] = clamp(rint(y[m, i] / s_y[m]), -127, 127)
+ *     y_i8[m, i] = rint(y[m, i] * (127 / max))
+ * (the fp32 product with a rounded factor: within 2^-22 of the quotient y / s_y, relative, so that
+ * a code differs from the quotient's only where that is as near to a half).
  *   y_i8  device output, int8 [M][H] packed, 8-byte aligned; H a multiple of 8, at most
  *         32768 (w4a8_gemm itself wants a multiple of 128).
  *   s_y   device output, float [M].
@@ -243,7 +246,9 @@ size_t dec_attn_workspace_bytes(const dec_attn_config* cfg, const dec_kv_cache* 
  * Results do not depend on how the work is split in time: the partial results are joined in
  * a fixed order, and equal inputs give equal bits.  A length outside its range is cut to it,
  * and a page index outside the cache leaves its tokens out; both record
- * W4A16_ERR_INVALID_ARG in the status word.
+ * W4A16_ERR_INVALID_ARG in the status word.  A wait inside the kernel that runs out
+ * records W4A16_ERR_DEVICE_TIMEOUT; the results are then undefined and the workspace has to be
+ * filled with zeros again.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const void* q,

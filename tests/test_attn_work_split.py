@@ -8,19 +8,22 @@ import pytest
 COST, WARPS = 8, 8
 
 
-def lay(n_steps, items, ctas):
+def lay(n_steps, items, ctas, join=4):
     """(end, share, apart): n_steps of each sequence, items per sequence."""
     seqs = [n for n in n_steps if n]
     total = sum(n + COST for n in seqs) * items
     share, apart = max(-(-total // ctas), 1), False
-    count = len(seqs) * items
+    count, rounds = len(seqs) * items, -(-share // WARPS)
     if 2 * count <= ctas:
         steps = total - count * COST
         left = (ctas - count) * WARPS
         r = max(-(-steps // left), 1)
         apart = r <= max(-(-steps // (ctas * WARPS)), 1) + 1
         if apart:
-            share = r * WARPS
+            rounds, share = r, r * WARPS
+    whole = -(-max(seqs, default=0) // WARPS)
+    if count <= ctas and whole < rounds + join + (not apart):
+        apart, share = True, max(whole * WARPS, 1)
     return total, share, apart
 
 
@@ -83,13 +86,14 @@ def segments(cta, n_steps, items, line):
         seg = after(seg, n_steps, items)
 
 
-@pytest.mark.parametrize("seed", range(120))
+@pytest.mark.parametrize("seed", range(400))
 def test_every_step_belongs_to_one_cta(seed):
     rng = random.Random(seed)
     ctas = rng.choice([1, 2, 7, 152])
-    n_steps = [rng.choice([0, 1, 2, 5, 40, rng.randrange(1, 3000)]) for _ in range(rng.randrange(1, 60))]
+    longest = rng.choice([1, 8, 30, 64, 3000])
+    n_steps = [min(longest, rng.choice([0, 1, 2, 5, 40, rng.randrange(1, 3000)])) for _ in range(rng.randrange(1, 60))]
     items = rng.choice([1, 2, 8, 32])
-    line = lay(n_steps, items, ctas)
+    line = lay(n_steps, items, ctas, rng.choice([0, 3, 4]))
     parts = {}
     for cta in range(ctas):
         segs = segments(cta, n_steps, items, line)

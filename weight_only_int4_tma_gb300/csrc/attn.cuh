@@ -4,10 +4,20 @@
 // The keys and values are read once and nothing else of size is: with G query heads per
 // key-value head the work is 2 G operations per cached 16-bit value, far below what the
 // tensor cores do in the time of the read, so the kernel is built to keep loads in flight.
+// Measured on the device (a copy reaches 6.78 TB/s there):
+//   64 sequences of up to 16384 tokens, 8 heads of 128, bf16: 2.37 GB in 365 us, 6.5 TB/s;
+//   16 sequences of up to 4096 tokens, 32 heads of 128, fp16: 0.54 GB in 90 us, 6.0 TB/s;
+//   one sequence of 131072 tokens, 8 heads of 128, bf16: 0.54 GB in 90 us, 6.0 TB/s;
+//   33 windows of up to 4096 tokens, 4 heads of 64, 8-bit: 0.049 GB in 22.5 us, 2.2 TB/s.  (Rows of
+//   64 bytes that stand 256 apart are fetched at 1.58 times their bytes);
+//   one sequence of 777 tokens: 8.2 us, which is lengths, page table, keys and the join, one
+//   after another.
 //
-// Data path.  Steps of 16 R tokens go through a ring in shared memory of about 190 KB (one CTA
-// per SM): four producer warps fill it with asynchronous copies, eight consumer warps take its
-// steps in turn, each working alone.  ldmatrix turns a step into mma.sync operands:
+// Data path.  Steps of 16 R tokens go through a ring in shared memory of 192 KB (one CTA per
+// SM): four producer warps fill it with asynchronous copies, eight consumer warps take its
+// steps in turn, each working alone.  mma.sync suffices: the tcgen05 form would need the
+// 128-row tiles that one token's few query heads do not fill.  ldmatrix turns a step into its
+// operands:
 //   S^T = K Q^T   tokens are the MMA's 16 rows, query heads its 8 columns (with 8 heads or
 //                 fewer per key-value head half of a 16-row query tile would be padding);
 //   O^T = V^T P^T head dimensions are the rows; ldmatrix's transposed form reads V^T.
@@ -36,7 +46,9 @@
 
 namespace w4g {
 
-constexpr int kItemCost = 8;       // of an item by itself, in steps: some 2 us
+// Of an item by itself, in steps: some 2 us.  (52 ragged sequences of 32 heads, 8-bit, pages of 8:
+// 42 us; 91 with shares of steps alone.)
+constexpr int kItemCost = 8;
 constexpr float kLag = 8.0f;       // scores may pass the reference by 2^8
 // The workspace: three counters per CTA, then for each CTA two parts (its first item if that began in
 // an earlier share, its last if that ends in a later one) of m[rows], l[rows], O[rows][dp].
@@ -131,6 +143,9 @@ struct AttnShape {
     // within an item: nobody waits for a stage two rounds ahead of it, which the barriers' one
     // bit of phase could not tell from the round at hand.
     static constexpr int NST = 2 * SLOT == 16384 ? 8 : 24;
+    // Joining an item's parts, in the warps' rounds.  By row one round of the steps is 2.0 us (64 bytes;
+    // 1 leaves 33 windows of up to 4096 tokens whole: 23.2 us against 22.5), 1.3, 1.05, 1.0.
+    static constexpr int WHOLE = PITCH == 64 ? 0 : PITCH == 256 ? 4 : 3;
     static constexpr int THREADS = 32 * (W + PW);
     static constexpr int RING = NST * 2 * SLOT;
     static constexpr int SMEM = RING + SO_BYTES + NST * (4 + 3 * 8);
@@ -195,9 +210,9 @@ __device__ __forceinline__ int parts_of(const Line& line, int n_steps) {
 
 // Fills `line` and prefix[thread], what lies before each thread's sequences (thread t has
 // sequences t * per_thread ...); by all threads of a CTA, which then meet at a barrier.
-template <int STEP, int THREADS, int WARPS>
+template <int STEP, int THREADS, int WARPS, int WHOLE>
 __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, int ctas, bool report,
-                                         Line& line, long long* prefix, long long* scan) {
+                                         Line& line, long long* prefix, long long* scan, int* tops) {
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int per_thread = (a.B + THREADS - 1) / THREADS;
     const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
@@ -205,23 +220,27 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
     constexpr int kSeqBit = 40;
     constexpr long long kLow = (1ll << kSeqBit) - 1;
     long long mine = 0;
+    int top = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const int n = span_steps<STEP>(visible(a, b, report));
         if (n) mine += n + kItemCost + (1ll << kSeqBit);
+        top = max(top, n);
     }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
         if (lane >= d) incl += o;
     }
-    if (lane == 31) scan[warp] = incl;
+    if (lane == 31) scan[warp] = incl, tops[warp] = top;
     __syncthreads();
     long long total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) incl += scan[w];
         total += scan[w];
+        top = max(top, tops[w]);
     }
     prefix[tid] = ((incl - mine) & kLow) * items_per_seq;
     if (tid == 0) {
@@ -232,12 +251,21 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
         // Few items: shares cut from one item each, in whole rounds of the warps, so that no CTA has
         // two partial items to write and join, if that takes at most one round more.
         line.apart = false;
+        long long rounds = (line.share + WARPS - 1) / WARPS;
         if (2 * items <= ctas) {
             const long long steps = total - items * kItemCost;
             const int slots = ctas * WARPS, left = static_cast<int>(ctas - items) * WARPS;
             const long long r = max(quotient(steps + left - 1, left), 1ll);
             line.apart = r <= max(quotient(steps + slots - 1, slots), 1ll) + 1;
-            if (line.apart) line.share = r * WARPS;
+            if (line.apart) rounds = r, line.share = r * WARPS;
+        }
+        // No item is cut where the longest takes not many rounds more than a share: joining takes some
+        // WHOLE of them, with items cut anywhere one more.  (8 heads of 128, one sequence of 400
+        // tokens, four rounds: 8.7 us whole, 9.5 in parts; of 600, five: 10.3 and 9.7; 16 sequences
+        // of 300 tokens: 8.0 and 14.4 us, of 500 9.6 and 15.4.)
+        if (items <= ctas && (top + WARPS - 1) / WARPS < rounds + WHOLE + (line.apart ? 0 : 1)) {
+            line.apart = true;
+            line.share = max((top + WARPS - 1) / WARPS * WARPS, 1);
         }
     }
 }
@@ -270,6 +298,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     __shared__ float sm_m[W][ROWS], sm_l[W][ROWS];
     __shared__ Line line;
     __shared__ long long scan[W + S::PW];
+    __shared__ int tops[W + S::PW];
     __shared__ long long prefix[S::THREADS];
     __shared__ Segment segs[2];                // the current one and the one after it, in turn
     __shared__ int share_n;
@@ -297,7 +326,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     }
     if (tid == 0) abort_flag = 0;
     grid_dep_wait();
-    lay_line<STEP, S::THREADS, W>(a, items_per_seq, ctas, cta == 0, line, prefix, scan);
+    lay_line<STEP, S::THREADS, W, S::WHOLE>(a, items_per_seq, ctas, cta == 0, line, prefix, scan, tops);
     const int per_thread = (a.B + S::THREADS - 1) / S::THREADS;
     // rows with nothing to attend to
     for (int b = cta; b < a.B; b += ctas) {
@@ -588,7 +617,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     };
     // Counts the parts written, and joins what they complete, a row per warp.  Over 32 parts are
     // joined in two rounds, runs of 16 first, so that several CTAs read them (one sequence of
-    // 131072 tokens with one head, 147 parts: @B@).
+    // 131072 tokens with one key-value head, 147 parts: 39.7 us in one round, 25.8 in two).
     auto settle = [&](int n_cuts) {
         auto fan_of = [](const Cut& c) { return c.n <= 32 ? 32 : 16; };
         __threadfence();

@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
             const KvView& c = is_v ? a.vc : a.kc;
             const int64_t off = page * c.page_stride + in_page * c.slot_stride + h * c.head_stride;
             if constexpr (E4M3) {
-                const float s = c.scale ? __frcp_rn(c.scale[h]) : 1.0f;
-                const uint32_t p = dec_e4m3x2(x0 * s, x1 * s);
+                const float s = c.scale ? c.scale[h] : 1.0f;
+                const uint32_t p = dec_e4m3x2(__fdiv_rn(x0, s), __fdiv_rn(x1, s));
                 static_cast<uint8_t*>(c.p)[off + i0] = static_cast<uint8_t>(p);
                 static_cast<uint8_t*>(c.p)[off + i1] = static_cast<uint8_t>(p >> 8);
             } else {
@@ -95,6 +95,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
             }
         }
     }
+}
+
+// x / s, rounded to nearest, given inv = 1 / s rounded to nearest: the product with inv, corrected by
+// its remainder (Markstein: exact rounding for normal results).  x * inv alone moves one code in a
+// million to the neighbour; a division instead takes 1003 tokens of 96 heads from 9.3 to 11.1
+// us.  Past E4M3's range nothing is corrected: an infinity would become a NaN.
+__device__ __forceinline__ float rope_quotient(float x, float s, float inv) {
+    const float q = x * inv;
+    return fabsf(q) < 1024.0f ? fmaf(fmaf(-q, s, x), inv, q) : q;
 }
 
 // Eight neighbouring values of a head, read once (evicted first: 1003 tokens of 96 heads 9.3
@@ -199,12 +208,11 @@ __global__ void __launch_bounds__(128) rope_units_kernel(RopeArgs a, RopeUnits n
     const int64_t page = n.page_shift >= 0 ? slot >> n.page_shift : slot / a.page_size;
     const int64_t off = page * kv.page_stride + (slot - page * a.page_size) * kv.slot_stride + h * kv.head_stride;
     if constexpr (E4M3) {
-        // times the rounded reciprocal: 2^-23 off the quotient, where E4M3's step is 2^-3
-        const float s = kv.scale ? __frcp_rn(kv.scale[h]) : 1.0f;
+        const float s = kv.scale ? kv.scale[h] : 1.0f, inv = __frcp_rn(s);
         auto pack = [&](const float (&x)[8]) {
             uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = dec_e4m3x2(x[2 * e] * s, x[2 * e + 1] * s);
+            for (int e = 0; e < 4; ++e) w[e] = dec_e4m3x2(rope_quotient(x[2 * e], s, inv), rope_quotient(x[2 * e + 1], s, inv));
             return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
         };
         uint8_t* dst = static_cast<uint8_t*>(kv.p) + off;
