@@ -9,7 +9,7 @@ COST, WARPS = 8, 8
 
 
 def lay(n_steps, items, ctas, join=4):
-    """(end, share, apart): n_steps of each sequence, items per sequence."""
+    """(end, share, apart, whole items): n_steps of each sequence, items per sequence."""
     seqs = [n for n in n_steps if n]
     total = sum(n + COST for n in seqs) * items
     share, apart = max(-(-total // ctas), 1), False
@@ -24,20 +24,22 @@ def lay(n_steps, items, ctas, join=4):
     whole = -(-max(seqs, default=0) // WARPS)
     if count <= ctas and whole < rounds + join + (not apart):
         apart, share = True, max(whole * WARPS, 1)
-    return total, share, apart
+    over = (join + 2) * WARPS
+    return total, share, apart, (count > ctas and max(seqs) + COST <= min(4 * over, share + over) and
+                                 -(-count // ctas) * (total // count) <= share + over)
 
 
-def after(seg, n_steps, items):
+def after(seg, n_steps, items, uncut):
     b, item = seg["b"], seg["item"] + 1
     if item == items:
         item, b = 0, b + 1
         while n_steps[b] == 0 and b + 1 < len(n_steps):
             b += 1
-    return dict(b=b, item=item, step=0, end=min(n_steps[b], seg["rest"] - COST), n=n_steps[b],
+    return dict(b=b, item=item, step=0, end=n_steps[b] if uncut else min(n_steps[b], seg["rest"] - COST), n=n_steps[b],
                 rest=seg["rest"] - COST - n_steps[b])
 
 
-def locate(cta, n_steps, items, end, share, apart):
+def locate(cta, n_steps, items, end, share, apart, uncut):
     if apart:
         done = 0
         for b, n in enumerate(n_steps):
@@ -60,30 +62,34 @@ def locate(cta, n_steps, items, end, share, apart):
     begin = at + item * (n + COST)
     rest = stop - begin - COST - n
     seg = dict(b=b, item=item, step=max(u - begin - COST, 0), end=min(n, n + rest), n=n, rest=rest)
-    if seg["step"] < seg["end"]:
+    if uncut:
+        seg["end"] = n
+    if u == begin if uncut else seg["step"] < seg["end"]:
         return seg
-    return after(seg, n_steps, items) if rest > COST else None
+    return after(seg, n_steps, items, uncut) if rest > (0 if uncut else COST) else None
 
 
 def segments(cta, n_steps, items, line):
     """[(segment, first CTA and number of the item's parts)]"""
-    end, share, apart = line
+    end, share, apart, uncut = line
     seg, got = locate(cta, n_steps, items, *line), []
     if seg is None:
         return got
     begin = min(end, share * (cta + 1)) - seg["rest"] - COST - seg["n"]
     while True:
         assert 0 <= seg["step"] < seg["end"] <= seg["n"]
-        if apart:
+        if seg["step"] == 0 and seg["end"] == seg["n"]:
+            c0, n = cta, 1
+        elif apart:
             c0, n = cta - seg["step"] // share, -(-seg["n"] // share)
         else:
             c0 = (begin + COST) // share
             n = (begin + COST + seg["n"] - 1) // share - c0 + 1
         got.append((seg, c0, n))
-        if seg["rest"] <= COST:
+        if seg["rest"] <= (0 if uncut else COST):
             return got
         begin += COST + seg["n"]
-        seg = after(seg, n_steps, items)
+        seg = after(seg, n_steps, items, uncut)
 
 
 @pytest.mark.parametrize("seed", range(400))
@@ -107,6 +113,13 @@ def test_every_step_belongs_to_one_cta(seed):
         assert [x[1] for x in p] == [0] + [x[2] for x in p[:-1]] and p[-1][2] == n_steps[b]
         assert all((c0, n) == (p[0][0], len(p)) for _, _, _, c0, n in p)
         assert [x[0] for x in p] == list(range(p[0][0], p[0][0] + len(p)))
+
+
+def test_one_long_item_among_short_ones_is_cut():
+    line = lay([700] + [9] * 40, 8, 152)
+    assert not line[2] and not line[3]
+    assert max(sum(s["end"] - s["step"] for s, _, _ in segments(c, [700] + [9] * 40, 8, line))
+               for c in range(152)) <= line[1]
 
 
 def test_shares_are_even():

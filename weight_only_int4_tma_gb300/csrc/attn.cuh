@@ -188,7 +188,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // One item's steps [step, step_end) of n_steps, as one CTA takes them.
 struct Segment {
     int b, item, step, step_end, n_steps;
-    int rest;   // what the CTA's share holds after this item; with more than kItemCost, more steps
+    int rest;   // what the CTA's share holds after this item
     Span span;
 };
 
@@ -202,6 +202,7 @@ struct Cut {
 struct Line {
     long long end, share;
     bool apart;   // a share is a part of one item
+    bool whole;   // a share is the items that begin in it, to their ends
 };
 // parts that an item of n_steps is cut in (`apart`)
 __device__ __forceinline__ int parts_of(const Line& line, int n_steps) {
@@ -267,6 +268,14 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
             line.apart = true;
             line.share = max((top + WARPS - 1) / WARPS * WARPS, 1);
         }
+        // Nor where there are more items than CTAs and whole ones make the fullest share at most kOver
+        // steps longer: by the mean length, with none that is longer than that by itself, and none
+        // over 4 kOver, as a share's last item may lie beyond it in full.  (Heads of 128, 8 of them:
+        // 32 sequences of 700 tokens 25.5 us cut, 21.7 whole, of 1500 41.4 and 36.6; 24 of 1500, 75
+        // steps over, 34.0 and 35.7.)
+        constexpr int kOver = (WHOLE + 2) * WARPS;
+        line.whole = items > ctas && top + kItemCost <= min(4ll * kOver, line.share + kOver) &&
+                     quotient(items + ctas - 1, ctas) * quotient(total, items) <= line.share + kOver;
     }
 }
 
@@ -339,7 +348,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     }
     __syncthreads();  // line, prefix, the barriers, and the zeroed ring
 
-    // the segment after `s`, where s.rest > kItemCost: the next item's first steps
+    // the segment after `s`, where more_after(s): the next item's first steps
     auto after = [&](const Segment& s) {
         Segment n = s;
         if (++n.item == items_per_seq) {
@@ -351,10 +360,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             } while (n.n_steps == 0 && n.b + 1 < a.B);
         }
         n.step = 0;
-        n.step_end = min(n.n_steps, s.rest - kItemCost);
+        n.step_end = line.whole ? n.n_steps : min(n.n_steps, s.rest - kItemCost);
         n.rest = s.rest - kItemCost - n.n_steps;
         return n;
     };
+
+    auto more_after = [&](const Segment& s) { return s.rest > (line.whole ? 0 : kItemCost); };
 
     // The first segment of the CTA's share; false: there is none.  By all lanes of a warp.
     const long long share_end = min(line.end, line.share * (cta + 1));   // in the line (not `apart`)
@@ -409,8 +420,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         const int step = max(static_cast<int>(u - begin) - kItemCost, 0);
         const int rest = static_cast<int>(share_end - begin) - kItemCost - n_steps;
         first = Segment{b, item, step, min(n_steps, n_steps + rest), n_steps, rest, span};
-        if (first.step < first.step_end) return true;
-        if (rest <= kItemCost) return false;   // the share ends before any step
+        if (line.whole ? u == begin : first.step < first.step_end) {
+            if (line.whole) first.step_end = n_steps;
+            return true;
+        }
+        if (!more_after(first)) return false;   // the share ends before any step
         first = after(first);
         return true;
     };
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             if (stage >= NST) stage -= NST, phase ^= 1u;
         }
         seg0 = seg_end;
-        more = ld.rest > kItemCost;
+        more = more_after(ld);
         if (more) ld = after(ld);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -702,7 +716,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     bool have_q = false;
     for (int turn = 0;; turn ^= 1) {
         const Segment& cur = segs[turn];
-        const bool more = cur.rest > kItemCost;
+        const bool more = more_after(cur);
         if (more && tid == 0) segs[turn ^ 1] = after(cur);
         const int kvh = cur.item / row_tiles, row0 = (cur.item - kvh * row_tiles) * ROWS;
         const int rows = min(ROWS, G - row0), head0 = kvh * G + row0;
