@@ -18,7 +18,7 @@ def lay(n_steps, items, ctas, join=4):
         steps = total - count * COST
         left = (ctas - count) * WARPS
         r = max(-(-steps // left), 1)
-        apart = r <= max(-(-steps // (ctas * WARPS)), 1) + 1
+        apart = r <= max(-(-steps // (ctas * WARPS)), 1) + 1 + join
         if apart:
             rounds, share = r, r * WARPS
     whole = -(-max(seqs, default=0) // WARPS)

@@ -250,14 +250,16 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
         line.end = total;
         line.share = max(quotient(total + ctas - 1, ctas), 1ll);
         // Few items: shares cut from one item each, in whole rounds of the warps, so that no CTA has
-        // two partial items to write and join, if that takes at most one round more.
+        // two partial items to write and join, if that takes few rounds more.  (Heads of 128: 14
+        // sequences of 4000 tokens, 4 heads with 16 rows, five more: 26.7 us with equal shares, 22.4
+        // so; with rows of 64 bytes 7 of 4000, two more, 16.7 and 18.8.)
         line.apart = false;
         long long rounds = (line.share + WARPS - 1) / WARPS;
         if (2 * items <= ctas) {
             const long long steps = total - items * kItemCost;
             const int slots = ctas * WARPS, left = static_cast<int>(ctas - items) * WARPS;
             const long long r = max(quotient(steps + left - 1, left), 1ll);
-            line.apart = r <= max(quotient(steps + slots - 1, slots), 1ll) + 1;
+            line.apart = r <= max(quotient(steps + slots - 1, slots), 1ll) + 1 + WHOLE;
             if (line.apart) rounds = r, line.share = r * WARPS;
         }
         // No item is cut where the longest takes not many rounds more than a share: joining takes some
