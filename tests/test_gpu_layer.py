@@ -194,6 +194,24 @@ def test_norm_mx(M, H, dtype):
     _within(rout, h, h.abs() * (U[dtype] + 2.0 ** -23) + TINY[dtype], "residual_out")
 
 
+@pytest.mark.parametrize("scale", [1e-19, 1e-17])
+def test_norm_i8_tiny_rows(scale):
+    """Rows whose 127 / max |y| passes fp32's range: the codes are as of any other row."""
+    M, H, dtype = 3, 512, torch.bfloat16
+    x, _, w = _norm_inputs(M, H, dtype, 17, residual=False)
+    w = (w.double() * scale).to(dtype)
+    x = (x.double() * 1e-18).to(dtype)  # eps decides: y = h * weight
+    codes, s = torch.empty(M, H, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    w4.dec_rms_norm_i8(x, None, w, M, H, CODE[dtype], 1.0, None, codes, s)
+    assert _status() == 0
+    _, y = od.rms_norm(x, None, w, 1.0)
+    _, want = od.quantize_i8(y)
+    assert float(want.max()) < 1e-33
+    # the products round to normal numbers down to 2^-126 and in steps of 2^-149 below
+    _within(s, want, want * 2 * NORM + 2.0 ** -149, "s_y")
+    _within(codes, y / want[:, None], 0.5 + 127 * 4 * NORM + 2.0 ** -149 / want[:, None].expand_as(y), "codes")
+
+
 def test_norm_feeds_the_w4a8_and_mx_gemms():
     """The 8-bit rows are what the GEMMs take: the product with the quantised rows themselves."""
     import numpy as np
@@ -313,6 +331,28 @@ def test_rope_in_place_without_cache(D, rot, inter):
     for x0, x, heads in ((q0, q, hq), (k0, k, hkv)):
         want, mag = od.rope(x0.view(T, heads, D), table[positions.long()], rot, inter)
         _within(x.view(T, heads, D), want, want.abs() * U[dtype] + mag * ROPE * 2, "rotated")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+def test_append_rounds_the_quotient_to_nearest(dtype):
+    """8-bit values are the nearest to the fp32 quotient, bit for bit; infinities saturate."""
+    T, h, D, page = 2048, 8, 128, 16
+    g = _gen(3)
+    k, v = (_randn((T, h * D), dtype, g, 8.0) for _ in range(2))
+    special = torch.tensor([math.inf, -math.inf, 65504.0, -65504.0, 0.0, -0.0, 2.0 ** -24, math.nan], device="cuda")
+    k[0, :8], v[5, -8:] = special.to(dtype), special.to(dtype)
+    kc, vc = _cache_tensors(T // page, page, h, D, E4M3, g)
+    ks, vs = (0.02 + torch.rand(h, device="cuda", generator=g) for _ in range(2))
+    cfg = w4.rope_config(0, h, D, CODE[dtype], None, 0)
+    w4.dec_rope_append(cfg, w4.kv_cache(kc, vc, ks, vs), None, k, v, T,
+                       torch.zeros(T, dtype=torch.int32, device="cuda"), torch.arange(T, device="cuda"), None)
+    assert _status() == 0
+    for c, x, scale in ((kc, k, ks), (vc, v, vs)):
+        want = (x.float().view(T, h, D) / scale[:, None]).clamp(-448, 448).to(E4M3).view(torch.uint8)
+        got = c.view(torch.uint8).view(T, h, D)
+        nan = x.view(T, h, D).isnan()
+        assert torch.equal(got[~nan], want[~nan])
+        assert bool((got[nan] & 0x7F == 0x7F).all())
 
 
 def test_rope_bad_positions_and_slots_are_reported_and_skipped():
@@ -448,6 +488,20 @@ def test_attn_many_short_sequences(kv):
     g = torch.Generator().manual_seed(3)
     lens = torch.randint(0, 60, (700,), generator=g).tolist()
     _attn_case(lens, 2, 1, 64, 16, torch.bfloat16, kv, seed=5)
+
+
+SPLITS = [
+    # few items, none cut; cut by themselves; in equal shares
+    ([260, 40, 300], 8), ([700], 4), ([900] * 14, 4), ([2500, 30, 2000, 1], 8),
+    # more items than CTAs: whole ones (ragged, with empty sequences), and a long one among short
+    (list(range(1, 300, 7)), 8), ([0, 500] * 20, 8), ([3000] + [9] * 50, 8), ([300] * 20, 8)]
+
+
+@pytest.mark.parametrize("kv", [None, E4M3], ids=str)
+@pytest.mark.parametrize("lens,heads", SPLITS, ids=lambda x: str(x)[:24].replace(" ", ""))
+def test_attn_every_way_of_splitting(lens, heads, kv):
+    """However the items are cut, the results are the statement's."""
+    _attn_case(lens, heads, heads, 64 if kv else 128, 16, torch.bfloat16, kv, seed=len(lens))
 
 
 def test_attn_long_sequence_is_split():

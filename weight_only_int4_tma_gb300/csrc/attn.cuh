@@ -8,9 +8,12 @@
 //   64 sequences of up to 16384 tokens, 8 heads of 128, bf16: 2.37 GB in 365 us, 6.5 TB/s;
 //   16 sequences of up to 4096 tokens, 32 heads of 128, fp16: 0.54 GB in 90 us, 6.0 TB/s;
 //   one sequence of 131072 tokens, 8 heads of 128, bf16: 0.54 GB in 90 us, 6.0 TB/s;
-//   33 windows of up to 4096 tokens, 4 heads of 64, 8-bit: 0.049 GB in 22.5 us, 2.2 TB/s.  (Rows of
-//   64 bytes that stand 256 apart are fetched at 1.58 times their bytes);
-//   one sequence of 777 tokens: 8.2 us, which is lengths, page table, keys and the join, one
+//   33 windows of up to 4096 tokens, 4 heads of 64, 8-bit: 0.049 GB in 22.5 us, 2.2 TB/s: a round of
+//   the warps' steps takes 2.0 us, of conversions and MMAs that wait for one another (16
+//   consumer warps with half the step each: 25.9 us);
+//   64 of 8000 tokens of it: 0.26 GB in 92 us, 2.9 TB/s, as DRAM fetches such short rows that
+//   stand apart at 1.6 times their bytes;
+//   one sequence of 777 tokens: 9.0 us, which is lengths, page table, keys and the join, one
 //   after another.
 //
 // Data path.  Steps of 16 R tokens go through a ring in shared memory of 192 KB (one CTA per
