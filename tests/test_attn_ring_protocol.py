@@ -9,14 +9,14 @@ import random
 
 import pytest
 
-W, PW = 8, 4
+PW = 4
 
 
 class Broken(Exception):
     pass
 
 
-def run(nst, segments, seed):
+def run(nst, segments, seed, W=8):
     """segments: (item, first step, steps) in order.  Raises Broken where the protocol fails."""
     rng = random.Random(seed)
     owner, seg_of = [], []           # consumer and segment of each step
@@ -76,10 +76,10 @@ def _segments(rng):
             for _ in range(rng.randrange(1, 7))]
 
 
-@pytest.mark.parametrize("nst", [8, 24])
-def test_every_step_is_read_once_by_its_consumer(nst):
+@pytest.mark.parametrize("nst,W", [(8, 8), (24, 8), (24, 4), (12, 4)])
+def test_every_step_is_read_once_by_its_consumer(nst, W):
     for seed in range(150):
-        run(nst, _segments(random.Random(seed)), seed)
+        run(nst, _segments(random.Random(seed)), seed, W)
 
 
 @pytest.mark.parametrize("nst", [22, 23])
@@ -99,4 +99,5 @@ def test_the_kernel_asserts_what_the_model_needs():
     src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                             "weight_only_int4_tma_gb300", "csrc", "attn.cuh")).read()
     assert "static_assert(NST % W == 0 && NST % PW == 0" in src
-    assert f"W = {W};" in src and f"PW = {PW};" in src
+    assert "W = DP == 256 && NT == 2 ? 4 : 8;" in src and f"PW = {PW};" in src
+    assert "NST = 2 * SLOT < 16384 ? 24 : W == 8 ? 8 : 12;" in src

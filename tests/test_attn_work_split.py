@@ -5,10 +5,10 @@ import random
 
 import pytest
 
-COST, WARPS = 8, 8
+COST = 8
 
 
-def lay(n_steps, items, ctas, join=4):
+def lay(n_steps, items, ctas, join=4, WARPS=8):
     """(end, share, apart, whole items): n_steps of each sequence, items per sequence."""
     seqs = [n for n in n_steps if n]
     total = sum(n + COST for n in seqs) * items
@@ -99,7 +99,7 @@ def test_every_step_belongs_to_one_cta(seed):
     longest = rng.choice([1, 8, 30, 64, 3000])
     n_steps = [min(longest, rng.choice([0, 1, 2, 5, 40, rng.randrange(1, 3000)])) for _ in range(rng.randrange(1, 60))]
     items = rng.choice([1, 2, 8, 32])
-    line = lay(n_steps, items, ctas, rng.choice([0, 3, 4]))
+    line = lay(n_steps, items, ctas, rng.choice([0, 3, 4]), rng.choice([4, 8]))
     parts = {}
     for cta in range(ctas):
         segs = segments(cta, n_steps, items, line)

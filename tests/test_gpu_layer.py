@@ -474,6 +474,9 @@ ATTN_CASES = [
     ([1000, 37], 4, 4, 128, 16, None, 1, False),           # the newest token alone
     ([600, 333], 16, 2, 128, 16, E4M3, 100, False),
     ([50, 700], 8, 4, 72, 7, None, 33, True),
+    ([900, 3, 0, 411], 24, 2, 256, 16, None, 0, False),     # two tiles of wide heads
+    ([1500, 64], 32, 2, 256, 8, E4M3, 0, True),
+    ([200] * 90, 18, 2, 136, 12, None, 0, False),
 ]
 
 

@@ -17,8 +17,8 @@
 //   after another.
 //
 // Data path.  Steps of 16 R tokens go through a ring in shared memory of 192 KB (one CTA per
-// SM): four producer warps fill it with asynchronous copies, eight consumer warps take its
-// steps in turn, each working alone.  mma.sync suffices: the tcgen05 form would need the
+// SM): four producer warps fill it with asynchronous copies, eight consumer warps (or four)
+// take its steps in turn, each working alone.  mma.sync suffices: the tcgen05 form would need the
 // 128-row tiles that one token's few query heads do not fill.  ldmatrix turns a step into its
 // operands:
 //   S^T = K Q^T   tokens are the MMA's 16 rows, query heads its 8 columns (with 8 heads or
@@ -134,18 +134,21 @@ struct AttnShape {
     static constexpr int NG = GROUPS ? 16 * R / PG : 1;   // groups of a step
     static constexpr int STEP = 16 * R;
     static constexpr int SLOT = STEP * PITCH;     // bytes of a step's keys, or values
-    static constexpr int W = 8;                   // consumer warps
+    // Consumer warps.  Four where two tiles of 256 values need the registers of the others (with
+    // eight they spill: 16 sequences of 4000 tokens, 4 heads with 16 rows, bf16 92.8 us, 69.1 with
+    // four; 8-bit 107.9 and 64.2; with one tile four are 2 % slower).
+    static constexpr int W = DP == 256 && NT == 2 ? 4 : 8;
     static constexpr int PW = 4;                  // producer warps
     static constexpr int MS = DP / 16;            // MMA steps over the head dimension
     static constexpr int OP = DP + 4;             // row of the warps' sums, in floats
     // warps' sums in shared memory at once
-    static constexpr int SOE = DP == 64 ? (NT == 1 ? 8 : 4) : DP == 256 && !E4M3 ? 4 : DP == 128 ? 4 / NT : 2 / NT;
+    static constexpr int SOE = DP == 64 ? (NT == 1 ? 8 : 4) : DP == 128 ? 4 / NT : E4M3 || NT == 2 ? 2 / NT : 4;
     static constexpr int SO_BYTES = SOE * ROWS * OP * 4;
-    // Steps of the ring: 192 KB of them (128 KB of those with 512-byte rows), in a multiple of W
-    // and of PW.  A stage then has the same producer in every round, and the same consumer
+    // Steps of the ring: 192 KB of them (128 KB with eight warps and 512-byte rows), in a multiple of
+    // W and of PW.  A stage then has the same producer in every round, and the same consumer
     // within an item: nobody waits for a stage two rounds ahead of it, which the barriers' one
     // bit of phase could not tell from the round at hand.
-    static constexpr int NST = 2 * SLOT == 16384 ? 8 : 24;
+    static constexpr int NST = 2 * SLOT < 16384 ? 24 : W == 8 ? 8 : 12;
     // Joining an item's parts, in the warps' rounds.  By row one round of the steps is 2.0 us (64 bytes;
     // 1 leaves 33 windows of up to 4096 tokens whole: 23.2 us against 22.5), 1.3, 1.05, 1.0.
     static constexpr int WHOLE = PITCH == 64 ? 0 : PITCH == 256 ? 4 : 3;
