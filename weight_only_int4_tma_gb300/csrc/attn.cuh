@@ -16,7 +16,7 @@
 //   one sequence of 777 tokens: 9.0 us, which is lengths, page table, keys and the join, one
 //   after another.
 //
-// Data path.  Steps of 16 R tokens go through a ring in shared memory of 192 KB (one CTA per
+// Data path.  Steps of 16 R tokens go through a ring in shared memory of 128 KB (one CTA per
 // SM): four producer warps fill it with asynchronous copies, eight consumer warps (or four)
 // take its steps in turn, each working alone.  mma.sync suffices: the tcgen05 form would need the
 // 128-row tiles that one token's few query heads do not fill.  ldmatrix turns a step into its
@@ -141,22 +141,22 @@ struct AttnShape {
     static constexpr int PW = 4;                  // producer warps
     static constexpr int MS = DP / 16;            // MMA steps over the head dimension
     static constexpr int OP = DP + 4;             // row of the warps' sums, in floats
-    // warps' sums in shared memory at once
-    static constexpr int SOE = DP == 64 ? (NT == 1 ? 8 : 4) : DP == 128 ? 4 / NT : E4M3 || NT == 2 ? 2 / NT : 4;
-    static constexpr int SO_BYTES = SOE * ROWS * OP * 4;
-    // Steps of the ring: 192 KB of them (128 KB with eight warps and 512-byte rows), in a multiple of
-    // W and of PW.  A stage then has the same producer in every round, and the same consumer
+    static constexpr int SO_BYTES = W * ROWS * OP * 4;   // the warps' sums
+    // Steps of the ring: 128 KB of them, in a multiple of W and of PW.  (192 KB leave room for half the
+    // warps' sums at a time: 64 sequences of up to 16384 tokens 353 us against 368, one of 131072
+    // 84.2 and 90.3; 64 KB: 352 against 343 in another run.)  A stage then has the same producer in every round, and the same consumer
     // within an item: nobody waits for a stage two rounds ahead of it, which the barriers' one
     // bit of phase could not tell from the round at hand.
-    static constexpr int NST = 2 * SLOT < 16384 ? 24 : W == 8 ? 8 : 12;
+    static constexpr int NST = (128 << 10) / (2 * SLOT);
     // Joining an item's parts, in the warps' rounds.  By row one round of the steps is 2.0 us (64 bytes;
-    // 1 leaves 33 windows of up to 4096 tokens whole: 23.2 us against 22.5), 1.3, 1.05, 1.0.
-    static constexpr int WHOLE = PITCH == 64 ? 0 : PITCH == 256 ? 4 : 3;
+    // 1 leaves 33 windows of up to 4096 tokens whole: 23.2 us against 22.5), 1.3, 1.05, 1.0.  With
+    // 16 rows the join is longer (64 bytes, one sequence of 1000 tokens 12.1 us with 0, 10.4 with 2).
+    static constexpr int WHOLE = PITCH == 64 ? (NT == 1 ? 0 : 2) : PITCH == 256 || W == 4 ? 4 : 3;
     static constexpr int THREADS = 32 * (W + PW);
     static constexpr int RING = NST * 2 * SLOT;
     static constexpr int SMEM = RING + SO_BYTES + NST * (4 + 3 * 8);
     static_assert(NST % W == 0 && NST % PW == 0, "a stage's producer and consumer are fixed");
-    static_assert(SMEM <= 219 * 1024 && W % SOE == 0, "the ring fits");
+    static_assert(SMEM <= 219 * 1024, "the ring fits");
 };
 
 // Byte offset of chunk c of token row r in a slot: the chunks of eight rows that ldmatrix
@@ -307,9 +307,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
     constexpr int T = S::BF ? 1 : 0;                  // type of the weights
     constexpr float kShift = S::BF ? 0.0f : 7.0f;     // see the weights below
     extern __shared__ __align__(1024) unsigned char smem[];
-    float* so = reinterpret_cast<float*>(smem + S::RING);        // [SOE][ROWS][OP]
+    float* so = reinterpret_cast<float*>(smem + S::RING);        // [W][ROWS][OP]
     // per step of the ring: its keys are there, its values are there, it may be refilled
-    uint64_t* bars = reinterpret_cast<uint64_t*>(so + S::SOE * ROWS * S::OP);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(so + W * ROWS * S::OP);
     uint32_t* metas = reinterpret_cast<uint32_t*>(bars + 3 * NST);   // which tokens have a page
     __shared__ int abort_flag;
     __shared__ float sm_m[W][ROWS], sm_l[W][ROWS];
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             if (stage >= NST) stage -= NST, phase ^= 1u;
         }
 
-        // ---- join the warps, SOE of them at a time ----
+        // ---- join the warps ----
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -948,40 +948,34 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w0 = 0; w0 < W; w0 += S::SOE) {
-            if (w0) consumers_sync<CT>();
-            if (warp >= w0 && warp < w0 + S::SOE) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int row = 8 * nt + 2 * i + c;
-                        if (row >= rows) continue;
-                        float* dst = so + ((warp - w0) * ROWS + row) * S::OP;
-#pragma unroll
-                        for (int ms = 0; ms < MS; ++ms) {
-                            dst[16 * ms + (S::E4M3 ? 2 * g : g)] = o[nt][ms][c];
-                            dst[16 * ms + (S::E4M3 ? 2 * g + 1 : g + 8)] = o[nt][ms][c + 2];
-                        }
-                    }
-            }
-            consumers_sync<CT>();
-            if (w0 == 0 && more) load_q(segs[turn ^ 1]), have_q = true;  // under way meanwhile
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+            for (int c = 0; c < 2; ++c) {
+                const int row = 8 * nt + 2 * i + c;
                 if (row >= rows) continue;
-                float top = -INFINITY;
+                float* dst = so + (warp * ROWS + row) * S::OP;
 #pragma unroll
-                for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w][row]);
-#pragma unroll
-                for (int w = 0; w < S::SOE; ++w) {
-                    const float mw = sm_m[w0 + w][row];
-                    const float f = mw == -INFINITY ? 0.0f : exp2_fast(mw - top);
-                    const float4 x = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * S::OP + d);
-                    acc[e].x = fmaf(x.x, f, acc[e].x), acc[e].y = fmaf(x.y, f, acc[e].y);
-                    acc[e].z = fmaf(x.z, f, acc[e].z), acc[e].w = fmaf(x.w, f, acc[e].w);
+                for (int ms = 0; ms < MS; ++ms) {
+                    dst[16 * ms + (S::E4M3 ? 2 * g : g)] = o[nt][ms][c];
+                    dst[16 * ms + (S::E4M3 ? 2 * g + 1 : g + 8)] = o[nt][ms][c + 2];
                 }
+            }
+        consumers_sync<CT>();
+        if (more) load_q(segs[turn ^ 1]), have_q = true;  // under way meanwhile
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int at = tid + e * CT, row = at / (DP / 4), d = 4 * (at % (DP / 4));
+            if (row >= rows) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w][row]);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float mw = sm_m[w][row];
+                const float f = mw == -INFINITY ? 0.0f : exp2_fast(mw - top);
+                const float4 x = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * S::OP + d);
+                acc[e].x = fmaf(x.x, f, acc[e].x), acc[e].y = fmaf(x.y, f, acc[e].y);
+                acc[e].z = fmaf(x.z, f, acc[e].z), acc[e].w = fmaf(x.w, f, acc[e].w);
             }
         }
         auto row_sum = [&](int row, float& top) {
