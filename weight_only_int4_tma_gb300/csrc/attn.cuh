@@ -5,13 +5,13 @@
 // key-value head the work is 2 G operations per cached 16-bit value, far below what the
 // tensor cores do in the time of the read, so the kernel is built to keep loads in flight.
 // Measured on the device (a copy reaches 6.78 TB/s there):
-//   64 sequences of up to 16384 tokens, 8 heads of 128, bf16: 2.37 GB in 365 us, 6.5 TB/s;
-//   16 sequences of up to 4096 tokens, 32 heads of 128, fp16: 0.54 GB in 90 us, 6.0 TB/s;
-//   one sequence of 131072 tokens, 8 heads of 128, bf16: 0.54 GB in 90 us, 6.0 TB/s;
+//   64 sequences of up to 16384 tokens, 8 heads of 128, bf16: 2.37 GB in 343 us, 6.9 TB/s;
+//   16 sequences of up to 4096 tokens, 32 heads of 128, fp16: 0.54 GB in 86 us, 6.3 TB/s;
+//   one sequence of 131072 tokens, 8 heads of 128, bf16: 0.54 GB in 82 us, 6.6 TB/s;
 //   33 windows of up to 4096 tokens, 4 heads of 64, 8-bit: 0.049 GB in 22.5 us, 2.2 TB/s: a round of
 //   the warps' steps takes 2.0 us, of conversions and MMAs that wait for one another (16
 //   consumer warps with half the step each: 25.9 us);
-//   64 of 8000 tokens of it: 0.26 GB in 92 us, 2.9 TB/s, as DRAM fetches such short rows that
+//   64 of 8000 tokens of it: 0.26 GB in 92 us, 2.8 TB/s, as DRAM fetches such short rows that
 //   stand apart at 1.6 times their bytes;
 //   one sequence of 777 tokens: 9.0 us, which is lengths, page table, keys and the join, one
 //   after another.
