@@ -9,14 +9,12 @@ import random
 
 import pytest
 
-PW = 4
-
 
 class Broken(Exception):
     pass
 
 
-def run(nst, segments, seed, W=8):
+def run(nst, segments, seed, W=8, PW=4):
     """segments: (item, first step, steps) in order.  Raises Broken where the protocol fails."""
     rng = random.Random(seed)
     owner, seg_of = [], []           # consumer and segment of each step
@@ -76,10 +74,10 @@ def _segments(rng):
             for _ in range(rng.randrange(1, 7))]
 
 
-@pytest.mark.parametrize("nst,W", [(8, 8), (16, 8), (32, 8), (16, 4), (8, 4)])
-def test_every_step_is_read_once_by_its_consumer(nst, W):
+@pytest.mark.parametrize("nst,W,PW", [(8, 8, 4), (16, 8, 4), (16, 8, 8), (32, 8, 8), (16, 4, 4), (8, 4, 4)])
+def test_every_step_is_read_once_by_its_consumer(nst, W, PW):
     for seed in range(150):
-        run(nst, _segments(random.Random(seed)), seed, W)
+        run(nst, _segments(random.Random(seed)), seed, W, PW)
 
 
 @pytest.mark.parametrize("nst", [22, 23])
@@ -99,5 +97,6 @@ def test_the_kernel_asserts_what_the_model_needs():
     src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                             "weight_only_int4_tma_gb300", "csrc", "attn.cuh")).read()
     assert "static_assert(NST % W == 0 && NST % PW == 0" in src
-    assert "W = DP == 256 && NT == 2 ? 4 : 8;" in src and f"PW = {PW};" in src
+    assert "W = DP == 256 && NT == 2 ? 4 : 8;" in src
+    assert "PW = NT == 1 && DP <= 128 ? 8 : 4;" in src
     assert "NST = (128 << 10) / (2 * SLOT);" in src

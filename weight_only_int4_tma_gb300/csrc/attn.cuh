@@ -8,7 +8,7 @@
 //   64 sequences of up to 16384 tokens, 8 heads of 128, bf16: 2.37 GB in 343 us, 6.9 TB/s;
 //   16 sequences of up to 4096 tokens, 32 heads of 128, fp16: 0.54 GB in 86 us, 6.3 TB/s;
 //   one sequence of 131072 tokens, 8 heads of 128, bf16: 0.54 GB in 82 us, 6.6 TB/s;
-//   33 windows of up to 4096 tokens, 4 heads of 64, 8-bit: 0.049 GB in 22.5 us, 2.2 TB/s: a round of
+//   33 windows of up to 4096 tokens, 4 heads of 64, 8-bit: 0.049 GB in 22.0 us, 2.2 TB/s: a round of
 //   the warps' steps takes 2.0 us, of conversions and MMAs that wait for one another (16
 //   consumer warps with half the step each: 25.9 us);
 //   64 of 8000 tokens of it: 0.26 GB in 92 us, 2.8 TB/s, as DRAM fetches such short rows that
@@ -17,8 +17,8 @@
 //   after another.
 //
 // Data path.  Steps of 16 R tokens go through a ring in shared memory of 128 KB (one CTA per
-// SM): four producer warps fill it with asynchronous copies, eight consumer warps (or four)
-// take its steps in turn, each working alone.  mma.sync suffices: the tcgen05 form would need the
+// SM): eight producer warps (or four) fill it with asynchronous copies, eight consumer warps
+// (or four) take its steps in turn, each working alone.  mma.sync suffices: the tcgen05 form would need the
 // 128-row tiles that one token's few query heads do not fill.  ldmatrix turns a step into its
 // operands:
 //   S^T = K Q^T   tokens are the MMA's 16 rows, query heads its 8 columns (with 8 heads or
@@ -138,7 +138,10 @@ struct AttnShape {
     // eight they spill: 16 sequences of 4000 tokens, 4 heads with 16 rows, bf16 92.8 us, 69.1 with
     // four; 8-bit 107.9 and 64.2; with one tile four are 2 % slower).
     static constexpr int W = DP == 256 && NT == 2 ? 4 : 8;
-    static constexpr int PW = 4;                  // producer warps
+    // Producer warps.  Eight where the consumers need no more than the 128 registers that leaves them
+    // (8 sequences of 2000 tokens, 8 heads of 128: bf16 21.6 us with four, 20.0 with eight, 8-bit
+    // 16.7 and 14.4; two query tiles spill then: 14 of 2000 tokens 21.9 and 29.1).
+    static constexpr int PW = NT == 1 && DP <= 128 ? 8 : 4;
     static constexpr int MS = DP / 16;            // MMA steps over the head dimension
     static constexpr int OP = DP + 4;             // row of the warps' sums, in floats
     static constexpr int SO_BYTES = W * ROWS * OP * 4;   // the warps' sums
