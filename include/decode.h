@@ -211,7 +211,9 @@ int dec_rope_append(const dec_rope_config* cfg, const dec_kv_cache* cache, const
  *     out[b, h, :] = sum_j exp(s_j) v_j[g, :] / sum_j exp(s_j),   lse[b, h] = log sum_j exp(s_j)
  * The new token's own key and value are cached before the call (dec_rope_append) and lens
  * counts them.  A sequence of length 0 gives out = 0 and lse = -infinity.  What the pages
- * hold outside those tokens is not used, whatever it is.
+ * hold outside those tokens is not used, whatever it is.  A score that is NaN gives NaN in the row's
+ * out and lse, one of +infinity NaN in out and +infinity in lse.  One of -infinity has the
+ * weight 0; a row with no other gives what a length of 0 does.
  */
 typedef struct dec_attn_config {
     int q_heads;         /* a multiple of the cache's kv_heads                              */

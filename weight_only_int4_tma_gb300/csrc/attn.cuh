@@ -32,7 +32,9 @@
 //
 // Softmax.  One pass with a running reference m per query head: weights are exp2(s - m), and
 // when a score passes m by more than 2^8 the sums so far are scaled to the new reference
-// (a warp vote finds out; exact in the end, since numerator and denominator share it).
+// (a warp vote finds out; exact in the end, since numerator and denominator share it).  All maxima
+// carry a NaN: from the step on in which a score is one it stands in m and in every sum.  With
+// an infinite score m is infinite and the sums are NaN, as inf / inf is.
 //
 // Work split.  All (sequence, head, row tile) items stand in one line, each as long as its steps
 // and kItemCost more for what an item costs by itself.  The line is cut in equal shares, one per
@@ -73,6 +75,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
+}
+// The larger, or NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
 }
 template <bool TRANS>
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -296,11 +309,12 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int b, int head, in
     uint16_t* dst = a.out + b * a.ldo + static_cast<int64_t>(head) * a.head_dim + d;
     *reinterpret_cast<uint2*>(dst) = make_uint2(dec_pack2<DT>(v.x * f, v.y * f), dec_pack2<DT>(v.z * f, v.w * f));
 }
-// m and l of a row to its log-sum-exp; `shift`: see the weights in attn_kernel.
+// m and l of a row to its log-sum-exp; `shift`: see the weights in attn_kernel.  l is NaN only where m
+// is +inf or NaN, which the log-sum-exp then is too.
 __device__ __forceinline__ void store_lse(const AttnArgs& a, int b, int head, float m, float l, float shift) {
     if (a.lse)
         a.lse[static_cast<int64_t>(b) * a.q_heads + head] =
-            l > 0.0f ? (m - shift) * 0.69314718055994531f + logf(l) : -INFINITY;
+            l > 0.0f ? (m - shift) * 0.69314718055994531f + logf(l) : l == 0.0f ? -INFINITY : m;
 }
 
 template <class S>
@@ -603,7 +617,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                             x[j][v] = __ldcg(reinterpret_cast<const float4*>(part_of(c, k_first + k * stride) + 2 * ROWS + row * DP + d));
                     }
                 if (k0 == 0) {  // the new maximum, and what it makes of the sums so far
-                    const float now = fmaxf(top, warp_max(pm));
+                    const float now = max_nan(top, warp_max_nan(pm));
                     const float old = top == -INFINITY ? 0.0f : exp2_fast(top - now);
                     top = now;
                     f = pm == -INFINITY ? 0.0f : exp2_fast(pm - now);
@@ -634,7 +648,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             if (lane == 0) to[row] = top, to[ROWS + row] = sum;
             return;
         }
-        const float f = sum > 0.0f ? c.vs / sum : 0.0f;
+        const float f = sum == 0.0f ? 0.0f : c.vs / sum;
 #pragma unroll
         for (int v = 0; v < JV; ++v)
             if (sub == 0 && l4 + 128 * v < a.head_dim) store_out<S::DT>(a, c.b, c.head0 + row, l4 + 128 * v, acc[v], f);
@@ -736,7 +750,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
         if (!have_q) load_q(cur);
         have_q = false;
         // With an 8-bit cache the MMA is fp16: bf16 queries are scaled there by a power of
-        // two per row that brings the largest to 2^8..2^9, undone in the row's factor.
+        // two per row that brings the largest to 2^8..2^9, undone in the row's factor (beside an
+        // infinity or a NaN, as for the largest finite number).
         float fct[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -751,9 +766,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                         top = max(top, max(qf[nt][ms][h] & 0x7FFFu, (qf[nt][ms][h] >> 16) & 0x7FFFu));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                const int e = static_cast<int>(top >> 7) - 127;
+                const int e = min(static_cast<int>(top >> 7) - 127, 127);
                 float up = 1.0f;
-                if (e > -119 && e < 128) {
+                if (e > -119) {
                     up = __uint_as_float(static_cast<uint32_t>(8 - e + 127) << 23);
                     f *= __uint_as_float(static_cast<uint32_t>(e - 8 + 127) << 23);
                 }
@@ -857,19 +872,19 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                 for (int c = 0; c < 2; ++c) {
                     float top = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < R; ++r) top = fmaxf(top, fmaxf(s[r][nt][c], s[r][nt][c + 2]));
+                    for (int r = 0; r < R; ++r) top = max_nan(top, max_nan(s[r][nt][c], s[r][nt][c + 2]));
                     tops[nt][c] = top;
-                    passed |= top > m[nt][c] + kLag;
+                    passed |= !(top <= m[nt][c] + kLag);
                 }
             if (__any_sync(0xFFFFFFFFu, passed)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float top = fmaxf(m[nt][c], tops[nt][c]);
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                        float top = max_nan(m[nt][c], tops[nt][c]);
+                        top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                        top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                        top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
                         const float f = top == m[nt][c] ? 1.0f : exp2_fast(m[nt][c] - top);
                         m[nt][c] = top;
                         ref[nt][c] = top == -INFINITY ? 0.0f : top - kShift;
@@ -971,7 +986,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             if (row >= rows) continue;
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w][row]);
+            for (int w = 0; w < W; ++w) top = max_nan(top, sm_m[w][row]);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 const float mw = sm_m[w][row];
@@ -985,7 +1000,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             top = -INFINITY;
             float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) top = fmaxf(top, sm_m[w][row]);
+            for (int w = 0; w < W; ++w) top = max_nan(top, sm_m[w][row]);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 const float mw = sm_m[w][row];
@@ -1004,7 +1019,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
             if (row >= rows || d >= a.head_dim) continue;
             if (whole) {
                 const float sum = row_sum(row, top);
-                store_out<S::DT>(a, cur.b, head0 + row, d, acc[e], sum > 0.0f ? vs / sum : 0.0f);
+                store_out<S::DT>(a, cur.b, head0 + row, d, acc[e], sum == 0.0f ? 0.0f : vs / sum);
             } else {
                 *reinterpret_cast<float4*>(part + 2 * ROWS + row * DP + d) = acc[e];
             }
