@@ -213,7 +213,9 @@ int dec_rope_append(const dec_rope_config* cfg, const dec_kv_cache* cache, const
  * counts them.  A sequence of length 0 gives out = 0 and lse = -infinity.  What the pages
  * hold outside those tokens is not used, whatever it is.  A score that is NaN gives NaN in the row's
  * out and lse, one of +infinity NaN in out and +infinity in lse.  One of -infinity has the
- * weight 0; a row with no other gives what a length of 0 does.
+ * weight 0; a row with no other gives what a length of 0 does.  An infinite value gives that infinity
+ * (NaN with one of the other sign) if its token's weight is at least 2^-28 of the row's
+ * largest, else that or NaN; a value that is NaN gives NaN.
  */
 typedef struct dec_attn_config {
     int q_heads;         /* a multiple of the cache's kv_heads                              */

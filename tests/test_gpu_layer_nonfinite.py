@@ -145,3 +145,49 @@ def test_an_infinite_query_reaches_every_score(value, lse, dtype, kv):
     else:
         assert bool(got[0][0, 1].isnan().all())
     _same_but(got, before, [(0, 1)])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("layout", LAYOUTS[:4], ids=str)
+@pytest.mark.parametrize("scores", ["flat", "spread", "below"])
+def test_an_infinite_value_gives_its_infinity(layout, dtype, scores):
+    """Values +inf, -inf, both and NaN in columns of their own; the other columns keep their bits.
+    flat: all weights are 1; below: the tokens with these values weigh some 2^-27 of the largest."""
+    c = _case(layout, dtype, 3)
+    b, head = len(c.lens) - 1, 0
+    n, G = c.lens[b], c.hq // c.hkv
+    at = [0, n // 3, n // 2, n - 1]
+    if scores == "flat":
+        c.q.zero_()
+    if scores == "below":  # one key apart is larger: e^18.5 is 2^26.7
+        c.k.fill_(0.25)
+        c.q.fill_(0.5)
+        c.put(c.k, b, n // 4, head, slice(0, 64), 0.25 + 18.5 / 4)
+    before = c.run()
+    for j, (d, value) in enumerate([(5, math.inf), (17, -math.inf), (40, math.inf), (63, math.nan)]):
+        c.put(c.v, b, at[j], head, d, value)
+    c.put(c.v, b, at[3], head, 40, -math.inf)
+    out, lse = c.run()
+    assert torch.equal(lse, before[1])
+    for h in range(head * G, head * G + G):
+        s, V = c.formula(b, h)
+        want = torch.softmax(s, 0) @ V
+        row = out[b, h].to(F64)
+        odd = ~want.isfinite()
+        assert odd.nonzero().squeeze(1).tolist() == [5, 17, 40, 63]
+        assert torch.equal(row[[5, 17]], want[[5, 17]]) and bool(row[[40, 63]].isnan().all()), row[odd]
+        assert torch.equal(out[b, h][~odd], before[0][b, h][~odd])
+    _same_but((out, lse), before, [(b, h) for h in range(head * G, head * G + G)])
+
+
+def test_an_infinite_value_before_the_maximum_moves():
+    """The sums so far are scaled when a larger score arrives: an infinity among them stays one."""
+    for dtype in (torch.float16, torch.bfloat16):
+        c = Case([2000], 1, 1, 64, dtype, seed=4)
+        ramp = torch.linspace(0.0, 4.0, 2000, device="cuda")  # scores rise by 16
+        c.q.fill_(0.5)
+        j = torch.arange(2000, device="cuda")
+        c.k[c.pages[0].long()[j // 16], j % 16, 0] = ramp[:, None].to(dtype)
+        c.put(c.v, 0, 3, 0, 8, -math.inf)
+        out, _ = c.run()
+        assert float(out[0, 0, 8]) == -math.inf and int((~out.isfinite()).sum()) == 1

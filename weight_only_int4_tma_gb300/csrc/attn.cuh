@@ -28,7 +28,8 @@
 // The probabilities leave S^T with tokens in rows and are wanted with tokens as the K index:
 // one 8 x 8 transpose of 16-bit pairs (movmatrix).  They are split in a high and a low
 // 16-bit part, each multiplied with V: a single 16-bit rounding of P (2^-9 for bf16) would
-// show in the result as much as the result's own.
+// show in the result as much as the result's own.  Both parts are positive (together within 2^-16
+// of the weight for bf16, 2^-21 for fp16), as 16-bit values may be infinite; 8-bit ones are not.
 //
 // Softmax.  One pass with a running reference m per query head: weights are exp2(s - m), and
 // when a score passes m by more than 2^8 the sums so far are scaled to the new reference
@@ -86,6 +87,22 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
     return v;
+}
+// Two weights >= 0 to 16 bits, each below the weight itself (by at most 2^-7 of it in bf16, 2^-9 and
+// 2^-23 in fp16), so that what is left of it is positive: a product of either part with an
+// infinite value is that infinity, not NaN.  0 stays 0; in fp16 a weight under 2^-22 may become 0.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_below(float lo, float hi) {
+    if constexpr (DT == 0) {
+        constexpr float kLess = 1.0f - 0x1p-10f;
+        uint32_t r;
+        asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;"
+            : "=r"(r) : "f"(fmaf(hi, kLess, -0x1p-24f)), "f"(fmaf(lo, kLess, -0x1p-24f)));
+        return r;
+    } else {
+        constexpr float kLess = 1.0f - 0x1p-23f;
+        return __byte_perm(__float_as_uint(lo * kLess), __float_as_uint(hi * kLess), 0x7632);
+    }
 }
 template <bool TRANS>
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -911,7 +928,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                             p[c] = exp2_fast(s[r][nt][2 * h + c] - ref[nt][c]);
                             l[nt][c] += p[c];
                         }
-                        const uint32_t hi = dec_pack2<T>(p[0], p[1]);
+                        const uint32_t hi = S::E4M3 ? dec_pack2<T>(p[0], p[1]) : pack_below<T>(p[0], p[1]);
                         const float low0 = p[0] - dec_to_f32<T>(static_cast<uint16_t>(hi & 0xFFFFu));
                         const float low1 = p[1] - dec_to_f32<T>(static_cast<uint16_t>(hi >> 16));
                         ph[r][nt][h] = transpose8x8(hi);
