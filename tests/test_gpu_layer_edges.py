@@ -1,0 +1,63 @@
+"""The decoder-layer operators (include/decode.h) at the ends of what their arguments may be."""
+import math
+
+import pytest
+import torch
+
+import weight_only_int4_tma_gb300 as w4
+from oracle import layer as od
+
+pytestmark = pytest.mark.gpu
+
+F64 = torch.float64
+E4M3 = torch.float8_e4m3fn
+U = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+CODE = {torch.float16: w4.W4A16_FP16, torch.bfloat16: w4.W4A16_BF16}
+DTYPES = [torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from weight_only_int4_tma_gb300 import build
+    build.build()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(shape, dtype, seed, scale=1.0):
+    return (torch.randn(shape, generator=_gen(seed), device="cuda") * scale).to(dtype)
+
+
+def _close(out, q, K, V, dtype):
+    """One row of attention against the statement: a score is a sum of D products, weights are carried
+    to 2^-15, one addition of 2^-23 per token, exp and the joins 2^-21."""
+    want, _, mag, spread = od.attn(q.to(F64), K.to(F64), V.to(F64), len(q) ** -0.5)
+    eps = 2 * spread * (len(q) + 8) * 2.0 ** -23 + 2.0 ** -15 + len(K) * 2.0 ** -23 + 2.0 ** -21
+    assert bool(((out.to(F64) - want).abs() <= want.abs() * U[dtype] + 2 * eps * mag + 2.0 ** -25).all())
+
+
+@pytest.mark.parametrize("page_size", [0x7FFF0000, 1 << 30])
+def test_one_page_of_any_size(page_size):
+    """A flat cache told as one page of up to 2^31 slots, of which the first hundred are there."""
+    n, h, D, dtype = 100, 2, 64, torch.float16
+    k, v = (torch.zeros(n, h, D, dtype=dtype, device="cuda") for _ in range(2))
+    cache = w4.KvCache(k.data_ptr(), v.data_ptr(), None, None, 0, h * D, D, 0, h * D, D, 1, page_size, h, D,
+                       w4.DEC_KV_FP16, 0)
+    new_k, new_v, q = (_randn((n, h * D), dtype, s) for s in range(3))
+    rc = w4.rope_config(0, h, D, CODE[dtype], None, 0)
+    w4.dec_rope_append(rc, cache, None, new_k, new_v, n, torch.zeros(n, dtype=torch.int32, device="cuda"),
+                       torch.arange(n, device="cuda"), None)
+    assert w4.w4a16_get_device_status() == 0
+    assert torch.equal(k.view(n, -1), new_k) and torch.equal(v.view(n, -1), new_v)
+    cfg = w4.attn_config(h, CODE[dtype], D ** -0.5, 1)
+    out = torch.empty(1, h * D, dtype=dtype, device="cuda")
+    w4.dec_attn_paged(cfg, cache, q[:1], torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                      torch.tensor([n], dtype=torch.int32, device="cuda"), 1, out, None, w4.attn_workspace(cfg, cache))
+    assert w4.w4a16_get_device_status() == 0
+    for i in range(h):
+        row = slice(i * D, (i + 1) * D)
+        _close(out[0, row], q[0, row], k[:, i], v[:, i], dtype)

@@ -1072,11 +1072,8 @@ int launch_attn_shape(const DeviceCtx& ctx, const AttnArgs& a, cudaStream_t stre
     if (cudaFuncSetAttribute(attn_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) !=
         cudaSuccess)
         return -3;
-    int shift = -1;
-    if ((a.page_size & (a.page_size - 1)) == 0)
-        for (shift = 0; (1 << shift) < a.page_size;) ++shift;
     return launch_dependent(attn_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)),
-                            dim3(S::THREADS), S::SMEM, stream, a, shift);
+                            dim3(S::THREADS), S::SMEM, stream, a, power_of_two(a.page_size));
 }
 
 template <int DT, bool E4M3, int DP>

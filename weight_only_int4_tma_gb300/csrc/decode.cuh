@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "launch.h"
+#include "launch_math.h"
 #include "ptx.cuh"
 
 namespace w4g {

@@ -249,13 +249,8 @@ int launch_rope(const DeviceCtx& ctx, const RopeArgs& a, int dtype, bool e4m3,
         n.per_head = (n.chunks + 1) / 2;
         n.heads = a.q_heads + a.kv_heads * (a.kc.p ? 2 : 1);
         const int units = n.per_head * n.heads;
-        auto log2_of = [](int v) {
-            int l = 0;
-            while ((1 << l) < v) ++l;
-            return (1 << l) == v ? l : -1;
-        };
-        n.head_shift = log2_of(n.per_head);
-        n.page_shift = log2_of(a.page_size);
+        n.head_shift = power_of_two(n.per_head);
+        n.page_shift = power_of_two(a.page_size);
         // as few idle threads as whole warps allow: 640 units (64 + 8 + 8 heads of 128) in five
         // CTAs of 128 rather than three of 224 (4096 tokens: 34 against 38 us)
         const int blocks = (units + 127) / 128;
