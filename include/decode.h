@@ -46,7 +46,7 @@ extern "C" {
  *   weight    device, dtype [H], or NULL (all ones).
  *   M, H      M >= 0 (0 is a no-op), 1 <= H <= 1048576.
  *   dtype     w4a16_dtype of x, residual, weight and residual_out (and of y).
- *   eps       >= 0, finite.
+ *   eps       >= 0, finite.  With 0 a zero row gives NaN in 16 bits (0 / 0) and zeros in 8 bits.
  *   residual_out  device output, rows ldr apart, or NULL (not written).  It may be
  *             `residual` itself, or x where ldx == ldr.
  *   ldx, ldr, ldy  row strides in elements, 0 = H; else at least H.

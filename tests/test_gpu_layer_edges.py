@@ -61,3 +61,29 @@ def test_one_page_of_any_size(page_size):
     for i in range(h):
         row = slice(i * D, (i + 1) * D)
         _close(out[0, row], q[0, row], k[:, i], v[:, i], dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("M,H", [(3, 128), (5, 4096), (200, 1152)])
+def test_a_zero_row_without_eps(M, H, dtype):
+    """eps = 0: int8 and MX write a zero row as zeros (scale 1, exponent byte 0), and its neighbours as
+    without it; the 16-bit form is 0 / 0."""
+    x = _randn((M, H), dtype, H)
+    x[M // 2] = 0
+    rows = [m for m in range(M) if m != M // 2]
+    codes, s = torch.empty(M, H, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    w4.dec_rms_norm_i8(x, None, None, M, H, CODE[dtype], 0.0, None, codes, s)
+    assert bool((codes[M // 2] == 0).all()) and float(s[M // 2]) == 1.0
+    _, y = od.rms_norm(x[rows], None, None, 0.0)
+    want, scale = od.quantize_i8(y)
+    # sums of at most 2^8 roundings, halved by the root, and products: 2^-16
+    assert bool(((s[rows].to(F64) - scale).abs() <= scale * 2.0 ** -15).all())
+    assert bool(((codes[rows].to(F64) - y / scale[:, None]).abs() <= 0.5 + 127 * 2.0 ** -14).all())
+    codes, s = torch.empty(M, H, dtype=torch.uint8, device="cuda"), torch.empty(M, H // 32, dtype=torch.uint8, device="cuda")
+    w4.dec_rms_norm_mx(x, None, None, M, H, CODE[dtype], 0.0, None, codes, s)
+    assert bool((codes[M // 2] == 0).all()) and bool((s[M // 2] == 0).all())
+    assert not bool((codes[rows] & 0x7F == 0x7F).any())
+    out = torch.empty_like(x)
+    w4.dec_rms_norm(x, None, None, M, H, CODE[dtype], 0.0, None, out)
+    assert bool(out[M // 2].isnan().all()) and bool(out[rows].isfinite().all())
+    assert w4.w4a16_get_device_status() == 0

@@ -116,7 +116,9 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int M, int row_t
         }
     }
     row_reduce<OUT == kNormI8>(ss, most, red, row_warp0, row_warps);
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
+    float r = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
+    // infinite for a zero row with eps = 0, whose 8-bit forms are zeros all the same: any finite r does
+    if (OUT != kNormSame && r == INFINITY) r = 1.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
