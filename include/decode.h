@@ -72,8 +72,8 @@ int dec_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
  *         32768 (w4a8_gemm itself wants a multiple of 128).
  *   s_y   device output, float [M].
  * x, residual, residual_out and weight have to be 16-byte aligned with ldx, ldr multiples
- * of 8 (INVALID_ARG otherwise).  A row that holds an infinity or a NaN gives undefined
- * codes.
+ * of 8 (INVALID_ARG otherwise).  A row whose h holds an infinity or a NaN gives undefined codes, and
+ * NaN as its scale.
  */
 int dec_rms_norm_i8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                     const void* weight, int M, int H, int dtype, float eps,

@@ -87,3 +87,19 @@ def test_a_zero_row_without_eps(M, H, dtype):
     w4.dec_rms_norm(x, None, None, M, H, CODE[dtype], 0.0, None, out)
     assert bool(out[M // 2].isnan().all()) and bool(out[rows].isfinite().all())
     assert w4.w4a16_get_device_status() == 0
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("M,H", [(3, 128), (5, 4096), (200, 1152), (2, 32768)])
+def test_int8_scale_of_a_row_with_infinities_or_nan(M, H, dtype, value):
+    """The scale is NaN, so that what is computed from the row is; its neighbours do not change."""
+    x = _randn((M, H), dtype, H + M)
+    codes, s = torch.empty(M, H, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    w4.dec_rms_norm_i8(x, None, None, M, H, CODE[dtype], 1e-5, None, codes, s)
+    want = codes.clone(), s.clone()
+    x[M - 1, H // 3] = value
+    w4.dec_rms_norm_i8(x, None, None, M, H, CODE[dtype], 1e-5, None, codes, s)
+    assert w4.w4a16_get_device_status() == 0
+    assert math.isnan(float(s[M - 1]))
+    assert torch.equal(codes[:-1], want[0][:-1]) and torch.equal(s[:-1], want[1][:-1])

@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int M, int row_t
         }
     } else if constexpr (OUT == kNormI8) {
         most *= r;
-        const float s = most > 0.0f ? __fdiv_rn(most, 127.0f) : 1.0f;
+        // NaN with an infinity or a NaN in the row, as r or r times the infinity is
+        const float s = most == 0.0f ? 1.0f : __fdiv_rn(most, 127.0f);
         // y / s as y * (127 / most): 2^-23 off, like y itself; the division for each value took
         // half of the kernel's time.  The sum with 1.5 * 2^23 rounds to the nearest integer
         // (ties to even) and leaves it in the low byte.
