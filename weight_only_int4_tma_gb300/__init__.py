@@ -451,8 +451,13 @@ def kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
 def rope_config(q_heads: int, kv_heads: int, head_dim: int, dtype: int, table, rot_dim: int,
                 layout: int = DEC_ROPE_HALF, *, ldq: int = 0, ldk: int = 0, ldv: int = 0,
                 ldqo: int = 0, ldko: int = 0) -> RopeConfig:
-    """dec_rope_append's settings; table: float32 [positions, rot_dim] (it has to outlive the
-    struct), or None with rot_dim 0 and no rotation (any non-negative position)."""
+    """dec_rope_append's settings; table: contiguous float32 [positions, rot_dim] or [positions, 2,
+    rot_dim / 2] (it has to outlive the struct), or None with rot_dim 0 and no rotation (any
+    non-negative position)."""
+    import torch
+    if rot_dim and (table is None or table.dtype != torch.float32 or table.dim() < 2
+                    or table.shape[1:].numel() != rot_dim or not table.is_contiguous()):
+        raise W4A16Error(W4A16_ERR_UNSUPPORTED, "rope_config")
     n = table.shape[0] if table is not None else 0x7FFFFFFF
     return RopeConfig(q_heads, kv_heads, head_dim, dtype, rot_dim, layout, n, 0, _ptr(table),
                       ldq, ldk, ldv, ldqo, ldko)
