@@ -103,3 +103,33 @@ def test_int8_scale_of_a_row_with_infinities_or_nan(M, H, dtype, value):
     assert w4.w4a16_get_device_status() == 0
     assert math.isnan(float(s[M - 1]))
     assert torch.equal(codes[:-1], want[0][:-1]) and torch.equal(s[:-1], want[1][:-1])
+
+
+@pytest.mark.parametrize("D,rot", [(128, 128), (16, 6)])  # both kernels
+def test_append_by_scales_of_any_size(D, rot):
+    """8-bit values are the nearest to the fp32 quotient for scales down to the smallest subnormal number
+    and up to the largest; zeros stay zeros."""
+    scales = [2.0 ** -149, 1e-39, 2.0 ** -128, 2.0 ** -126, 2.0 ** -100, 3e-25, 0.05, 1e24, 1e30, 3e38, math.inf]
+    h, T, page, dtype = len(scales), 512, 16, torch.bfloat16
+    s = torch.tensor(scales, device="cuda")
+    x = torch.randn(T, h, D, generator=_gen(1), device="cuda") * 8
+    x = (x.double() * s.double().clamp(max=3e35)[:, None]).float().to(dtype)  # subnormal numbers among them
+    x[:, :, 0], x[:, :, 1] = 0.0, -0.0
+    x[:, :, 2], x[:, :, 3], x[:, :, 4] = math.inf, 3e38, -1e-38
+    table = torch.zeros(1, rot, device="cuda")
+    table[:, :rot // 2] = 1  # turned by nothing
+    kc, vc = (torch.zeros(T // page, page, h, D, device="cuda").to(E4M3) for _ in range(2))
+    cfg = w4.rope_config(0, h, D, CODE[dtype], table, rot, w4.DEC_ROPE_INTERLEAVED)
+    rows = x.view(T, h * D)
+    w4.dec_rope_append(cfg, w4.kv_cache(kc, vc, s, s), None, rows, rows, T,
+                       torch.zeros(T, dtype=torch.int32, device="cuda"), torch.arange(T, device="cuda"), None)
+    assert w4.w4a16_get_device_status() == 0
+    value = x.cpu().float()
+    a, b = value[..., 0:rot:2], value[..., 1:rot:2]  # the turn itself loses zeros' signs, and infinities
+    turned = torch.stack([a * 1.0 - b * 0.0, b * 1.0 + a * 0.0], -1).flatten(-2)
+    for c, v in ((vc, value), (kc, torch.cat([turned, value[..., rot:]], -1))):
+        want = (v / s.cpu()[:, None]).clamp(-448, 448).to(E4M3).view(torch.uint8)
+        got = c.view(torch.uint8).view(T, h, D).cpu()
+        nan = want & 0x7F == 0x7F
+        assert bool((got[nan] & 0x7F == 0x7F).all())
+        assert torch.equal(got[~nan], want[~nan]), ((got != want) & ~nan).sum((0, 2))

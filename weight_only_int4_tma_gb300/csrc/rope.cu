@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
 // its remainder (Markstein: exact rounding for normal results).  x * inv alone moves one code in a
 // million to the neighbour.  1003 tokens of 96 heads: 9.9 us, 9.3 by x * inv, 11.1 by division.
 // Only quotients of 2^-12 .. 2^10 are corrected, beyond which E4M3 has no two numbers to choose
-// from: an infinity would become a NaN, and -0 lose its sign.
+// from: an infinity would become a NaN, and -0 lose its sign.  inv has to be a normal number and the
+// remainder's last bit (2^-48 of x) representable: 2^-80 <= |s| <= 2^80.
 __device__ __forceinline__ float rope_quotient(float x, float s, float inv) {
     const float q = x * inv;
     const uint32_t lo = __float_as_uint(0x1p-12f), hi = __float_as_uint(0x1p10f);
@@ -212,7 +213,15 @@ __global__ void __launch_bounds__(128) rope_units_kernel(RopeArgs a, RopeUnits n
     const int64_t page = n.page_shift >= 0 ? slot >> n.page_shift : slot / a.page_size;
     const int64_t off = page * kv.page_stride + (slot - page * a.page_size) * kv.slot_stride + h * kv.head_stride;
     if constexpr (E4M3) {
-        const float s = kv.scale ? kv.scale[h] : 1.0f, inv = __frcp_rn(s);
+        float s = kv.scale ? kv.scale[h] : 1.0f;
+        if (!(fabsf(s) >= 0x1p-80f && fabsf(s) <= 0x1p80f)) {
+            // the same quotients of numbers by a power of two off, exact where a quotient is in range
+            const float by = fabsf(s) < 1.0f ? 0x1p100f : 0x1p-100f;
+            s *= by;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x0[e] *= by, x1[e] *= by;
+        }
+        const float inv = __frcp_rn(s);
         auto pack = [&](const float (&x)[8]) {
             uint32_t w[4];
 #pragma unroll
