@@ -133,3 +133,22 @@ def test_append_by_scales_of_any_size(D, rot):
         nan = want & 0x7F == 0x7F
         assert bool((got[nan] & 0x7F == 0x7F).all())
         assert torch.equal(got[~nan], want[~nan]), ((got != want) & ~nan).sum((0, 2))
+
+
+def test_as_many_rows_and_tokens_as_an_int_counts():
+    """2^31 - 1 rows of 8 values, normed and turned in place."""
+    M, dtype = 0x7FFFFFFF, torch.bfloat16
+    if torch.cuda.mem_get_info()[0] < (64 << 30):
+        pytest.skip("not enough memory")
+    x = torch.full((M, 8), 2.0, dtype=dtype, device="cuda")  # 32 GiB
+    w4.dec_rms_norm(x, None, None, M, 8, CODE[dtype], 0.0, None, x)
+    assert w4.w4a16_get_device_status() == 0
+    for part in x.view(-1).split(1 << 31):
+        assert bool((part == 1).all())
+    positions = torch.zeros(M, dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0.0] * 4 + [1.0] * 4], device="cuda")  # a quarter turn
+    x[:, :4] = 3
+    w4.dec_rope_append(w4.rope_config(1, 0, 8, CODE[dtype], table, 8), None, x, None, None, M, positions, None, x)
+    assert w4.w4a16_get_device_status() == 0
+    for part in x.split(1 << 28):
+        assert bool((part[:, :4] == -1).all()) and bool((part[:, 4:] == 3).all())

@@ -216,7 +216,7 @@ template <int DT, int OUT, int V>
 int launch_norm_v(const NormArgs& a, int M, int row_threads, cudaStream_t stream) {
     // several short rows share a CTA
     const int rows = row_threads >= 256 ? 1 : 256 / row_threads;
-    return launch_dependent(norm_kernel<DT, OUT, V>, dim3(static_cast<unsigned>((M + rows - 1) / rows)),
+    return launch_dependent(norm_kernel<DT, OUT, V>, dim3(blocks_for(M, rows)),
                             rows * row_threads, 0, stream, a, M, row_threads);
 }
 

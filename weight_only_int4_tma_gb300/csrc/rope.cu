@@ -268,7 +268,7 @@ int launch_rope(const DeviceCtx& ctx, const RopeArgs& a, int dtype, bool e4m3,
         auto kern = dtype == 0 ? (e4m3 ? rope_units_kernel<0, true> : rope_units_kernel<0, false>)
                                : (e4m3 ? rope_units_kernel<1, true> : rope_units_kernel<1, false>);
         if (blocks <= 65535)
-            return launch_dependent(kern, dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens),
+            return launch_dependent(kern, dim3(blocks_for(a.T, tokens),
                                                static_cast<unsigned>(blocks)),
                                     dim3(threads, tokens), 0, stream, a, n);
     }
