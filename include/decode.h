@@ -242,11 +242,11 @@ size_t dec_attn_workspace_bytes(const dec_attn_config* cfg, const dec_kv_cache* 
  *   block_table  device, int32 [B] rows of max_pages page indexes: token j of sequence b is
  *                in slot j % page_size of page block_table[b][j / page_size].  Columns past
  *                the sequence's length (or before its window) are not read.
- *   lens         device, int32 [B], 0 .. max_pages * page_size.
+ *   lens         device, int32 [B], 0 .. max_pages * page_size; together, times q_heads, below 2^39.
  *   out          device output, dtype, rows ldo apart, 16-byte aligned.
  *   lse          device output, float [B][q_heads], or NULL.
  *   workspace    device, 16-byte aligned, ws_bytes >= dec_attn_workspace_bytes(cfg, cache).
- *   B            0 is a no-op.
+ *   B            0 .. 2^27 - 1 (more: UNSUPPORTED); 0 is a no-op.
  * Results do not depend on how the work is split in time: the partial results are joined in
  * a fixed order, and equal inputs give equal bits.  A length outside its range is cut to it,
  * and a page index outside the cache leaves its tokens out; both record

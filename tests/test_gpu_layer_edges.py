@@ -152,3 +152,18 @@ def test_as_many_rows_and_tokens_as_an_int_counts():
     assert w4.w4a16_get_device_status() == 0
     for part in x.split(1 << 28):
         assert bool((part[:, :4] == -1).all()) and bool((part[:, 4:] == 3).all())
+
+
+@pytest.mark.parametrize("B", [3 << 17, (5 << 21) + 5])
+def test_attention_of_millions_of_sequences(B):
+    """One token each, every ninth sequence empty: the output is the token's value."""
+    D, pages, dtype = 8, 4096, torch.bfloat16
+    kc, vc = (_randn((pages, 1, 1, D), dtype, s) for s in range(2))
+    q = torch.full((B, D), 0.5, dtype=dtype, device="cuda")
+    table = torch.randint(0, pages, (B, 1), generator=_gen(2), device="cuda").int()
+    lens = (torch.arange(B, device="cuda") % 9 != 8).int()
+    cfg, cache = w4.attn_config(1, CODE[dtype], 1.0, 1), w4.kv_cache(kc, vc)
+    out = torch.full((B, D), 7.0, dtype=dtype, device="cuda")
+    w4.dec_attn_paged(cfg, cache, q, table, lens, B, out, None, w4.attn_workspace(cfg, cache))
+    assert w4.w4a16_get_device_status() == 0
+    assert torch.equal(out, vc.view(pages, D)[table[:, 0].long()] * lens[:, None].to(dtype))

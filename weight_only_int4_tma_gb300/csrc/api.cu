@@ -745,6 +745,7 @@ int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const 
     int rc = check_attn(cfg, cache);
     if (rc != W4A16_OK) return rc;
     if (B < 0) return W4A16_ERR_INVALID_ARG;
+    if (B >= (1 << 27)) return W4A16_ERR_UNSUPPORTED;  // what the kernel counts sequences up to
     AttnArgs a{};
     const int64_t nq = static_cast<int64_t>(cfg->q_heads) * cache->head_dim;
     a.ldq = cfg->ldq, a.ldo = cfg->ldo;

@@ -256,8 +256,10 @@ __device__ __forceinline__ void lay_line(const AttnArgs& a, int items_per_seq, i
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     const int per_thread = (a.B + THREADS - 1) / THREADS;
     const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
-    // their length in the line in the low bits, the number that have any steps above
-    constexpr int kSeqBit = 40;
+    // their length in the line in the low bits, the number that have any steps above: below 2^27
+    // sequences, whose 2^39 tokens are 2^35 steps of 16, and 8 for each sequence
+    constexpr int kSeqBit = 36;
+    static_assert((1ll << 35) + (1ll << 27) * kItemCost < (1ll << kSeqBit), "the lengths stay below the count");
     constexpr long long kLow = (1ll << kSeqBit) - 1;
     long long mine = 0;
     int top = 0;
