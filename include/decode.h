@@ -190,8 +190,9 @@ typedef struct dec_rope_config {
  *              if kv_heads is 0; v may be NULL without a cache.
  *   positions  device, int32 [T]: row of the table.
  *   slots      device, int64 [T]: page * page_size + slot of the token in the cache; negative
- *              = the token is not cached.  Two tokens with the same slot: either may stay.
- *              May be NULL without a cache.
+ *              = the token is not cached (so for padding).  A token's values are written by threads
+ *              of their own: a slot that two tokens share holds a mix of both, each of its
+ *              values from either.  May be NULL without a cache.
  *   q_out      device output, rows ldqo apart; it may be q itself (ldqo == ldq).
  *   k_out      device output, rows ldko apart, or NULL; it may be k itself.
  *   T          0 is a no-op.

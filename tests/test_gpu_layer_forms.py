@@ -1,7 +1,7 @@
 """Forms of the decoder-layer operators' calls (include/decode.h) that a server meets besides the plain
 ones: strided rows and no weight for the 8-bit norms, four pieces per thread with the last ones
-empty, wide block tables, keys and values laid out apart, two streams, and graphs whose lengths move
-from one way of splitting to another.
+empty, wide block tables, keys and values laid out apart, two streams, graphs whose lengths move from one
+way of splitting to another, and two tokens for one slot.
 
 Tolerances: the norm's sums take at most 2^8 roundings of 2^-24, halved by the root, and a few for the
 products: NORM = 2^-16 relative; U, half a step of the stored type."""
@@ -198,3 +198,23 @@ def test_a_graph_whose_lengths_move_between_the_splits():
             K, V = (od.cached_tokens(c, table[b], 16, 0, now[b], h // 3) for c in (k, v))
             _close(out[b, h * 64:(h + 1) * 64], q[b, h * 64:(h + 1) * 64], K, V, dtype)
     assert w4.w4a16_get_device_status() == 0
+
+
+@pytest.mark.parametrize("D,rot", [(128, 128), (80, 40)])  # both kernels
+def test_tokens_that_share_a_slot_leave_values_of_them_alone(D, rot):
+    """Which of two tokens' values a shared slot keeps may differ from value to value, and is one of
+    theirs for each; every other slot is as without them."""
+    T, h, page, dtype = 600, 4, 16, torch.bfloat16
+    table = od.rope_table(od.rope_frequencies(rot, 10000.0), 700).float().cuda()
+    k, v = (_randn((T, h * D), dtype, s) for s in range(2))
+    kc, vc = (torch.zeros(T // page + 1, page, h, D, dtype=dtype, device="cuda") for _ in range(2))
+    ko = torch.empty_like(k)
+    slots = torch.arange(T, device="cuda")
+    slots[1::2] = slots[0::2]  # pairs of tokens
+    w4.dec_rope_append(w4.rope_config(0, h, D, CODE[dtype], table, rot), w4.kv_cache(kc, vc), None, k, v, T,
+                       torch.arange(T, device="cuda").int(), slots, None, ko)
+    assert w4.w4a16_get_device_status() == 0
+    for c, new in ((kc, ko), (vc, v)):
+        got = c.view(-1, h * D)
+        assert bool(((got[0:T:2] == new[0::2]) | (got[0:T:2] == new[1::2])).all())
+        assert bool((got[1:T:2] == 0).all()) and bool((got[T:] == 0).all())
