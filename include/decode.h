@@ -18,7 +18,8 @@
  * can capture, w4a16_status return codes, kernel-detected errors in the device status word
  * read by w4a16_get_device_status().  Every kernel here is launched with programmatic
  * dependent launch and reads and writes memory only after the previous kernel in the
- * stream has finished.  Strides ("ld...") count elements; 0 stands for packed rows.
+ * stream has finished (of them only the norm of aligned rows lets the next one start before it
+ * ends itself).  Strides ("ld...") count elements; 0 stands for packed rows.
  */
 #ifndef DECODE_H_
 #define DECODE_H_
@@ -216,7 +217,8 @@ int dec_rope_append(const dec_rope_config* cfg, const dec_kv_cache* cache, const
  * out and lse, one of +infinity NaN in out and +infinity in lse.  One of -infinity has the
  * weight 0; a row with no other gives what a length of 0 does.  An infinite value gives that infinity
  * (NaN with one of the other sign) if its token's weight is at least 2^-28 of the row's
- * largest, else that or NaN; a value that is NaN gives NaN.
+ * largest, else that or NaN; a value that is NaN gives NaN.  Otherwise the weights are exact to 2^-15,
+ * and with fp16 or 8-bit caches to 2^-32 of the row's largest.
  */
 typedef struct dec_attn_config {
     int q_heads;         /* a multiple of the cache's kv_heads                              */

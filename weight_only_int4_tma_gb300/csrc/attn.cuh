@@ -4,16 +4,17 @@
 // The keys and values are read once and nothing else of size is: with G query heads per
 // key-value head the work is 2 G operations per cached 16-bit value, far below what the
 // tensor cores do in the time of the read, so the kernel is built to keep loads in flight.
-// Measured on the device (a copy reaches 6.78 TB/s there):
-//   64 sequences of up to 16384 tokens, 8 heads of 128, bf16: 2.37 GB in 343 us, 6.9 TB/s;
-//   16 sequences of up to 4096 tokens, 32 heads of 128, fp16: 0.54 GB in 86 us, 6.3 TB/s;
-//   one sequence of 131072 tokens, 8 heads of 128, bf16: 0.54 GB in 82 us, 6.6 TB/s;
+// Measured on several devices (a copy reaches 6.78 TB/s):
+//   64 sequences of up to 16384 tokens, 8 heads of 128, bf16: 2.37 GB in 342 to 355 us, 6.7 to 6.9
+//   TB/s; with 8 bits 1.18 GB in 190 to 208 us, 5.7 to 6.2 TB/s;
+//   16 sequences of up to 4096 tokens, 32 heads of 128, fp16: 0.54 GB in 86 to 88 us, 6.2 TB/s;
+//   one sequence of 131072 tokens, 8 heads of 128, bf16: 0.54 GB in 81 to 84 us, 6.4 to 6.6 TB/s;
 //   33 windows of up to 4096 tokens, 4 heads of 64, 8-bit: 0.049 GB in 22.0 us, 2.2 TB/s: a round of
 //   the warps' steps takes 2.0 us, of conversions and MMAs that wait for one another (16
 //   consumer warps with half the step each: 25.9 us);
-//   64 of 8000 tokens of it: 0.26 GB in 92 us, 2.8 TB/s, as DRAM fetches such short rows that
+//   64 of 8000 tokens of it: 0.26 GB in 88 to 92 us, 2.9 TB/s, as DRAM fetches such short rows that
 //   stand apart at 1.6 times their bytes;
-//   one sequence of 777 tokens: 9.0 us, which is lengths, page table, keys and the join, one
+//   one sequence of 777 tokens: 8.9 to 9.3 us, which is lengths, page table, keys and the join, one
 //   after another.
 //
 // Data path.  Steps of 16 R tokens go through a ring in shared memory of 128 KB (one CTA per
@@ -90,7 +91,7 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 }
 // Two weights >= 0 to 16 bits, each below the weight itself (by at most 2^-7 of it in bf16, 2^-9 and
 // 2^-23 in fp16), so that what is left of it is positive: a product of either part with an
-// infinite value is that infinity, not NaN.  0 stays 0; in fp16 a weight under 2^-22 may become 0.
+// infinite value is that infinity, not NaN.  0 stays 0; of a weight under 2^-22 fp16's high part may be 0.
 template <int DT>
 __device__ __forceinline__ uint32_t pack_below(float lo, float hi) {
     if constexpr (DT == 0) {
@@ -164,9 +165,10 @@ struct AttnShape {
     static constexpr int NG = GROUPS ? 16 * R / PG : 1;   // groups of a step
     static constexpr int STEP = 16 * R;
     static constexpr int SLOT = STEP * PITCH;     // bytes of a step's keys, or values
-    // Consumer warps.  Four where two tiles of 256 values need the registers of the others (with
-    // eight they spill: 16 sequences of 4000 tokens, 4 heads with 16 rows, bf16 92.8 us, 69.1 with
-    // four; 8-bit 107.9 and 64.2; with one tile four are 2 % slower).
+    // Consumer warps.  Four where two tiles of 256 values need the registers of the others (16
+    // sequences of 4000 tokens, 4 heads with 16 rows, bf16 92.8 us with eight, 69.1 with four; 8-bit
+    // 107.9 and 64.2; with one tile four are 2 % slower).  They spill a little all the same: 32 to
+    // 68 bytes at 255 registers, and with eight warps two tiles of 8-bit heads of 128 60 to 72 at 168.
     static constexpr int W = DP == 256 && NT == 2 ? 4 : 8;
     // Producer warps.  Eight where the consumers need no more than the 128 registers that leaves them
     // (8 sequences of 2000 tokens, 8 heads of 128: bf16 21.6 us with four, 20.0 with eight, 8-bit
@@ -916,7 +918,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attn_kernel(AttnArgs a, int pag
                     }
             }
             // weights, split in 16-bit parts, as B fragments.  fp16 keeps 2^-14 as its
-            // smallest full number: its weights are scaled by 2^7 (at most 2^15 with the lag).
+            // smallest full number: its weights are scaled by 2^7 (at most 2^15 with the lag).  What is
+            // below 2^-25 of it, 2^-32 of the row's largest weight, is lost.
             uint32_t ph[R][NT][2], pl[R][NT][2];
 #pragma unroll
             for (int r = 0; r < R; ++r)

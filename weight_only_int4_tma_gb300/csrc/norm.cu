@@ -7,8 +7,9 @@
 // A row is read once: its threads hold it in registers, in 16-byte pieces of 8 values, from
 // the loads over the reduction to the stores.  Bound by HBM for many rows, by the latency of
 // one load, one block reduction and one store for few.  With residual, on the device: 4096 x
-// 8192 bf16 41.4 us, 6.5 TB/s; to int8 42.0 us, 5.6 TB/s; 1 x 8192 2.5 us and 8 x 8192 to
-// int8 2.7 us in a graph.
+// 8192 bf16 41.5 us, 6.5 TB/s; to int8 42.6 us, 5.5 TB/s; to MX 38.7 us, 6.1 TB/s; 1 x 8192 2.5 us, 8 x
+// 8192 to int8 2.7 us and to MX 2.6 us in a graph.  (Rows of up to 1024 threads leave a thread 64
+// registers: with four pieces each it spills 70 to 84 bytes.)
 #include "decode.cuh"
 
 namespace w4g {
@@ -181,7 +182,7 @@ constexpr int kNormThreads = 256;
 
 // Rows that are not 16-byte aligned, of a length that is no multiple of 8, or longer than
 // 32768: one CTA per row, one value per thread and step, the row read twice (the second time
-// from L1 or L2).
+// from L1 or L2).  Bound by its many short loads: 800 x 4100 bf16 with residual 7.4 us, 3.5 TB/s.
 template <int DT>
 __global__ void __launch_bounds__(kNormThreads) norm_any_kernel(NormArgs a) {
     __shared__ float2 red[kNormThreads / 32];

@@ -35,7 +35,9 @@ __global__ void __launch_bounds__(256) rope_table_kernel(RopeTableArgs a) {
 
 constexpr int kRopeThreads = 256;
 
-// Any rot_dim: one pair per thread; heads 0..q_heads-1 are queries, then keys, then values.
+// Any rot_dim: one pair per thread; heads 0..q_heads-1 are queries, then keys, then values.  Bound by
+// its 2-byte loads and stores and a division per pair (4096 tokens of 32 + 32 + 32 heads of 96 with 24
+// turned, bf16: 0.15 GB in 78 us, 1.9 TB/s).
 template <int DT, bool E4M3>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
     grid_dep_wait();
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
 
 // x / s, rounded to nearest, given inv = 1 / s rounded to nearest: the product with inv, corrected by
 // its remainder (Markstein: exact rounding for normal results).  x * inv alone moves one code in a
-// million to the neighbour.  1003 tokens of 96 heads: 9.9 us, 9.3 by x * inv, 11.1 by division.
+// million to the neighbour.  1003 tokens of 96 heads: 10.0 us, 9.3 by x * inv, 11.1 by division.
 // Only quotients of 2^-12 .. 2^10 are corrected, beyond which E4M3 has no two numbers to choose
 // from: an infinity would become a NaN, and -0 lose its sign.  inv has to be a normal number and the
 // remainder's last bit (2^-48 of x) representable: 2^-80 <= |s| <= 2^80.
@@ -142,8 +144,8 @@ struct RopeUnits {
 
 // One unit per thread, loaded and stored in 16-byte pieces; a token's position, slot and table
 // row come through L1, which its threads share.  Bound by HBM for many tokens (2 + 2 bytes per
-// value: 4096 tokens of 64 + 8 + 8 heads of 128, bf16, 0.17 GB in 30.5 us, 5.6 TB/s; with two tokens a
-// thread 30.1), by the chain position -> table row -> store for few (one token 1.5 us in a
+// value: 4096 tokens of 64 + 8 + 8 heads of 128, bf16, 0.17 GB in 30.7 us, 5.5 TB/s; with two tokens a
+// thread 30.1 against 30.5; to an 8-bit cache 30.9, 5.2 TB/s), by the chain position -> table row -> store for few (one token 1.5 us in a
 // graph).
 template <int DT, bool E4M3>
 __global__ void __launch_bounds__(128) rope_units_kernel(RopeArgs a, RopeUnits n) {
@@ -261,7 +263,7 @@ int launch_rope(const DeviceCtx& ctx, const RopeArgs& a, int dtype, bool e4m3,
         n.head_shift = power_of_two(n.per_head);
         n.page_shift = power_of_two(a.page_size);
         // as few idle threads as whole warps allow: 640 units (64 + 8 + 8 heads of 128) in five
-        // CTAs of 128 rather than three of 224 (4096 tokens: 34 against 38 us)
+        // CTAs of 128 rather than three of 224 (4096 tokens: 30.7 against 33.7 us)
         const int blocks = (units + 127) / 128;
         const int threads = ((units + blocks - 1) / blocks + 31) / 32 * 32;
         const int tokens = blocks > 1 ? 1 : 128 / threads;
