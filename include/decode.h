@@ -9,9 +9,15 @@
  *   dec_rope_append          rotary positions on new queries and keys; keys and values
  *                            written to their slots of a paged cache
  *   dec_attn_paged           attention of one new token per sequence over that cache
+ *   dec_attn_tree            attention of up to 64 drafted tokens per sequence, in a tree or a chain,
+ *                            over that cache; sliding window with first tokens that stay visible
+ *   dec_token_logprobs       log probabilities of given tokens, entropy and largest logits
+ *   dec_kv_move              cached tokens moved to other slots (the accepted ones of a tree)
  *
  * A decoder layer runs them as  norm -> QKV GEMM -> rope + append -> attention -> output
- * GEMM (residual fused) -> norm -> feed-forward GEMMs.
+ * GEMM (residual fused) -> norm -> feed-forward GEMMs.  With drafted tokens the attention is
+ * dec_attn_tree; the model's last GEMM is followed by dec_token_logprobs, from which the program
+ * chooses the accepted path, and dec_kv_move then closes every layer's cache up.
  *
  * Conventions are those of w4a16.h: device pointers on the current device, caller-owned
  * buffers, `stream` a cudaStream_t passed as void*, asynchronous calls that a CUDA graph
@@ -261,6 +267,138 @@ size_t dec_attn_workspace_bytes(const dec_attn_config* cfg, const dec_kv_cache* 
 int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const void* q,
                    const int32_t* block_table, const int32_t* lens, int B, void* out,
                    float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- attention of drafted tokens ---------------------------------------------------------
+ *
+ * Sequence b has n = starts[b+1] - starts[b] drafted tokens, rows starts[b] .. starts[b+1] - 1 of
+ * q and out, whose keys and values are the last n of its lens[b] cached tokens: drafted token j
+ * is cached token ctx + j, ctx = lens[b] - n.  (Rotary positions are the caller's: tokens of one
+ * depth of the tree have the same.)  With mask word w, row i of the sequence sees
+ *     the cached tokens j < ctx with  j < sinks  or  j >= ctx + popcount(w) - window
+ *         (all of them with window = 0; popcount over the bits below n), and
+ *     the drafted tokens j with bit j of w set: its ancestors in the tree and itself.
+ * Without a mask the drafted tokens are a chain: w has the bits 0 .. i.  A row then sees the sinks
+ * and the newest `window` tokens of its path (and no fewer than what w names).  Over the tokens it sees
+ *     s_j = scale * sum_d q[h, d] k_j[g, d],   g = h / (q_heads / kv_heads)
+ *     out[h, :] = sum_j exp(s_j) v_j[g, :] / sum_j exp(s_j),   lse[h] = log sum_j exp(s_j)
+ * and a row that sees none gives out = 0 and lse = -infinity.  Nothing that a row does not see
+ * changes its result, whatever it holds.  A score that is NaN gives NaN in the row's out and lse,
+ * one of +infinity NaN in out and +infinity in lse; one of -infinity has the weight 0.  An
+ * infinite value gives that infinity (NaN with one of the other sign) if its token's weight is at
+ * least 2^-20 of the row's largest, else that or NaN; a value that is NaN gives NaN.  Otherwise the weights are
+ * exact to 2^-15, and with fp16 or 8-bit caches to 2^-24 of the row's largest.
+ */
+typedef struct dec_tree_config {
+    int q_heads;         /* a multiple of the cache's kv_heads                              */
+    int dtype;           /* w4a16_dtype of q and out                                        */
+    int max_pages;       /* columns of block_table                                          */
+    int window;          /* newest tokens of its path that a row sees; 0 = all              */
+    int sinks;           /* first tokens that stay visible outside the window, >= 0         */
+    float scale;         /* finite                                                          */
+    int64_t ldq, ldo;    /* row strides of q and out; 0 = q_heads * head_dim; multiples of 8 */
+    int64_t ld_table;    /* row stride of block_table; 0 = max_pages                        */
+} dec_tree_config;
+
+/*
+ * Bytes of workspace that dec_attn_tree needs on the current device, for any batch and any
+ * lengths; 0 for arguments that it refuses.  Its contents before a call do not matter.  Calls that
+ * may run at the same time (other streams) need workspaces of their own.
+ */
+size_t dec_attn_tree_workspace_bytes(const dec_tree_config* cfg, const dec_kv_cache* cache);
+
+/*
+ *   cfg, cache   host structs, read during the call.  The cache's dtype is cfg's, or E4M3.
+ *   q            device, dtype [T] rows of q_heads * head_dim, 16-byte aligned.
+ *   block_table  device, int32 [B] rows of max_pages page indexes, as for dec_attn_paged.
+ *   lens         device, int32 [B], n .. max_pages * page_size; together, times q_heads, below 2^39.
+ *   starts       device, int32 [B + 1], ascending, 0 .. T; 0 .. 64 tokens each.  A sequence
+ *                without drafted tokens costs nothing (its lens is not read).
+ *   mask         device, uint64 [T], or NULL (chains).  Bits from n on are ignored.
+ *   B            0 .. 2^24 (more: UNSUPPORTED); 0 is a no-op.
+ *   T            rows of q, out, mask and lse; 0 is a no-op.
+ *   out          device output, dtype, rows ldo apart, 16-byte aligned.  Rows before
+ *                starts[0] and from starts[B] on (padding) are left as they were.
+ *   lse          device output, float [T][q_heads], or NULL.
+ *   workspace    device, 16-byte aligned, ws_bytes >= dec_attn_tree_workspace_bytes(cfg, cache).
+ * Equal inputs give equal bits.  A sequence whose starts or lens are out of range is left out (its
+ * rows stay as they were), and a page index outside the cache leaves its tokens out; both record
+ * W4A16_ERR_INVALID_ARG in the status word.  A wait inside the kernel that runs out records
+ * W4A16_ERR_DEVICE_TIMEOUT; the results are then undefined.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dec_attn_tree(const dec_tree_config* cfg, const dec_kv_cache* cache, const void* q,
+                  const int32_t* block_table, const int32_t* lens, const int32_t* starts,
+                  const uint64_t* mask, int B, int T, void* out, float* lse, void* workspace,
+                  size_t ws_bytes, void* stream);
+
+/* ---- log probabilities --------------------------------------------------------------------
+ *
+ * For row t of logits x, with z[t, i] = factor[t] * x[t, i]:
+ *     lse[t]          = log sum_i exp(z[t, i])
+ *     logprobs[t, c]  = z[t, ids[t, c]] - lse[t]
+ *     entropy[t]      = lse[t] - sum_i p_i z[t, i],   p_i = exp(z[t, i] - lse[t])
+ *     top_ids[t, 0 .. top-1]   the tokens of the row's largest logits x, in descending order, the
+ *                              lowest index first among equals (-0 equals 0)
+ *     top_logprobs[t, c]       = z[t, top_ids[t, c]] - lse[t]
+ * all in fp32 or more.  A logit of -infinity (a token that is masked out) has probability 0 and adds
+ * nothing; in a row of nothing else lse and all log probabilities are -infinity and the entropy
+ * is 0.  With a logit of +infinity lse is +infinity, finite logits' log probabilities are -infinity and
+ * the infinite ones' and the entropy NaN; with a NaN all three are NaN.  Among the largest logits NaN
+ * counts as larger than any number.
+ */
+typedef enum dec_logits_dtype {
+    DEC_LOGITS_FP16 = 0,
+    DEC_LOGITS_BF16 = 1,
+    DEC_LOGITS_FP32 = 2
+} dec_logits_dtype;
+
+typedef struct dec_logprob_config {
+    int vocab;           /* logits of a row, 1 .. 2^24                                      */
+    int dtype;           /* dec_logits_dtype                                                */
+    int n_ids;           /* given tokens of a row, 0 .. 65536                               */
+    int top;             /* largest logits of a row, 0 .. min(32, vocab)                    */
+    int64_t ld;          /* row stride of the logits in elements; 0 = vocab, else at least that */
+} dec_logprob_config;
+
+/*
+ *   cfg           host struct, read during the call.
+ *   logits        device, T rows, aligned to their element.  Any stride and length; rows whose
+ *                 first elements are 16-byte aligned alike take no slow beginning.
+ *   factor        device, float [T], 1 / temperature, or NULL (all 1).  One that is not positive and finite
+ *                 gives NaN in the row's lse, entropy and log probabilities.
+ *   ids           device, int32 [T][n_ids]; NULL only if n_ids is 0.  A negative one stands for no
+ *                 token: its log probability is written as 0.  One of vocab or more gives NaN and
+ *                 records W4A16_ERR_INVALID_ARG in the status word.
+ *   T             0 is a no-op.
+ *   logprobs      device output, float [T][n_ids]; NULL only if n_ids is 0.
+ *   lse, entropy  device output, float [T], or NULL.
+ *   top_ids       device output, int32 [T][top]; NULL only if top is 0.
+ *   top_logprobs  device output, float [T][top], or NULL.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, vocab, n_ids, top), CUDA.
+ */
+int dec_token_logprobs(const dec_logprob_config* cfg, const void* logits, const float* factor,
+                       const int32_t* ids, int T, float* logprobs, float* lse, float* entropy,
+                       int32_t* top_ids, float* top_logprobs, void* stream);
+
+/* ---- cached tokens to other slots ------------------------------------------------------------
+ *
+ * Copies the keys and values of all heads in slot src[i] to slot dst[i] (slots numbered page *
+ * page_size + slot, as in dec_rope_append) for the moves i of group b, starts[b] <= i <
+ * starts[b+1], one after another in their order: a slot that an earlier move of the group wrote
+ * is read as written, and of two moves to one slot the later stands.  Groups (one per sequence)
+ * run at the same time and may not touch one another's slots.  To keep the path i0 < i1 < ... of
+ * a tree cached from slot(ctx) on, move slot(ctx + ij) to slot(ctx + j) for every j.
+ *   cache     host struct, read during the call.
+ *   src, dst  device, int64 [N].  A negative one stands for no move; one outside the cache moves
+ *             nothing and records W4A16_ERR_INVALID_ARG in the status word.
+ *   starts    device, int32 [B + 1], ascending, 0 .. N; a group that is out of range moves nothing
+ *             and records W4A16_ERR_INVALID_ARG.
+ *   B         groups, 0 is a no-op.
+ *   N         0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dec_kv_move(const dec_kv_cache* cache, const int64_t* src, const int64_t* dst,
+                const int32_t* starts, int B, int N, void* stream);
 
 #ifdef __cplusplus
 }

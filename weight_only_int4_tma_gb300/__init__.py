@@ -47,6 +47,10 @@ DEC_KV_FP16 = 0
 DEC_KV_BF16 = 1
 DEC_KV_E4M3 = 2
 
+DEC_LOGITS_FP16 = 0
+DEC_LOGITS_BF16 = 1
+DEC_LOGITS_FP32 = 2
+
 DEC_ROPE_HALF = 0
 DEC_ROPE_INTERLEAVED = 1
 
@@ -105,6 +109,19 @@ class AttnConfig(ctypes.Structure):
     _fields_ = [("q_heads", ctypes.c_int), ("dtype", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("window", ctypes.c_int), ("scale", ctypes.c_float), ("reserved", ctypes.c_int),
                 ("ldq", ctypes.c_int64), ("ldo", ctypes.c_int64), ("ld_table", ctypes.c_int64)]
+
+
+class TreeConfig(ctypes.Structure):
+    """dec_tree_config (tree_config() fills it)."""
+    _fields_ = [("q_heads", ctypes.c_int), ("dtype", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float),
+                ("ldq", ctypes.c_int64), ("ldo", ctypes.c_int64), ("ld_table", ctypes.c_int64)]
+
+
+class LogprobConfig(ctypes.Structure):
+    """dec_logprob_config (logprob_config() fills it)."""
+    _fields_ = [("vocab", ctypes.c_int), ("dtype", ctypes.c_int), ("n_ids", ctypes.c_int),
+                ("top", ctypes.c_int), ("ld", ctypes.c_int64)]
 
 
 def lib() -> ctypes.CDLL:
@@ -178,6 +195,17 @@ def lib() -> ctypes.CDLL:
             L.dec_attn_paged.argtypes = [ctypes.POINTER(AttnConfig), ctypes.POINTER(KvCache),
                                          P, P, P, I, P, P, P, Z, P]
             L.dec_attn_paged.restype = I
+            L.dec_attn_tree_workspace_bytes.argtypes = [ctypes.POINTER(TreeConfig),
+                                                        ctypes.POINTER(KvCache)]
+            L.dec_attn_tree_workspace_bytes.restype = Z
+            L.dec_attn_tree.argtypes = [ctypes.POINTER(TreeConfig), ctypes.POINTER(KvCache),
+                                        P, P, P, P, P, I, I, P, P, P, Z, P]
+            L.dec_attn_tree.restype = I
+            L.dec_token_logprobs.argtypes = [ctypes.POINTER(LogprobConfig), P, P, P, I, P, P, P,
+                                             P, P, P]
+            L.dec_token_logprobs.restype = I
+            L.dec_kv_move.argtypes = [ctypes.POINTER(KvCache), P, P, P, I, I, P]
+            L.dec_kv_move.restype = I
             _lib = L
     return _lib
 
@@ -399,6 +427,31 @@ def dec_attn_paged(cfg: AttnConfig, cache: KvCache, q, block_table, lens, B: int
            "dec_attn_paged")
 
 
+def dec_attn_tree_workspace_bytes(cfg: TreeConfig, cache: KvCache) -> int:
+    return int(lib().dec_attn_tree_workspace_bytes(cfg, cache))
+
+
+def dec_attn_tree(cfg: TreeConfig, cache: KvCache, q, block_table, lens, starts, mask, B: int,
+                  T: int, out, lse, workspace, ws_bytes: int | None = None, stream=None) -> None:
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().dec_attn_tree(cfg, cache, _ptr(q), _ptr(block_table), _ptr(lens), _ptr(starts),
+                               _ptr(mask), B, T, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                               _stream(stream)), "dec_attn_tree")
+
+
+def dec_token_logprobs(cfg: LogprobConfig, logits, factor, ids, T: int, logprobs, lse, entropy,
+                       top_ids=None, top_logprobs=None, stream=None) -> None:
+    _check(lib().dec_token_logprobs(cfg, _ptr(logits), _ptr(factor), _ptr(ids), T,
+                                    _ptr(logprobs), _ptr(lse), _ptr(entropy), _ptr(top_ids),
+                                    _ptr(top_logprobs), _stream(stream)), "dec_token_logprobs")
+
+
+def dec_kv_move(cache: KvCache, src, dst, starts, B: int, N: int, stream=None) -> None:
+    _check(lib().dec_kv_move(cache, _ptr(src), _ptr(dst), _ptr(starts), B, N, _stream(stream)),
+           "dec_kv_move")
+
+
 # ---- torch-friendly helpers (allocation + the calls above) ---------------------------
 
 def repack(qweight, scales, qzeros, N: int, K: int, group: int, dtype: int,
@@ -476,3 +529,36 @@ def attn_workspace(cfg: AttnConfig, cache: KvCache, device="cuda"):
     if nbytes == 0:
         raise W4A16Error(W4A16_ERR_UNSUPPORTED, "dec_attn_workspace_bytes")
     return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def tree_config(q_heads: int, dtype: int, scale: float, max_pages: int, *, window: int = 0,
+                sinks: int = 0, ldq: int = 0, ldo: int = 0, ld_table: int = 0) -> TreeConfig:
+    """dec_attn_tree's settings."""
+    return TreeConfig(q_heads, dtype, max_pages, window, sinks, scale, ldq, ldo, ld_table)
+
+
+def tree_workspace(cfg: TreeConfig, cache: KvCache, device="cuda"):
+    """A workspace for dec_attn_tree (a uint8 tensor)."""
+    import torch
+    nbytes = dec_attn_tree_workspace_bytes(cfg, cache)
+    if nbytes == 0:
+        raise W4A16Error(W4A16_ERR_UNSUPPORTED, "dec_attn_tree_workspace_bytes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def tree_mask(parents) -> list[int]:
+    """The mask words of one sequence's drafted tokens from their parents: parents[i] < i is the
+    number of token i's parent, or -1 for a root (which follows the cached context).  As signed
+    64-bit numbers, for a torch.int64 tensor."""
+    words = []
+    for i, p in enumerate(parents):
+        if not -1 <= p < i or i >= 64:
+            raise W4A16Error(W4A16_ERR_INVALID_ARG, "tree_mask")
+        words.append((words[p] if p >= 0 else 0) | 1 << i)
+    return [w - (1 << 64) if w >> 63 else w for w in words]
+
+
+def logprob_config(vocab: int, dtype: int, *, n_ids: int = 1, top: int = 0,
+                   ld: int = 0) -> LogprobConfig:
+    """dec_token_logprobs' settings."""
+    return LogprobConfig(vocab, dtype, n_ids, top, ld)

@@ -612,6 +612,22 @@ int check_attn(const dec_attn_config* cfg, const dec_kv_cache* cache) {
         return W4A16_ERR_UNSUPPORTED;
     return W4A16_OK;
 }
+
+int check_tree(const dec_tree_config* cfg, const dec_kv_cache* cache) {
+    if (!cfg || !cache) return W4A16_ERR_INVALID_ARG;
+    int rc = check_cache(cache);
+    if (rc != W4A16_OK) return rc;
+    if (!dtype_ok(cfg->dtype) || (cache->dtype != DEC_KV_E4M3 && cache->dtype != cfg->dtype))
+        return W4A16_ERR_UNSUPPORTED;
+    if (cfg->q_heads < 1 || cfg->q_heads % cache->kv_heads != 0 || cfg->max_pages < 1 ||
+        cfg->window < 0 || cfg->sinks < 0 || !std::isfinite(cfg->scale))
+        return W4A16_ERR_INVALID_ARG;
+    // token numbers are 32-bit, with room for steps past the end; so are rows of 64 tokens' heads
+    if (static_cast<int64_t>(cfg->max_pages) * cache->page_size > 0x7FFF0000LL ||
+        cfg->q_heads > (1 << 20))
+        return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
 }  // namespace
 
 int dec_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
@@ -782,6 +798,121 @@ int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const 
     a.timeout_ns = ctx->timeout_ns;
     a.status = ctx->status;
     return launch_attn(*ctx, a, cfg->dtype, e4m3, static_cast<cudaStream_t>(stream));
+}
+
+size_t dec_attn_tree_workspace_bytes(const dec_tree_config* cfg, const dec_kv_cache* cache) {
+    if (check_tree(cfg, cache) != W4A16_OK) return 0;
+    const DeviceCtx* ctx = nullptr;
+    if (get_ctx(&ctx) != W4A16_OK) return 0;
+    return tree_workspace_bytes(*ctx, cache->head_dim);
+}
+
+int dec_attn_tree(const dec_tree_config* cfg, const dec_kv_cache* cache, const void* q,
+                  const int32_t* block_table, const int32_t* lens, const int32_t* starts,
+                  const uint64_t* mask, int B, int T, void* out, float* lse, void* workspace,
+                  size_t ws_bytes, void* stream) {
+    int rc = check_tree(cfg, cache);
+    if (rc != W4A16_OK) return rc;
+    if (B < 0 || T < 0) return W4A16_ERR_INVALID_ARG;
+    if (B > (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+    TreeArgs a{};
+    const int64_t nq = static_cast<int64_t>(cfg->q_heads) * cache->head_dim;
+    a.ldq = cfg->ldq, a.ldo = cfg->ldo;
+    if ((rc = resolve_ld(&a.ldq, nq)) || (rc = resolve_ld(&a.ldo, nq))) return rc;
+    a.ld_table = cfg->ld_table ? cfg->ld_table : cfg->max_pages;
+    if (a.ld_table < cfg->max_pages) return W4A16_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return W4A16_OK;
+    if (!q || !block_table || !lens || !starts || !out || !workspace) return W4A16_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
+        !aligned(starts, 4) || !aligned(mask, 8) || !aligned(lse, 4) || !aligned(workspace, 16))
+        return W4A16_ERR_INVALID_ARG;
+    const DeviceCtx* ctx = nullptr;
+    if ((rc = get_ctx(&ctx)) != W4A16_OK) return rc;
+    if (ws_bytes < tree_workspace_bytes(*ctx, cache->head_dim)) return W4A16_ERR_INVALID_ARG;
+    a.q = static_cast<const uint16_t*>(q);
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.block_table = block_table;
+    a.lens = lens;
+    a.starts = starts;
+    a.mask = mask;
+    a.kc = key_view(*cache);
+    a.vc = value_view(*cache);
+    a.scale = cfg->scale;
+    a.B = B;
+    a.T = T;
+    a.q_heads = cfg->q_heads;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.page_size = cache->page_size;
+    a.num_pages = cache->num_pages;
+    a.max_pages = cfg->max_pages;
+    a.window = cfg->window;
+    a.sinks = cfg->sinks;
+    a.workspace = workspace;
+    a.timeout_ns = ctx->timeout_ns;
+    a.status = ctx->status;
+    return launch_tree(*ctx, a, cfg->dtype, cache->dtype == DEC_KV_E4M3,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int dec_token_logprobs(const dec_logprob_config* cfg, const void* logits, const float* factor,
+                       const int32_t* ids, int T, float* logprobs, float* lse, float* entropy,
+                       int32_t* top_ids, float* top_logprobs, void* stream) {
+    if (!cfg || T < 0 || cfg->vocab < 1 || cfg->n_ids < 0 || cfg->top < 0 || cfg->ld < 0)
+        return W4A16_ERR_INVALID_ARG;
+    if (cfg->dtype < DEC_LOGITS_FP16 || cfg->dtype > DEC_LOGITS_FP32 || cfg->vocab > (1 << 24) ||
+        cfg->n_ids > 65536 || cfg->top > 32)
+        return W4A16_ERR_UNSUPPORTED;
+    LogprobArgs a{};
+    a.ld = cfg->ld ? cfg->ld : cfg->vocab;
+    if (a.ld < cfg->vocab || cfg->top > cfg->vocab) return W4A16_ERR_INVALID_ARG;
+    if (T == 0) return W4A16_OK;
+    if (!logits || (cfg->n_ids && (!ids || !logprobs)) || (cfg->top && !top_ids))
+        return W4A16_ERR_INVALID_ARG;
+    if (!aligned(logits, cfg->dtype == DEC_LOGITS_FP32 ? 4 : 2) || !aligned(factor, 4) ||
+        !aligned(ids, 4) || !aligned(logprobs, 4) || !aligned(lse, 4) || !aligned(entropy, 4) ||
+        !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+        return W4A16_ERR_INVALID_ARG;
+    const DeviceCtx* ctx = nullptr;
+    const int rc = get_ctx(&ctx);
+    if (rc != W4A16_OK) return rc;
+    a.x = logits;
+    a.factor = factor;
+    a.ids = ids;
+    a.logprobs = logprobs;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = cfg->top ? top_logprobs : nullptr;
+    a.T = T;
+    a.V = cfg->vocab;
+    a.n_ids = cfg->n_ids;
+    a.top = cfg->top;
+    a.status = ctx->status;
+    return launch_logprob(*ctx, a, cfg->dtype, static_cast<cudaStream_t>(stream));
+}
+
+int dec_kv_move(const dec_kv_cache* cache, const int64_t* src, const int64_t* dst,
+                const int32_t* starts, int B, int N, void* stream) {
+    if (!cache || B < 0 || N < 0) return W4A16_ERR_INVALID_ARG;
+    int rc = check_cache(cache);
+    if (rc != W4A16_OK) return rc;
+    if (cache->kv_heads > (1 << 20)) return W4A16_ERR_UNSUPPORTED;
+    if (B == 0 || N == 0) return W4A16_OK;
+    if (!src || !dst || !starts || !aligned(src, 8) || !aligned(dst, 8) || !aligned(starts, 4))
+        return W4A16_ERR_INVALID_ARG;
+    const DeviceCtx* ctx = nullptr;
+    if ((rc = get_ctx(&ctx)) != W4A16_OK) return rc;
+    const int es = cache->dtype == DEC_KV_E4M3 ? 1 : 2;
+    auto in_bytes = [&](KvView v) {
+        v.page_stride *= es, v.slot_stride *= es, v.head_stride *= es;
+        return v;
+    };
+    const MoveArgs a{in_bytes(key_view(*cache)), in_bytes(value_view(*cache)), src, dst, starts,
+                     static_cast<int64_t>(cache->num_pages) * cache->page_size, B, N,
+                     cache->kv_heads, cache->page_size, cache->head_dim * es / 16, ctx->status};
+    return launch_move(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

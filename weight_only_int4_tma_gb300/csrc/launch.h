@@ -140,6 +140,47 @@ size_t attn_workspace_bytes(const DeviceCtx& ctx, int q_heads, int kv_heads, int
 int launch_attn(const DeviceCtx& ctx, const AttnArgs& a, int dtype, bool e4m3,
                 cudaStream_t stream);
 
+struct TreeArgs {
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;            // or null
+    const int32_t* block_table;
+    const int32_t* lens;
+    const int32_t* starts;
+    const uint64_t* mask;  // or null: chains
+    KvView kc, vc;
+    int64_t ldq, ldo, ld_table;
+    float scale;
+    int B, T, q_heads, kv_heads, head_dim, page_size, num_pages, max_pages, window, sinks;
+    void* workspace;
+    int* status;
+    uint64_t timeout_ns;   // limit of every bounded wait
+};
+size_t tree_workspace_bytes(const DeviceCtx& ctx, int head_dim);
+int launch_tree(const DeviceCtx& ctx, const TreeArgs& a, int dtype, bool e4m3, cudaStream_t stream);
+
+struct LogprobArgs {
+    const void* x;
+    const float* factor;  // or null
+    const int32_t* ids;
+    float *logprobs, *lse, *entropy, *top_logprobs;  // or null
+    int32_t* top_ids;
+    int64_t ld;
+    int T, V, n_ids, top;
+    int* status;
+};
+int launch_logprob(const DeviceCtx& ctx, const LogprobArgs& a, int dtype, cudaStream_t stream);
+
+struct MoveArgs {
+    KvView kc, vc;        // strides in bytes
+    const int64_t *src, *dst;
+    const int32_t* starts;
+    int64_t num_slots;
+    int B, N, kv_heads, page_size, row_chunks;  // row_chunks: 16-byte pieces of a head's row
+    int* status;
+};
+int launch_move(const MoveArgs& a, cudaStream_t stream);
+
 // Rows of A staged per 64-K chunk (8 or 16 for decode tiles, else the tile height).
 int tc_a_rows(int tile_m, int M);
 // 128-K weight blocks per ring stage (one bulk copy each stage).
