@@ -1,0 +1,1079 @@
+// Attention of drafted tokens over a paged key-value cache (include/decode.h).
+//
+// With G query heads per key-value head, n drafted tokens are G n rows that read the same keys and
+// values: 2 G n operations per byte of a 16-bit cache, 512 rows for 64 tokens of 8 heads.  The
+// kernel reads the cache once per item (up to 256 rows of one sequence and key-value head) and
+// multiplies on tcgen05 in tiles of 128 rows:
+//   S = Q K^T   128 rows x 128 tokens, fp32 in TMEM; both operands in shared memory, K-major;
+//   O += P V    P in TMEM, in the place of S; V in shared memory, its rows as they come from the
+//               cache: the MN-major operand.
+// (mma.sync, which dec_attn_paged uses for its few rows, would be short from some 40 rows on.)
+// Padding rows cost nothing while the cache streams from HBM: a step's S and P V take 1600 cycles of
+// the tensor pipe per tile, its 64 KB 2800 of the memory.
+//
+// P is carried as two 16-bit parts, each multiplied with V (a single rounding to bf16, 2^-9, would
+// show in the result as much as the result's own); a block of 16 tokens' S, 16 columns, holds both
+// parts of its P.  The softmax's state and all sums are fp32.
+//
+// Roles: two softmax warpgroups (a thread per row), one warp that issues the MMAs, eight
+// producer warps.  There are two streams of (S, O) in TMEM, one per warpgroup.  An item of more
+// than 128 rows has a stream per tile of 128; one of fewer gives its steps to the streams in
+// turn, whose sums are joined at its end.  While one stream's softmax runs the tensor pipe works on
+// the other's products.  (Heads of more than 128 values: one stream, whose S alternates between two
+// places; O alone takes half of TMEM.)
+//
+// Softmax.  A running reference m per row: weights are exp2(s - m); only when a score passes m by
+// more than 2^8 is O, in TMEM, scaled to a new reference.  Maxima carry NaN.
+//
+// Masks are applied to S by index (words of 32 tokens per row) in the steps that need them: the
+// drafted tokens' and those at the window's edges.  Values of such tokens that are infinite or NaN are
+// replaced by 0 in shared memory, as 0 times them would reach the rows that do not see them, and
+// added at the end to the rows that do.
+//
+// Work split.  All items of the batch stand in one line, each as long as its steps and
+// kTreeItemCost, cut in equal shares, one per CTA.  An item that is cut leaves (m, l, O) of each
+// part in fp32 in the workspace, and a second kernel joins the parts in their order.
+#pragma once
+#include "decode.cuh"
+
+namespace w4g {
+
+constexpr int kTreeItemCost = 1;   // of an item by itself, in steps
+constexpr float kTreeLag = 8.0f;   // scores may pass the reference by 2^8
+constexpr int kTreeRows = 128;     // of a tile: the MMA's M
+
+// Of the workspace: a TreePart per CTA, then two parts per CTA (an item begun by an earlier CTA, one left
+// to a later) of m[rows], l[rows], O[rows][dp], rows being 128 for each stream.
+struct TreePart {
+    int n;       // parts of the item that this CTA begins and another ends; 0: none
+    int row0;    // its first row in q and out is that of token row0 / G, head head0 + row0 % G
+    int rows, head0, first;
+    float vs;    // the values' scale
+    int pad[2];
+};
+__host__ __device__ constexpr size_t tree_part_floats(int rows, int dp) {
+    return static_cast<size_t>(rows) * (dp + 2);
+}
+constexpr int tree_dp(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+__host__ __device__ constexpr int tree_streams(int dp) { return dp <= 128 ? 2 : 1; }
+inline size_t tree_workspace(int ctas, int dp) {
+    return sizeof(TreePart) * ctas + 2ull * ctas * tree_part_floats(kTreeRows * tree_streams(dp), dp) * 4;
+}
+
+namespace {
+
+__device__ __forceinline__ float tree_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float tree_max(float a, float b) {  // NaN if either is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ void tree_copy16(uint32_t dst, const char* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void tree_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void tree_wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tree_store16(uint32_t dst, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+        "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+        "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+// D[tmem] (+)= A[smem] . B[smem]^T, kind::f16.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc),
+        "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The MN-major operand with 128-byte swizzle: atoms of 64 values (M or N) x 8 (K), 1024 bytes
+// apart along K and `block` bytes along M or N.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t block) {
+    return sw128_desc(saddr & 0x3FFFFu) & ~(0x3FFFull << 16) | static_cast<uint64_t>(block >> 4) << 16;
+}
+constexpr uint32_t kIdescBMajorMn = 1u << 16;
+
+// Zeros in the place of values that are infinite or NaN; true if there were any.  BF: bf16, else fp16.
+template <bool BF>
+__device__ __forceinline__ bool tree_scrub(uint4& v) {
+    constexpr uint32_t kExp = BF ? 0x7F80u : 0x7C00u;
+    uint32_t* w = &v.x;
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool lo = (w[e] & kExp) == kExp, hi = (w[e] >> 16 & kExp) == kExp;
+        if (lo) w[e] &= 0xFFFF0000u;
+        if (hi) w[e] &= 0x0000FFFFu;
+        any |= lo | hi;
+    }
+    return any;
+}
+// The same of E4M3, whose only such values are NaN, 0x7F and 0xFF.
+__device__ __forceinline__ bool tree_scrub_e4m3(uint4& v) {
+    uint32_t* w = &v.x;
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t nan = __vcmpeq4(w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        w[e] &= ~nan;
+        any |= nan != 0;
+    }
+    return any;
+}
+
+// DT: 0 fp16, 1 bf16 (queries, output).  E4M3: 8-bit cache.  DP: head dimension rounded up.
+template <int DT_, bool E4M3_, int DP_>
+struct TreeShape {
+    static constexpr int DT = DT_, DP = DP_;
+    static constexpr bool E4M3 = E4M3_;
+    static constexpr bool BF = DT == 1 && !E4M3;   // type of the MMA's operands
+    static constexpr int ES = E4M3 ? 1 : 2;
+    static constexpr int STREAMS = tree_streams(DP);
+    static constexpr int STEP = DP <= 128 ? 128 : 64;        // tokens of a step
+    static constexpr int ROWS = kTreeRows * STREAMS;         // of an item
+    static constexpr int BLOCKS = DP / 64;                   // 64-value blocks of a row
+    static constexpr int SLOT = STEP * DP * 2;               // bytes of a step's keys, or values
+    static constexpr int QTILE = kTreeRows * DP * 2;
+    static constexpr int NSLOT = DP == 64 ? 10 : 5;          // of the ring: 160 KB
+    static constexpr int PW = 8;                             // producer warps
+    static constexpr int SW = 4 * STREAMS;                   // softmax warps
+    static constexpr int THREADS = 32 * (SW + 1 + PW);
+    static constexpr int RW = STEP / PW;                     // token rows of a step per producer warp
+    static constexpr int CH = DP / 8;                        // 16-byte chunks of a row in shared memory
+    static constexpr int TM_O = 2 * STEP;                    // TMEM columns: S twice, then O of each stream
+    // Shared memory: TreeControl, the queries' tiles, the ring.  The tiles' 1024-byte alignment follows
+    // from the declared alignment of the dynamic part.
+    static constexpr int CONTROL = 3072;
+    static constexpr int SMEM = CONTROL + STREAMS * QTILE + NSLOT * SLOT;
+    static_assert(TM_O + STREAMS * DP <= 512, "TMEM");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(THREADS * 8 <= STREAMS * QTILE, "the prefix sums lie in the queries' place");
+};
+
+// The line's shares, the same in every CTA.
+struct TreeLine {
+    long long end, share;
+};
+
+template <class S>
+struct TreeControl {
+    uint64_t bars[2 * S::NSLOT + 9];
+    TreeLine line;
+    long long scan[S::THREADS / 32];
+    uint32_t tmem_base;
+    int abort_flag;
+    int bad_page;                                   // a page lay outside the cache: masks look again
+    int dirty;                                      // infinite values or NaN were replaced by 0
+    float2 stats[S::STREAMS][kTreeRows];            // (m, l) of the streams, at the end of an item
+    int8_t qe[S::STREAMS][kTreeRows];               // exponents of the rows' scaling of the queries
+};
+
+// A sequence as the kernel sees it.
+struct TreeSeq {
+    int first, n, len;     // rows first .. first + n - 1
+    int sink_tiles, tile0; // steps: tiles 0 .. sink_tiles - 1, then from tile0 on
+    int steps, row_tiles;  // row_tiles: items of a key-value head
+};
+template <class S>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
+    TreeSeq s{};
+    const int first = a.starts[b], last = a.starts[b + 1], len = a.lens[b];
+    if (first == last && first >= 0 && first <= a.T) return s;
+    const int n = last - first;
+    if (first < 0 || last < first || last > a.T || n > 64 || len < n || len > a.max_pages * a.page_size) {
+        if (report) record_status(a.status, kDecInvalidArg);
+        return s;
+    }
+    s.first = first, s.n = n, s.len = len;
+    const int lo = a.window > 0 ? max(0, len - n - a.window) : 0;  // a row without bits sees from here
+    s.sink_tiles = a.window > 0 ? (min(a.sinks, len) + S::STEP - 1) / S::STEP : 0;
+    s.tile0 = lo / S::STEP;
+    if (s.sink_tiles >= s.tile0) s.sink_tiles = s.tile0 = 0;
+    s.steps = s.sink_tiles + (len + S::STEP - 1) / S::STEP - s.tile0;
+    s.row_tiles = (n * (a.q_heads / a.kv_heads) + S::ROWS - 1) / S::ROWS;
+    return s;
+}
+
+// Steps [step, step_end) of an item as one CTA takes them.
+struct TreeSeg {
+    TreeSeq seq;
+    int b, item, step, step_end;
+    long long rest;   // what the CTA's share holds after this item
+};
+
+template <class S>
+__device__ __forceinline__ long long tree_items(const TreeArgs& a, const TreeSeq& s) {
+    return static_cast<long long>(s.row_tiles) * a.kv_heads;
+}
+
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {  // bits lo .. hi - 1 of 0 .. 31
+    lo = max(lo, 0), hi = min(hi, 32);
+    return lo < hi ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0;
+}
+
+// What one row sees of the tokens t0 .. t0 + 31.
+struct TreeRow {
+    uint64_t word;
+    int ctx, from, sinks;
+    __device__ __forceinline__ uint32_t seen(int t0) const {
+        uint32_t v = 0;
+        if (t0 < ctx) v = range_bits(from - t0, ctx - t0) | range_bits(-t0, min(sinks, ctx) - t0);
+        const int sh = t0 - ctx;
+        if (sh > -32 && sh < 64)
+            v |= static_cast<uint32_t>(sh >= 0 ? word >> sh : word << -sh);
+        return v;
+    }
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int page_shift) {
+    constexpr int STEP = S::STEP, DP = S::DP, STREAMS = S::STREAMS, NSLOT = S::NSLOT, SW = S::SW, PW = S::PW;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    static_assert(sizeof(TreeControl<S>) <= S::CONTROL, "the control block fits");
+    // the tiles begin at a multiple of 1024, the control block lies before or behind them
+    TreeControl<S>& ctl = *reinterpret_cast<TreeControl<S>*>(smem_raw);
+    TreeLine& line = ctl.line;
+    long long* prefix = reinterpret_cast<long long*>(smem_raw + S::CONTROL);  // until the queries come
+
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+    const int G = a.q_heads / a.kv_heads;
+    const uint32_t base = smem_addr(smem_raw) + S::CONTROL;
+    const uint32_t q_smem = base, ring = base + STREAMS * S::QTILE;
+    const uint32_t bar0 = smem_addr(ctl.bars);
+    const uint32_t full = bar0, empty = full + 8 * NSLOT, q_full = empty + 8 * NSLOT, q_empty = q_full + 8;
+    const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, o_free = o_full + 8;
+    const uint32_t pv_done = o_free + 8;
+    TreePart* heads = static_cast<TreePart*>(a.workspace);
+    float* parts = reinterpret_cast<float*>(heads + ctas);
+
+    // columns past the head dimension are never copied: zero, so that they add nothing
+    if (a.head_dim < DP)
+        for (uint32_t e = tid; e < (STREAMS * S::QTILE + NSLOT * S::SLOT) / 16; e += S::THREADS)
+            tree_store16(base + 16 * e, make_uint4(0, 0, 0, 0));
+    if (tid < NSLOT) {
+        mbar_init(full + 8 * tid, PW);
+        mbar_init(empty + 8 * tid, 1);
+    }
+    if (tid == 0) {
+        mbar_init(q_full, PW);
+        mbar_init(q_empty, 1 + SW);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(s_full + 8 * s, 2);  // the MMAs are done; what the producers noted can be seen
+            mbar_init(p_full + 8 * s, 4);
+        }
+        mbar_init(o_full, 2);
+        mbar_init(o_free, SW);
+        mbar_init(pv_done, 1);
+        fence_mbar_init();
+        ctl.abort_flag = ctl.bad_page = ctl.dirty = 0;
+    }
+    fence_proxy_async_smem();  // the zeros
+    grid_dep_wait();
+    grid_dep_launch();
+    if (warp == SW) {
+        tmem_alloc(smem_addr(&ctl.tmem_base), 512);
+        tmem_relinquish();
+    }
+
+    // ---- the line: prefix[t] is what lies before thread t's sequences ----
+    const int per_thread = (a.B + S::THREADS - 1) / S::THREADS;
+    {
+        const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
+        long long mine = 0;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const TreeSeq s = tree_seq<S>(a, b, cta == 0);
+            mine += tree_items<S>(a, s) * (s.steps + kTreeItemCost);
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) ctl.scan[warp] = incl;
+        __syncthreads();
+        long long total = 0;
+        for (int w = 0; w < S::THREADS / 32; ++w) {
+            if (w < warp) incl += ctl.scan[w];
+            total += ctl.scan[w];
+        }
+        prefix[tid] = incl - mine;
+        if (tid == 0) line = TreeLine{total, max((total + ctas - 1) / ctas, 1ll)};
+    }
+    if (tid == 0) heads[cta] = TreePart{};
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem_base;
+    const long long share_end = min(line.end, line.share * (cta + 1));
+
+    auto open_item = [&](TreeSeg& s, long long begin, long long from) {  // its steps at or after `from`
+        const long long at0 = begin + kTreeItemCost;
+        s.step = static_cast<int>(max(from - at0, 0ll));
+        s.step_end = static_cast<int>(min(static_cast<long long>(s.seq.steps), share_end - at0));
+        s.rest = share_end - at0 - s.seq.steps;
+    };
+    // The segment after s; false: there is none.
+    auto after = [&](TreeSeg& s) {
+        if (s.rest <= kTreeItemCost) return false;
+        if (++s.item == tree_items<S>(a, s.seq)) {
+            s.item = 0;
+            do {
+                s.seq = tree_seq<S>(a, ++s.b, false);
+            } while (s.seq.steps == 0 && s.b + 1 < a.B);
+        }
+        open_item(s, share_end - s.rest, 0);
+        return s.step < s.step_end;
+    };
+    // The first segment of the CTA's share; false: there is none.  By all lanes of a warp.
+    auto locate = [&](TreeSeg& s) {
+        const long long u = line.share * cta;
+        if (u >= line.end) return false;
+        int t = 0;
+        for (int t0 = 0; t0 < S::THREADS && t0 * per_thread < a.B; t0 += 32)
+            t += __popc(__ballot_sync(0xFFFFFFFFu, prefix[t0 + lane] <= u));
+        --t;
+        long long at = prefix[t];
+        s.b = t * per_thread;
+        s.seq = tree_seq<S>(a, s.b, false);
+        while (at + tree_items<S>(a, s.seq) * (s.seq.steps + kTreeItemCost) <= u && s.b + 1 < a.B) {
+            at += tree_items<S>(a, s.seq) * (s.seq.steps + kTreeItemCost);
+            s.seq = tree_seq<S>(a, ++s.b, false);
+        }
+        const long long per = s.seq.steps + kTreeItemCost;
+        s.item = static_cast<int>((u - at) / per);
+        open_item(s, at + s.item * per, u);
+        return s.step < s.step_end || after(s);
+    };
+    // Row tiles of an item are neighbours in the line, so that they find its tokens in L2.
+    auto head_of = [&](const TreeSeg& s) { return s.item / s.seq.row_tiles; };
+    auto row0_of = [&](const TreeSeg& s) { return s.item % s.seq.row_tiles * S::ROWS; };
+    auto rows_of = [&](const TreeSeg& s) { return min(S::ROWS, s.seq.n * G - row0_of(s)); };
+    auto tile_of = [&](const TreeSeq& s, int step) {
+        return step < s.sink_tiles ? step : s.tile0 + step - s.sink_tiles;
+    };
+    auto wait = [&](uint32_t bar, uint32_t phase) { mbar_wait_warp(bar, phase, &ctl.abort_flag, a.status, a.timeout_ns); };
+
+    TreeSeg seg{};
+    bool more = locate(seg);
+    // the prefix sums have been read; where they stood may be zeros that the queries need
+    __syncthreads();
+    if (a.head_dim < DP) {
+        for (uint32_t e = tid; e < (S::THREADS * 8 + 15) / 16; e += S::THREADS)
+            tree_store16(base + 16 * e, make_uint4(0, 0, 0, 0));
+        fence_proxy_async_smem();
+        __syncthreads();
+    }
+
+    if (warp > SW) {
+        // ================= producers =================
+        const int pw = warp - SW - 1;
+        constexpr int CH = S::CH, RW = S::RW;
+        const int row_chunks = a.head_dim / 8;        // of 16-bit values
+        auto page_of = [&](int tok) { return page_shift >= 0 ? tok >> page_shift : tok / a.page_size; };
+        // the shared-memory address of chunk c of row r, from a tile of `rows` rows
+        auto at_smem = [](int rows, int r, int c) {
+            return static_cast<uint32_t>((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        };
+        int slot = 0;
+        uint32_t phase = 0, q_phase = 0;
+        // slots whose copies are under way, the newest first
+        uint32_t pend[3] = {0, 0, 0};
+        auto signal = [&](uint32_t bar) {  // this warp's part of it is there
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        auto push = [&](uint32_t bar) {
+            tree_commit();
+            if (pend[2]) {
+                tree_wait_copies<3>();
+                signal(pend[2]);
+            }
+            pend[2] = pend[1], pend[1] = pend[0], pend[0] = bar;
+        };
+        auto flush = [&]() {
+            if (pend[2]) { tree_wait_copies<2>(); signal(pend[2]); }
+            if (pend[1]) { tree_wait_copies<1>(); signal(pend[1]); }
+            if (pend[0]) { tree_wait_copies<0>(); signal(pend[0]); }
+            pend[0] = pend[1] = pend[2] = 0;
+        };
+        // waits until a slot (or the queries' place) is free; what is under way is handed on first, as the
+        // consumers may need it to free anything
+        auto wait_free = [&](uint32_t bar, uint32_t ph) {
+            if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, ph))) return;
+            flush();
+            wait(bar, ph);
+        };
+        auto next_slot = [&]() {
+            if (++slot == NSLOT) slot = 0, phase ^= 1u;
+        };
+        while (more) {
+            const TreeSeq& sq = seg.seq;
+            const int ctx = sq.len - sq.n, kvh = head_of(seg);
+            const int32_t* table = a.block_table + seg.b * a.ld_table;
+            // the first token that the row with the fewest bits sees in the window
+            int lo = 0;
+            if (a.window > 0) {
+                int least = 1;
+                if (a.mask) {
+                    const uint64_t all = sq.n == 64 ? ~0ull : (1ull << sq.n) - 1;
+                    least = 64;
+                    for (int i = lane; i < sq.n; i += 32) least = min(least, __popcll(a.mask[sq.first + i] & all));
+                    least = __reduce_min_sync(0xFFFFFFFFu, least);
+                }
+                lo = max(0, min(ctx, ctx + least - a.window));
+            }
+            const int edge = a.window > 0 ? ctx + sq.n - a.window : 0;  // tokens from here on are in every window
+            auto token_of = [&](int step) { return tile_of(sq, step) * STEP + pw * RW + lane; };
+            auto wants = [&](int step, int tok) {
+                return step < seg.step_end && lane < RW && tok < sq.len && (tok >= lo || tok < a.sinks);
+            };
+            auto fetch = [&](int step) {  // the page of this lane's token
+                const int tok = token_of(step);
+                return wants(step, tok) ? table[page_of(tok)] : 0;
+            };
+            const char* kbase = static_cast<const char*>(a.kc.p) + kvh * a.kc.head_stride * S::ES;
+            const char* vbase = static_cast<const char*>(a.vc.p) + kvh * a.vc.head_stride * S::ES;
+            int pid = fetch(seg.step), pid1 = fetch(seg.step + 1);
+
+            // this lane's row of a step: where its key and value stand (-1: nowhere)
+            int64_t kat, vat;
+            uint32_t mixed;   // rows of this warp that not every query row sees
+            auto look = [&](int step) {
+                const int tok = token_of(step);
+                const bool wanted = wants(step, tok);
+                const bool ok = wanted && static_cast<unsigned>(pid) < static_cast<unsigned>(a.num_pages);
+                if (wanted && !ok) {
+                    record_status(a.status, kDecInvalidArg);
+                    *static_cast<volatile int*>(&ctl.bad_page) = 1;
+                }
+                const int64_t in_page = tok - page_of(tok) * a.page_size;
+                kat = ok ? (pid * a.kc.page_stride + in_page * a.kc.slot_stride) * S::ES : -1;
+                vat = ok ? (pid * a.vc.page_stride + in_page * a.vc.slot_stride) * S::ES : -1;
+                mixed = __ballot_sync(0xFFFFFFFFu, ok && (tok >= ctx || (tok < edge && tok >= a.sinks)));
+                pid = pid1;
+                pid1 = fetch(step + 2);
+            };
+            // one side of a step by asynchronous copies
+            auto copy = [&](uint32_t dst, const char* from, int64_t at) {
+                constexpr int RPI = 32 / CH;
+                const int c = lane % CH, sub = lane / CH;
+#pragma unroll
+                for (int r0 = 0; r0 < RW; r0 += RPI) {
+                    const int64_t off = __shfl_sync(0xFFFFFFFFu, at, r0 + sub);
+                    const int r = pw * RW + r0 + sub;
+                    if (c < row_chunks)
+                        tree_copy16(dst + at_smem(STEP, r, c), off >= 0 ? from + off + 16 * c : from, off >= 0 ? 16 : 0);
+                }
+            };
+            // the same through registers, with values that some row must not see made finite
+            constexpr int FC = DP * S::ES / 16;            // chunks of a row in the cache
+            constexpr int LR = 32 / FC > 0 ? 32 / FC : 1;  // rows of one load of the warp
+            constexpr int LN = RW / LR;                    // loads
+            auto load = [&](uint4 (&v)[LN], const char* from, int64_t at) {
+                const int c = lane % FC, sub = lane / FC;
+#pragma unroll
+                for (int x = 0; x < LN; ++x) {
+                    const int64_t off = __shfl_sync(0xFFFFFFFFu, at, x * LR + sub);
+                    v[x] = make_uint4(0, 0, 0, 0);
+                    if (off >= 0 && 16 * c < a.head_dim * S::ES) v[x] = __ldg(reinterpret_cast<const uint4*>(from + off) + c);
+                }
+            };
+            auto store = [&](uint32_t dst, uint4 (&v)[LN], uint32_t some) {
+                const int c = lane % FC, sub = lane / FC;
+#pragma unroll
+                for (int x = 0; x < LN; ++x) {
+                    const int r = pw * RW + x * LR + sub;
+                    if ((some >> (x * LR + sub)) & 1u) {
+                        bool any;
+                        if constexpr (S::E4M3) any = tree_scrub_e4m3(v[x]);
+                        else any = tree_scrub<S::BF>(v[x]);
+                        if (any) *static_cast<volatile int*>(&ctl.dirty) = 1;
+                    }
+                    if constexpr (S::E4M3) {
+                        if (2 * c >= row_chunks) continue;
+                        const uint32_t* w = &v[x].x;
+                        uint32_t h[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            h[2 * e] = dec_e4m3x2_to_f16x2(w[e]);
+                            h[2 * e + 1] = dec_e4m3x2_to_f16x2(w[e] >> 16);
+                        }
+                        tree_store16(dst + at_smem(STEP, r, 2 * c), make_uint4(h[0], h[1], h[2], h[3]));
+                        tree_store16(dst + at_smem(STEP, r, 2 * c + 1), make_uint4(h[4], h[5], h[6], h[7]));
+                    } else if (c < row_chunks) {
+                        tree_store16(dst + at_smem(STEP, r, c), v[x]);
+                    }
+                }
+            };
+            auto load_queries = [&]() {
+                // f = |scale k_scale|; a negative or zero product is folded into the queries
+                const float f = a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f);
+                const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu, flip = f < 0.0f ? 0x80008000u : 0u;
+                const int row0 = row0_of(seg), rows = rows_of(seg), tiles = rows > kTreeRows ? 2 : 1;
+                constexpr int RPI = 32 / CH;
+                const int c = lane % CH, sub = lane / CH;
+                wait_free(q_empty, q_phase ^ 1u);
+                q_phase ^= 1u;
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t dst = q_smem + t * S::QTILE;
+                    constexpr int PER = kTreeRows / PW, AT = 4 * RPI < PER ? 4 * RPI : PER;
+                    for (int r0 = pw * PER; r0 < (pw + 1) * PER; r0 += AT) {
+                        uint4 v[AT / RPI];
+#pragma unroll
+                        for (int x = 0; x < AT / RPI; ++x) {
+                            const int r = r0 + x * RPI + sub, row = row0 + t * kTreeRows + r;
+                            v[x] = make_uint4(0, 0, 0, 0);
+                            if (t * kTreeRows + r < rows && c < row_chunks) {
+                                const int i = row / G, h = row - i * G;
+                                v[x] = *(reinterpret_cast<const uint4*>(
+                                    a.q + static_cast<int64_t>(sq.first + i) * a.ldq +
+                                    static_cast<int64_t>(kvh * G + h) * a.head_dim) + c);
+                            }
+                        }
+#pragma unroll
+                        for (int x = 0; x < AT / RPI; ++x) {
+                            const int r = r0 + x * RPI + sub;
+                            uint32_t* w = &v[x].x;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ flip;
+                            // bf16 queries against an 8-bit cache, whose MMA is fp16: scaled by a power of two
+                            // that brings the row's largest to 2^8 .. 2^9
+                            int exponent = 0;
+                            if constexpr (S::E4M3 && S::DT == 1) {
+                                uint32_t top = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+#pragma unroll
+                                for (int d = CH / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                                const int e2 = min(static_cast<int>(top >> 7) - 127, 127);
+                                if (e2 > -119) exponent = e2 - 8;
+                                const float up = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = dec_pack2<0>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                            }
+                            if (c < row_chunks) tree_store16(dst + at_smem(kTreeRows, r, c), v[x]);
+                            if (S::E4M3 && S::DT == 1 && c == 0) ctl.qe[t][r] = static_cast<int8_t>(exponent);
+                        }
+                    }
+                }
+                signal(q_full);
+            };
+
+            if constexpr (S::E4M3) {
+                uint4 k[LN], v[LN];
+                look(seg.step);
+                load(k, kbase, kat);
+                load(v, vbase, vat);
+                uint32_t some = mixed;
+                for (int st = seg.step; st < seg.step_end; ++st) {
+                    const bool again = st + 1 < seg.step_end;
+                    if (again) look(st + 1);
+                    wait_free(empty + 8 * slot, phase ^ 1u);
+                    store(ring + slot * S::SLOT, k, 0u);
+                    signal(full + 8 * slot);
+                    next_slot();
+                    if (again) load(k, kbase, kat);
+                    wait_free(empty + 8 * slot, phase ^ 1u);
+                    store(ring + slot * S::SLOT, v, some);
+                    signal(full + 8 * slot);
+                    next_slot();
+                    if (again) load(v, vbase, vat);
+                    some = mixed;
+                    if (st == seg.step) load_queries();
+                }
+            } else {
+                for (int st = seg.step; st < seg.step_end; ++st) {
+                    look(st);
+                    wait_free(empty + 8 * slot, phase ^ 1u);
+                    copy(ring + slot * S::SLOT, kbase, kat);
+                    push(full + 8 * slot);
+                    next_slot();
+                    wait_free(empty + 8 * slot, phase ^ 1u);
+                    if (mixed) {
+                        uint4 v[LN];
+                        load(v, vbase, vat);
+                        store(ring + slot * S::SLOT, v, mixed);
+                        signal(full + 8 * slot);
+                    } else {
+                        copy(ring + slot * S::SLOT, vbase, vat);
+                        push(full + 8 * slot);
+                    }
+                    next_slot();
+                    if (st == seg.step) load_queries();
+                }
+            }
+            more = after(seg);
+        }
+        flush();
+    } else if (warp == SW) {
+        // ================= the MMAs =================
+        constexpr int TYPE = S::BF ? 1 : 0;
+        constexpr uint32_t idesc_s = idesc_f16(TYPE, 128, STEP), idesc_o = idesc_f16(TYPE, 128, DP) | kIdescBMajorMn;
+        int slot = 0;                       // of the ring, in the order in which the producers fill it
+        uint32_t q_phase = 0, free_phase = 0;
+        uint32_t job = 0;                   // of the CTA: S buffer job & 1
+        uint32_t ring_phase = 0;
+        uint32_t p_phase = 0;               // bit s: of p_full[s]
+        // the job whose P V is still to be issued
+        bool open = false, p_fresh = false, p_last = false, p_begins = false;
+        int p_slot = 0, p_buf = 0;
+        uint32_t p_ring_phase = 0;
+        bool p_frees = false;
+        auto issue_pv = [&]() {
+            wait(p_full + 8 * p_buf, (p_phase >> p_buf) & 1u);
+            p_phase ^= 1u << p_buf;
+            wait(full + 8 * p_slot, p_ring_phase);
+            if (p_begins) {  // the previous item's sums have been read
+                wait(o_free, free_phase ^ 1u);
+                free_phase ^= 1u;
+            }
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t d = tmem + S::TM_O + (STREAMS == 2 ? p_buf : 0) * DP;
+                const uint32_t p = tmem + p_buf * STEP;
+                const uint32_t v = ring + p_slot * S::SLOT;
+#pragma unroll
+                for (int kb = 0; kb < STEP / 16; ++kb) {
+                    const uint64_t desc = sw128_desc_mn(v + kb * 2048, STEP * 128);
+                    tc_mma_ts(d, p + 16 * kb, desc, idesc_o, kb > 0 || !p_fresh);
+                    tc_mma_ts(d, p + 16 * kb + 8, desc, idesc_o, 1);
+                }
+                if (p_frees) tc_commit(empty + 8 * p_slot);
+                if (STREAMS == 1) tc_commit(pv_done);
+                if (p_last) {
+                    tc_commit(o_full);
+                    mbar_arrive(o_full);
+                }
+            }
+            __syncwarp();
+            open = false;
+        };
+        while (more) {
+            const int rows = rows_of(seg);
+            const bool dual = rows > kTreeRows;
+            const int steps = seg.step_end - seg.step, jobs = dual ? 2 * steps : steps;
+            int k_slot = slot;
+            uint32_t k_phase = ring_phase;
+            for (int j = 0; j < jobs; ++j, ++job) {
+                const int buf = job & 1;
+                if (j == 0) {
+                    wait(q_full, q_phase);
+                    q_phase ^= 1u;
+                }
+                const bool second = dual && (j & 1);
+                if (!second) {
+                    k_slot = slot, k_phase = ring_phase;
+                    if (++slot == NSLOT) slot = 0, ring_phase ^= 1u;
+                }
+                wait(full + 8 * k_slot, k_phase);
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t q = q_smem + (second ? S::QTILE : 0), k = ring + k_slot * S::SLOT;
+#pragma unroll
+                    for (int c = 0; c < DP / 16; ++c)
+                        tc_mma_ss(tmem + buf * STEP, sw128_desc(q + (c >> 2) * kTreeRows * 128 + (c & 3) * 32),
+                                  sw128_desc(k + (c >> 2) * STEP * 128 + (c & 3) * 32), idesc_s, c > 0);
+                    tc_commit(s_full + 8 * buf);
+                    mbar_arrive(s_full + 8 * buf);
+                    if (!dual || second) tc_commit(empty + 8 * k_slot);
+                    if (j == jobs - 1) tc_commit(q_empty);
+                }
+                __syncwarp();
+                if (open) issue_pv();
+                open = true;
+                p_buf = buf;
+                p_begins = j == 0;
+                // the first of its stream: it begins the sums
+                p_fresh = STREAMS == 2 ? j < 2 : j == 0;
+                p_last = j == jobs - 1;
+                p_frees = !dual || second;
+                if (!second) {
+                    p_slot = slot, p_ring_phase = ring_phase;
+                    if (++slot == NSLOT) slot = 0, ring_phase ^= 1u;
+                }
+            }
+            more = after(seg);
+        }
+        if (open) issue_pv();
+    } else {
+        // ================= softmax =================
+        constexpr float kShift = S::BF ? 0.0f : 7.0f;  // fp16 weights are scaled by 2^7
+        const int stream = warp >> 2;
+        const int r = tid & (kTreeRows - 1);
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's lanes of TMEM
+        uint32_t s_phase = 0, o_phase = 0, job = 0, pv_jobs = 0;
+        while (more) {
+            const TreeSeq& sq = seg.seq;
+            const int kvh = head_of(seg), row0 = row0_of(seg), rows = rows_of(seg);
+            const bool dual = rows > kTreeRows;
+            const int steps = seg.step_end - seg.step, jobs = dual ? 2 * steps : steps;
+            const uint32_t job0 = job;
+            job += jobs;
+            const int ctx = sq.len - sq.n;
+            // dual: the stream's tile alternates with the number of jobs before
+            const int tile = dual ? (stream ^ (job0 & 1)) : 0;
+            const int in_item = tile * kTreeRows + r;
+            const bool live = in_item < rows;
+            const int row = row0 + in_item, i = live ? row / G : 0, head = kvh * G + (live ? row - i * G : 0);
+            TreeRow see{0, ctx, 0, a.window > 0 ? a.sinks : 0};
+            if (live) {
+                const uint64_t all = sq.n == 64 ? ~0ull : (1ull << sq.n) - 1;
+                see.word = (a.mask ? a.mask[sq.first + i] : ~0ull >> (63 - i)) & all;
+                if (a.window > 0) see.from = max(0, ctx + __popcll(see.word) - a.window);
+            }
+            const int edge = a.window > 0 ? ctx + sq.n - a.window : 0;
+            const int32_t* table = a.block_table + seg.b * a.ld_table;
+            const float fabs_scale = fabsf(a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f));
+            float f = (fabs_scale == 0.0f ? 1.0f : fabs_scale) * 1.4426950408889634f;
+            float m = -INFINITY, ref = 0.0f, l = 0.0f;
+            bool first = true;
+            // jobs of this stream
+            const int j0 = STREAMS == 2 ? (stream ^ (job0 & 1)) : 0;
+            constexpr int JS = STREAMS;
+            if (j0 >= jobs) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_empty);
+            }
+            for (int j = j0; j < jobs; j += JS) {
+                const int buf = (job0 + j) & 1;
+                const int tok0 = tile_of(sq, seg.step + (dual ? j >> 1 : j)) * STEP;
+                const uint32_t s_at = tmem + lanes + buf * STEP;
+                const uint32_t o_at = tmem + lanes + S::TM_O + (STREAMS == 2 ? buf : 0) * DP;
+                wait(s_full + 8 * buf, (s_phase >> buf) & 1u);
+                s_phase ^= 1u << buf;
+                tc_fence_after();
+                if (first) {
+                    if constexpr (S::E4M3 && S::DT == 1) f *= __uint_as_float(static_cast<uint32_t>(ctl.qe[tile][r] + 127) << 23);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_empty);
+                }
+                const bool bad = *static_cast<volatile int*>(&ctl.bad_page) != 0;
+                const bool masked = bad || tok0 + STEP > ctx ||
+                                    (a.window > 0 && tok0 < edge && tok0 + STEP > a.sinks);
+                auto seen_of = [&](int t0) {
+                    uint32_t v = see.seen(t0);
+                    if (bad)
+                        for (uint32_t left = v; left; left &= left - 1) {
+                            const int bit = __ffs(left) - 1, tok = t0 + bit;
+                            if (static_cast<unsigned>(table[page_shift >= 0 ? tok >> page_shift : tok / a.page_size]) >=
+                                static_cast<unsigned>(a.num_pages))
+                                v &= ~(1u << bit);
+                        }
+                    return v;
+                };
+                auto work = [&](auto MASKED) {
+                    uint32_t x[32];
+                    uint32_t seen[STEP / 32];
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < STEP / 32; ++c) {
+                        tmem_ld32(s_at + 32 * c, x);
+                        if (MASKED) seen[c] = seen_of(tok0 + 32 * c);
+                        tmem_wait_ld();
+                        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float v = __uint_as_float(x[e]);
+                            if (MASKED) v = (seen[c] >> e) & 1u ? v : -INFINITY;
+                            t4[e & 3] = tree_max(t4[e & 3], v);
+                        }
+                        top = tree_max(top, tree_max(tree_max(t4[0], t4[1]), tree_max(t4[2], t4[3])));
+                    }
+                    top *= f;
+                    if (__any_sync(0xFFFFFFFFu, !(top <= m + kTreeLag))) {
+                        const float now = tree_max(m, top);
+                        const float scale = now == m ? 1.0f : tree_exp2(m - now);
+                        m = now;
+                        ref = now == -INFINITY ? 0.0f : now - kShift;
+                        l *= scale;
+                        if (!first) {
+                            if constexpr (STREAMS == 1) wait(pv_done, (pv_jobs - 1) & 1u);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < DP; c += 32) {
+                                tmem_ld32(o_at + c, x);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * scale);
+                                tmem_st32(o_at + c, x);
+                            }
+                        }
+                    }
+                    float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < STEP / 32; ++c) {
+                        tmem_ld32(s_at + 32 * c, x);
+                        tmem_wait_ld();
+                        uint32_t y[32];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float p[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float v = __uint_as_float(x[e + h]);
+                                if (MASKED) v = (seen[c] >> (e + h)) & 1u ? v : -INFINITY;
+                                p[h] = tree_exp2(fmaf(v, f, -ref));
+                                l4[(e + h) & 3] += p[h];
+                            }
+                            // two parts, both positive over 16-bit caches so that an infinite value gives its infinity
+                            uint32_t hi;
+                            float low0, low1;
+                            if constexpr (S::BF) {
+                                hi = __byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632);
+                                low0 = fmaf(p[0], 1.0f + 0x1p-22f, -__uint_as_float(__float_as_uint(p[0]) & 0xFFFF0000u));
+                                low1 = fmaf(p[1], 1.0f + 0x1p-22f, -__uint_as_float(__float_as_uint(p[1]) & 0xFFFF0000u));
+                            } else {
+                                if constexpr (S::E4M3) {
+                                    hi = dec_pack2<0>(p[0], p[1]);
+                                } else {
+                                    constexpr float kLess = 1.0f - 0x1p-10f;
+                                    asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;"
+                                        : "=r"(hi) : "f"(fmaf(p[1], kLess, -0x1p-24f)), "f"(fmaf(p[0], kLess, -0x1p-24f)));
+                                }
+                                low0 = p[0] - dec_to_f32<0>(static_cast<uint16_t>(hi & 0xFFFFu));
+                                low1 = p[1] - dec_to_f32<0>(static_cast<uint16_t>(hi >> 16));
+                            }
+                            // of a block of 16 tokens the high parts in columns 0 .. 7, the low ones in 8 .. 15
+                            const int at = (e & 16) + (e & 15) / 2;
+                            y[at] = hi;
+                            y[at + 8] = dec_pack2<S::BF ? 1 : 0>(low0, low1);
+                        }
+                        tmem_st32(s_at + 32 * c, y);
+                    }
+                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                };
+                if (masked) work(std::true_type{});
+                else work(std::false_type{});
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * buf);
+                first = false;
+                if constexpr (STREAMS == 1) ++pv_jobs;
+            }
+
+            // ---- the end of the segment ----
+            wait(o_full, o_phase);
+            o_phase ^= 1u;
+            tc_fence_after();
+            const bool begins = seg.step == 0, ends = seg.step_end == sq.steps, whole = begins && ends;
+            float* part = parts + (2 * cta + (begins ? 1 : 0)) * tree_part_floats(S::ROWS, DP);
+            const float vs = S::E4M3 && a.vc.scale ? a.vc.scale[kvh] : 1.0f;
+            // the sums of stream x times fx[x]
+            float fx[2] = {1.0f, 1.0f};
+            int c0 = 0, c1 = DP;             // columns of this thread
+            bool use[2] = {stream == 0, stream == 1};
+            if (STREAMS == 2 && !dual) {     // the streams' sums of the same rows are joined
+                // (they have been read before the next item's first P V, which o_free holds back)
+                float2 (&st)[STREAMS][kTreeRows] = ctl.stats;
+                st[stream][r] = make_float2(m, l);
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * SW) : "memory");
+                const float2 s0 = st[0][r], s1 = st[STREAMS - 1][r];
+                m = tree_max(s0.x, s1.x);
+                fx[0] = s0.x == -INFINITY ? 0.0f : tree_exp2(s0.x - m);
+                fx[1] = s1.x == -INFINITY ? 0.0f : tree_exp2(s1.x - m);
+                l = s0.y * fx[0] + s1.y * fx[1];
+                // a stream that had no job has nothing in its place
+                use[0] = jobs > 1 || (job0 & 1) == 0;
+                use[1] = jobs > 1 || (job0 & 1) == 1;
+                c0 = stream * (DP / 2), c1 = c0 + DP / 2;
+            }
+            const int64_t out_row = sq.first + i;
+            const float inv = l == 0.0f ? 0.0f : vs / l;
+            const bool patch = *static_cast<volatile int*>(&ctl.dirty) != 0;
+#pragma unroll 1
+            for (int c = c0; c < c1; c += 32) {
+                uint32_t x[32];
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < STREAMS; ++s) {
+                    if (!use[s]) continue;
+                    tmem_ld32(tmem + lanes + S::TM_O + s * DP + c, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(STREAMS == 2 && !dual) || fx[s] != 0.0f) o[e] = fmaf(__uint_as_float(x[e]), fx[s], o[e]);
+                }
+                if (patch && live && l != 0.0f) {  // infinite values and NaN of tokens that this row sees
+                    for (int st = seg.step; st < seg.step_end; ++st) {
+                        const int tok0 = tile_of(sq, st) * STEP;
+                        for (int t0 = tok0; t0 < tok0 + STEP; t0 += 32)
+                            for (uint32_t left = see.seen(t0); left; left &= left - 1) {
+                                const int tok = t0 + __ffs(left) - 1;
+                                if (!(tok >= ctx || (tok < edge && tok >= a.sinks))) continue;
+                                const int in = page_shift >= 0 ? tok >> page_shift : tok / a.page_size;
+                                const int page = table[in];
+                                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) continue;
+                                const int64_t at = page * a.vc.page_stride + (tok - in * a.page_size) * a.vc.slot_stride +
+                                                   kvh * a.vc.head_stride + c;
+                                for (int e = 0; e < 32 && c + e < a.head_dim; ++e) {
+                                    float v;
+                                    if constexpr (S::E4M3)
+                                        v = (static_cast<const uint8_t*>(a.vc.p)[at + e] & 0x7F) == 0x7F ? NAN : 0.0f;
+                                    else
+                                        v = dec_to_f32<S::DT>(static_cast<const uint16_t*>(a.vc.p)[at + e]);
+                                    if (!(fabsf(v) < INFINITY)) {
+#pragma unroll
+                                        for (int q = 0; q < 32; ++q)
+                                            if (q == e) o[q] += v;
+                                    }
+                                }
+                            }
+                    }
+                }
+                if (!live) continue;
+                if (whole) {
+                    uint16_t* dst = a.out + out_row * a.ldo + static_cast<int64_t>(head) * a.head_dim + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (c + e < a.head_dim)
+                            *reinterpret_cast<uint4*>(dst + e) = make_uint4(
+                                dec_pack2<S::DT>(o[e] * inv, o[e + 1] * inv), dec_pack2<S::DT>(o[e + 2] * inv, o[e + 3] * inv),
+                                dec_pack2<S::DT>(o[e + 4] * inv, o[e + 5] * inv), dec_pack2<S::DT>(o[e + 6] * inv, o[e + 7] * inv));
+                } else {
+                    float* dst = part + 2 * S::ROWS + static_cast<int64_t>(in_item) * DP + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+            if (live && c0 == 0) {
+                if (!whole) part[in_item] = m, part[S::ROWS + in_item] = l;
+                else if (a.lse)
+                    a.lse[out_row * a.q_heads + head] =
+                        l > 0.0f ? (m - kShift) * 0.69314718055994531f + logf(l) : l == 0.0f ? -INFINITY : m;
+            }
+            if (begins && !ends && tid == 0) {
+                const long long at0 = share_end - seg.rest - sq.steps;  // of the item's first step in the line
+                heads[cta] = TreePart{static_cast<int>((at0 + sq.steps - 1) / line.share) - cta + 1, row0, rows, kvh * G,
+                                      sq.first, vs, {0, 0}};
+            }
+            more = after(seg);
+        }
+    }
+    // every MMA is done before TMEM is given back: the last ones were waited for by the softmax warps
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == SW) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of items that several CTAs hold: a warp per row, blockIdx.x the CTA that began the item.
+template <int DT, int DP, bool SHIFT>
+__global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a, int ctas) {
+    constexpr float kShift = SHIFT ? 7.0f : 0.0f;
+    constexpr int ROWS = kTreeRows * tree_streams(DP), V = DP >= 128 ? DP / 128 : 1;
+    grid_dep_wait();
+    const TreePart* heads = static_cast<const TreePart*>(a.workspace);
+    const TreePart h = heads[blockIdx.x];
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const float* parts = reinterpret_cast<const float*>(heads + ctas);
+    const int G = a.q_heads / a.kv_heads;
+    if (h.n <= 0) return;
+    auto part_of = [&](int k) {
+        return parts + (2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0)) * tree_part_floats(ROWS, DP);
+    };
+    for (int row = static_cast<int>(blockIdx.y) * 4 + (static_cast<int>(threadIdx.x) >> 5); row < h.rows; row += 4 * gridDim.y) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int k = lane; k < h.n; k += 32) top = tree_max(top, part_of(k)[row]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = tree_max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        float4 acc[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = 0; k < h.n; ++k) {
+            const float* p = part_of(k);
+            const float m = p[row], f = m == -INFINITY ? 0.0f : tree_exp2(m - top);
+            sum += p[ROWS + row] * f;
+            if (f == 0.0f) continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int d = 4 * lane + 128 * v;
+                if (d >= a.head_dim) continue;
+                const float4 x = *reinterpret_cast<const float4*>(p + 2 * ROWS + static_cast<int64_t>(row) * DP + d);
+                acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y);
+                acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
+            }
+        }
+        const float inv = sum == 0.0f ? 0.0f : h.vs / sum;
+        const int r = h.row0 + row, i = r / G, head = h.head0 + r - i * G;
+        uint16_t* out = a.out + static_cast<int64_t>(h.first + i) * a.ldo + static_cast<int64_t>(head) * a.head_dim;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int d = 4 * lane + 128 * v;
+            if (d < a.head_dim)
+                *reinterpret_cast<uint2*>(out + d) = make_uint2(dec_pack2<DT>(acc[v].x * inv, acc[v].y * inv),
+                                                               dec_pack2<DT>(acc[v].z * inv, acc[v].w * inv));
+        }
+        if (a.lse && lane == 0)
+            a.lse[static_cast<int64_t>(h.first + i) * a.q_heads + head] =
+                sum > 0.0f ? (top - kShift) * 0.69314718055994531f + logf(sum) : sum == 0.0f ? -INFINITY : top;
+    }
+}
+
+template <class S>
+int launch_tree_shape(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(tree_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess)
+        return -3;
+    const int rc = launch_dependent(tree_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), dim3(S::THREADS),
+                                    S::SMEM, stream, a, power_of_two(a.page_size));
+    if (rc != 0) return rc;
+    return launch_dependent(tree_join_kernel<S::DT, S::DP, !S::BF>, dim3(static_cast<unsigned>(ctx.num_sms), 16),
+                            dim3(128), 0, stream, a, ctx.num_sms);
+}
+
+template <int DT, bool E4M3>
+int launch_tree_dp(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stream) {
+    if (a.head_dim <= 64) return launch_tree_shape<TreeShape<DT, E4M3, 64>>(ctx, a, stream);
+    if (a.head_dim <= 128) return launch_tree_shape<TreeShape<DT, E4M3, 128>>(ctx, a, stream);
+    return launch_tree_shape<TreeShape<DT, E4M3, 256>>(ctx, a, stream);
+}
+
+}  // namespace
+
+// One instance per translation unit (tree_*.cu), which compile in parallel.
+template <int DT, bool E4M3>
+int launch_tree_typed(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stream);
+
+}  // namespace w4g
