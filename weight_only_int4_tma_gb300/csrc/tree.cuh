@@ -72,6 +72,30 @@ __device__ __forceinline__ float tree_max(float a, float b) {  // NaN if either 
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
+__device__ __forceinline__ float tree_max3(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// Two fp32 values by one instruction.
+__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void tree_copy16(uint32_t dst, const char* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
@@ -97,25 +121,69 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+// Waits for this thread's loads; names the registers that they fill, which are not to be used before.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :: "memory");
+    asm volatile(""
+                 : "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :: "memory");
+}
+// Four MMAs, kind::f16, issued by lane 0 while the whole warp executes the statement (no branch
+// around it, so that the operands stay warp-uniform; with one around single MMAs the warp took 130 cycles
+// for each): D[tmem] (+)= A[smem] . B[smem]^T, both K-major, over the 64 values of a 128-byte row.
+__device__ __forceinline__ void tc_mma_ss4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
-        "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
-        "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b32 l;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "mov.u32 l, %%laneid;\n\t"
+        "setp.eq.u32 e, l, 0;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %3, 0;\n\t"  // idesc is never 0: a true predicate
+        "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
         : "memory");
 }
-// D[tmem] (+)= A[smem] . B[smem]^T, kind::f16.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// Two blocks of 16 tokens: D (+)= (P high + P low) . V, the parts 8 TMEM columns apart, the blocks 16
+// columns and 2048 bytes of V (MN-major).
+__device__ __forceinline__ void tc_mma_pv2(uint32_t d_tmem, uint32_t p_tmem, uint64_t v, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc),
-        "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b32 l;\n\t.reg .b64 v1;\n\t"
+        "mov.u32 l, %%laneid;\n\t"
+        "setp.eq.u32 e, l, 0;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "add.u64 v1, %5, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %6, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %5, %6, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], v1, %6, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], v1, %6, q;\n\t}" ::"r"(d_tmem), "r"(p_tmem),
+        "r"(p_tmem + 8), "r"(p_tmem + 16), "r"(p_tmem + 24), "l"(v), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// tc_commit by lane 0 of a converged warp, if `wanted`.
+__device__ __forceinline__ void tc_commit_lane0(uint32_t bar, bool wanted = true) {
+    asm volatile(
+        "{\n\t.reg .pred e, c;\n\t.reg .b32 l;\n\t"
+        "mov.u32 l, %%laneid;\n\t"
+        "setp.eq.u32 e, l, 0;\n\t"
+        "setp.ne.b32 c, %1, 0;\n\t"
+        "and.pred e, e, c;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(wanted))
         : "memory");
 }
 // The MN-major operand with 128-byte swizzle: atoms of 64 values (M or N) x 8 (K), 1024 bytes
@@ -167,9 +235,10 @@ struct TreeShape {
     static constexpr int SLOT = STEP * DP * 2;               // bytes of a step's keys, or values
     static constexpr int QTILE = kTreeRows * DP * 2;
     static constexpr int NSLOT = DP == 64 ? 10 : 5;          // of the ring: 160 KB
-    static constexpr int PW = 8;                             // producer warps
+    static constexpr int PW = 4;                             // producer warps
     static constexpr int SW = 4 * STREAMS;                   // softmax warps
-    static constexpr int THREADS = 32 * (SW + 1 + PW);
+    static constexpr int MMA_WARP = SW + PW;                 // (three more fill its warpgroup)
+    static constexpr int THREADS = 32 * (SW + PW + 4);
     static constexpr int RW = STEP / PW;                     // token rows of a step per producer warp
     static constexpr int CH = DP / 8;                        // 16-byte chunks of a row in shared memory
     static constexpr int TM_O = 2 * STEP;                    // TMEM columns: S twice, then O of each stream
@@ -303,7 +372,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
     fence_proxy_async_smem();  // the zeros
     grid_dep_wait();
     grid_dep_launch();
-    if (warp == SW) {
+    if (warp == S::MMA_WARP) {
         tmem_alloc(smem_addr(&ctl.tmem_base), 512);
         tmem_relinquish();
     }
@@ -398,9 +467,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
         __syncthreads();
     }
 
-    if (warp > SW) {
+    if (warp >= SW && warp < S::MMA_WARP) {
         // ================= producers =================
-        const int pw = warp - SW - 1;
+        const int pw = warp - SW;
         constexpr int CH = S::CH, RW = S::RW;
         const int row_chunks = a.head_dim / 8;        // of 16-bit values
         auto page_of = [&](int tok) { return page_shift >= 0 ? tok >> page_shift : tok / a.page_size; };
@@ -500,25 +569,25 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                         tree_copy16(dst + at_smem(STEP, r, c), off >= 0 ? from + off + 16 * c : from, off >= 0 ? 16 : 0);
                 }
             };
-            // the same through registers, with values that some row must not see made finite
+            // the same through registers, eight loads at a time, with values that some row must not see made finite
             constexpr int FC = DP * S::ES / 16;            // chunks of a row in the cache
-            constexpr int LR = 32 / FC > 0 ? 32 / FC : 1;  // rows of one load of the warp
-            constexpr int LN = RW / LR;                    // loads
-            auto load = [&](uint4 (&v)[LN], const char* from, int64_t at) {
+            constexpr int LR = 32 / FC;                    // rows of one load of the warp
+            constexpr int LN = RW / LR < 8 ? RW / LR : 8;  // loads
+            auto load = [&](uint4 (&v)[LN], const char* from, int64_t at, int r0) {
                 const int c = lane % FC, sub = lane / FC;
 #pragma unroll
                 for (int x = 0; x < LN; ++x) {
-                    const int64_t off = __shfl_sync(0xFFFFFFFFu, at, x * LR + sub);
+                    const int64_t off = __shfl_sync(0xFFFFFFFFu, at, r0 + x * LR + sub);
                     v[x] = make_uint4(0, 0, 0, 0);
                     if (off >= 0 && 16 * c < a.head_dim * S::ES) v[x] = __ldg(reinterpret_cast<const uint4*>(from + off) + c);
                 }
             };
-            auto store = [&](uint32_t dst, uint4 (&v)[LN], uint32_t some) {
+            auto store = [&](uint32_t dst, uint4 (&v)[LN], uint32_t some, int r0) {
                 const int c = lane % FC, sub = lane / FC;
 #pragma unroll
                 for (int x = 0; x < LN; ++x) {
-                    const int r = pw * RW + x * LR + sub;
-                    if ((some >> (x * LR + sub)) & 1u) {
+                    const int in = r0 + x * LR + sub, r = pw * RW + in;
+                    if ((some >> in) & 1u) {
                         bool any;
                         if constexpr (S::E4M3) any = tree_scrub_e4m3(v[x]);
                         else any = tree_scrub<S::BF>(v[x]);
@@ -596,25 +665,33 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
             };
 
             if constexpr (S::E4M3) {
-                uint4 k[LN], v[LN];
+                // a step's keys and values as one line of loads, those of the next eight under way
+                constexpr int PER = LN * LR, PIECES = 2 * RW / PER;  // rows of a piece, pieces of a step
+                uint4 v0[LN];
                 look(seg.step);
-                load(k, kbase, kat);
-                load(v, vbase, vat);
-                uint32_t some = mixed;
+                load(v0, kbase, kat, 0);
                 for (int st = seg.step; st < seg.step_end; ++st) {
-                    const bool again = st + 1 < seg.step_end;
-                    if (again) look(st + 1);
-                    wait_free(empty + 8 * slot, phase ^ 1u);
-                    store(ring + slot * S::SLOT, k, 0u);
-                    signal(full + 8 * slot);
-                    next_slot();
-                    if (again) load(k, kbase, kat);
-                    wait_free(empty + 8 * slot, phase ^ 1u);
-                    store(ring + slot * S::SLOT, v, some);
-                    signal(full + 8 * slot);
-                    next_slot();
-                    if (again) load(v, vbase, vat);
-                    some = mixed;
+                    const uint32_t some = mixed;
+#pragma unroll
+                    for (int x = 0; x < PIECES; ++x) {
+                        const int r0 = x * PER % RW;
+                        if (r0 == 0) wait_free(empty + 8 * slot, phase ^ 1u);
+                        uint4 v1[LN];
+                        if (x + 1 < PIECES) {
+                            const bool values = (x + 1) * PER >= RW;
+                            load(v1, values ? vbase : kbase, values ? vat : kat, (x + 1) * PER % RW);
+                        } else if (st + 1 < seg.step_end) {
+                            look(st + 1);
+                            load(v1, kbase, kat, 0);
+                        }
+                        store(ring + slot * S::SLOT, v0, x * PER >= RW ? some : 0u, r0);
+                        if (r0 + PER == RW) {
+                            signal(full + 8 * slot);
+                            next_slot();
+                        }
+#pragma unroll
+                        for (int e = 0; e < LN; ++e) v0[e] = v1[e];
+                    }
                     if (st == seg.step) load_queries();
                 }
             } else {
@@ -626,9 +703,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                     next_slot();
                     wait_free(empty + 8 * slot, phase ^ 1u);
                     if (mixed) {
-                        uint4 v[LN];
-                        load(v, vbase, vat);
-                        store(ring + slot * S::SLOT, v, mixed);
+#pragma unroll 1
+                        for (int r0 = 0; r0 < RW; r0 += LN * LR) {
+                            uint4 v[LN];
+                            load(v, vbase, vat, r0);
+                            store(ring + slot * S::SLOT, v, mixed, r0);
+                        }
                         signal(full + 8 * slot);
                     } else {
                         copy(ring + slot * S::SLOT, vbase, vat);
@@ -641,8 +721,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
             more = after(seg);
         }
         flush();
-    } else if (warp == SW) {
+    } else if (warp >= S::MMA_WARP) {
         // ================= the MMAs =================
+        if (warp != S::MMA_WARP) more = false;
         constexpr int TYPE = S::BF ? 1 : 0;
         constexpr uint32_t idesc_s = idesc_f16(TYPE, 128, STEP), idesc_o = idesc_f16(TYPE, 128, DP) | kIdescBMajorMn;
         int slot = 0;                       // of the ring, in the order in which the producers fill it
@@ -664,23 +745,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                 free_phase ^= 1u;
             }
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t d = tmem + S::TM_O + (STREAMS == 2 ? p_buf : 0) * DP;
-                const uint32_t p = tmem + p_buf * STEP;
-                const uint32_t v = ring + p_slot * S::SLOT;
+            const uint32_t d = tmem + S::TM_O + (STREAMS == 2 ? p_buf : 0) * DP, p = tmem + p_buf * STEP;
+            const uint64_t v = sw128_desc_mn(ring + p_slot * S::SLOT, STEP * 128);
 #pragma unroll
-                for (int kb = 0; kb < STEP / 16; ++kb) {
-                    const uint64_t desc = sw128_desc_mn(v + kb * 2048, STEP * 128);
-                    tc_mma_ts(d, p + 16 * kb, desc, idesc_o, kb > 0 || !p_fresh);
-                    tc_mma_ts(d, p + 16 * kb + 8, desc, idesc_o, 1);
-                }
-                if (p_frees) tc_commit(empty + 8 * p_slot);
-                if (STREAMS == 1) tc_commit(pv_done);
-                if (p_last) {
-                    tc_commit(o_full);
-                    mbar_arrive(o_full);
-                }
-            }
+            for (int kb = 0; kb < STEP / 16; kb += 2) tc_mma_pv2(d, p + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || !p_fresh);
+            tc_commit_lane0(empty + 8 * p_slot, p_frees);
+            if (STREAMS == 1) tc_commit_lane0(pv_done);
+            tc_commit_lane0(o_full, p_last);
+            if (p_last && lane == 0) mbar_arrive(o_full);
             __syncwarp();
             open = false;
         };
@@ -703,17 +775,14 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                 }
                 wait(full + 8 * k_slot, k_phase);
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t q = q_smem + (second ? S::QTILE : 0), k = ring + k_slot * S::SLOT;
+                const uint64_t q = sw128_desc(q_smem + (second ? S::QTILE : 0)), k = sw128_desc(ring + k_slot * S::SLOT);
 #pragma unroll
-                    for (int c = 0; c < DP / 16; ++c)
-                        tc_mma_ss(tmem + buf * STEP, sw128_desc(q + (c >> 2) * kTreeRows * 128 + (c & 3) * 32),
-                                  sw128_desc(k + (c >> 2) * STEP * 128 + (c & 3) * 32), idesc_s, c > 0);
-                    tc_commit(s_full + 8 * buf);
-                    mbar_arrive(s_full + 8 * buf);
-                    if (!dual || second) tc_commit(empty + 8 * k_slot);
-                    if (j == jobs - 1) tc_commit(q_empty);
-                }
+                for (int c = 0; c < S::BLOCKS; ++c)
+                    tc_mma_ss4(tmem + buf * STEP, q + c * (kTreeRows * 128 >> 4), k + c * (STEP * 128 >> 4), idesc_s, c > 0);
+                tc_commit_lane0(s_full + 8 * buf);
+                tc_commit_lane0(empty + 8 * k_slot, !dual || second);
+                tc_commit_lane0(q_empty, j == jobs - 1);
+                if (lane == 0) mbar_arrive(s_full + 8 * buf);
                 __syncwarp();
                 if (open) issue_pv();
                 open = true;
@@ -751,6 +820,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
             const int in_item = tile * kTreeRows + r;
             const bool live = in_item < rows;
             const int row = row0 + in_item, i = live ? row / G : 0, head = kvh * G + (live ? row - i * G : 0);
+            const bool any_live = __any_sync(0xFFFFFFFFu, live);
             TreeRow see{0, ctx, 0, a.window > 0 ? a.sinks : 0};
             if (live) {
                 const uint64_t all = sq.n == 64 ? ~0ull : (1ull << sq.n) - 1;
@@ -783,6 +853,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                     __syncwarp();
                     if (lane == 0) mbar_arrive(q_empty);
                 }
+                if (!any_live) {  // what these rows of P hold reaches only rows that nobody reads
+                    if (lane == 0) mbar_arrive(p_full + 8 * buf);
+                    first = false;
+                    if constexpr (STREAMS == 1) ++pv_jobs;
+                    continue;
+                }
                 const bool bad = *static_cast<volatile int*>(&ctl.bad_page) != 0;
                 const bool masked = bad || tok0 + STEP > ctx ||
                                     (a.window > 0 && tok0 < edge && tok0 + STEP > a.sinks);
@@ -797,89 +873,110 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                         }
                     return v;
                 };
-                auto work = [&](auto MASKED) {
-                    uint32_t x[32];
-                    uint32_t seen[STEP / 32];
-                    float top = -INFINITY;
+                // Twice over S, 16 tokens at a time, the next ones' load under way.
+                constexpr int NC = STEP / 16;
+                uint32_t xa[16], xb[16];
+                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                uint32_t seen = ~0u;     // of 32 tokens
+                auto hide = [&](uint32_t (&x)[16], uint32_t bits) {
+                    if (!masked) return;
 #pragma unroll
-                    for (int c = 0; c < STEP / 32; ++c) {
-                        tmem_ld32(s_at + 32 * c, x);
-                        if (MASKED) seen[c] = seen_of(tok0 + 32 * c);
-                        tmem_wait_ld();
-                        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float v = __uint_as_float(x[e]);
-                            if (MASKED) v = (seen[c] >> e) & 1u ? v : -INFINITY;
-                            t4[e & 3] = tree_max(t4[e & 3], v);
-                        }
-                        top = tree_max(top, tree_max(tree_max(t4[0], t4[1]), tree_max(t4[2], t4[3])));
-                    }
-                    top *= f;
-                    if (__any_sync(0xFFFFFFFFu, !(top <= m + kTreeLag))) {
-                        const float now = tree_max(m, top);
-                        const float scale = now == m ? 1.0f : tree_exp2(m - now);
-                        m = now;
-                        ref = now == -INFINITY ? 0.0f : now - kShift;
-                        l *= scale;
-                        if (!first) {
-                            if constexpr (STREAMS == 1) wait(pv_done, (pv_jobs - 1) & 1u);
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < DP; c += 32) {
-                                tmem_ld32(o_at + c, x);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * scale);
-                                tmem_st32(o_at + c, x);
-                            }
-                        }
-                    }
-                    float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int c = 0; c < STEP / 32; ++c) {
-                        tmem_ld32(s_at + 32 * c, x);
-                        tmem_wait_ld();
-                        uint32_t y[32];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float p[2];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float v = __uint_as_float(x[e + h]);
-                                if (MASKED) v = (seen[c] >> (e + h)) & 1u ? v : -INFINITY;
-                                p[h] = tree_exp2(fmaf(v, f, -ref));
-                                l4[(e + h) & 3] += p[h];
-                            }
-                            // two parts, both positive over 16-bit caches so that an infinite value gives its infinity
-                            uint32_t hi;
-                            float low0, low1;
-                            if constexpr (S::BF) {
-                                hi = __byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632);
-                                low0 = fmaf(p[0], 1.0f + 0x1p-22f, -__uint_as_float(__float_as_uint(p[0]) & 0xFFFF0000u));
-                                low1 = fmaf(p[1], 1.0f + 0x1p-22f, -__uint_as_float(__float_as_uint(p[1]) & 0xFFFF0000u));
-                            } else {
-                                if constexpr (S::E4M3) {
-                                    hi = dec_pack2<0>(p[0], p[1]);
-                                } else {
-                                    constexpr float kLess = 1.0f - 0x1p-10f;
-                                    asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;"
-                                        : "=r"(hi) : "f"(fmaf(p[1], kLess, -0x1p-24f)), "f"(fmaf(p[0], kLess, -0x1p-24f)));
-                                }
-                                low0 = p[0] - dec_to_f32<0>(static_cast<uint16_t>(hi & 0xFFFFu));
-                                low1 = p[1] - dec_to_f32<0>(static_cast<uint16_t>(hi >> 16));
-                            }
-                            // of a block of 16 tokens the high parts in columns 0 .. 7, the low ones in 8 .. 15
-                            const int at = (e & 16) + (e & 15) / 2;
-                            y[at] = hi;
-                            y[at + 8] = dec_pack2<S::BF ? 1 : 0>(low0, low1);
-                        }
-                        tmem_st32(s_at + 32 * c, y);
-                    }
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    for (int e = 0; e < 16; ++e) x[e] = (bits >> e) & 1u ? x[e] : 0xFF800000u;
                 };
-                if (masked) work(std::true_type{});
-                else work(std::false_type{});
+                auto highest = [&](const uint32_t (&x)[16]) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2)
+                        t4[e / 2 & 3] = tree_max3(t4[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                };
+                tmem_ld16(s_at, xa);
+#pragma unroll 1
+                for (int c = 0; c < NC; c += 2) {
+                    if (masked) seen = seen_of(tok0 + 16 * c);
+                    tmem_wait_ld16(xa);
+                    tmem_ld16(s_at + 16 * (c + 1), xb);
+                    hide(xa, seen);
+                    highest(xa);
+                    tmem_wait_ld16(xb);
+                    tmem_ld16(s_at + 16 * ((c + 2) & (NC - 1)), xa);
+                    hide(xb, seen >> 16);
+                    highest(xb);
+                }
+                const float top = f * tree_max(tree_max(t4[0], t4[1]), tree_max(t4[2], t4[3]));
+                if (__any_sync(0xFFFFFFFFu, !(top <= m + kTreeLag))) {
+                    const float now = tree_max(m, top);
+                    const float scale = now == m ? 1.0f : tree_exp2(m - now);
+                    m = now;
+                    ref = now == -INFINITY ? 0.0f : now - kShift;
+                    l *= scale;
+                    if (!first) {
+                        if constexpr (STREAMS == 1) wait(pv_done, (pv_jobs - 1) & 1u);
+                        tc_fence_after();
+                        tmem_wait_ld16(xa);
+#pragma unroll 1
+                        for (int c = 0; c < DP; c += 16) {
+                            tmem_ld16(o_at + c, xb);
+                            tmem_wait_ld16(xb);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) xb[e] = __float_as_uint(__uint_as_float(xb[e]) * scale);
+                            tmem_st16(o_at + c, xb);
+                        }
+                    }
+                }
+                uint64_t l2[2] = {0, 0};
+                const uint64_t f2 = pack_f2(f, f), ref2 = pack_f2(-ref, -ref);
+                auto weights = [&](const uint32_t (&x)[16], int c) {
+                    uint32_t y[16];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float p0, p1;
+                        unpack_f2(fma_f2(pack_f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2, ref2), p0, p1);
+                        p0 = tree_exp2(p0);
+                        p1 = tree_exp2(p1);
+                        l2[e / 2 & 1] = add_f2(l2[e / 2 & 1], pack_f2(p0, p1));
+                        // two parts, both positive over 16-bit caches so that an infinite value gives its infinity
+                        uint32_t hi;
+                        float low0, low1;
+                        if constexpr (S::BF) {
+                            // the high part is cut off, not rounded; the rest and 2^-22 of the weight are never 0
+                            const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                            hi = __byte_perm(b0, b1, 0x7632);
+                            const uint64_t cut = pack_f2(__uint_as_float((b0 & 0xFFFF0000u) ^ 0x80000000u),
+                                                         __uint_as_float((b1 & 0xFFFF0000u) ^ 0x80000000u));
+                            unpack_f2(fma_f2(pack_f2(p0, p1), pack_f2(1.0f + 0x1p-22f, 1.0f + 0x1p-22f), cut), low0, low1);
+                        } else {
+                            if constexpr (S::E4M3) {
+                                hi = dec_pack2<0>(p0, p1);
+                            } else {
+                                constexpr float kLess = 1.0f - 0x1p-10f;
+                                asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;"
+                                    : "=r"(hi) : "f"(fmaf(p1, kLess, -0x1p-24f)), "f"(fmaf(p0, kLess, -0x1p-24f)));
+                            }
+                            low0 = p0 - dec_to_f32<0>(static_cast<uint16_t>(hi & 0xFFFFu));
+                            low1 = p1 - dec_to_f32<0>(static_cast<uint16_t>(hi >> 16));
+                        }
+                        // of a block of 16 tokens the high parts in columns 0 .. 7, the low ones in 8 .. 15
+                        y[e / 2] = hi;
+                        y[e / 2 + 8] = dec_pack2<S::BF ? 1 : 0>(low0, low1);
+                    }
+                    tmem_st16(s_at + 16 * c, y);
+                };
+#pragma unroll 1
+                for (int c = 0; c < NC; c += 2) {
+                    if (masked) seen = seen_of(tok0 + 16 * c);
+                    tmem_wait_ld16(xa);
+                    tmem_ld16(s_at + 16 * (c + 1), xb);
+                    hide(xa, seen);
+                    weights(xa, c);
+                    tmem_wait_ld16(xb);
+                    if (c + 2 < NC) tmem_ld16(s_at + 16 * (c + 2), xa);
+                    hide(xb, seen >> 16);
+                    weights(xb, c + 1);
+                }
+                {
+                    float s0, s1;
+                    unpack_f2(add_f2(l2[0], l2[1]), s0, s1);
+                    l += s0 + s1;
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -927,7 +1024,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                 for (int s = 0; s < STREAMS; ++s) {
                     if (!use[s]) continue;
                     tmem_ld32(tmem + lanes + S::TM_O + s * DP + c, x);
-                    tmem_wait_ld();
+                    tmem_wait_ld32(x);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (!(STREAMS == 2 && !dual) || fx[s] != 0.0f) o[e] = fmaf(__uint_as_float(x[e]), fx[s], o[e]);
@@ -996,7 +1093,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == SW) tmem_dealloc(tmem, 512);
+    if (warp == S::MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of items that several CTAs hold: a warp per row, blockIdx.x the CTA that began the item.
