@@ -72,30 +72,6 @@ __device__ __forceinline__ float tree_max(float a, float b) {  // NaN if either 
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-__device__ __forceinline__ float tree_max3(float a, float b, float c) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-// Two fp32 values by one instruction.
-__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack_f2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ void tree_copy16(uint32_t dst, const char* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
@@ -886,7 +862,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                 auto highest = [&](const uint32_t (&x)[16]) {
 #pragma unroll
                     for (int e = 0; e < 16; e += 2)
-                        t4[e / 2 & 3] = tree_max3(t4[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        t4[e / 2 & 3] = max3_nan(t4[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                 };
                 tmem_ld16(s_at, xa);
 #pragma unroll 1
