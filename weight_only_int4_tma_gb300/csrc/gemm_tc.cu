@@ -1048,31 +1048,12 @@ w4a16_tc_kernel(const __grid_constant__ CUtensorMap tmap_a, const TcArgs args) {
 
 // ---- host side ---------------------------------------------------------------------
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 template <int BM, int NWG, int DT, int DQ = kDqMagic, bool IL = (BM <= 32), bool PROBE = false>
 int launch_tc_instance(const DeviceCtx& ctx, const void* A, const void* packed, int M, int N,
                        int K, int group, void* Y, const GemmPlan& plan,
                        const EpilogueArgs& epi, cudaStream_t stream,
                        uint64_t timeout_ns = 0) {
-    EncodeTiledFn enc = encode_fn();
+    EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return -3;
     const int a_rows = tc_a_rows(BM, M);
     const int kps = tc_blocks_per_stage(BM);
@@ -1314,6 +1295,20 @@ int launch_tc_splitk_probe(const DeviceCtx& ctx, const void* A, const void* pack
                      ctx, A, packed, M, N, K, group, Y, plan, none, stream, timeout_ns)
                : launch_tc_instance<16, W4A16_SMALL_TILE_WG, 1, kDqMagic, true, true>(
                      ctx, A, packed, M, N, K, group, Y, plan, none, stream, timeout_ns);
+}
+
+EncodeTiledFn tensor_map_encoder() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
 }
 
 }  // namespace w4g

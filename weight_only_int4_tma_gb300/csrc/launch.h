@@ -2,6 +2,7 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "epilogue.cuh"
@@ -30,6 +31,13 @@ struct GemmPlan {
     bool whole_blocks;      // tensor-core kernel: each dequant warpgroup unpacks whole blocks
     int nwg;                // tensor-core kernel: dequant warpgroups
 };
+
+// cuTensorMapEncodeTiled, fetched from the driver once; null if it has none.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn tensor_map_encoder();
 
 // Launchers return a w4a16_status code.
 int launch_repack(const DeviceCtx& ctx, const uint32_t* qweight, const void* scales,

@@ -223,6 +223,16 @@ __device__ __forceinline__ void tma_tensor_3d_g2s(uint32_t dst, const CUtensorMa
         : "memory");
 }
 
+// 4-D tiled tensor copy global -> shared; coordinates {c0 (innermost), c1, c2, c3}.
+__device__ __forceinline__ void tma_tensor_4d_g2s(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                                  int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }

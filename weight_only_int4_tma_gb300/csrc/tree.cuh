@@ -60,6 +60,11 @@ inline size_t tree_workspace(int ctas, int dp) {
     return sizeof(TreePart) * ctas + 2ull * ctas * tree_part_floats(kTreeRows * tree_streams(dp), dp) * 4;
 }
 
+// One side of the cache as a tensor of [page][head][slot][value], in boxes of `box` tokens of one head: with 16-bit
+// values 64 columns each, 128-byte swizzled; with 8-bit ones whole rows of dp bytes.  Values from head_dim on and
+// pages from num_pages on are outside: zeros.  False if there is no such view.
+bool tree_map(CUtensorMap* map, const TreeArgs& a, const KvView& kv, bool e4m3, int dp, int box);
+
 namespace {
 
 __device__ __forceinline__ float tree_exp2(float x) {
@@ -71,15 +76,6 @@ __device__ __forceinline__ float tree_max(float a, float b) {  // NaN if either 
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
-}
-__device__ __forceinline__ void tree_copy16(uint32_t dst, const char* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void tree_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void tree_wait_copies() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void tree_store16(uint32_t dst, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -113,6 +109,19 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                    "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                  :: "memory");
+}
+// Waits for the phase of the given parity, by all lanes of a warp; gives up like mbar_wait_warp.  A
+// function, as the kernel's loops have to fit in the instruction cache; its first tests read no
+// clock, as the global timer's read would add to the latency of every hand-over.
+static __device__ __noinline__ void tree_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                   uint64_t limit_ns) {
+    for (int n = 0; n < 64; ++n)
+        if (mbar_try_wait(bar, parity)) return;
+    mbar_wait_bounded(bar, parity, abort_flag, status, limit_ns);
+}
+__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, uint64_t limit_ns) {
+    if (!mbar_try_wait(bar, parity)) tree_wait_slow(bar, parity, abort_flag, status, limit_ns);
+    __syncwarp();
 }
 // Four MMAs, kind::f16, issued by lane 0 while the whole warp executes the statement (no branch
 // around it, so that the operands stay warp-uniform; with one around single MMAs the warp took 130 cycles
@@ -210,18 +219,20 @@ struct TreeShape {
     static constexpr int BLOCKS = DP / 64;                   // 64-value blocks of a row
     static constexpr int SLOT = STEP * DP * 2;               // bytes of a step's keys, or values
     static constexpr int QTILE = kTreeRows * DP * 2;
-    static constexpr int NSLOT = DP == 64 ? 10 : 5;          // of the ring: 160 KB
-    static constexpr int PW = 4;                             // producer warps
+    static constexpr int NSLOT = E4M3 ? (DP == 64 ? 8 : 4) : (DP == 64 ? 10 : 5);  // of the ring: 128 or 160 KB
+    // 8-bit tiles as they come from the cache, before they are converted into the ring
+    static constexpr int RAW = STEP * DP, NRAW = E4M3 ? (DP == 64 ? 4 : 2) : 0;
     static constexpr int SW = 4 * STREAMS;                   // softmax warps
-    static constexpr int MMA_WARP = SW + PW;                 // (three more fill its warpgroup)
-    static constexpr int THREADS = 32 * (SW + PW + 4);
-    static constexpr int RW = STEP / PW;                     // token rows of a step per producer warp
+    static constexpr int LW = 3;                             // loader warps
+    static constexpr int MMA_WARP = SW + LW;
+    static constexpr int THREADS = 32 * (SW + LW + 1);       // 384: 168 registers each
     static constexpr int CH = DP / 8;                        // 16-byte chunks of a row in shared memory
+    static constexpr int GROUPS = STEP / 16;                 // of 16 tokens: loader warp w has w, w + LW, ...
     static constexpr int TM_O = 2 * STEP;                    // TMEM columns: S twice, then O of each stream
     // Shared memory: TreeControl, the queries' tiles, the ring.  The tiles' 1024-byte alignment follows
     // from the declared alignment of the dynamic part.
     static constexpr int CONTROL = 3072;
-    static constexpr int SMEM = CONTROL + STREAMS * QTILE + NSLOT * SLOT;
+    static constexpr int SMEM = CONTROL + STREAMS * QTILE + NSLOT * SLOT + NRAW * RAW;
     static_assert(TM_O + STREAMS * DP <= 512, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(THREADS * 8 <= STREAMS * QTILE, "the prefix sums lie in the queries' place");
@@ -234,7 +245,7 @@ struct TreeLine {
 
 template <class S>
 struct TreeControl {
-    uint64_t bars[2 * S::NSLOT + 9];
+    uint64_t bars[2 * S::NSLOT + 9 + S::NRAW];
     TreeLine line;
     long long scan[S::THREADS / 32];
     uint32_t tmem_base;
@@ -302,9 +313,13 @@ struct TreeRow {
     }
 };
 
+// box_rows: tokens of a box of the tensor maps (a power of two that divides the page size), or 0: the
+// cache is read without them.
 template <class S>
-__global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int page_shift) {
-    constexpr int STEP = S::STEP, DP = S::DP, STREAMS = S::STREAMS, NSLOT = S::NSLOT, SW = S::SW, PW = S::PW;
+__global__ void __launch_bounds__(S::THREADS, 1)
+tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CUtensorMap kmap,
+            const __grid_constant__ CUtensorMap vmap) {
+    constexpr int STEP = S::STEP, DP = S::DP, STREAMS = S::STREAMS, NSLOT = S::NSLOT, SW = S::SW, LW = S::LW;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     static_assert(sizeof(TreeControl<S>) <= S::CONTROL, "the control block fits");
     // the tiles begin at a multiple of 1024, the control block lies before or behind them
@@ -320,7 +335,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
     const uint32_t bar0 = smem_addr(ctl.bars);
     const uint32_t full = bar0, empty = full + 8 * NSLOT, q_full = empty + 8 * NSLOT, q_empty = q_full + 8;
     const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, o_free = o_full + 8;
-    const uint32_t pv_done = o_free + 8;
+    const uint32_t pv_done = o_free + 8, raw_full = pv_done + 8;
     TreePart* heads = static_cast<TreePart*>(a.workspace);
     float* parts = reinterpret_cast<float*>(heads + ctas);
 
@@ -329,11 +344,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
         for (uint32_t e = tid; e < (STREAMS * S::QTILE + NSLOT * S::SLOT) / 16; e += S::THREADS)
             tree_store16(base + 16 * e, make_uint4(0, 0, 0, 0));
     if (tid < NSLOT) {
-        mbar_init(full + 8 * tid, PW);
+        mbar_init(full + 8 * tid, 1);
         mbar_init(empty + 8 * tid, 1);
     }
     if (tid == 0) {
-        mbar_init(q_full, PW);
+        mbar_init(q_full, 1);
+        for (int s = 0; s < S::NRAW; ++s) mbar_init(raw_full + 8 * s, 1);
         mbar_init(q_empty, 1 + SW);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + 8 * s, 2);  // the MMAs are done; what the producers noted can be seen
@@ -430,7 +446,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
     auto tile_of = [&](const TreeSeq& s, int step) {
         return step < s.sink_tiles ? step : s.tile0 + step - s.sink_tiles;
     };
-    auto wait = [&](uint32_t bar, uint32_t phase) { mbar_wait_warp(bar, phase, &ctl.abort_flag, a.status, a.timeout_ns); };
+    auto wait = [&](uint32_t bar, uint32_t phase) { tree_wait(bar, phase, &ctl.abort_flag, a.status, a.timeout_ns); };
 
     TreeSeg seg{};
     bool more = locate(seg);
@@ -444,9 +460,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
     }
 
     if (warp >= SW && warp < S::MMA_WARP) {
-        // ================= producers =================
-        const int pw = warp - SW;
-        constexpr int CH = S::CH, RW = S::RW;
+        // ================= loaders =================
+        // Steps whose tokens all rows see come by tensor copies, issued by one warp (keys) and another
+        // (values), a box per lane.  The others, at the ends of what is visible, are loaded by all three: a row
+        // of zeros for what no row sees, and values made finite where some row does not see them.
+        const int lw = warp - SW;
+        constexpr int CH = S::CH;
         const int row_chunks = a.head_dim / 8;        // of 16-bit values
         auto page_of = [&](int tok) { return page_shift >= 0 ? tok >> page_shift : tok / a.page_size; };
         // the shared-memory address of chunk c of row r, from a tile of `rows` rows
@@ -455,36 +474,18 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
         };
         int slot = 0;
         uint32_t phase = 0, q_phase = 0;
-        // slots whose copies are under way, the newest first
-        uint32_t pend[3] = {0, 0, 0};
-        auto signal = [&](uint32_t bar) {  // this warp's part of it is there
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-        };
-        auto push = [&](uint32_t bar) {
-            tree_commit();
-            if (pend[2]) {
-                tree_wait_copies<3>();
-                signal(pend[2]);
-            }
-            pend[2] = pend[1], pend[1] = pend[0], pend[0] = bar;
-        };
-        auto flush = [&]() {
-            if (pend[2]) { tree_wait_copies<2>(); signal(pend[2]); }
-            if (pend[1]) { tree_wait_copies<1>(); signal(pend[1]); }
-            if (pend[0]) { tree_wait_copies<0>(); signal(pend[0]); }
-            pend[0] = pend[1] = pend[2] = 0;
-        };
-        // waits until a slot (or the queries' place) is free; what is under way is handed on first, as the
-        // consumers may need it to free anything
-        auto wait_free = [&](uint32_t bar, uint32_t ph) {
-            if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, ph))) return;
-            flush();
-            wait(bar, ph);
-        };
+        int raw_in = 0, raw_out = 0;        // of the 8-bit tiles
+        uint32_t raw_phase = 0;
+        bool first_segment = true;
         auto next_slot = [&]() {
             if (++slot == NSLOT) slot = 0, phase ^= 1u;
+        };
+        auto loaders_sync = [&]() { asm volatile("bar.sync 2, %0;" ::"n"(32 * LW) : "memory"); };
+        // what all loaders wrote is there: for the MMAs, which read it through the other proxy
+        auto all_there = [&](uint32_t bar) {
+            fence_proxy_async_smem();
+            loaders_sync();
+            if (lw == 0 && lane == 0) mbar_arrive(bar);
         };
         while (more) {
             const TreeSeq& sq = seg.seq;
@@ -503,85 +504,100 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                 lo = max(0, min(ctx, ctx + least - a.window));
             }
             const int edge = a.window > 0 ? ctx + sq.n - a.window : 0;  // tokens from here on are in every window
-            auto token_of = [&](int step) { return tile_of(sq, step) * STEP + pw * RW + lane; };
-            auto wants = [&](int step, int tok) {
-                return step < seg.step_end && lane < RW && tok < sq.len && (tok >= lo || tok < a.sinks);
+            auto clean = [&](int step) {   // all rows see all tokens
+                const int tok0 = tile_of(sq, step) * STEP;
+                return box_rows > 0 && tok0 + STEP <= ctx && (tok0 >= edge || tok0 + STEP <= a.sinks);
             };
-            auto fetch = [&](int step) {  // the page of this lane's token
-                const int tok = token_of(step);
-                return wants(step, tok) ? table[page_of(tok)] : 0;
+            auto bad = [&]() {
+                record_status(a.status, kDecInvalidArg);
+                *static_cast<volatile int*>(&ctl.bad_page) = 1;
             };
-            const char* kbase = static_cast<const char*>(a.kc.p) + kvh * a.kc.head_stride * S::ES;
-            const char* vbase = static_cast<const char*>(a.vc.p) + kvh * a.vc.head_stride * S::ES;
-            int pid = fetch(seg.step), pid1 = fetch(seg.step + 1);
 
-            // this lane's row of a step: where its key and value stand (-1: nowhere)
-            int64_t kat, vat;
-            uint32_t mixed;   // rows of this warp that not every query row sees
+            // ---- tensor copies: lane -> box of box_rows tokens and, of 16-bit values, 64 columns ----
+            const int boxes = box_rows > 0 ? STEP / box_rows : 1;   // of a step's tokens
+            const int bg = lane % boxes, bb = lane / boxes;
+            const bool has_box = bb < (S::E4M3 ? 1 : S::BLOCKS);
+            auto box_page = [&](int step) {
+                return has_box && step < seg.step_end && clean(step) ? table[page_of(tile_of(sq, step) * STEP + bg * box_rows)] : 0;
+            };
+            auto issue = [&](uint32_t dst, uint32_t bar, uint32_t bytes, const CUtensorMap* map, int step, int page) {
+                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                __syncwarp();
+                if (has_box) {
+                    const int tok = tile_of(sq, step) * STEP + bg * box_rows;
+                    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) bad(), page = a.num_pages;  // zeros
+                    const uint32_t to = S::E4M3 ? dst + bg * box_rows * DP : dst + bb * STEP * 128 + bg * box_rows * 128;
+                    tma_tensor_4d_g2s(to, map, 64 * bb, tok - page_of(tok) * a.page_size, kvh, page, bar);
+                }
+                __syncwarp();
+            };
+
+            // ---- by all loaders: lanes 0 .. 15 and 16 .. 31 have the tokens of the warp's first two groups, ----
+            // ---- those of its third are in a second set of registers                                      ----
+            constexpr int MINE = (S::GROUPS + LW - 1) / LW, SETS = (MINE + 1) / 2;
+            int64_t kat[SETS], vat[SETS];   // where their keys and values stand (-1: nowhere)
+            uint32_t mixed[SETS];           // tokens that not every row sees
             auto look = [&](int step) {
-                const int tok = token_of(step);
-                const bool wanted = wants(step, tok);
-                const bool ok = wanted && static_cast<unsigned>(pid) < static_cast<unsigned>(a.num_pages);
-                if (wanted && !ok) {
-                    record_status(a.status, kDecInvalidArg);
-                    *static_cast<volatile int*>(&ctl.bad_page) = 1;
-                }
-                const int64_t in_page = tok - page_of(tok) * a.page_size;
-                kat = ok ? (pid * a.kc.page_stride + in_page * a.kc.slot_stride) * S::ES : -1;
-                vat = ok ? (pid * a.vc.page_stride + in_page * a.vc.slot_stride) * S::ES : -1;
-                mixed = __ballot_sync(0xFFFFFFFFu, ok && (tok >= ctx || (tok < edge && tok >= a.sinks)));
-                pid = pid1;
-                pid1 = fetch(step + 2);
-            };
-            // one side of a step by asynchronous copies
-            auto copy = [&](uint32_t dst, const char* from, int64_t at) {
-                constexpr int RPI = 32 / CH;
-                const int c = lane % CH, sub = lane / CH;
 #pragma unroll
-                for (int r0 = 0; r0 < RW; r0 += RPI) {
-                    const int64_t off = __shfl_sync(0xFFFFFFFFu, at, r0 + sub);
-                    const int r = pw * RW + r0 + sub;
-                    if (c < row_chunks)
-                        tree_copy16(dst + at_smem(STEP, r, c), off >= 0 ? from + off + 16 * c : from, off >= 0 ? 16 : 0);
+                for (int s = 0; s < SETS; ++s) {
+                    const int group = lw + LW * (2 * s + lane / 16);
+                    const int tok = tile_of(sq, step) * STEP + group * 16 + lane % 16;
+                    const bool wanted = group < S::GROUPS && tok < sq.len && (tok >= lo || tok < a.sinks);
+                    const int in = wanted ? page_of(tok) : 0, pid = wanted ? table[in] : 0;
+                    const bool ok = wanted && static_cast<unsigned>(pid) < static_cast<unsigned>(a.num_pages);
+                    if (wanted && !ok) bad();
+                    const int64_t in_page = tok - static_cast<int64_t>(in) * a.page_size;
+                    kat[s] = ok ? (pid * a.kc.page_stride + in_page * a.kc.slot_stride + kvh * a.kc.head_stride) * S::ES : -1;
+                    vat[s] = ok ? (pid * a.vc.page_stride + in_page * a.vc.slot_stride + kvh * a.vc.head_stride) * S::ES : -1;
+                    mixed[s] = __ballot_sync(0xFFFFFFFFu, ok && (tok >= ctx || (tok < edge && tok >= a.sinks)));
                 }
             };
-            // the same through registers, eight loads at a time, with values that some row must not see made finite
             constexpr int FC = DP * S::ES / 16;            // chunks of a row in the cache
             constexpr int LR = 32 / FC;                    // rows of one load of the warp
-            constexpr int LN = RW / LR < 8 ? RW / LR : 8;  // loads
-            auto load = [&](uint4 (&v)[LN], const char* from, int64_t at, int r0) {
-                const int c = lane % FC, sub = lane / FC;
+            constexpr int LN = 16 / LR < 8 ? 16 / LR : 8;  // loads at a time
+            const int fc = lane % FC, fsub = lane / FC;
+            auto put = [&](uint32_t dst, uint4 v, int r) { // chunk fc of row r, from the cache's type
+                if constexpr (S::E4M3) {
+                    if (2 * fc >= row_chunks) return;
+                    const uint32_t* w = &v.x;
+                    uint32_t h[8];
 #pragma unroll
-                for (int x = 0; x < LN; ++x) {
-                    const int64_t off = __shfl_sync(0xFFFFFFFFu, at, r0 + x * LR + sub);
-                    v[x] = make_uint4(0, 0, 0, 0);
-                    if (off >= 0 && 16 * c < a.head_dim * S::ES) v[x] = __ldg(reinterpret_cast<const uint4*>(from + off) + c);
+                    for (int e = 0; e < 4; ++e) {
+                        h[2 * e] = dec_e4m3x2_to_f16x2(w[e]);
+                        h[2 * e + 1] = dec_e4m3x2_to_f16x2(w[e] >> 16);
+                    }
+                    tree_store16(dst + at_smem(STEP, r, 2 * fc), make_uint4(h[0], h[1], h[2], h[3]));
+                    tree_store16(dst + at_smem(STEP, r, 2 * fc + 1), make_uint4(h[4], h[5], h[6], h[7]));
+                } else {
+                    if (fc < row_chunks) tree_store16(dst + at_smem(STEP, r, fc), v);
                 }
             };
-            auto store = [&](uint32_t dst, uint4 (&v)[LN], uint32_t some, int r0) {
-                const int c = lane % FC, sub = lane / FC;
+            auto fill = [&](uint32_t dst, const void* from, const int64_t (&at)[SETS], bool values) {
 #pragma unroll
-                for (int x = 0; x < LN; ++x) {
-                    const int in = r0 + x * LR + sub, r = pw * RW + in;
-                    if ((some >> in) & 1u) {
-                        bool any;
-                        if constexpr (S::E4M3) any = tree_scrub_e4m3(v[x]);
-                        else any = tree_scrub<S::BF>(v[x]);
-                        if (any) *static_cast<volatile int*>(&ctl.dirty) = 1;
-                    }
-                    if constexpr (S::E4M3) {
-                        if (2 * c >= row_chunks) continue;
-                        const uint32_t* w = &v[x].x;
-                        uint32_t h[8];
+                for (int n = 0; n < MINE; ++n) {
+                    const int group = lw + LW * n;
+                    if (group >= S::GROUPS) break;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < 16; r0 += LN * LR) {
+                        uint4 v[LN];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            h[2 * e] = dec_e4m3x2_to_f16x2(w[e]);
-                            h[2 * e + 1] = dec_e4m3x2_to_f16x2(w[e] >> 16);
+                        for (int x = 0; x < LN; ++x) {
+                            const int64_t off = __shfl_sync(0xFFFFFFFFu, at[n / 2], n % 2 * 16 + r0 + x * LR + fsub);
+                            v[x] = make_uint4(0, 0, 0, 0);
+                            if (off >= 0 && 16 * fc < a.head_dim * S::ES)
+                                v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(from) + off) + fc);
                         }
-                        tree_store16(dst + at_smem(STEP, r, 2 * c), make_uint4(h[0], h[1], h[2], h[3]));
-                        tree_store16(dst + at_smem(STEP, r, 2 * c + 1), make_uint4(h[4], h[5], h[6], h[7]));
-                    } else if (c < row_chunks) {
-                        tree_store16(dst + at_smem(STEP, r, c), v[x]);
+#pragma unroll
+                        for (int x = 0; x < LN; ++x) {
+                            const int in = r0 + x * LR + fsub;
+                            if (values && (mixed[n / 2] >> (n % 2 * 16 + in) & 1u)) {
+                                bool any;
+                                if constexpr (S::E4M3) any = tree_scrub_e4m3(v[x]);
+                                else any = tree_scrub<S::BF>(v[x]);
+                                if (any) *static_cast<volatile int*>(&ctl.dirty) = 1;
+                            }
+                            put(dst, v[x], group * 16 + in);
+                        }
                     }
                 }
             };
@@ -589,117 +605,129 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                 // f = |scale k_scale|; a negative or zero product is folded into the queries
                 const float f = a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f);
                 const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu, flip = f < 0.0f ? 0x80008000u : 0u;
-                const int row0 = row0_of(seg), rows = rows_of(seg), tiles = rows > kTreeRows ? 2 : 1;
+                const int row0 = row0_of(seg), rows = rows_of(seg), padded = rows > kTreeRows ? 2 * kTreeRows : kTreeRows;
                 constexpr int RPI = 32 / CH;
                 const int c = lane % CH, sub = lane / CH;
-                wait_free(q_empty, q_phase ^ 1u);
+                wait(q_empty, q_phase ^ 1u);
                 q_phase ^= 1u;
-                for (int t = 0; t < tiles; ++t) {
-                    const uint32_t dst = q_smem + t * S::QTILE;
-                    constexpr int PER = kTreeRows / PW, AT = 4 * RPI < PER ? 4 * RPI : PER;
-                    for (int r0 = pw * PER; r0 < (pw + 1) * PER; r0 += AT) {
-                        uint4 v[AT / RPI];
+                constexpr int AT = 8;   // loads at a time
+#pragma unroll 1
+                for (int n0 = lw * RPI + sub; n0 < padded; n0 += AT * LW * RPI) {
+                    uint4 v[AT];
 #pragma unroll
-                        for (int x = 0; x < AT / RPI; ++x) {
-                            const int r = r0 + x * RPI + sub, row = row0 + t * kTreeRows + r;
-                            v[x] = make_uint4(0, 0, 0, 0);
-                            if (t * kTreeRows + r < rows && c < row_chunks) {
-                                const int i = row / G, h = row - i * G;
-                                v[x] = *(reinterpret_cast<const uint4*>(
-                                    a.q + static_cast<int64_t>(sq.first + i) * a.ldq +
-                                    static_cast<int64_t>(kvh * G + h) * a.head_dim) + c);
-                            }
+                    for (int x = 0; x < AT; ++x) {
+                        const int n = n0 + x * LW * RPI, row = row0 + n, i = row / G;
+                        v[x] = make_uint4(0, 0, 0, 0);
+                        if (n < rows && c < row_chunks)
+                            v[x] = *(reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(sq.first + i) * a.ldq +
+                                                                    static_cast<int64_t>(kvh * G + row - i * G) * a.head_dim) + c);
+                    }
+#pragma unroll
+                    for (int x = 0; x < AT; ++x) {
+                        const int n = n0 + x * LW * RPI, t = n / kTreeRows, r = n % kTreeRows;
+                        uint32_t* w = &v[x].x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ flip;
+                        // bf16 queries against an 8-bit cache, whose MMA is fp16: scaled by a power of two
+                        // that brings the row's largest to 2^8 .. 2^9
+                        if constexpr (S::E4M3 && S::DT == 1) {
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+#pragma unroll
+                            for (int d = CH / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                            const int e2 = min(static_cast<int>(top >> 7) - 127, 127);
+                            const int exponent = e2 > -119 ? e2 - 8 : 0;
+                            const float up = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = dec_pack2<0>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                            if (c == 0 && n < padded) ctl.qe[t][r] = static_cast<int8_t>(exponent);
                         }
-#pragma unroll
-                        for (int x = 0; x < AT / RPI; ++x) {
-                            const int r = r0 + x * RPI + sub;
-                            uint32_t* w = &v[x].x;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ flip;
-                            // bf16 queries against an 8-bit cache, whose MMA is fp16: scaled by a power of two
-                            // that brings the row's largest to 2^8 .. 2^9
-                            int exponent = 0;
-                            if constexpr (S::E4M3 && S::DT == 1) {
-                                uint32_t top = 0;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
-#pragma unroll
-                                for (int d = CH / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                                const int e2 = min(static_cast<int>(top >> 7) - 127, 127);
-                                if (e2 > -119) exponent = e2 - 8;
-                                const float up = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = dec_pack2<0>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-                            }
-                            if (c < row_chunks) tree_store16(dst + at_smem(kTreeRows, r, c), v[x]);
-                            if (S::E4M3 && S::DT == 1 && c == 0) ctl.qe[t][r] = static_cast<int8_t>(exponent);
-                        }
+                        if (n < padded && c < row_chunks) tree_store16(q_smem + t * S::QTILE + at_smem(kTreeRows, r, c), v[x]);
                     }
                 }
-                signal(q_full);
+                all_there(q_full);
             };
-
+            // At the CTA's start the queries come first; else behind the first step, as their place is taken
+            // until the item before has its last scores.
+            auto fill_step = [&](int st) {
+                look(st);
+                wait(empty + 8 * slot, phase ^ 1u);
+                fill(ring + slot * S::SLOT, a.kc.p, kat, false);
+                all_there(full + 8 * slot);
+                next_slot();
+                wait(empty + 8 * slot, phase ^ 1u);
+                fill(ring + slot * S::SLOT, a.vc.p, vat, true);
+                all_there(full + 8 * slot);
+                next_slot();
+            };
             if constexpr (S::E4M3) {
-                // a step's keys and values as one line of loads, those of the next eight under way
-                constexpr int PER = LN * LR, PIECES = 2 * RW / PER;  // rows of a piece, pieces of a step
-                uint4 v0[LN];
-                look(seg.step);
-                load(v0, kbase, kat, 0);
-                for (int st = seg.step; st < seg.step_end; ++st) {
-                    const uint32_t some = mixed;
-#pragma unroll
-                    for (int x = 0; x < PIECES; ++x) {
-                        const int r0 = x * PER % RW;
-                        if (r0 == 0) wait_free(empty + 8 * slot, phase ^ 1u);
-                        uint4 v1[LN];
-                        if (x + 1 < PIECES) {
-                            const bool values = (x + 1) * PER >= RW;
-                            load(v1, values ? vbase : kbase, values ? vat : kat, (x + 1) * PER % RW);
-                        } else if (st + 1 < seg.step_end) {
-                            look(st + 1);
-                            load(v1, kbase, kat, 0);
-                        }
-                        store(ring + slot * S::SLOT, v0, x * PER >= RW ? some : 0u, r0);
-                        if (r0 + PER == RW) {
-                            signal(full + 8 * slot);
-                            next_slot();
-                        }
-#pragma unroll
-                        for (int e = 0; e < LN; ++e) v0[e] = v1[e];
+                constexpr int NRAW = S::NRAW;
+                const uint32_t raw = ring + NSLOT * S::SLOT;
+                // tensor copies run ahead of the conversions: 2 st + side of the next one to issue
+                int ahead = 2 * seg.step, pid = box_page(seg.step);
+                auto issue_next = [&]() {
+                    while (ahead < 2 * seg.step_end && !clean(ahead >> 1)) {
+                        ahead += 2;
+                        pid = box_page(ahead >> 1);
                     }
-                    if (st == seg.step) load_queries();
+                    if (ahead >= 2 * seg.step_end) return;
+                    if (lw == 0) {
+                        issue(raw + raw_in * S::RAW, raw_full + 8 * raw_in, S::RAW, ahead & 1 ? &vmap : &kmap, ahead >> 1, pid);
+                        if (ahead & 1) pid = box_page((ahead + 1) >> 1);
+                    }
+                    ++ahead;
+                    if (++raw_in == NRAW) raw_in = 0;
+                };
+                for (int x = 0; x < NRAW; ++x) issue_next();
+                load_queries();
+                for (int st = seg.step; st < seg.step_end; ++st) {
+                    if (!clean(st)) {
+                        fill_step(st);
+                        continue;
+                    }
+#pragma unroll 1
+                    for (int side = 0; side < 2; ++side) {
+                        wait(empty + 8 * slot, phase ^ 1u);
+                        wait(raw_full + 8 * raw_out, raw_phase);
+                        const uint32_t from = raw + raw_out * S::RAW, dst = ring + slot * S::SLOT;
+#pragma unroll 4
+                        for (int r = lw * LR + fsub; r < STEP; r += LW * LR) put(dst, lds_v4(from + r * DP + 16 * fc), r);
+                        all_there(full + 8 * slot);
+                        next_slot();
+                        if (++raw_out == NRAW) raw_out = 0, raw_phase ^= 1u;
+                        issue_next();
+                    }
                 }
             } else {
+                const bool queries_first = first_segment;
+                first_segment = false;
+                if (queries_first) load_queries();
+                int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
                 for (int st = seg.step; st < seg.step_end; ++st) {
-                    look(st);
-                    wait_free(empty + 8 * slot, phase ^ 1u);
-                    copy(ring + slot * S::SLOT, kbase, kat);
-                    push(full + 8 * slot);
-                    next_slot();
-                    wait_free(empty + 8 * slot, phase ^ 1u);
-                    if (mixed) {
-#pragma unroll 1
-                        for (int r0 = 0; r0 < RW; r0 += LN * LR) {
-                            uint4 v[LN];
-                            load(v, vbase, vat, r0);
-                            store(ring + slot * S::SLOT, v, mixed, r0);
+                    if (clean(st)) {
+                        // Keys by warp 0, values by warp 1.  All wait for the slots and for one another: no
+                        // warp is ever a round of the ring ahead of or behind a barrier's one bit of phase.
+                        for (int side = 0; side < 2; ++side) {
+                            wait(empty + 8 * slot, phase ^ 1u);
+                            if (lw == side)
+                                issue(ring + slot * S::SLOT, full + 8 * slot, S::SLOT, side ? &vmap : &kmap, st, pid);
+                            next_slot();
                         }
-                        signal(full + 8 * slot);
+                        loaders_sync();
                     } else {
-                        copy(ring + slot * S::SLOT, vbase, vat);
-                        push(full + 8 * slot);
+                        fill_step(st);
                     }
-                    next_slot();
-                    if (st == seg.step) load_queries();
+                    pid = pid1;
+                    pid1 = box_page(st + 2);
+                    if (st == seg.step && !queries_first) load_queries();
                 }
             }
             more = after(seg);
         }
-        flush();
-    } else if (warp >= S::MMA_WARP) {
+    } else if (warp == S::MMA_WARP) {
         // ================= the MMAs =================
-        if (warp != S::MMA_WARP) more = false;
         constexpr int TYPE = S::BF ? 1 : 0;
         constexpr uint32_t idesc_s = idesc_f16(TYPE, 128, STEP), idesc_o = idesc_f16(TYPE, 128, DP) | kIdescBMajorMn;
         int slot = 0;                       // of the ring, in the order in which the producers fill it
@@ -723,7 +751,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
             tc_fence_after();
             const uint32_t d = tmem + S::TM_O + (STREAMS == 2 ? p_buf : 0) * DP, p = tmem + p_buf * STEP;
             const uint64_t v = sw128_desc_mn(ring + p_slot * S::SLOT, STEP * 128);
-#pragma unroll
+#pragma unroll 2
             for (int kb = 0; kb < STEP / 16; kb += 2) tc_mma_pv2(d, p + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || !p_fresh);
             tc_commit_lane0(empty + 8 * p_slot, p_frees);
             if (STREAMS == 1) tc_commit_lane0(pv_done);
@@ -732,19 +760,22 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
             __syncwarp();
             open = false;
         };
-        while (more) {
-            const int rows = rows_of(seg);
-            const bool dual = rows > kTreeRows;
-            const int steps = seg.step_end - seg.step, jobs = dual ? 2 * steps : steps;
-            int k_slot = slot;
-            uint32_t k_phase = ring_phase;
-            for (int j = 0; j < jobs; ++j, ++job) {
-                const int buf = job & 1;
-                if (j == 0) {
-                    wait(q_full, q_phase);
-                    q_phase ^= 1u;
-                }
-                const bool second = dual && (j & 1);
+        // S of a job, then P V of the job before, across the ends of items.
+        int j = 0, jobs = 0, k_slot = 0;
+        uint32_t k_phase = 0;
+        bool dual = false, fresh = true;   // fresh: seg has not been begun
+        for (;;) {
+            if (more && fresh) {
+                dual = rows_of(seg) > kTreeRows;
+                jobs = (seg.step_end - seg.step) << (dual ? 1 : 0);
+                j = 0;
+                fresh = false;
+                wait(q_full, q_phase);
+                q_phase ^= 1u;
+            }
+            const int buf = job & 1;
+            const bool second = dual && (j & 1);
+            if (more) {
                 if (!second) {
                     k_slot = slot, k_phase = ring_phase;
                     if (++slot == NSLOT) slot = 0, ring_phase ^= 1u;
@@ -760,22 +791,26 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                 tc_commit_lane0(q_empty, j == jobs - 1);
                 if (lane == 0) mbar_arrive(s_full + 8 * buf);
                 __syncwarp();
-                if (open) issue_pv();
-                open = true;
-                p_buf = buf;
-                p_begins = j == 0;
-                // the first of its stream: it begins the sums
-                p_fresh = STREAMS == 2 ? j < 2 : j == 0;
-                p_last = j == jobs - 1;
-                p_frees = !dual || second;
-                if (!second) {
-                    p_slot = slot, p_ring_phase = ring_phase;
-                    if (++slot == NSLOT) slot = 0, ring_phase ^= 1u;
-                }
             }
-            more = after(seg);
+            if (open) issue_pv();
+            if (!more) break;
+            open = true;
+            p_buf = buf;
+            p_begins = j == 0;
+            // the first of its stream: it begins the sums
+            p_fresh = STREAMS == 2 ? j < 2 : j == 0;
+            p_last = j == jobs - 1;
+            p_frees = !dual || second;
+            if (!second) {
+                p_slot = slot, p_ring_phase = ring_phase;
+                if (++slot == NSLOT) slot = 0, ring_phase ^= 1u;
+            }
+            ++job;
+            if (++j == jobs) {
+                more = after(seg);
+                fresh = true;
+            }
         }
-        if (open) issue_pv();
     } else {
         // ================= softmax =================
         constexpr float kShift = S::BF ? 0.0f : 7.0f;  // fp16 weights are scaled by 2^7
@@ -849,32 +884,38 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                         }
                     return v;
                 };
-                // Twice over S, 16 tokens at a time, the next ones' load under way.
-                constexpr int NC = STEP / 16;
-                uint32_t xa[16], xb[16];
+                if (masked) {  // -infinity, in TMEM, for what the row does not see
+#pragma unroll 1
+                    for (int c = 0; c < STEP; c += 16) {
+                        const uint32_t seen = seen_of(tok0 + c);
+                        uint32_t x[16];
+                        tmem_ld16(s_at + c, x);
+                        tmem_wait_ld16(x);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = (seen >> e) & 1u ? x[e] : 0xFF800000u;
+                        tmem_st16(s_at + c, x);
+                    }
+                    tmem_wait_st();
+                }
+                // Twice over S, 32 tokens at a time, the next ones' load (some 200 cycles beside the MMAs) under
+                // way.  In loops: with the row's code in one line the roles' code is fetched anew from beyond the
+                // SM in every step (32 ragged sequences, trees of 32: 336 us).
+                constexpr int NC = STEP / 32;
+                uint32_t xa[32], xb[32];
                 float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                uint32_t seen = ~0u;     // of 32 tokens
-                auto hide = [&](uint32_t (&x)[16], uint32_t bits) {
-                    if (!masked) return;
+                auto highest = [&](const uint32_t (&x)[32]) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = (bits >> e) & 1u ? x[e] : 0xFF800000u;
-                };
-                auto highest = [&](const uint32_t (&x)[16]) {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2)
+                    for (int e = 0; e < 32; e += 2)
                         t4[e / 2 & 3] = max3_nan(t4[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                 };
-                tmem_ld16(s_at, xa);
+                tmem_ld32(s_at, xa);
 #pragma unroll 1
                 for (int c = 0; c < NC; c += 2) {
-                    if (masked) seen = seen_of(tok0 + 16 * c);
-                    tmem_wait_ld16(xa);
-                    tmem_ld16(s_at + 16 * (c + 1), xb);
-                    hide(xa, seen);
+                    tmem_wait_ld32(xa);
+                    tmem_ld32(s_at + 32 * (c + 1), xb);
                     highest(xa);
-                    tmem_wait_ld16(xb);
-                    tmem_ld16(s_at + 16 * ((c + 2) & (NC - 1)), xa);
-                    hide(xb, seen >> 16);
+                    tmem_wait_ld32(xb);
+                    tmem_ld32(s_at + 32 * ((c + 2) & (NC - 1)), xa);
                     highest(xb);
                 }
                 const float top = f * tree_max(tree_max(t4[0], t4[1]), tree_max(t4[2], t4[3]));
@@ -887,25 +928,27 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                     if (!first) {
                         if constexpr (STREAMS == 1) wait(pv_done, (pv_jobs - 1) & 1u);
                         tc_fence_after();
-                        tmem_wait_ld16(xa);
+                        tmem_wait_ld32(xa);
 #pragma unroll 1
                         for (int c = 0; c < DP; c += 16) {
-                            tmem_ld16(o_at + c, xb);
-                            tmem_wait_ld16(xb);
+                            uint32_t y[16];
+                            tmem_ld16(o_at + c, y);
+                            tmem_wait_ld16(y);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) xb[e] = __float_as_uint(__uint_as_float(xb[e]) * scale);
-                            tmem_st16(o_at + c, xb);
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * scale);
+                            tmem_st16(o_at + c, y);
                         }
                     }
                 }
                 uint64_t l2[2] = {0, 0};
                 const uint64_t f2 = pack_f2(f, f), ref2 = pack_f2(-ref, -ref);
-                auto weights = [&](const uint32_t (&x)[16], int c) {
+                auto weights = [&](const uint32_t (&x)[32], int h, uint32_t to) {
                     uint32_t y[16];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
+                        const uint32_t* xe = &x[h + e];
                         float p0, p1;
-                        unpack_f2(fma_f2(pack_f2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2, ref2), p0, p1);
+                        unpack_f2(fma_f2(pack_f2(__uint_as_float(xe[0]), __uint_as_float(xe[1])), f2, ref2), p0, p1);
                         p0 = tree_exp2(p0);
                         p1 = tree_exp2(p1);
                         l2[e / 2 & 1] = add_f2(l2[e / 2 & 1], pack_f2(p0, p1));
@@ -920,33 +963,31 @@ __global__ void __launch_bounds__(S::THREADS, 1) tree_kernel(TreeArgs a, int pag
                                                          __uint_as_float((b1 & 0xFFFF0000u) ^ 0x80000000u));
                             unpack_f2(fma_f2(pack_f2(p0, p1), pack_f2(1.0f + 0x1p-22f, 1.0f + 0x1p-22f), cut), low0, low1);
                         } else {
-                            if constexpr (S::E4M3) {
-                                hi = dec_pack2<0>(p0, p1);
-                            } else {
-                                constexpr float kLess = 1.0f - 0x1p-10f;
-                                asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;"
-                                    : "=r"(hi) : "f"(fmaf(p1, kLess, -0x1p-24f)), "f"(fmaf(p0, kLess, -0x1p-24f)));
-                            }
-                            low0 = p0 - dec_to_f32<0>(static_cast<uint16_t>(hi & 0xFFFFu));
-                            low1 = p1 - dec_to_f32<0>(static_cast<uint16_t>(hi >> 16));
+                            // likewise, to 10 bits; over 16-bit caches of a weight less 2^-10 of it
+                            float c0 = p0, c1 = p1;
+                            if constexpr (!S::E4M3)
+                                unpack_f2(mul_f2(pack_f2(p0, p1), pack_f2(1.0f - 0x1p-10f, 1.0f - 0x1p-10f)), c0, c1);
+                            asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(c1), "f"(c0));
+                            const uint64_t cut = pack_f2(__uint_as_float((__float_as_uint(c0) & 0xFFFFE000u) ^ 0x80000000u),
+                                                         __uint_as_float((__float_as_uint(c1) & 0xFFFFE000u) ^ 0x80000000u));
+                            unpack_f2(add_f2(pack_f2(p0, p1), cut), low0, low1);
                         }
                         // of a block of 16 tokens the high parts in columns 0 .. 7, the low ones in 8 .. 15
                         y[e / 2] = hi;
                         y[e / 2 + 8] = dec_pack2<S::BF ? 1 : 0>(low0, low1);
                     }
-                    tmem_st16(s_at + 16 * c, y);
+                    tmem_st16(to, y);
                 };
 #pragma unroll 1
                 for (int c = 0; c < NC; c += 2) {
-                    if (masked) seen = seen_of(tok0 + 16 * c);
-                    tmem_wait_ld16(xa);
-                    tmem_ld16(s_at + 16 * (c + 1), xb);
-                    hide(xa, seen);
-                    weights(xa, c);
-                    tmem_wait_ld16(xb);
-                    if (c + 2 < NC) tmem_ld16(s_at + 16 * (c + 2), xa);
-                    hide(xb, seen >> 16);
-                    weights(xb, c + 1);
+                    tmem_wait_ld32(xa);
+                    tmem_ld32(s_at + 32 * (c + 1), xb);
+                    weights(xa, 0, s_at + 32 * c);
+                    weights(xa, 16, s_at + 32 * c + 16);
+                    tmem_wait_ld32(xb);
+                    if (c + 2 < NC) tmem_ld32(s_at + 32 * (c + 2), xa);
+                    weights(xb, 0, s_at + 32 * c + 32);
+                    weights(xb, 16, s_at + 32 * c + 48);
                 }
                 {
                     float s0, s1;
@@ -1129,8 +1170,15 @@ template <class S>
 int launch_tree_shape(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stream) {
     if (cudaFuncSetAttribute(tree_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess)
         return -3;
+    // Boxes of the largest power of two of tokens that divides the pages: from 8 on, the rows of one
+    // swizzle pattern.  Other pages, and heads or slots of stride 0, are read without tensor maps.
+    int box = a.page_size & -a.page_size;
+    box = box < S::STEP ? box : S::STEP;
+    CUtensorMap maps[2] = {};
+    if (box < 8 || !tree_map(&maps[0], a, a.kc, S::E4M3, S::DP, box) || !tree_map(&maps[1], a, a.vc, S::E4M3, S::DP, box))
+        box = 0;
     const int rc = launch_dependent(tree_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), dim3(S::THREADS),
-                                    S::SMEM, stream, a, power_of_two(a.page_size));
+                                    S::SMEM, stream, a, power_of_two(a.page_size), box, maps[0], maps[1]);
     if (rc != 0) return rc;
     return launch_dependent(tree_join_kernel<S::DT, S::DP, !S::BF>, dim3(static_cast<unsigned>(ctx.num_sms), 16),
                             dim3(128), 0, stream, a, ctx.num_sms);
