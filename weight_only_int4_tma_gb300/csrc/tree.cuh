@@ -123,52 +123,26 @@ __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatil
     if (!mbar_try_wait(bar, parity)) tree_wait_slow(bar, parity, abort_flag, status, limit_ns);
     __syncwarp();
 }
-// Four MMAs, kind::f16, issued by lane 0 while the whole warp executes the statement (no branch
-// around it, so that the operands stay warp-uniform; with one around single MMAs the warp took 130 cycles
-// for each): D[tmem] (+)= A[smem] . B[smem]^T, both K-major, over the 64 values of a 128-byte row.
-__device__ __forceinline__ void tc_mma_ss4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One lane of a converged warp, always the same: a branch on it is known to be a single thread's.
+__device__ __forceinline__ bool tree_elect() {
+    uint32_t p;
     asm volatile(
-        "{\n\t.reg .pred p, q, e;\n\t.reg .b32 l;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-        "mov.u32 l, %%laneid;\n\t"
-        "setp.eq.u32 e, l, 0;\n\t"
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// A value that is the same in all lanes, known to be.
+__device__ __forceinline__ uint32_t tree_uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+// D[tmem] (+)= A[smem] . B[smem]^T, kind::f16.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %3, 0;\n\t"  // idesc is never 0: a true predicate
-        "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
-        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc),
-        "r"(accumulate)
-        : "memory");
-}
-// Two blocks of 16 tokens: D (+)= (P high + P low) . V, the parts 8 TMEM columns apart, the blocks 16
-// columns and 2048 bytes of V (MN-major).
-__device__ __forceinline__ void tc_mma_pv2(uint32_t d_tmem, uint32_t p_tmem, uint64_t v, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q, e;\n\t.reg .b32 l;\n\t.reg .b64 v1;\n\t"
-        "mov.u32 l, %%laneid;\n\t"
-        "setp.eq.u32 e, l, 0;\n\t"
-        "setp.ne.b32 p, %7, 0;\n\t"
-        "setp.ne.b32 q, %6, 0;\n\t"
-        "add.u64 v1, %5, 128;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %6, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %5, %6, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], v1, %6, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], v1, %6, q;\n\t}" ::"r"(d_tmem), "r"(p_tmem),
-        "r"(p_tmem + 8), "r"(p_tmem + 16), "r"(p_tmem + 24), "l"(v), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// tc_commit by lane 0 of a converged warp, if `wanted`.
-__device__ __forceinline__ void tc_commit_lane0(uint32_t bar, bool wanted = true) {
-    asm volatile(
-        "{\n\t.reg .pred e, c;\n\t.reg .b32 l;\n\t"
-        "mov.u32 l, %%laneid;\n\t"
-        "setp.eq.u32 e, l, 0;\n\t"
-        "setp.ne.b32 c, %1, 0;\n\t"
-        "and.pred e, e, c;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-        "r"(static_cast<uint32_t>(wanted))
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc),
+        "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // The MN-major operand with 128-byte swizzle: atoms of 64 values (M or N) x 8 (K), 1024 bytes
@@ -224,7 +198,8 @@ struct TreeShape {
     static constexpr int RAW = STEP * DP, NRAW = E4M3 ? (DP == 64 ? 4 : 2) : 0;
     static constexpr int SW = 4 * STREAMS;                   // softmax warps
     static constexpr int LW = 3;                             // loader warps
-    static constexpr int MMA_WARP = SW + LW;
+    // The MMAs' warp and the loaders come first: the scheduler takes the oldest warp that is ready.
+    static constexpr int MMA_WARP = 0, LOADERS = 1, SOFTMAX = 4;
     static constexpr int THREADS = 32 * (SW + LW + 1);       // 384: 168 registers each
     static constexpr int CH = DP / 8;                        // 16-byte chunks of a row in shared memory
     static constexpr int GROUPS = STEP / 16;                 // of 16 tokens: loader warp w has w, w + LW, ...
@@ -394,7 +369,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
         prefix[tid] = incl - mine;
         if (tid == 0) line = TreeLine{total, max((total + ctas - 1) / ctas, 1ll)};
     }
-    if (tid == 0) heads[cta] = TreePart{};
+    if (tid == 32 * S::SOFTMAX) heads[cta] = TreePart{};
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -459,12 +434,12 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
         __syncthreads();
     }
 
-    if (warp >= SW && warp < S::MMA_WARP) {
+    if (warp >= S::LOADERS && warp < S::SOFTMAX) {
         // ================= loaders =================
         // Steps whose tokens all rows see come by tensor copies, issued by one warp (keys) and another
         // (values), a box per lane.  The others, at the ends of what is visible, are loaded by all three: a row
         // of zeros for what no row sees, and values made finite where some row does not see them.
-        const int lw = warp - SW;
+        const int lw = warp - S::LOADERS;
         constexpr int CH = S::CH;
         const int row_chunks = a.head_dim / 8;        // of 16-bit values
         auto page_of = [&](int tok) { return page_shift >= 0 ? tok >> page_shift : tok / a.page_size; };
@@ -749,14 +724,22 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                 free_phase ^= 1u;
             }
             tc_fence_after();
-            const uint32_t d = tmem + S::TM_O + (STREAMS == 2 ? p_buf : 0) * DP, p = tmem + p_buf * STEP;
-            const uint64_t v = sw128_desc_mn(ring + p_slot * S::SLOT, STEP * 128);
-#pragma unroll 2
-            for (int kb = 0; kb < STEP / 16; kb += 2) tc_mma_pv2(d, p + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || !p_fresh);
-            tc_commit_lane0(empty + 8 * p_slot, p_frees);
-            if (STREAMS == 1) tc_commit_lane0(pv_done);
-            tc_commit_lane0(o_full, p_last);
-            if (p_last && lane == 0) mbar_arrive(o_full);
+            const uint32_t d = tree_uniform(tmem + S::TM_O + (STREAMS == 2 ? p_buf : 0) * DP);
+            const uint32_t p = tree_uniform(tmem + p_buf * STEP), tile = tree_uniform(ring + p_slot * S::SLOT);
+            if (tree_elect()) {
+                const uint64_t v = sw128_desc_mn(tile, STEP * 128);
+#pragma unroll
+                for (int kb = 0; kb < STEP / 16; ++kb) {
+                    tc_mma_ts(d, p + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || !p_fresh);
+                    tc_mma_ts(d, p + 16 * kb + 8, v + 128 * kb, idesc_o, 1);
+                }
+                if (p_frees) tc_commit(empty + 8 * p_slot);
+                if (STREAMS == 1) tc_commit(pv_done);
+                if (p_last) {
+                    tc_commit(o_full);
+                    mbar_arrive(o_full);
+                }
+            }
             __syncwarp();
             open = false;
         };
@@ -782,14 +765,19 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                 }
                 wait(full + 8 * k_slot, k_phase);
                 tc_fence_after();
-                const uint64_t q = sw128_desc(q_smem + (second ? S::QTILE : 0)), k = sw128_desc(ring + k_slot * S::SLOT);
+                const uint32_t q_at = tree_uniform(q_smem + (second ? S::QTILE : 0)), k_at = tree_uniform(ring + k_slot * S::SLOT);
+                const uint32_t d = tree_uniform(tmem + buf * STEP);
+                if (tree_elect()) {
+                    const uint64_t q = sw128_desc(q_at), k = sw128_desc(k_at);
 #pragma unroll
-                for (int c = 0; c < S::BLOCKS; ++c)
-                    tc_mma_ss4(tmem + buf * STEP, q + c * (kTreeRows * 128 >> 4), k + c * (STEP * 128 >> 4), idesc_s, c > 0);
-                tc_commit_lane0(s_full + 8 * buf);
-                tc_commit_lane0(empty + 8 * k_slot, !dual || second);
-                tc_commit_lane0(q_empty, j == jobs - 1);
-                if (lane == 0) mbar_arrive(s_full + 8 * buf);
+                    for (int c = 0; c < DP / 16; ++c)
+                        tc_mma_ss(d, q + (c >> 2) * (kTreeRows * 128 >> 4) + (c & 3) * 2,
+                                  k + (c >> 2) * (STEP * 128 >> 4) + (c & 3) * 2, idesc_s, c > 0);
+                    tc_commit(s_full + 8 * buf);
+                    if (!dual || second) tc_commit(empty + 8 * k_slot);
+                    if (j == jobs - 1) tc_commit(q_empty);
+                    mbar_arrive(s_full + 8 * buf);
+                }
                 __syncwarp();
             }
             if (open) issue_pv();
@@ -814,7 +802,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
     } else {
         // ================= softmax =================
         constexpr float kShift = S::BF ? 0.0f : 7.0f;  // fp16 weights are scaled by 2^7
-        const int stream = warp >> 2;
+        const int stream = (warp - S::SOFTMAX) >> 2;
         const int r = tid & (kTreeRows - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's lanes of TMEM
         uint32_t s_phase = 0, o_phase = 0, job = 0, pv_jobs = 0;
@@ -1098,7 +1086,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                     a.lse[out_row * a.q_heads + head] =
                         l > 0.0f ? (m - kShift) * 0.69314718055994531f + logf(l) : l == 0.0f ? -INFINITY : m;
             }
-            if (begins && !ends && tid == 0) {
+            if (begins && !ends && tid == 32 * S::SOFTMAX) {
                 const long long at0 = share_end - seg.rest - sq.steps;  // of the item's first step in the line
                 heads[cta] = TreePart{static_cast<int>((at0 + sq.steps - 1) / line.share) - cta + 1, row0, rows, kvh * G,
                                       sq.first, vs, {0, 0}};
