@@ -27,6 +27,21 @@ bool tree_map(CUtensorMap* map, const TreeArgs& a, const KvView& kv, bool e4m3, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tree_query_map(CUtensorMap* map, const TreeArgs& a, int box) {
+    const EncodeTiledFn encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim), static_cast<cuuint64_t>(a.q_heads),
+                                static_cast<cuuint64_t>(a.T), 1};
+    const cuuint64_t token = static_cast<cuuint64_t>(a.ldq) * 2;
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.head_dim) * 2, token, token};
+    if (token >= 1ull << 40) return false;
+    const cuuint32_t shape[4] = {64, static_cast<cuuint32_t>(a.q_heads / a.kv_heads), static_cast<cuuint32_t>(box), 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<uint16_t*>(a.q), dims, strides, shape, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t tree_workspace_bytes(const DeviceCtx& ctx, int head_dim) {
     return tree_workspace(ctx.num_sms, tree_dp(head_dim));
 }

@@ -64,6 +64,8 @@ inline size_t tree_workspace(int ctas, int dp) {
 // values 64 columns each, 128-byte swizzled; with 8-bit ones whole rows of dp bytes.  Values from head_dim on and
 // pages from num_pages on are outside: zeros.  False if there is no such view.
 bool tree_map(CUtensorMap* map, const TreeArgs& a, const KvView& kv, bool e4m3, int dp, int box);
+// The queries as [token][head][value], in boxes of 64 columns of a key-value head's heads of `box` tokens.
+bool tree_query_map(CUtensorMap* map, const TreeArgs& a, int box);
 
 namespace {
 
@@ -220,7 +222,7 @@ struct TreeLine {
 
 template <class S>
 struct TreeControl {
-    uint64_t bars[2 * S::NSLOT + 9 + S::NRAW];
+    uint64_t bars[2 * S::NSLOT + 10 + S::NRAW];
     TreeLine line;
     long long scan[S::THREADS / 32];
     uint32_t tmem_base;
@@ -288,12 +290,12 @@ struct TreeRow {
     }
 };
 
-// box_rows: tokens of a box of the tensor maps (a power of two that divides the page size), or 0: the
-// cache is read without them.
+// box_rows: tokens of a box of the cache's tensor maps (a power of two that divides the page size), or 0: it is
+// read without them.  q_box: tokens of a tile of queries, in boxes of qmap, or 0.
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1)
-tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CUtensorMap kmap,
-            const __grid_constant__ CUtensorMap vmap) {
+tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_constant__ CUtensorMap kmap,
+            const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
     constexpr int STEP = S::STEP, DP = S::DP, STREAMS = S::STREAMS, NSLOT = S::NSLOT, SW = S::SW, LW = S::LW;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     static_assert(sizeof(TreeControl<S>) <= S::CONTROL, "the control block fits");
@@ -310,7 +312,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
     const uint32_t bar0 = smem_addr(ctl.bars);
     const uint32_t full = bar0, empty = full + 8 * NSLOT, q_full = empty + 8 * NSLOT, q_empty = q_full + 8;
     const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, o_free = o_full + 8;
-    const uint32_t pv_done = o_free + 8, raw_full = pv_done + 8;
+    const uint32_t pv_done = o_free + 8, fix_full = pv_done + 8, raw_full = fix_full + 8;
     TreePart* heads = static_cast<TreePart*>(a.workspace);
     float* parts = reinterpret_cast<float*>(heads + ctas);
 
@@ -333,6 +335,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
         mbar_init(o_full, 2);
         mbar_init(o_free, SW);
         mbar_init(pv_done, 1);
+        mbar_init(fix_full, 1);
         fence_mbar_init();
         ctl.abort_flag = ctl.bad_page = ctl.dirty = 0;
     }
@@ -414,6 +417,11 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
         open_item(s, at + s.item * per, u);
         return s.step < s.step_end || after(s);
     };
+    // row / G: by a multiplication where that is exact (rows are below 64 G)
+    const uint32_t g_inv = G > 1 && G < 8192 ? static_cast<uint32_t>((0x100000000ull + G - 1) / G) : 0;
+    auto token_of_row = [&](int row) {
+        return G == 1 ? row : g_inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), g_inv)) : row / G;
+    };
     // Row tiles of an item are neighbours in the line, so that they find its tokens in L2.
     auto head_of = [&](const TreeSeg& s) { return s.item / s.seq.row_tiles; };
     auto row0_of = [&](const TreeSeg& s) { return s.item % s.seq.row_tiles * S::ROWS; };
@@ -436,9 +444,10 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
 
     if (warp >= S::LOADERS && warp < S::SOFTMAX) {
         // ================= loaders =================
-        // Steps whose tokens all rows see come by tensor copies, issued by one warp (keys) and another
-        // (values), a box per lane.  The others, at the ends of what is visible, are loaded by all three: a row
-        // of zeros for what no row sees, and values made finite where some row does not see them.
+        // Keys and values come by tensor copies, a box per lane, the keys' issued by one warp, the
+        // values' by another.  In steps that not all rows see in full, at the ends of what is visible, all three
+        // look through the values: zeros for tokens that no row sees, and finite ones where some row does not
+        // see a token.  (Keys need no such care: their scores are masked.)
         const int lw = warp - S::LOADERS;
         constexpr int CH = S::CH;
         const int row_chunks = a.head_dim / 8;        // of 16-bit values
@@ -450,7 +459,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
         int slot = 0;
         uint32_t phase = 0, q_phase = 0;
         int raw_in = 0, raw_out = 0;        // of the 8-bit tiles
-        uint32_t raw_phase = 0;
+        uint32_t raw_phase = 0, fix_phase = 0;
         bool first_segment = true;
         auto next_slot = [&]() {
             if (++slot == NSLOT) slot = 0, phase ^= 1u;
@@ -481,8 +490,10 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
             const int edge = a.window > 0 ? ctx + sq.n - a.window : 0;  // tokens from here on are in every window
             auto clean = [&](int step) {   // all rows see all tokens
                 const int tok0 = tile_of(sq, step) * STEP;
-                return box_rows > 0 && tok0 + STEP <= ctx && (tok0 >= edge || tok0 + STEP <= a.sinks);
+                return tok0 + STEP <= ctx && (tok0 >= edge || tok0 + STEP <= a.sinks);
             };
+            auto wanted = [&](int tok) { return tok < sq.len && (tok >= lo || tok < a.sinks); };   // some row sees it
+            auto some_not = [&](int tok) { return tok >= ctx || (tok < edge && tok >= a.sinks); }; // and some may not
             auto bad = [&]() {
                 record_status(a.status, kDecInvalidArg);
                 *static_cast<volatile int*>(&ctl.bad_page) = 1;
@@ -492,15 +503,20 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
             const int boxes = box_rows > 0 ? STEP / box_rows : 1;   // of a step's tokens
             const int bg = lane % boxes, bb = lane / boxes;
             const bool has_box = bb < (S::E4M3 ? 1 : S::BLOCKS);
-            auto box_page = [&](int step) {
-                return has_box && step < seg.step_end && clean(step) ? table[page_of(tile_of(sq, step) * STEP + bg * box_rows)] : 0;
+            auto box_page = [&](int step) {  // num_pages, which gives zeros, where nobody sees a token
+                const int tok = tile_of(sq, step) * STEP + bg * box_rows;
+                return has_box && step < seg.step_end && tok < sq.len && (tok + box_rows > lo || tok < a.sinks)
+                           ? table[page_of(tok)] : a.num_pages;
             };
             auto issue = [&](uint32_t dst, uint32_t bar, uint32_t bytes, const CUtensorMap* map, int step, int page) {
                 if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
                 __syncwarp();
                 if (has_box) {
                     const int tok = tile_of(sq, step) * STEP + bg * box_rows;
-                    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) bad(), page = a.num_pages;  // zeros
+                    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
+                        if (page != a.num_pages) bad();
+                        page = a.num_pages;
+                    }
                     const uint32_t to = S::E4M3 ? dst + bg * box_rows * DP : dst + bb * STEP * 128 + bg * box_rows * 128;
                     tma_tensor_4d_g2s(to, map, 64 * bb, tok - page_of(tok) * a.page_size, kvh, page, bar);
                 }
@@ -517,19 +533,18 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                 for (int s = 0; s < SETS; ++s) {
                     const int group = lw + LW * (2 * s + lane / 16);
                     const int tok = tile_of(sq, step) * STEP + group * 16 + lane % 16;
-                    const bool wanted = group < S::GROUPS && tok < sq.len && (tok >= lo || tok < a.sinks);
-                    const int in = wanted ? page_of(tok) : 0, pid = wanted ? table[in] : 0;
-                    const bool ok = wanted && static_cast<unsigned>(pid) < static_cast<unsigned>(a.num_pages);
-                    if (wanted && !ok) bad();
+                    const bool want = group < S::GROUPS && wanted(tok);
+                    const int in = want ? page_of(tok) : 0, pid = want ? table[in] : 0;
+                    const bool ok = want && static_cast<unsigned>(pid) < static_cast<unsigned>(a.num_pages);
+                    if (want && !ok) bad();
                     const int64_t in_page = tok - static_cast<int64_t>(in) * a.page_size;
                     kat[s] = ok ? (pid * a.kc.page_stride + in_page * a.kc.slot_stride + kvh * a.kc.head_stride) * S::ES : -1;
                     vat[s] = ok ? (pid * a.vc.page_stride + in_page * a.vc.slot_stride + kvh * a.vc.head_stride) * S::ES : -1;
-                    mixed[s] = __ballot_sync(0xFFFFFFFFu, ok && (tok >= ctx || (tok < edge && tok >= a.sinks)));
+                    mixed[s] = __ballot_sync(0xFFFFFFFFu, ok && some_not(tok));
                 }
             };
             constexpr int FC = DP * S::ES / 16;            // chunks of a row in the cache
             constexpr int LR = 32 / FC;                    // rows of one load of the warp
-            constexpr int LN = 16 / LR < 8 ? 16 / LR : 8;  // loads at a time
             const int fc = lane % FC, fsub = lane / FC;
             auto put = [&](uint32_t dst, uint4 v, int r) { // chunk fc of row r, from the cache's type
                 if constexpr (S::E4M3) {
@@ -547,32 +562,33 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                     if (fc < row_chunks) tree_store16(dst + at_smem(STEP, r, fc), v);
                 }
             };
+            auto finite = [&](uint4& v) {  // zeros for infinite values and NaN, which the end of the item adds
+                bool any;
+                if constexpr (S::E4M3) any = tree_scrub_e4m3(v);
+                else any = tree_scrub<S::BF>(v);
+                if (any) *static_cast<volatile int*>(&ctl.dirty) = 1;
+                return any;
+            };
             auto fill = [&](uint32_t dst, const void* from, const int64_t (&at)[SETS], bool values) {
+                constexpr int LN = 16 / LR;   // loads of a group; all groups' are under way together
+                uint4 v[MINE][LN];
+#pragma unroll
+                for (int n = 0; n < MINE; ++n)
+#pragma unroll
+                    for (int x = 0; x < LN; ++x) {
+                        const int64_t off = __shfl_sync(0xFFFFFFFFu, at[n / 2], n % 2 * 16 + x * LR + fsub);
+                        v[n][x] = make_uint4(0, 0, 0, 0);
+                        if (off >= 0 && 16 * fc < a.head_dim * S::ES)
+                            v[n][x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(from) + off) + fc);
+                    }
 #pragma unroll
                 for (int n = 0; n < MINE; ++n) {
                     const int group = lw + LW * n;
                     if (group >= S::GROUPS) break;
-#pragma unroll 1
-                    for (int r0 = 0; r0 < 16; r0 += LN * LR) {
-                        uint4 v[LN];
 #pragma unroll
-                        for (int x = 0; x < LN; ++x) {
-                            const int64_t off = __shfl_sync(0xFFFFFFFFu, at[n / 2], n % 2 * 16 + r0 + x * LR + fsub);
-                            v[x] = make_uint4(0, 0, 0, 0);
-                            if (off >= 0 && 16 * fc < a.head_dim * S::ES)
-                                v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(from) + off) + fc);
-                        }
-#pragma unroll
-                        for (int x = 0; x < LN; ++x) {
-                            const int in = r0 + x * LR + fsub;
-                            if (values && (mixed[n / 2] >> (n % 2 * 16 + in) & 1u)) {
-                                bool any;
-                                if constexpr (S::E4M3) any = tree_scrub_e4m3(v[x]);
-                                else any = tree_scrub<S::BF>(v[x]);
-                                if (any) *static_cast<volatile int*>(&ctl.dirty) = 1;
-                            }
-                            put(dst, v[x], group * 16 + in);
-                        }
+                    for (int x = 0; x < LN; ++x) {
+                        if (values && (mixed[n / 2] >> (n % 2 * 16 + x * LR + fsub) & 1u)) finite(v[n][x]);
+                        put(dst, v[n][x], group * 16 + x * LR + fsub);
                     }
                 }
             };
@@ -585,13 +601,28 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                 const int c = lane % CH, sub = lane / CH;
                 wait(q_empty, q_phase ^ 1u);
                 q_phase ^= 1u;
-                constexpr int AT = 8;   // loads at a time
+                if (q_box > 0 && f > 0.0f) {
+                    // Tokens of G heads are G rows, one after another.  Rows behind the sequence's are another's,
+                    // or zeros: nobody reads what they give.
+                    if (lw == 0) {
+                        if (lane == 0) mbar_arrive_expect_tx(q_full, padded * DP * 2);
+                        __syncwarp();
+                        const int tile = lane / S::BLOCKS, block = lane % S::BLOCKS;
+                        if (tile * kTreeRows < padded)
+                            tma_tensor_4d_g2s(q_smem + tile * S::QTILE + block * kTreeRows * 128, &qmap, 64 * block, kvh * G,
+                                              sq.first + row0 / G + tile * q_box, 0, q_full);
+                        __syncwarp();
+                    }
+                    loaders_sync();
+                    return;
+                }
+                constexpr int AT = 16;  // loads at a time
 #pragma unroll 1
                 for (int n0 = lw * RPI + sub; n0 < padded; n0 += AT * LW * RPI) {
                     uint4 v[AT];
 #pragma unroll
                     for (int x = 0; x < AT; ++x) {
-                        const int n = n0 + x * LW * RPI, row = row0 + n, i = row / G;
+                        const int n = n0 + x * LW * RPI, row = row0 + n, i = token_of_row(row);
                         v[x] = make_uint4(0, 0, 0, 0);
                         if (n < rows && c < row_chunks)
                             v[x] = *(reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(sq.first + i) * a.ldq +
@@ -624,8 +655,6 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                 }
                 all_there(q_full);
             };
-            // At the CTA's start the queries come first; else behind the first step, as their place is taken
-            // until the item before has its last scores.
             auto fill_step = [&](int st) {
                 look(st);
                 wait(empty + 8 * slot, phase ^ 1u);
@@ -637,63 +666,84 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
                 all_there(full + 8 * slot);
                 next_slot();
             };
-            if constexpr (S::E4M3) {
+            if (box_rows == 0) {  // pages that no tensor map describes
+                for (int st = seg.step; st < seg.step_end; ++st) {
+                    fill_step(st);
+                    if (st == seg.step) load_queries();
+                }
+            } else if constexpr (S::E4M3) {
                 constexpr int NRAW = S::NRAW;
                 const uint32_t raw = ring + NSLOT * S::SLOT;
                 // tensor copies run ahead of the conversions: 2 st + side of the next one to issue
-                int ahead = 2 * seg.step, pid = box_page(seg.step);
+                int ahead = 2 * seg.step, pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
                 auto issue_next = [&]() {
-                    while (ahead < 2 * seg.step_end && !clean(ahead >> 1)) {
-                        ahead += 2;
-                        pid = box_page(ahead >> 1);
-                    }
                     if (ahead >= 2 * seg.step_end) return;
                     if (lw == 0) {
                         issue(raw + raw_in * S::RAW, raw_full + 8 * raw_in, S::RAW, ahead & 1 ? &vmap : &kmap, ahead >> 1, pid);
-                        if (ahead & 1) pid = box_page((ahead + 1) >> 1);
+                        if (ahead & 1) pid = pid1, pid1 = box_page((ahead + 3) >> 1);
                     }
                     ++ahead;
                     if (++raw_in == NRAW) raw_in = 0;
                 };
                 for (int x = 0; x < NRAW; ++x) issue_next();
                 load_queries();
-                for (int st = seg.step; st < seg.step_end; ++st) {
-                    if (!clean(st)) {
-                        fill_step(st);
-                        continue;
-                    }
 #pragma unroll 1
-                    for (int side = 0; side < 2; ++side) {
-                        wait(empty + 8 * slot, phase ^ 1u);
-                        wait(raw_full + 8 * raw_out, raw_phase);
-                        const uint32_t from = raw + raw_out * S::RAW, dst = ring + slot * S::SLOT;
+                for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
+                    wait(empty + 8 * slot, phase ^ 1u);
+                    wait(raw_full + 8 * raw_out, raw_phase);
+                    const uint32_t from = raw + raw_out * S::RAW, dst = ring + slot * S::SLOT;
+                    const int tok0 = tile_of(sq, half >> 1) * STEP;
+                    const bool care = (half & 1) && !clean(half >> 1);
 #pragma unroll 4
-                        for (int r = lw * LR + fsub; r < STEP; r += LW * LR) put(dst, lds_v4(from + r * DP + 16 * fc), r);
-                        all_there(full + 8 * slot);
-                        next_slot();
-                        if (++raw_out == NRAW) raw_out = 0, raw_phase ^= 1u;
-                        issue_next();
+                    for (int r = lw * LR + fsub; r < STEP; r += LW * LR) {
+                        uint4 v = lds_v4(from + r * DP + 16 * fc);
+                        if (care) {
+                            if (!wanted(tok0 + r)) v = make_uint4(0, 0, 0, 0);
+                            else if (some_not(tok0 + r)) finite(v);
+                        }
+                        put(dst, v, r);
                     }
+                    all_there(full + 8 * slot);
+                    next_slot();
+                    if (++raw_out == NRAW) raw_out = 0, raw_phase ^= 1u;
+                    issue_next();
                 }
             } else {
+                // At the CTA's start the queries come first; else behind the first step, as their place is taken
+                // until the item before has its last scores.
                 const bool queries_first = first_segment;
                 first_segment = false;
                 if (queries_first) load_queries();
                 int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
                 for (int st = seg.step; st < seg.step_end; ++st) {
-                    if (clean(st)) {
-                        // Keys by warp 0, values by warp 1.  All wait for the slots and for one another: no
-                        // warp is ever a round of the ring ahead of or behind a barrier's one bit of phase.
-                        for (int side = 0; side < 2; ++side) {
-                            wait(empty + 8 * slot, phase ^ 1u);
-                            if (lw == side)
-                                issue(ring + slot * S::SLOT, full + 8 * slot, S::SLOT, side ? &vmap : &kmap, st, pid);
-                            next_slot();
-                        }
+                    const bool as_it_is = clean(st);
+                    // All wait for the slots and for one another: no warp is ever a round of the ring ahead of
+                    // or behind a barrier's one bit of phase.
+                    wait(empty + 8 * slot, phase ^ 1u);
+                    if (lw == 0) issue(ring + slot * S::SLOT, full + 8 * slot, S::SLOT, &kmap, st, pid);
+                    next_slot();
+                    wait(empty + 8 * slot, phase ^ 1u);
+                    const uint32_t tile = ring + slot * S::SLOT;
+                    if (lw == 1) issue(tile, as_it_is ? full + 8 * slot : fix_full, S::SLOT, &vmap, st, pid);
+                    if (as_it_is) {
                         loaders_sync();
                     } else {
-                        fill_step(st);
+                        wait(fix_full, fix_phase);
+                        fix_phase ^= 1u;
+                        const int tok0 = tile_of(sq, st) * STEP;
+#pragma unroll 4
+                        for (int r = lw * LR + fsub; r < STEP; r += LW * LR) {
+                            const uint32_t at = tile + at_smem(STEP, r, fc);
+                            if (!wanted(tok0 + r)) {
+                                tree_store16(at, make_uint4(0, 0, 0, 0));
+                            } else if (some_not(tok0 + r)) {
+                                uint4 v = lds_v4(at);
+                                if (finite(v)) tree_store16(at, v);
+                            }
+                        }
+                        all_there(full + 8 * slot);
                     }
+                    next_slot();
                     pid = pid1;
                     pid1 = box_page(st + 2);
                     if (st == seg.step && !queries_first) load_queries();
@@ -818,7 +868,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, const __grid_constant__ CU
             const int tile = dual ? (stream ^ (job0 & 1)) : 0;
             const int in_item = tile * kTreeRows + r;
             const bool live = in_item < rows;
-            const int row = row0 + in_item, i = live ? row / G : 0, head = kvh * G + (live ? row - i * G : 0);
+            const int row = row0 + in_item, i = live ? token_of_row(row) : 0, head = kvh * G + (live ? row - i * G : 0);
             const bool any_live = __any_sync(0xFFFFFFFFu, live);
             TreeRow see{0, ctx, 0, a.window > 0 ? a.sinks : 0};
             if (live) {
@@ -1162,11 +1212,15 @@ int launch_tree_shape(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stre
     // swizzle pattern.  Other pages, and heads or slots of stride 0, are read without tensor maps.
     int box = a.page_size & -a.page_size;
     box = box < S::STEP ? box : S::STEP;
-    CUtensorMap maps[2] = {};
+    CUtensorMap maps[3] = {};
     if (box < 8 || !tree_map(&maps[0], a, a.kc, S::E4M3, S::DP, box) || !tree_map(&maps[1], a, a.vc, S::E4M3, S::DP, box))
         box = 0;
+    // Queries by tensor copies where a tile of rows is whole tokens and the MMA takes them as they are.
+    const int G = a.q_heads / a.kv_heads;
+    int q_box = kTreeRows % G == 0 && !(S::E4M3 && S::DT == 1) ? kTreeRows / G : 0;
+    if (q_box > 0 && !tree_query_map(&maps[2], a, q_box)) q_box = 0;
     const int rc = launch_dependent(tree_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), dim3(S::THREADS),
-                                    S::SMEM, stream, a, power_of_two(a.page_size), box, maps[0], maps[1]);
+                                    S::SMEM, stream, a, power_of_two(a.page_size), box, q_box, maps[0], maps[1], maps[2]);
     if (rc != 0) return rc;
     return launch_dependent(tree_join_kernel<S::DT, S::DP, !S::BF>, dim3(static_cast<unsigned>(ctx.num_sms), 16),
                             dim3(128), 0, stream, a, ctx.num_sms);
