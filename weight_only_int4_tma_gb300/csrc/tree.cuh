@@ -43,7 +43,7 @@ constexpr float kTreeLag = 8.0f;   // scores may pass the reference by 2^8
 constexpr int kTreeRows = 128;     // of a tile: the MMA's M
 
 // Of the workspace: a TreePart per CTA, then two parts per CTA (an item begun by an earlier CTA, one left
-// to a later) of m[rows], l[rows], O[rows][dp], rows being 128 for each stream.
+// to a later) of m[rows], l[rows], O[dp / 4][rows][4], rows being 128 for each stream.
 struct TreePart {
     int n;       // parts of the item that this CTA begins and another ends; 0: none
     int row0;    // its first row in q and out is that of token row0 / G, head head0 + row0 % G
@@ -199,10 +199,11 @@ struct TreeShape {
     // 8-bit tiles as they come from the cache, before they are converted into the ring
     static constexpr int RAW = STEP * DP, NRAW = E4M3 ? (DP == 64 ? 4 : 2) : 0;
     static constexpr int SW = 4 * STREAMS;                   // softmax warps
-    static constexpr int LW = 3;                             // loader warps
-    // The MMAs' warp and the loaders come first: the scheduler takes the oldest warp that is ready.
-    static constexpr int MMA_WARP = 0, LOADERS = 1, SOFTMAX = 4;
-    static constexpr int THREADS = 32 * (SW + LW + 1);       // 384: 168 registers each
+    // Loader warps: with an 8-bit cache they convert.  The MMAs' warp and they come first: the scheduler takes
+    // the oldest warp that is ready.
+    static constexpr int LW = E4M3 ? 7 : 3;
+    static constexpr int LOADERS = 1, SOFTMAX = 1 + LW;
+    static constexpr int THREADS = 32 * (SOFTMAX + SW);      // 384: 168 registers each; 512: 128
     static constexpr int CH = DP / 8;                        // 16-byte chunks of a row in shared memory
     static constexpr int GROUPS = STEP / 16;                 // of 16 tokens: loader warp w has w, w + LW, ...
     static constexpr int TM_O = 2 * STEP;                    // TMEM columns: S twice, then O of each stream
@@ -269,6 +270,13 @@ struct TreeSeg {
 template <class S>
 __device__ __forceinline__ long long tree_items(const TreeArgs& a, const TreeSeq& s) {
     return static_cast<long long>(s.row_tiles) * a.kv_heads;
+}
+
+// a / b for numbers >= 0; the long division, out of line, only where 32 bits do not hold them.
+static __device__ __noinline__ long long tree_long_quotient(long long a, long long b) { return a / b; }
+__device__ __forceinline__ long long tree_quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return tree_long_quotient(a, b);
 }
 
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {  // bits lo .. hi - 1 of 0 .. 31
@@ -340,9 +348,14 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         ctl.abort_flag = ctl.bad_page = ctl.dirty = 0;
     }
     fence_proxy_async_smem();  // the zeros
+    if (tid == 32) {
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+        prefetch_tensormap(&qmap);
+    }
     grid_dep_wait();
     grid_dep_launch();
-    if (warp == S::MMA_WARP) {
+    if (warp == 0) {
         tmem_alloc(smem_addr(&ctl.tmem_base), 512);
         tmem_relinquish();
     }
@@ -370,7 +383,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             total += ctl.scan[w];
         }
         prefix[tid] = incl - mine;
-        if (tid == 0) line = TreeLine{total, max((total + ctas - 1) / ctas, 1ll)};
+        if (tid == 0) line = TreeLine{total, max(tree_quotient(total + ctas - 1, ctas), 1ll)};
     }
     if (tid == 32 * S::SOFTMAX) heads[cta] = TreePart{};
     tc_fence_before();
@@ -413,12 +426,12 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             s.seq = tree_seq<S>(a, ++s.b, false);
         }
         const long long per = s.seq.steps + kTreeItemCost;
-        s.item = static_cast<int>((u - at) / per);
+        s.item = static_cast<int>(tree_quotient(u - at, per));
         open_item(s, at + s.item * per, u);
         return s.step < s.step_end || after(s);
     };
     // row / G: by a multiplication where that is exact (rows are below 64 G)
-    const uint32_t g_inv = G > 1 && G < 8192 ? static_cast<uint32_t>((0x100000000ull + G - 1) / G) : 0;
+    const uint32_t g_inv = G > 1 && G < 8192 ? 0xFFFFFFFFu / static_cast<uint32_t>(G) + 1 : 0;
     auto token_of_row = [&](int row) {
         return G == 1 ? row : g_inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), g_inv)) : row / G;
     };
@@ -713,8 +726,8 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 // until the item before has its last scores.
                 const bool queries_first = first_segment;
                 first_segment = false;
-                if (queries_first) load_queries();
                 int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
+                if (queries_first) load_queries();
                 for (int st = seg.step; st < seg.step_end; ++st) {
                     const bool as_it_is = clean(st);
                     // All wait for the slots and for one another: no warp is ever a round of the ring ahead of
@@ -751,7 +764,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             }
             more = after(seg);
         }
-    } else if (warp == S::MMA_WARP) {
+    } else if (warp == 0) {
         // ================= the MMAs =================
         constexpr int TYPE = S::BF ? 1 : 0;
         constexpr uint32_t idesc_s = idesc_f16(TYPE, 128, STEP), idesc_o = idesc_f16(TYPE, 128, DP) | kIdescBMajorMn;
@@ -922,16 +935,20 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         }
                     return v;
                 };
+                uint32_t xa[32], xb[32];
                 if (masked) {  // -infinity, in TMEM, for what the row does not see
-#pragma unroll 1
-                    for (int c = 0; c < STEP; c += 16) {
+                    auto hide = [&](uint32_t (&x)[32], int c) {
                         const uint32_t seen = seen_of(tok0 + c);
-                        uint32_t x[16];
-                        tmem_ld16(s_at + c, x);
-                        tmem_wait_ld16(x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] = (seen >> e) & 1u ? x[e] : 0xFF800000u;
-                        tmem_st16(s_at + c, x);
+                        for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? x[e] : 0xFF800000u;
+                        tmem_st16(s_at + c, reinterpret_cast<uint32_t(&)[16]>(x[0]));
+                        tmem_st16(s_at + c + 16, reinterpret_cast<uint32_t(&)[16]>(x[16]));
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < STEP; c += 32) {
+                        tmem_ld32(s_at + c, xa);
+                        tmem_wait_ld32(xa);
+                        hide(xa, c);
                     }
                     tmem_wait_st();
                 }
@@ -939,7 +956,6 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 // way.  In loops: with the row's code in one line the roles' code is fetched anew from beyond the
                 // SM in every step (32 ragged sequences, trees of 32: 336 us).
                 constexpr int NC = STEP / 32;
-                uint32_t xa[32], xb[32];
                 float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 auto highest = [&](const uint32_t (&x)[32]) {
 #pragma unroll
@@ -1121,10 +1137,9 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                                 dec_pack2<S::DT>(o[e] * inv, o[e + 1] * inv), dec_pack2<S::DT>(o[e + 2] * inv, o[e + 3] * inv),
                                 dec_pack2<S::DT>(o[e + 4] * inv, o[e + 5] * inv), dec_pack2<S::DT>(o[e + 6] * inv, o[e + 7] * inv));
                 } else {
-                    float* dst = part + 2 * S::ROWS + static_cast<int64_t>(in_item) * DP + c;
+                    float4* dst = reinterpret_cast<float4*>(part + 2 * S::ROWS) + c / 4 * S::ROWS + in_item;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 32; e += 4) dst[e / 4 * S::ROWS] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
             tc_fence_before();
@@ -1138,7 +1153,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             }
             if (begins && !ends && tid == 32 * S::SOFTMAX) {
                 const long long at0 = share_end - seg.rest - sq.steps;  // of the item's first step in the line
-                heads[cta] = TreePart{static_cast<int>((at0 + sq.steps - 1) / line.share) - cta + 1, row0, rows, kvh * G,
+                heads[cta] = TreePart{static_cast<int>(tree_quotient(at0 + sq.steps - 1, line.share)) - cta + 1, row0, rows, kvh * G,
                                       sq.first, vs, {0, 0}};
             }
             more = after(seg);
@@ -1148,59 +1163,73 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == S::MMA_WARP) tmem_dealloc(tmem, 512);
+    if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of items that several CTAs hold: a warp per row, blockIdx.x the CTA that began the item.
+// Joins the parts of items that several CTAs hold.  blockIdx.x: the CTA that began the item; blockIdx.y: 32 of its
+// rows, a lane each; a warp has every eighth piece of four columns.
+constexpr int kTreeJoinThreads = 256;
 template <int DT, int DP, bool SHIFT>
-__global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a, int ctas) {
+__global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(TreeArgs a, int ctas) {
     constexpr float kShift = SHIFT ? 7.0f : 0.0f;
-    constexpr int ROWS = kTreeRows * tree_streams(DP), V = DP >= 128 ? DP / 128 : 1;
+    constexpr int ROWS = kTreeRows * tree_streams(DP), WARPS = kTreeJoinThreads / 32, V = DP / 4 / WARPS;
+    constexpr int PITCH = DP + 4;   // of a staged row, so that lanes' 8 bytes fall in different banks
+    __shared__ __align__(16) uint16_t staged[32 * PITCH];
     grid_dep_wait();
     const TreePart* heads = static_cast<const TreePart*>(a.workspace);
     const TreePart h = heads[blockIdx.x];
-    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int row0 = 32 * static_cast<int>(blockIdx.y), row = row0 + lane;
+    if (h.n <= 0 || row0 >= h.rows) return;
     const float* parts = reinterpret_cast<const float*>(heads + ctas);
     const int G = a.q_heads / a.kv_heads;
-    if (h.n <= 0) return;
+    // (rows behind the last hold whatever they held: they are not stored)
     auto part_of = [&](int k) {
         return parts + (2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0)) * tree_part_floats(ROWS, DP);
     };
-    for (int row = static_cast<int>(blockIdx.y) * 4 + (static_cast<int>(threadIdx.x) >> 5); row < h.rows; row += 4 * gridDim.y) {
-        float top = -INFINITY, sum = 0.0f;
-        for (int k = lane; k < h.n; k += 32) top = tree_max(top, part_of(k)[row]);
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < h.n; ++k) top = tree_max(top, part_of(k)[row]);
+    float4 acc[V];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = tree_max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        float4 acc[V];
+    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int k = 0; k < h.n; ++k) {
+        const float* p = part_of(k);
+        const float m = p[row], l = p[ROWS + row];
+        const float4* o = reinterpret_cast<const float4*>(p + 2 * ROWS) + warp * ROWS + row;
+        float4 x[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = 0; k < h.n; ++k) {
-            const float* p = part_of(k);
-            const float m = p[row], f = m == -INFINITY ? 0.0f : tree_exp2(m - top);
-            sum += p[ROWS + row] * f;
-            if (f == 0.0f) continue;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int d = 4 * lane + 128 * v;
-                if (d >= a.head_dim) continue;
-                const float4 x = *reinterpret_cast<const float4*>(p + 2 * ROWS + static_cast<int64_t>(row) * DP + d);
-                acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y);
-                acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
-            }
-        }
-        const float inv = sum == 0.0f ? 0.0f : h.vs / sum;
-        const int r = h.row0 + row, i = r / G, head = h.head0 + r - i * G;
-        uint16_t* out = a.out + static_cast<int64_t>(h.first + i) * a.ldo + static_cast<int64_t>(head) * a.head_dim;
+        for (int v = 0; v < V; ++v) x[v] = o[v * WARPS * ROWS];
+        const float f = m == -INFINITY ? 0.0f : tree_exp2(m - top);
+        sum += l * f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int d = 4 * lane + 128 * v;
-            if (d < a.head_dim)
-                *reinterpret_cast<uint2*>(out + d) = make_uint2(dec_pack2<DT>(acc[v].x * inv, acc[v].y * inv),
-                                                               dec_pack2<DT>(acc[v].z * inv, acc[v].w * inv));
+            if (f == 0.0f) continue;
+            acc[v].x = fmaf(x[v].x, f, acc[v].x), acc[v].y = fmaf(x[v].y, f, acc[v].y);
+            acc[v].z = fmaf(x[v].z, f, acc[v].z), acc[v].w = fmaf(x[v].w, f, acc[v].w);
         }
-        if (a.lse && lane == 0)
-            a.lse[static_cast<int64_t>(h.first + i) * a.q_heads + head] =
-                sum > 0.0f ? (top - kShift) * 0.69314718055994531f + logf(sum) : sum == 0.0f ? -INFINITY : top;
+    }
+    const float inv = sum == 0.0f ? 0.0f : h.vs / sum;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        *reinterpret_cast<uint2*>(staged + lane * PITCH + 4 * (warp + v * WARPS)) =
+            make_uint2(dec_pack2<DT>(acc[v].x * inv, acc[v].y * inv), dec_pack2<DT>(acc[v].z * inv, acc[v].w * inv));
+    if (warp == 0 && row < h.rows && a.lse) {
+        const int r = h.row0 + row, i = r / G, head = h.head0 + r - i * G;
+        a.lse[static_cast<int64_t>(h.first + i) * a.q_heads + head] =
+            sum > 0.0f ? (top - kShift) * 0.69314718055994531f + logf(sum) : sum == 0.0f ? -INFINITY : top;
+    }
+    __syncthreads();
+    const int chunks = a.head_dim / 8;
+    for (int e = tid; e < 32 * chunks; e += kTreeJoinThreads) {
+        const int in = e / chunks, c = e - in * chunks;
+        if (row0 + in >= h.rows) break;
+        const int r = h.row0 + row0 + in, i = r / G, head = h.head0 + r - i * G;
+        const uint16_t* from = staged + in * PITCH + 8 * c;
+        const uint2 lo = *reinterpret_cast<const uint2*>(from), hi = *reinterpret_cast<const uint2*>(from + 4);
+        *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(h.first + i) * a.ldo +
+                                  static_cast<int64_t>(head) * a.head_dim + 8 * c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
 }
 
@@ -1222,8 +1251,8 @@ int launch_tree_shape(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stre
     const int rc = launch_dependent(tree_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), dim3(S::THREADS),
                                     S::SMEM, stream, a, power_of_two(a.page_size), box, q_box, maps[0], maps[1], maps[2]);
     if (rc != 0) return rc;
-    return launch_dependent(tree_join_kernel<S::DT, S::DP, !S::BF>, dim3(static_cast<unsigned>(ctx.num_sms), 16),
-                            dim3(128), 0, stream, a, ctx.num_sms);
+    return launch_dependent(tree_join_kernel<S::DT, S::DP, !S::BF>, dim3(static_cast<unsigned>(ctx.num_sms), S::ROWS / 32),
+                            dim3(kTreeJoinThreads), 0, stream, a, ctx.num_sms);
 }
 
 template <int DT, bool E4M3>
