@@ -457,8 +457,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
 
     if (warp >= S::LOADERS && warp < S::SOFTMAX) {
         // ================= loaders =================
-        // Keys and values come by tensor copies, a box per lane, the keys' issued by one warp, the
-        // values' by another.  In steps that not all rows see in full, at the ends of what is visible, all three
+        // Keys and values come by tensor copies, a box per lane.  In steps that not all rows see in full, at the ends of what is visible, all three
         // look through the values: zeros for tokens that no row sees, and finite ones where some row does not
         // see a token.  (Keys need no such care: their scores are masked.)
         const int lw = warp - S::LOADERS;
@@ -473,7 +472,6 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         uint32_t phase = 0, q_phase = 0;
         int raw_in = 0, raw_out = 0;        // of the 8-bit tiles
         uint32_t raw_phase = 0, fix_phase = 0;
-        bool first_segment = true;
         auto next_slot = [&]() {
             if (++slot == NSLOT) slot = 0, phase ^= 1u;
         };
@@ -605,6 +603,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     }
                 }
             };
+            constexpr int Q_WARP = S::E4M3 ? 0 : 1;
             auto load_queries = [&]() {
                 // f = |scale k_scale|; a negative or zero product is folded into the queries
                 const float f = a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f);
@@ -612,21 +611,20 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 const int row0 = row0_of(seg), rows = rows_of(seg), padded = rows > kTreeRows ? 2 * kTreeRows : kTreeRows;
                 constexpr int RPI = 32 / CH;
                 const int c = lane % CH, sub = lane / CH;
-                wait(q_empty, q_phase ^ 1u);
+                const bool by_copy = q_box > 0 && f > 0.0f;
+                if (!by_copy || lw == Q_WARP) wait(q_empty, q_phase ^ 1u);
                 q_phase ^= 1u;
-                if (q_box > 0 && f > 0.0f) {
+                if (by_copy) {
                     // Tokens of G heads are G rows, one after another.  Rows behind the sequence's are another's,
                     // or zeros: nobody reads what they give.
-                    if (lw == 0) {
-                        if (lane == 0) mbar_arrive_expect_tx(q_full, padded * DP * 2);
-                        __syncwarp();
-                        const int tile = lane / S::BLOCKS, block = lane % S::BLOCKS;
-                        if (tile * kTreeRows < padded)
-                            tma_tensor_4d_g2s(q_smem + tile * S::QTILE + block * kTreeRows * 128, &qmap, 64 * block, kvh * G,
-                                              sq.first + row0 / G + tile * q_box, 0, q_full);
-                        __syncwarp();
-                    }
-                    loaders_sync();
+                    if (lw != Q_WARP) return;
+                    if (lane == 0) mbar_arrive_expect_tx(q_full, padded * DP * 2);
+                    __syncwarp();
+                    const int tile = lane / S::BLOCKS, block = lane % S::BLOCKS;
+                    if (tile * kTreeRows < padded)
+                        tma_tensor_4d_g2s(q_smem + tile * S::QTILE + block * kTreeRows * 128, &qmap, 64 * block, kvh * G,
+                                          sq.first + token_of_row(row0) + tile * q_box, 0, q_full);
+                    __syncwarp();
                     return;
                 }
                 constexpr int AT = 16;  // loads at a time
@@ -722,27 +720,34 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     issue_next();
                 }
             } else {
-                // At the CTA's start the queries come first; else behind the first step, as their place is taken
-                // until the item before has its last scores.
-                const bool queries_first = first_segment;
-                first_segment = false;
-                int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
-                if (queries_first) load_queries();
+                // Keys and values by the first warp, queries by the second (or all, behind the first step, where
+                // their place is taken until the item before has its last scores).
+                if (q_box > 0) load_queries();
+                int pid = 0, pid1 = 0;
+                if (lw == 0) pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
+#pragma unroll 1
                 for (int st = seg.step; st < seg.step_end; ++st) {
                     const bool as_it_is = clean(st);
-                    // All wait for the slots and for one another: no warp is ever a round of the ring ahead of
-                    // or behind a barrier's one bit of phase.
-                    wait(empty + 8 * slot, phase ^ 1u);
-                    if (lw == 0) issue(ring + slot * S::SLOT, full + 8 * slot, S::SLOT, &kmap, st, pid);
-                    next_slot();
-                    wait(empty + 8 * slot, phase ^ 1u);
-                    const uint32_t tile = ring + slot * S::SLOT;
-                    if (lw == 1) issue(tile, as_it_is ? full + 8 * slot : fix_full, S::SLOT, &vmap, st, pid);
-                    if (as_it_is) {
-                        loaders_sync();
+                    if (lw == 0) {
+#pragma unroll 1
+                        for (int side = 0; side < 2; ++side) {
+                            wait(empty + 8 * slot, phase ^ 1u);
+                            issue(ring + slot * S::SLOT, side && !as_it_is ? fix_full : full + 8 * slot, S::SLOT,
+                                  side ? &vmap : &kmap, st, pid);
+                            if (!side) next_slot();
+                        }
+                        pid = pid1;
+                        pid1 = box_page(st + 2);
                     } else {
-                        wait(fix_full, fix_phase);
-                        fix_phase ^= 1u;
+                        next_slot();
+                    }
+                    if (!as_it_is) {
+                        if (lw == 0) {  // the only one to wait on barriers: no other could tell their phases apart
+                            wait(fix_full, fix_phase);
+                            fix_phase ^= 1u;
+                        }
+                        loaders_sync();
+                        const uint32_t tile = ring + slot * S::SLOT;
                         const int tok0 = tile_of(sq, st) * STEP;
 #pragma unroll 4
                         for (int r = lw * LR + fsub; r < STEP; r += LW * LR) {
@@ -757,9 +762,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         all_there(full + 8 * slot);
                     }
                     next_slot();
-                    pid = pid1;
-                    pid1 = box_page(st + 2);
-                    if (st == seg.step && !queries_first) load_queries();
+                    if (st == seg.step && q_box == 0) load_queries();
                 }
             }
             more = after(seg);
@@ -1066,7 +1069,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             // the sums of stream x times fx[x]
             float fx[2] = {1.0f, 1.0f};
             int c0 = 0, c1 = DP;             // columns of this thread
-            bool use[2] = {stream == 0, stream == 1};
+            bool use[2] = {stream == 0 || STREAMS == 1, stream == 1};
             if (STREAMS == 2 && !dual) {     // the streams' sums of the same rows are joined
                 // (they have been read before the next item's first P V, which o_free holds back)
                 float2 (&st)[STREAMS][kTreeRows] = ctl.stats;
@@ -1078,32 +1081,34 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 fx[1] = s1.x == -INFINITY ? 0.0f : tree_exp2(s1.x - m);
                 l = s0.y * fx[0] + s1.y * fx[1];
                 // a stream that had no job has nothing in its place
-                use[0] = jobs > 1 || (job0 & 1) == 0;
-                use[1] = jobs > 1 || (job0 & 1) == 1;
+                use[0] = fx[0] != 0.0f && (jobs > 1 || (job0 & 1) == 0);
+                use[1] = fx[1] != 0.0f && (jobs > 1 || (job0 & 1) == 1);
                 c0 = stream * (DP / 2), c1 = c0 + DP / 2;
             }
             const int64_t out_row = sq.first + i;
             const float inv = l == 0.0f ? 0.0f : vs / l;
             const bool patch = *static_cast<volatile int*>(&ctl.dirty) != 0;
+            // (in short pieces, as code that runs once per item comes from beyond the SM)
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 32) {
-                uint32_t x[32];
-                float o[32];
+            for (int c = c0; c < c1; c += 16) {
+                uint32_t x[STREAMS][16];
+                float o[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                for (int s = 0; s < STREAMS; ++s) tmem_ld16(tmem + lanes + S::TM_O + s * DP + c, x[s]);
 #pragma unroll
-                for (int s = 0; s < STREAMS; ++s) {
-                    if (!use[s]) continue;
-                    tmem_ld32(tmem + lanes + S::TM_O + s * DP + c, x);
-                    tmem_wait_ld32(x);
+                for (int s = 0; s < STREAMS; ++s) tmem_wait_ld16(x[s]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(STREAMS == 2 && !dual) || fx[s] != 0.0f) o[e] = fmaf(__uint_as_float(x[e]), fx[s], o[e]);
+                for (int e = 0; e < 16; ++e) {
+                    o[e] = use[0] ? __uint_as_float(x[0][e]) * fx[0] : 0.0f;
+                    if (STREAMS == 2 && use[1]) o[e] = fmaf(__uint_as_float(x[STREAMS - 1][e]), fx[1], o[e]);
                 }
                 if (patch && live && l != 0.0f) {  // infinite values and NaN of tokens that this row sees
+#pragma unroll 1
                     for (int st = seg.step; st < seg.step_end; ++st) {
                         const int tok0 = tile_of(sq, st) * STEP;
+#pragma unroll 1
                         for (int t0 = tok0; t0 < tok0 + STEP; t0 += 32)
+#pragma unroll 1
                             for (uint32_t left = see.seen(t0); left; left &= left - 1) {
                                 const int tok = t0 + __ffs(left) - 1;
                                 if (!(tok >= ctx || (tok < edge && tok >= a.sinks))) continue;
@@ -1112,17 +1117,15 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                                 if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) continue;
                                 const int64_t at = page * a.vc.page_stride + (tok - in * a.page_size) * a.vc.slot_stride +
                                                    kvh * a.vc.head_stride + c;
-                                for (int e = 0; e < 32 && c + e < a.head_dim; ++e) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    if (c + e >= a.head_dim) continue;
                                     float v;
                                     if constexpr (S::E4M3)
                                         v = (static_cast<const uint8_t*>(a.vc.p)[at + e] & 0x7F) == 0x7F ? NAN : 0.0f;
                                     else
                                         v = dec_to_f32<S::DT>(static_cast<const uint16_t*>(a.vc.p)[at + e]);
-                                    if (!(fabsf(v) < INFINITY)) {
-#pragma unroll
-                                        for (int q = 0; q < 32; ++q)
-                                            if (q == e) o[q] += v;
-                                    }
+                                    if (!(fabsf(v) < INFINITY)) o[e] += v;
                                 }
                             }
                     }
@@ -1131,7 +1134,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 if (whole) {
                     uint16_t* dst = a.out + out_row * a.ldo + static_cast<int64_t>(head) * a.head_dim + c;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
+                    for (int e = 0; e < 16; e += 8)
                         if (c + e < a.head_dim)
                             *reinterpret_cast<uint4*>(dst + e) = make_uint4(
                                 dec_pack2<S::DT>(o[e] * inv, o[e + 1] * inv), dec_pack2<S::DT>(o[e + 2] * inv, o[e + 3] * inv),
@@ -1139,7 +1142,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 } else {
                     float4* dst = reinterpret_cast<float4*>(part + 2 * S::ROWS) + c / 4 * S::ROWS + in_item;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) dst[e / 4 * S::ROWS] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 16; e += 4) dst[e / 4 * S::ROWS] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
             tc_fence_before();
