@@ -195,14 +195,15 @@ struct TreeShape {
     static constexpr int BLOCKS = DP / 64;                   // 64-value blocks of a row
     static constexpr int SLOT = STEP * DP * 2;               // bytes of a step's keys, or values
     static constexpr int QTILE = kTreeRows * DP * 2;
-    static constexpr int NSLOT = E4M3 ? (DP == 64 ? 8 : 4) : (DP == 64 ? 10 : 5);  // of the ring: 128 or 160 KB
+    // Slots of the ring, 128 KB: the steps' keys in the even ones, their values in the odd ones.  A multiple
+    // of four: with one stream per step a slot then is always the same stream's.
+    static constexpr int NSLOT = DP == 64 ? 8 : 4;
     // 8-bit tiles as they come from the cache, before they are converted into the ring
     static constexpr int RAW = STEP * DP, NRAW = E4M3 ? (DP == 64 ? 4 : 2) : 0;
     static constexpr int SW = 4 * STREAMS;                   // softmax warps
-    // Loader warps: with an 8-bit cache they convert.  The MMAs' warp and they come first: the scheduler takes
-    // the oldest warp that is ready.
-    static constexpr int LW = E4M3 ? 7 : 3;
-    static constexpr int LOADERS = 1, SOFTMAX = 1 + LW;
+    // A warp for the MMAs of each stream, then the loaders, which with an 8-bit cache convert.
+    static constexpr int LW = E4M3 ? 6 : 2;
+    static constexpr int LOADERS = 2, SOFTMAX = LOADERS + LW;
     static constexpr int THREADS = 32 * (SOFTMAX + SW);      // 384: 168 registers each; 512: 128
     static constexpr int CH = DP / 8;                        // 16-byte chunks of a row in shared memory
     static constexpr int GROUPS = STEP / 16;                 // of 16 tokens: loader warp w has w, w + LW, ...
@@ -213,6 +214,7 @@ struct TreeShape {
     static constexpr int SMEM = CONTROL + STREAMS * QTILE + NSLOT * SLOT + NRAW * RAW;
     static_assert(TM_O + STREAMS * DP <= 512, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(NSLOT % 4 == 0 && SOFTMAX % 4 == 0, "see above; a warp's lanes of TMEM");
     static_assert(THREADS * 8 <= STREAMS * QTILE, "the prefix sums lie in the queries' place");
 };
 
@@ -223,7 +225,7 @@ struct TreeLine {
 
 template <class S>
 struct TreeControl {
-    uint64_t bars[2 * S::NSLOT + 10 + S::NRAW];
+    uint64_t bars[2 * S::NSLOT + 12 + S::NRAW];
     TreeLine line;
     long long scan[S::THREADS / 32];
     uint32_t tmem_base;
@@ -319,7 +321,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     const uint32_t q_smem = base, ring = base + STREAMS * S::QTILE;
     const uint32_t bar0 = smem_addr(ctl.bars);
     const uint32_t full = bar0, empty = full + 8 * NSLOT, q_full = empty + 8 * NSLOT, q_empty = q_full + 8;
-    const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, o_free = o_full + 8;
+    const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 32, o_free = o_full + 8;
     const uint32_t pv_done = o_free + 8, fix_full = pv_done + 8, raw_full = fix_full + 8;
     TreePart* heads = static_cast<TreePart*>(a.workspace);
     float* parts = reinterpret_cast<float*>(heads + ctas);
@@ -330,17 +332,18 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             tree_store16(base + 16 * e, make_uint4(0, 0, 0, 0));
     if (tid < NSLOT) {
         mbar_init(full + 8 * tid, 1);
-        mbar_init(empty + 8 * tid, 1);
+        mbar_init(empty + 8 * tid, STREAMS);
     }
     if (tid == 0) {
         mbar_init(q_full, 1);
         for (int s = 0; s < S::NRAW; ++s) mbar_init(raw_full + 8 * s, 1);
-        mbar_init(q_empty, 1 + SW);
+        mbar_init(q_empty, STREAMS + SW);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + 8 * s, 2);  // the MMAs are done; what the producers noted can be seen
-            mbar_init(p_full + 8 * s, 4);
+            mbar_init(p_full + 16 * s, 4);      // of a place, its first half of the tokens, its second
+            mbar_init(p_full + 16 * s + 8, 4);
         }
-        mbar_init(o_full, 2);
+        mbar_init(o_full, 2 * STREAMS);
         mbar_init(o_free, SW);
         mbar_init(pv_done, 1);
         mbar_init(fix_full, 1);
@@ -510,28 +513,39 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 *static_cast<volatile int*>(&ctl.bad_page) = 1;
             };
 
-            // ---- tensor copies: lane -> box of box_rows tokens and, of 16-bit values, 64 columns ----
-            const int boxes = box_rows > 0 ? STEP / box_rows : 1;   // of a step's tokens
-            const int bg = lane % boxes, bb = lane / boxes;
-            const bool has_box = bb < (S::E4M3 ? 1 : S::BLOCKS);
+            // ---- tensor copies: lane g has the page of the step's box g of box_rows tokens; one thread issues
+            // them in turn, as copies of different lanes take several times as long ----
+            const int boxes = box_rows > 0 ? STEP / box_rows : 0;
             auto box_page = [&](int step) {  // num_pages, which gives zeros, where nobody sees a token
-                const int tok = tile_of(sq, step) * STEP + bg * box_rows;
-                return has_box && step < seg.step_end && tok < sq.len && (tok + box_rows > lo || tok < a.sinks)
+                const int tok = tile_of(sq, step) * STEP + lane * box_rows;
+                return lane < boxes && step < seg.step_end && tok < sq.len && (tok + box_rows > lo || tok < a.sinks)
                            ? table[page_of(tok)] : a.num_pages;
             };
             auto issue = [&](uint32_t dst, uint32_t bar, uint32_t bytes, const CUtensorMap* map, int step, int page) {
+                if (static_cast<unsigned>(page) > static_cast<unsigned>(a.num_pages)) bad(), page = a.num_pages;
+                else if (page == a.num_pages && lane < boxes) {
+                    const int tok = tile_of(sq, step) * STEP + lane * box_rows;
+                    if (tok < sq.len && (tok + box_rows > lo || tok < a.sinks)) bad();   // the table says so
+                }
+                const int tok0 = tile_of(sq, step) * STEP;
+                int in_page = tok0 - page_of(tok0) * a.page_size;
+                __syncwarp();   // what bad() noted comes before the arrival
                 if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
                 __syncwarp();
-                if (has_box) {
-                    const int tok = tile_of(sq, step) * STEP + bg * box_rows;
-                    if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
-                        if (page != a.num_pages) bad();
-                        page = a.num_pages;
+#pragma unroll 1
+                for (int g = 0; g < boxes; ++g) {
+                    const int at = static_cast<int>(tree_uniform(in_page));
+                    const int from = __shfl_sync(0xFFFFFFFFu, page, g);
+                    const uint32_t to = tree_uniform(dst + g * box_rows * (S::E4M3 ? DP : 128));
+                    if (tree_elect()) {
+#pragma unroll
+                        for (int block = 0; block < (S::E4M3 ? 1 : S::BLOCKS); ++block)
+                            tma_tensor_4d_g2s(to + block * STEP * 128, map, 64 * block, at, kvh, from, bar);
                     }
-                    const uint32_t to = S::E4M3 ? dst + bg * box_rows * DP : dst + bb * STEP * 128 + bg * box_rows * 128;
-                    tma_tensor_4d_g2s(to, map, 64 * bb, tok - page_of(tok) * a.page_size, kvh, page, bar);
+                    __syncwarp();
+                    in_page += box_rows;
+                    if (in_page == a.page_size) in_page = 0;
                 }
-                __syncwarp();
             };
 
             // ---- by all loaders: lanes 0 .. 15 and 16 .. 31 have the tokens of the warp's first two groups, ----
@@ -720,34 +734,26 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     issue_next();
                 }
             } else {
-                // Keys and values by the first warp, queries by the second (or all, behind the first step, where
-                // their place is taken until the item before has its last scores).
+                // Keys by the first warp, queries and values by the second (or the queries by both, behind the
+                // first step, as their place is taken until the item before has its last scores).  Each waits
+                // for slots of its own alone.
                 if (q_box > 0) load_queries();
-                int pid = 0, pid1 = 0;
-                if (lw == 0) pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
+                int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
 #pragma unroll 1
                 for (int st = seg.step; st < seg.step_end; ++st) {
                     const bool as_it_is = clean(st);
-                    if (lw == 0) {
-#pragma unroll 1
-                        for (int side = 0; side < 2; ++side) {
-                            wait(empty + 8 * slot, phase ^ 1u);
-                            issue(ring + slot * S::SLOT, side && !as_it_is ? fix_full : full + 8 * slot, S::SLOT,
-                                  side ? &vmap : &kmap, st, pid);
-                            if (!side) next_slot();
-                        }
-                        pid = pid1;
-                        pid1 = box_page(st + 2);
-                    } else {
-                        next_slot();
-                    }
+                    const int mine = slot + lw;
+                    wait(empty + 8 * mine, phase ^ 1u);
+                    issue(ring + mine * S::SLOT, lw && !as_it_is ? fix_full : full + 8 * mine, S::SLOT, lw ? &vmap : &kmap, st, pid);
+                    pid = pid1;
+                    pid1 = box_page(st + 2);
                     if (!as_it_is) {
-                        if (lw == 0) {  // the only one to wait on barriers: no other could tell their phases apart
+                        if (lw == 1) {  // the only one to wait for it: the other could not tell its phases apart
                             wait(fix_full, fix_phase);
                             fix_phase ^= 1u;
                         }
                         loaders_sync();
-                        const uint32_t tile = ring + slot * S::SLOT;
+                        const uint32_t tile = ring + (slot + 1) * S::SLOT;
                         const int tok0 = tile_of(sq, st) * STEP;
 #pragma unroll 4
                         for (int r = lw * LR + fsub; r < STEP; r += LW * LR) {
@@ -759,111 +765,105 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                                 if (finite(v)) tree_store16(at, v);
                             }
                         }
-                        all_there(full + 8 * slot);
+                        all_there(full + 8 * (slot + 1));
                     }
+                    next_slot();
                     next_slot();
                     if (st == seg.step && q_box == 0) load_queries();
                 }
             }
             more = after(seg);
         }
-    } else if (warp == 0) {
+    } else if (warp < S::LOADERS) {
         // ================= the MMAs =================
+        // Each stream's by a warp of its own (one thread issues them), so that neither waits for the
+        // other's softmax.  With one stream, which has two places for S, the next S goes ahead of P V.
         constexpr int TYPE = S::BF ? 1 : 0;
         constexpr uint32_t idesc_s = idesc_f16(TYPE, 128, STEP), idesc_o = idesc_f16(TYPE, 128, DP) | kIdescBMajorMn;
-        int slot = 0;                       // of the ring, in the order in which the producers fill it
-        uint32_t q_phase = 0, free_phase = 0;
-        uint32_t job = 0;                   // of the CTA: S buffer job & 1
-        uint32_t ring_phase = 0;
-        uint32_t p_phase = 0;               // bit s: of p_full[s]
-        // the job whose P V is still to be issued
-        bool open = false, p_fresh = false, p_last = false, p_begins = false;
-        int p_slot = 0, p_buf = 0;
-        uint32_t p_ring_phase = 0;
-        bool p_frees = false;
-        auto issue_pv = [&]() {
-            wait(p_full + 8 * p_buf, (p_phase >> p_buf) & 1u);
-            p_phase ^= 1u << p_buf;
-            wait(full + 8 * p_slot, p_ring_phase);
-            if (p_begins) {  // the previous item's sums have been read
-                wait(o_free, free_phase ^ 1u);
-                free_phase ^= 1u;
-            }
-            tc_fence_after();
-            const uint32_t d = tree_uniform(tmem + S::TM_O + (STREAMS == 2 ? p_buf : 0) * DP);
-            const uint32_t p = tree_uniform(tmem + p_buf * STEP), tile = tree_uniform(ring + p_slot * S::SLOT);
-            if (tree_elect()) {
-                const uint64_t v = sw128_desc_mn(tile, STEP * 128);
-#pragma unroll
-                for (int kb = 0; kb < STEP / 16; ++kb) {
-                    tc_mma_ts(d, p + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || !p_fresh);
-                    tc_mma_ts(d, p + 16 * kb + 8, v + 128 * kb, idesc_o, 1);
-                }
-                if (p_frees) tc_commit(empty + 8 * p_slot);
-                if (STREAMS == 1) tc_commit(pv_done);
-                if (p_last) {
-                    tc_commit(o_full);
-                    mbar_arrive(o_full);
-                }
-            }
-            __syncwarp();
-            open = false;
-        };
-        // S of a job, then P V of the job before, across the ends of items.
-        int j = 0, jobs = 0, k_slot = 0;
-        uint32_t k_phase = 0;
-        bool dual = false, fresh = true;   // fresh: seg has not been begun
-        for (;;) {
-            if (more && fresh) {
-                dual = rows_of(seg) > kTreeRows;
-                jobs = (seg.step_end - seg.step) << (dual ? 1 : 0);
-                j = 0;
-                fresh = false;
-                wait(q_full, q_phase);
-                q_phase ^= 1u;
-            }
-            const int buf = job & 1;
-            const bool second = dual && (j & 1);
-            if (more) {
-                if (!second) {
-                    k_slot = slot, k_phase = ring_phase;
-                    if (++slot == NSLOT) slot = 0, ring_phase ^= 1u;
-                }
-                wait(full + 8 * k_slot, k_phase);
+        const int stream = warp;
+        if (stream >= STREAMS) more = false;
+        uint32_t q_phase = 0, free_phase = 0, p_phase = 0;  // p_phase: bit x of place x
+        int step0 = 0;                                      // the CTA's steps before this item
+#pragma unroll 1
+        while (more) {
+            const bool dual = rows_of(seg) > kTreeRows;
+            const int steps = seg.step_end - seg.step;
+            // the stream's steps: all, or every other one of the CTA's; those that it has alone it frees for both
+            const bool alone = STREAMS == 2 && !dual;
+            const int first = alone ? (stream ^ step0) & 1 : 0, stride = alone ? 2 : 1;
+            wait(q_full, q_phase);
+            q_phase ^= 1u;
+            auto issue_s = [&](int st) {
+                const int at = step0 + st, slot = 2 * at % NSLOT, place = STREAMS == 2 ? stream : at & 1;
+                wait(full + 8 * slot, (2 * at / NSLOT) & 1);
                 tc_fence_after();
-                const uint32_t q_at = tree_uniform(q_smem + (second ? S::QTILE : 0)), k_at = tree_uniform(ring + k_slot * S::SLOT);
-                const uint32_t d = tree_uniform(tmem + buf * STEP);
+                const uint32_t q_at = tree_uniform(q_smem + (dual ? stream * S::QTILE : 0));
+                const uint32_t k_at = tree_uniform(ring + slot * S::SLOT), d = tree_uniform(tmem + place * STEP);
                 if (tree_elect()) {
                     const uint64_t q = sw128_desc(q_at), k = sw128_desc(k_at);
 #pragma unroll
                     for (int c = 0; c < DP / 16; ++c)
                         tc_mma_ss(d, q + (c >> 2) * (kTreeRows * 128 >> 4) + (c & 3) * 2,
                                   k + (c >> 2) * (STEP * 128 >> 4) + (c & 3) * 2, idesc_s, c > 0);
-                    tc_commit(s_full + 8 * buf);
-                    if (!dual || second) tc_commit(empty + 8 * k_slot);
-                    if (j == jobs - 1) tc_commit(q_empty);
-                    mbar_arrive(s_full + 8 * buf);
+                    tc_commit(s_full + 8 * place);
+                    tc_commit(empty + 8 * slot);
+                    if (alone) tc_commit(empty + 8 * slot);
+                    if (st + stride >= steps) tc_commit(q_empty);
+                    mbar_arrive(s_full + 8 * place);
                 }
                 __syncwarp();
+            };
+            if (first < steps) {
+                issue_s(first);
+            } else if (lane == 0) {
+                mbar_arrive(q_empty);
             }
-            if (open) issue_pv();
-            if (!more) break;
-            open = true;
-            p_buf = buf;
-            p_begins = j == 0;
-            // the first of its stream: it begins the sums
-            p_fresh = STREAMS == 2 ? j < 2 : j == 0;
-            p_last = j == jobs - 1;
-            p_frees = !dual || second;
-            if (!second) {
-                p_slot = slot, p_ring_phase = ring_phase;
-                if (++slot == NSLOT) slot = 0, ring_phase ^= 1u;
+            wait(o_free, free_phase ^ 1u);  // the previous item's sums have been read
+            free_phase ^= 1u;
+            // (only now: o_full's phase before this item's is complete, so that no arrival counts for it)
+            if (first >= steps && lane == 0) {
+                mbar_arrive(o_full);
+                mbar_arrive(o_full);
             }
-            ++job;
-            if (++j == jobs) {
-                more = after(seg);
-                fresh = true;
+#pragma unroll 1
+            for (int st = first; st < steps; st += stride) {
+                const int at = step0 + st, slot = 2 * at % NSLOT + 1, place = STREAMS == 2 ? stream : at & 1;
+                if (STREAMS == 1 && st + 1 < steps) issue_s(st + 1);
+                wait(full + 8 * slot, (2 * at / NSLOT) & 1);
+                const uint32_t d = tree_uniform(tmem + S::TM_O + stream * DP);
+                const uint32_t p = tree_uniform(tmem + place * STEP), tile = tree_uniform(ring + slot * S::SLOT);
+                const uint32_t fresh = st == first;   // it begins the sums
+                constexpr int HALF = STEP / 32;       // blocks of 16 tokens
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {         // the first half's product runs beside the second's softmax
+                    wait(p_full + 16 * place + 8 * h, (p_phase >> place) & 1u);
+                    tc_fence_after();
+                    const uint32_t ph = tree_uniform(p + 16 * HALF * h), vh = tree_uniform(tile + 2048 * HALF * h);
+                    if (tree_elect()) {
+                        const uint64_t v = sw128_desc_mn(vh, STEP * 128);
+#pragma unroll
+                        for (int kb = 0; kb < HALF; ++kb) {
+                            tc_mma_ts(d, ph + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || h > 0 || !fresh);
+                            tc_mma_ts(d, ph + 16 * kb + 8, v + 128 * kb, idesc_o, 1);
+                        }
+                    }
+                    __syncwarp();
+                }
+                p_phase ^= 1u << place;
+                if (tree_elect()) {
+                    tc_commit(empty + 8 * slot);
+                    if (alone) tc_commit(empty + 8 * slot);
+                    if (STREAMS == 1) tc_commit(pv_done);
+                    if (st + stride >= steps) {
+                        tc_commit(o_full);
+                        mbar_arrive(o_full);
+                    }
+                }
+                __syncwarp();
+                if (STREAMS == 2 && st + stride < steps) issue_s(st + stride);
             }
+            step0 += steps;
+            more = after(seg);
         }
     } else {
         // ================= softmax =================
@@ -871,17 +871,15 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         const int stream = (warp - S::SOFTMAX) >> 2;
         const int r = tid & (kTreeRows - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's lanes of TMEM
-        uint32_t s_phase = 0, o_phase = 0, job = 0, pv_jobs = 0;
+        uint32_t s_phase = 0, o_phase = 0, pv_jobs = 0;
+        int step0 = 0;
         while (more) {
             const TreeSeq& sq = seg.seq;
             const int kvh = head_of(seg), row0 = row0_of(seg), rows = rows_of(seg);
             const bool dual = rows > kTreeRows;
-            const int steps = seg.step_end - seg.step, jobs = dual ? 2 * steps : steps;
-            const uint32_t job0 = job;
-            job += jobs;
+            const int steps = seg.step_end - seg.step;
             const int ctx = sq.len - sq.n;
-            // dual: the stream's tile alternates with the number of jobs before
-            const int tile = dual ? (stream ^ (job0 & 1)) : 0;
+            const int tile = dual ? stream : 0;
             const int in_item = tile * kTreeRows + r;
             const bool live = in_item < rows;
             const int row = row0 + in_item, i = live ? token_of_row(row) : 0, head = kvh * G + (live ? row - i * G : 0);
@@ -898,18 +896,17 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             float f = (fabs_scale == 0.0f ? 1.0f : fabs_scale) * 1.4426950408889634f;
             float m = -INFINITY, ref = 0.0f, l = 0.0f;
             bool first = true;
-            // jobs of this stream
-            const int j0 = STREAMS == 2 ? (stream ^ (job0 & 1)) : 0;
-            constexpr int JS = STREAMS;
-            if (j0 >= jobs) {
+            const bool alone = STREAMS == 2 && !dual;
+            const int first_step = alone ? (stream ^ step0) & 1 : 0;
+            if (first_step >= steps) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_empty);
             }
-            for (int j = j0; j < jobs; j += JS) {
-                const int buf = (job0 + j) & 1;
-                const int tok0 = tile_of(sq, seg.step + (dual ? j >> 1 : j)) * STEP;
+            for (int st = first_step; st < steps; st += alone ? 2 : 1) {
+                const int buf = STREAMS == 2 ? stream : (step0 + st) & 1;
+                const int tok0 = tile_of(sq, seg.step + st) * STEP;
                 const uint32_t s_at = tmem + lanes + buf * STEP;
-                const uint32_t o_at = tmem + lanes + S::TM_O + (STREAMS == 2 ? buf : 0) * DP;
+                const uint32_t o_at = tmem + lanes + S::TM_O + stream * DP;
                 wait(s_full + 8 * buf, (s_phase >> buf) & 1u);
                 s_phase ^= 1u << buf;
                 tc_fence_after();
@@ -919,7 +916,10 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (lane == 0) mbar_arrive(q_empty);
                 }
                 if (!any_live) {  // what these rows of P hold reaches only rows that nobody reads
-                    if (lane == 0) mbar_arrive(p_full + 8 * buf);
+                    if (lane == 0) {
+                        mbar_arrive(p_full + 16 * buf);
+                        mbar_arrive(p_full + 16 * buf + 8);
+                    }
                     first = false;
                     if constexpr (STREAMS == 1) ++pv_jobs;
                     continue;
@@ -1045,16 +1045,21 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (c + 2 < NC) tmem_ld32(s_at + 32 * (c + 2), xa);
                     weights(xb, 0, s_at + 32 * c + 32);
                     weights(xb, 16, s_at + 32 * c + 48);
+                    if (NC == 4 || c + 2 == NC) {  // a half (of 64 tokens: both at once)
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (NC == 4) mbar_arrive(p_full + 16 * buf + 4 * c);
+                            else mbar_arrive(p_full + 16 * buf), mbar_arrive(p_full + 16 * buf + 8);
+                        }
+                    }
                 }
                 {
                     float s0, s1;
                     unpack_f2(add_f2(l2[0], l2[1]), s0, s1);
                     l += s0 + s1;
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * buf);
                 first = false;
                 if constexpr (STREAMS == 1) ++pv_jobs;
             }
@@ -1081,8 +1086,8 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 fx[1] = s1.x == -INFINITY ? 0.0f : tree_exp2(s1.x - m);
                 l = s0.y * fx[0] + s1.y * fx[1];
                 // a stream that had no job has nothing in its place
-                use[0] = fx[0] != 0.0f && (jobs > 1 || (job0 & 1) == 0);
-                use[1] = fx[1] != 0.0f && (jobs > 1 || (job0 & 1) == 1);
+                use[0] = fx[0] != 0.0f && (steps > 1 || (step0 & 1) == 0);
+                use[1] = fx[1] != 0.0f && (steps > 1 || (step0 & 1) == 1);
                 c0 = stream * (DP / 2), c1 = c0 + DP / 2;
             }
             const int64_t out_row = sq.first + i;
@@ -1159,6 +1164,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 heads[cta] = TreePart{static_cast<int>(tree_quotient(at0 + sq.steps - 1, line.share)) - cta + 1, row0, rows, kvh * G,
                                       sq.first, vs, {0, 0}};
             }
+            step0 += steps;
             more = after(seg);
         }
     }
