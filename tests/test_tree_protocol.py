@@ -56,7 +56,8 @@ class Kernel:
         self.empty = [Bar(streams) for _ in range(nslot)]
         sw = 4 * streams
         self.q_full, self.q_empty = Bar(1), Bar(streams + sw)
-        self.s_full, self.p_full = [Bar(2) for _ in range(2)], [[Bar(4), Bar(4)] for _ in range(2)]
+        self.s_full, self.p_full = [Bar(2) for _ in range(2)], [Bar(4) for _ in range(2)]
+        self.turn = [Bar(1), Bar(1)]
         self.o_full, self.o_free, self.pv_done, self.fix = Bar(2 * streams), Bar(sw), Bar(1), Bar(1)
         self.loaders, self.softmaxes = Sync(2), Sync(sw)
         self.slots, self.q = [None] * nslot, None
@@ -108,18 +109,22 @@ class Kernel:
 
     # ---- the MMAs of a stream ----
     def mma(self, stream):
-        q_phase, free_phase, p_phase, step0 = 0, 0, [0, 0], 0
+        q_phase, free_phase, p_phase, step0, turns = 0, 0, [0, 0], 0, 0
+        queue = self.queues[stream]
         for n, (steps, dual, _) in enumerate(self.segs):
             alone = self.streams == 2 and not dual
             first, stride = ((stream ^ step0) & 1, 2) if alone else (0, 1)
             yield self.q_full, q_phase
             q_phase ^= 1
-            queue = self.queues[stream]
 
-            def issue_s(st):
+            def keys(st):
+                at = step0 + st
+                return self.full[2 * at % self.nslot], (2 * at // self.nslot) & 1
+
+            def scores(st):
                 at = step0 + st
                 slot, place = 2 * at % self.nslot, stream if self.streams == 2 else at & 1
-                yield self.full[slot], (2 * at // self.nslot) & 1
+                yield keys(st)
 
                 def run(at=at, slot=slot, place=place, n=n):
                     assert self.slots[slot] == ("K", at, True), (self.slots[slot], at)
@@ -135,45 +140,56 @@ class Kernel:
                     queue.append(self.q_empty.arrive)
                 self.s_full[place].arrive()
 
-            if first < steps:
-                yield from issue_s(first)
-            else:
-                self.q_empty.arrive()
-            yield self.o_free, free_phase ^ 1
-            free_phase ^= 1
             if first >= steps:
+                self.q_empty.arrive()
+                yield self.o_free, free_phase ^ 1
+                free_phase ^= 1
                 self.o_full.arrive()
                 self.o_full.arrive()
-            for st in range(first, steps, stride):
-                at = step0 + st
-                slot, place = 2 * at % self.nslot + 1, stream if self.streams == 2 else at & 1
-                if self.streams == 1 and st + 1 < steps:
-                    yield from issue_s(st + 1)
-                yield self.full[slot], (2 * at // self.nslot) & 1
-                for h in range(2):
-                    yield self.p_full[place][h], p_phase[place]
+            for st in range(first - stride, steps, stride):
+                again = st + stride < steps
+                if self.streams == 1 and again:
+                    yield from scores(st + stride)
+                if st >= first:
+                    at = step0 + st
+                    slot, place = 2 * at % self.nslot + 1, stream if self.streams == 2 else at & 1
+                    if st == first:
+                        yield self.o_free, free_phase ^ 1
+                        free_phase ^= 1
+                    yield self.full[slot], (2 * at // self.nslot) & 1
+                    yield self.p_full[place], p_phase[place]
+                    p_phase[place] ^= 1
+                    if dual:
+                        yield self.turn[stream], (turns & 1) ^ (stream == 0)
 
-                    def run(at=at, slot=slot, place=place, h=h, fresh=st == first and h == 0):
+                    def run(at=at, slot=slot, place=place, fresh=st == first):
                         assert self.slots[slot] == ("V", at, True), (self.slots[slot], at)
                         p = self.places[place]
-                        assert isinstance(p, dict) and p["at"] == at and p["done"][h] == 4, (p, at, h)
+                        assert isinstance(p, dict) and p["at"] == at and p["done"] == 4, (p, at)
                         if fresh:
                             self.o[stream] = []
-                        self.o[stream].append((at, h))
-                        if h:
-                            self.places[place] = None
+                        self.o[stream].append(at)
+                        self.places[place] = None
                     queue.append(run)
-                p_phase[place] ^= 1
-                queue.append(self.empty[slot].arrive)
-                if alone:
                     queue.append(self.empty[slot].arrive)
-                if self.streams == 1:
-                    queue.append(self.pv_done.arrive)
-                if st + stride >= steps:
-                    queue.append(self.o_full.arrive)
-                    self.o_full.arrive()
-                if self.streams == 2 and st + stride < steps:
-                    yield from issue_s(st + stride)
+                    if alone:
+                        queue.append(self.empty[slot].arrive)
+                    if self.streams == 1:
+                        queue.append(self.pv_done.arrive)
+                    if st + stride >= steps:
+                        queue.append(self.o_full.arrive)
+                        self.o_full.arrive()
+                    if dual:
+                        there = again and keys(st + 1)[0].passes(keys(st + 1)[1])
+                        if there:
+                            yield from scores(st + 1)
+                        self.turn[stream ^ 1].arrive()
+                        turns += 1
+                        if again and not there:
+                            yield from scores(st + 1)
+                        continue
+                if self.streams == 2 and again:
+                    yield from scores(st + stride)
             step0 += steps
 
     # ---- a softmax warp ----
@@ -196,16 +212,15 @@ class Kernel:
                     if self.streams == 1:
                         yield self.pv_done, (jobs - 1) & 1
                     before = at - (2 if alone else 1)
-                    assert self.o[stream][-1] == (before, 1), (self.o[stream], before)
-                for h in range(2):
-                    p = self.places[place]
-                    if isinstance(p, tuple):
-                        assert p == ("S", at, stream), (p, at)
-                        p = self.places[place] = {"at": at, "done": [0, 0]}
-                    assert p["at"] == at
-                    p["done"][h] += 1
-                    yield None
-                    self.p_full[place][h].arrive()
+                    assert self.o[stream][-1] == before, (self.o[stream], before)
+                p = self.places[place]
+                if isinstance(p, tuple):
+                    assert p == ("S", at, stream), (p, at)
+                    p = self.places[place] = {"at": at, "done": 0}
+                assert p["at"] == at
+                p["done"] += 1
+                yield None
+                self.p_full[place].arrive()
                 jobs += 1
             yield self.o_full, o_phase
             o_phase ^= 1
@@ -215,7 +230,7 @@ class Kernel:
                 mine = range(step0, step0 + steps) if not alone else \
                     [at for at in range(step0, step0 + steps) if at & 1 == x]
                 if (alone or x == stream) and len(mine):
-                    assert self.o[x] == [(at, h) for at in mine for h in range(2)], (x, self.o[x], mine)
+                    assert self.o[x] == list(mine), (x, self.o[x], mine)
             yield None
             self.o_free.arrive()
             step0 += steps

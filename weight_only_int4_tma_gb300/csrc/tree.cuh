@@ -321,8 +321,9 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     const uint32_t q_smem = base, ring = base + STREAMS * S::QTILE;
     const uint32_t bar0 = smem_addr(ctl.bars);
     const uint32_t full = bar0, empty = full + 8 * NSLOT, q_full = empty + 8 * NSLOT, q_empty = q_full + 8;
-    const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 32, o_free = o_full + 8;
-    const uint32_t pv_done = o_free + 8, fix_full = pv_done + 8, raw_full = fix_full + 8;
+    const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, o_free = o_full + 8;
+    const uint32_t pv_done = o_free + 8, fix_full = pv_done + 8, turn = fix_full + 8;
+    const uint32_t raw_full = turn + 16;
     TreePart* heads = static_cast<TreePart*>(a.workspace);
     float* parts = reinterpret_cast<float*>(heads + ctas);
 
@@ -340,8 +341,8 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         mbar_init(q_empty, STREAMS + SW);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + 8 * s, 2);  // the MMAs are done; what the producers noted can be seen
-            mbar_init(p_full + 16 * s, 4);      // of a place, its first half of the tokens, its second
-            mbar_init(p_full + 16 * s + 8, 4);
+            mbar_init(p_full + 8 * s, 4);
+            mbar_init(turn + 8 * s, 1);
         }
         mbar_init(o_full, 2 * STREAMS);
         mbar_init(o_free, SW);
@@ -783,7 +784,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         const int stream = warp;
         if (stream >= STREAMS) more = false;
         uint32_t q_phase = 0, free_phase = 0, p_phase = 0;  // p_phase: bit x of place x
-        int step0 = 0;                                      // the CTA's steps before this item
+        int step0 = 0, turns = 0;                           // the CTA's steps before this item; those of both streams
 #pragma unroll 1
         while (more) {
             const bool dual = rows_of(seg) > kTreeRows;
@@ -793,7 +794,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             const int first = alone ? (stream ^ step0) & 1 : 0, stride = alone ? 2 : 1;
             wait(q_full, q_phase);
             q_phase ^= 1u;
-            auto issue_s = [&](int st) {
+            auto scores = [&](int st) {
                 const int at = step0 + st, slot = 2 * at % NSLOT, place = STREAMS == 2 ? stream : at & 1;
                 wait(full + 8 * slot, (2 * at / NSLOT) & 1);
                 tc_fence_after();
@@ -813,44 +814,27 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 }
                 __syncwarp();
             };
-            if (first < steps) {
-                issue_s(first);
-            } else if (lane == 0) {
-                mbar_arrive(q_empty);
-            }
-            wait(o_free, free_phase ^ 1u);  // the previous item's sums have been read
-            free_phase ^= 1u;
-            // (only now: o_full's phase before this item's is complete, so that no arrival counts for it)
-            if (first >= steps && lane == 0) {
-                mbar_arrive(o_full);
-                mbar_arrive(o_full);
-            }
-#pragma unroll 1
-            for (int st = first; st < steps; st += stride) {
+            auto values = [&](int st) {
                 const int at = step0 + st, slot = 2 * at % NSLOT + 1, place = STREAMS == 2 ? stream : at & 1;
-                if (STREAMS == 1 && st + 1 < steps) issue_s(st + 1);
+                if (st == first) {
+                    wait(o_free, free_phase ^ 1u);  // the previous item's sums have been read
+                    free_phase ^= 1u;
+                }
                 wait(full + 8 * slot, (2 * at / NSLOT) & 1);
                 const uint32_t d = tree_uniform(tmem + S::TM_O + stream * DP);
                 const uint32_t p = tree_uniform(tmem + place * STEP), tile = tree_uniform(ring + slot * S::SLOT);
                 const uint32_t fresh = st == first;   // it begins the sums
-                constexpr int HALF = STEP / 32;       // blocks of 16 tokens
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {         // the first half's product runs beside the second's softmax
-                    wait(p_full + 16 * place + 8 * h, (p_phase >> place) & 1u);
-                    tc_fence_after();
-                    const uint32_t ph = tree_uniform(p + 16 * HALF * h), vh = tree_uniform(tile + 2048 * HALF * h);
-                    if (tree_elect()) {
-                        const uint64_t v = sw128_desc_mn(vh, STEP * 128);
-#pragma unroll
-                        for (int kb = 0; kb < HALF; ++kb) {
-                            tc_mma_ts(d, ph + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || h > 0 || !fresh);
-                            tc_mma_ts(d, ph + 16 * kb + 8, v + 128 * kb, idesc_o, 1);
-                        }
-                    }
-                    __syncwarp();
-                }
+                wait(p_full + 8 * place, (p_phase >> place) & 1u);
                 p_phase ^= 1u << place;
+                if (dual) wait(turn + 8 * stream, (turns & 1) ^ (stream == 0));
+                tc_fence_after();
                 if (tree_elect()) {
+                    const uint64_t v = sw128_desc_mn(tile, STEP * 128);
+#pragma unroll
+                    for (int kb = 0; kb < STEP / 16; ++kb) {
+                        tc_mma_ts(d, p + 16 * kb, v + 128 * kb, idesc_o, kb > 0 || !fresh);
+                        tc_mma_ts(d, p + 16 * kb + 8, v + 128 * kb, idesc_o, 1);
+                    }
                     tc_commit(empty + 8 * slot);
                     if (alone) tc_commit(empty + 8 * slot);
                     if (STREAMS == 1) tc_commit(pv_done);
@@ -860,7 +844,37 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     }
                 }
                 __syncwarp();
-                if (STREAMS == 2 && st + stride < steps) issue_s(st + stride);
+            };
+            if (first >= steps) {  // the one step is the other stream's
+                if (lane == 0) mbar_arrive(q_empty);
+                wait(o_free, free_phase ^ 1u);
+                free_phase ^= 1u;
+                // (only now: o_full's phase before this item's is complete, so that no arrival counts for it)
+                if (lane == 0) {
+                    mbar_arrive(o_full);
+                    mbar_arrive(o_full);
+                }
+            }
+#pragma unroll 1
+            for (int st = first - stride; st < steps; st += stride) {
+                const bool again = st + stride < steps;
+                if (STREAMS == 1 && again) scores(st + stride);
+                if (st >= first) {
+                    values(st);
+                    // With both streams at work their products go in turn, a stream's P V and next S as one: the
+                    // streams then are half a round apart, and one's softmax has the cores while the other's
+                    // products run.  The turn is not held for keys that are not there yet.
+                    if (dual) {
+                        const int at = step0 + st + 1, slot = 2 * at % NSLOT;
+                        const bool there = again && __all_sync(0xFFFFFFFFu, mbar_test_wait(full + 8 * slot, (2 * at / NSLOT) & 1));
+                        if (there) scores(st + 1);
+                        if (lane == 0) mbar_arrive(turn + 8 * (stream ^ 1));
+                        ++turns;
+                        if (again && !there) scores(st + 1);
+                        continue;
+                    }
+                }
+                if (STREAMS == 2 && again) scores(st + stride);
             }
             step0 += steps;
             more = after(seg);
@@ -916,10 +930,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (lane == 0) mbar_arrive(q_empty);
                 }
                 if (!any_live) {  // what these rows of P hold reaches only rows that nobody reads
-                    if (lane == 0) {
-                        mbar_arrive(p_full + 16 * buf);
-                        mbar_arrive(p_full + 16 * buf + 8);
-                    }
+                    if (lane == 0) mbar_arrive(p_full + 8 * buf);
                     first = false;
                     if constexpr (STREAMS == 1) ++pv_jobs;
                     continue;
@@ -1045,16 +1056,11 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (c + 2 < NC) tmem_ld32(s_at + 32 * (c + 2), xa);
                     weights(xb, 0, s_at + 32 * c + 32);
                     weights(xb, 16, s_at + 32 * c + 48);
-                    if (NC == 4 || c + 2 == NC) {  // a half (of 64 tokens: both at once)
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (NC == 4) mbar_arrive(p_full + 16 * buf + 4 * c);
-                            else mbar_arrive(p_full + 16 * buf), mbar_arrive(p_full + 16 * buf + 8);
-                        }
-                    }
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * buf);
                 {
                     float s0, s1;
                     unpack_f2(add_f2(l2[0], l2[1]), s0, s1);
