@@ -95,6 +95,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "r"(taddr)
         : "memory");
 }
+// The same, and the largest of the 32 values (NaN if one is).
+__device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t (&v)[32], uint32_t& most) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.NaN.f32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+          "=r"(most)
+        : "r"(taddr)
+        : "memory");
+}
 // Waits for this thread's loads; names the registers that they fill, which are not to be used before.
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -949,7 +963,6 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         }
                     return v;
                 };
-                uint32_t xa[32], xb[32];
                 if (masked) {  // -infinity, in TMEM, for what the row does not see
                     auto hide = [&](uint32_t (&x)[32], int c) {
                         const uint32_t seen = seen_of(tok0 + c);
@@ -960,33 +973,32 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     };
 #pragma unroll 1
                     for (int c = 0; c < STEP; c += 32) {
-                        tmem_ld32(s_at + c, xa);
-                        tmem_wait_ld32(xa);
-                        hide(xa, c);
+                        uint32_t x[32];
+                        tmem_ld32(s_at + c, x);
+                        tmem_wait_ld32(x);
+                        hide(x, c);
                     }
                     tmem_wait_st();
                 }
-                // Twice over S, 32 tokens at a time, the next ones' load (some 200 cycles beside the MMAs) under
-                // way.  In loops: with the row's code in one line the roles' code is fetched anew from beyond the
-                // SM in every step (32 ragged sequences, trees of 32: 336 us).
+                // The row's maximum comes with the loads; the last 64 tokens stay in registers, the first come again
+                // while those are at work.  In loops: with a whole row's code in one line the roles' code no
+                // longer fits in the instruction cache and is fetched anew in every step.
                 constexpr int NC = STEP / 32;
-                float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto highest = [&](const uint32_t (&x)[32]) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        t4[e / 2 & 3] = max3_nan(t4[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                };
-                tmem_ld32(s_at, xa);
-#pragma unroll 1
-                for (int c = 0; c < NC; c += 2) {
+                uint32_t xa[32], xb[32], most[4] = {0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u};
+                if (NC == 4) {
+                    tmem_ld32_max(s_at, xa, most[0]);
+                    tmem_ld32_max(s_at + 32, xb, most[1]);
                     tmem_wait_ld32(xa);
-                    tmem_ld32(s_at + 32 * (c + 1), xb);
-                    highest(xa);
                     tmem_wait_ld32(xb);
-                    tmem_ld32(s_at + 32 * ((c + 2) & (NC - 1)), xa);
-                    highest(xb);
+                    asm volatile("" : "+r"(most[0]), "+r"(most[1]));
                 }
-                const float top = f * tree_max(tree_max(t4[0], t4[1]), tree_max(t4[2], t4[3]));
+                tmem_ld32_max(s_at + STEP - 64, xa, most[2]);
+                tmem_ld32_max(s_at + STEP - 32, xb, most[3]);
+                tmem_wait_ld32(xa);
+                tmem_wait_ld32(xb);
+                asm volatile("" : "+r"(most[2]), "+r"(most[3]));
+                const float top = f * tree_max(tree_max(__uint_as_float(most[0]), __uint_as_float(most[1])),
+                                               tree_max(__uint_as_float(most[2]), __uint_as_float(most[3])));
                 if (__any_sync(0xFFFFFFFFu, !(top <= m + kTreeLag))) {
                     const float now = tree_max(m, top);
                     const float scale = now == m ? 1.0f : tree_exp2(m - now);
@@ -996,7 +1008,6 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (!first) {
                         if constexpr (STREAMS == 1) wait(pv_done, (pv_jobs - 1) & 1u);
                         tc_fence_after();
-                        tmem_wait_ld32(xa);
 #pragma unroll 1
                         for (int c = 0; c < DP; c += 16) {
                             uint32_t y[16];
@@ -1047,15 +1058,17 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     tmem_st16(to, y);
                 };
 #pragma unroll 1
-                for (int c = 0; c < NC; c += 2) {
-                    tmem_wait_ld32(xa);
-                    tmem_ld32(s_at + 32 * (c + 1), xb);
+                for (int c = NC - 2; c >= 0; c -= 2) {
                     weights(xa, 0, s_at + 32 * c);
                     weights(xa, 16, s_at + 32 * c + 16);
-                    tmem_wait_ld32(xb);
-                    if (c + 2 < NC) tmem_ld32(s_at + 32 * (c + 2), xa);
+                    if (c > 0) tmem_ld32(s_at, xa);
                     weights(xb, 0, s_at + 32 * c + 32);
                     weights(xb, 16, s_at + 32 * c + 48);
+                    if (c > 0) {
+                        tmem_ld32(s_at + 32, xb);
+                        tmem_wait_ld32(xa);
+                        tmem_wait_ld32(xb);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
