@@ -7,8 +7,9 @@ namespace w4g {
 namespace {
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveBatch = 8;
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(MoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(MoveArgs a, int page_shift) {
     grid_dep_wait();
     const int side = a.kv_heads * a.row_chunks;  // pieces of a slot's keys
     const int piece = static_cast<int>(blockIdx.y) * kMoveThreads + static_cast<int>(threadIdx.x);
@@ -18,7 +19,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(MoveArgs a) {
     const int head = p / a.row_chunks;
     char* base = static_cast<char*>(kv.p) + head * kv.head_stride + 16 * (p - head * a.row_chunks);
     auto at = [&](int64_t slot) {
-        const int64_t page = slot / a.page_size;
+        const int64_t page = page_shift >= 0 ? slot >> page_shift : slot / a.page_size;
         return reinterpret_cast<uint4*>(base + page * kv.page_stride + (slot - page * a.page_size) * kv.slot_stride);
     };
     for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -27,14 +28,39 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(MoveArgs a) {
             record_status(a.status, kDecInvalidArg);
             continue;
         }
-        for (int i = first; i < last; ++i) {
-            const int64_t src = a.src[i], dst = a.dst[i];
-            if (src < 0 || dst < 0) continue;
-            if (src >= a.num_slots || dst >= a.num_slots) {
-                record_status(a.status, kDecInvalidArg);
-                continue;
+        // Eight moves at a time: their loads go together, unless one reads what another of them writes.
+        for (int i0 = first; i0 < last; i0 += kMoveBatch) {
+            int64_t src[kMoveBatch], dst[kMoveBatch];
+            bool apart = true;
+#pragma unroll
+            for (int j = 0; j < kMoveBatch; ++j) {
+                src[j] = dst[j] = -1;
+                if (i0 + j < last) src[j] = a.src[i0 + j], dst[j] = a.dst[i0 + j];
             }
-            *at(dst) = *at(src);
+#pragma unroll
+            for (int j = 0; j < kMoveBatch; ++j) {
+                if (src[j] >= 0 && dst[j] >= 0 && (src[j] >= a.num_slots || dst[j] >= a.num_slots)) {
+                    record_status(a.status, kDecInvalidArg);
+                    src[j] = -1;
+                }
+                if (src[j] < 0) dst[j] = -1;
+                if (dst[j] < 0) src[j] = -1;
+#pragma unroll
+                for (int k = 0; k < j; ++k) apart &= src[j] != dst[k] || src[j] < 0;
+            }
+            uint4 v[kMoveBatch];
+            if (apart) {
+#pragma unroll
+                for (int j = 0; j < kMoveBatch; ++j)
+                    if (src[j] >= 0) v[j] = *at(src[j]);
+#pragma unroll
+                for (int j = 0; j < kMoveBatch; ++j)
+                    if (src[j] >= 0) *at(dst[j]) = v[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < kMoveBatch; ++j)
+                    if (src[j] >= 0) *at(dst[j]) = *at(src[j]);
+            }
         }
     }
 }
@@ -45,7 +71,7 @@ int launch_move(const MoveArgs& a, cudaStream_t stream) {
     const unsigned blocks = blocks_for(2 * a.kv_heads * a.row_chunks, kMoveThreads);
     if (blocks > 65535) return -2;
     return launch_dependent(move_kernel, dim3(static_cast<unsigned>(a.B < 65536 ? a.B : 65536), blocks),
-                            dim3(kMoveThreads), 0, stream, a);
+                            dim3(kMoveThreads), 0, stream, a, power_of_two(a.page_size));
 }
 
 }  // namespace w4g

@@ -239,7 +239,7 @@ struct TreeLine {
 
 template <class S>
 struct TreeControl {
-    uint64_t bars[2 * S::NSLOT + 12 + S::NRAW];
+    uint64_t bars[2 * S::NSLOT + 12 + 2 * S::NRAW];
     TreeLine line;
     long long scan[S::THREADS / 32];
     uint32_t tmem_base;
@@ -247,6 +247,7 @@ struct TreeControl {
     int bad_page;                                   // a page lay outside the cache: masks look again
     int dirty;                                      // infinite values or NaN were replaced by 0
     float2 stats[S::STREAMS][kTreeRows];            // (m, l) of the streams, at the end of an item
+    int pages[2][16];                               // of a step's boxes, for the thread that copies them
     int8_t qe[S::STREAMS][kTreeRows];               // exponents of the rows' scaling of the queries
 };
 
@@ -337,7 +338,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     const uint32_t full = bar0, empty = full + 8 * NSLOT, q_full = empty + 8 * NSLOT, q_empty = q_full + 8;
     const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, o_free = o_full + 8;
     const uint32_t pv_done = o_free + 8, fix_full = pv_done + 8, turn = fix_full + 8;
-    const uint32_t raw_full = turn + 16;
+    const uint32_t raw_full = turn + 16, raw_empty = raw_full + 8 * S::NRAW;
     TreePart* heads = static_cast<TreePart*>(a.workspace);
     float* parts = reinterpret_cast<float*>(heads + ctas);
 
@@ -351,7 +352,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     }
     if (tid == 0) {
         mbar_init(q_full, 1);
-        for (int s = 0; s < S::NRAW; ++s) mbar_init(raw_full + 8 * s, 1);
+        for (int s = 0; s < 2 * S::NRAW; ++s) mbar_init(raw_full + 8 * s, 1);
         mbar_init(q_empty, STREAMS + SW);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + 8 * s, 2);  // the MMAs are done; what the producers noted can be seen
@@ -488,7 +489,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         };
         int slot = 0;
         uint32_t phase = 0, q_phase = 0;
-        int raw_in = 0, raw_out = 0;        // of the 8-bit tiles
+        int raw_at = 0;                     // of the 8-bit tiles
         uint32_t raw_phase = 0, fix_phase = 0;
         auto next_slot = [&]() {
             if (++slot == NSLOT) slot = 0, phase ^= 1u;
@@ -529,7 +530,8 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             };
 
             // ---- tensor copies: lane g has the page of the step's box g of box_rows tokens; one thread issues
-            // them in turn, as copies of different lanes take several times as long ----
+            // them all (copies of different lanes take several times as long), the pages handed to it through
+            // shared memory ----
             const int boxes = box_rows > 0 ? STEP / box_rows : 0;
             auto box_page = [&](int step) {  // num_pages, which gives zeros, where nobody sees a token
                 const int tok = tile_of(sq, step) * STEP + lane * box_rows;
@@ -537,30 +539,31 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                            ? table[page_of(tok)] : a.num_pages;
             };
             auto issue = [&](uint32_t dst, uint32_t bar, uint32_t bytes, const CUtensorMap* map, int step, int page) {
-                if (static_cast<unsigned>(page) > static_cast<unsigned>(a.num_pages)) bad(), page = a.num_pages;
-                else if (page == a.num_pages && lane < boxes) {
-                    const int tok = tile_of(sq, step) * STEP + lane * box_rows;
-                    if (tok < sq.len && (tok + box_rows > lo || tok < a.sinks)) bad();   // the table says so
+                const int tok0 = tile_of(sq, step) * STEP, tok = tok0 + lane * box_rows;
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.num_pages)) {
+                    // (num_pages itself may stand in the table)
+                    if (page != a.num_pages || (lane < boxes && tok < sq.len && (tok + box_rows > lo || tok < a.sinks))) bad();
+                    page = a.num_pages;
                 }
-                const int tok0 = tile_of(sq, step) * STEP;
-                int in_page = tok0 - page_of(tok0) * a.page_size;
-                __syncwarp();   // what bad() noted comes before the arrival
-                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                int* pages = ctl.pages[lw & 1];
+                if (lane < boxes) pages[lane] = page;
+                const uint32_t to = tree_uniform(dst), done = tree_uniform(bar), head = tree_uniform(kvh);
+                uint32_t in_page = tree_uniform(tok0 - page_of(tok0) * a.page_size);
                 __syncwarp();
-#pragma unroll 1
-                for (int g = 0; g < boxes; ++g) {
-                    const int at = static_cast<int>(tree_uniform(in_page));
-                    const int from = __shfl_sync(0xFFFFFFFFu, page, g);
-                    const uint32_t to = tree_uniform(dst + g * box_rows * (S::E4M3 ? DP : 128));
-                    if (tree_elect()) {
+                if (tree_elect()) {
+                    mbar_arrive_expect_tx(done, bytes);
+#pragma unroll 2
+                    for (int g = 0; g < boxes; ++g) {
+                        const int from = pages[g];
 #pragma unroll
                         for (int block = 0; block < (S::E4M3 ? 1 : S::BLOCKS); ++block)
-                            tma_tensor_4d_g2s(to + block * STEP * 128, map, 64 * block, at, kvh, from, bar);
+                            tma_tensor_4d_g2s(to + g * box_rows * (S::E4M3 ? DP : 128) + block * STEP * 128, map, 64 * block,
+                                              in_page, head, from, done);
+                        in_page += box_rows;
+                        if (in_page == static_cast<uint32_t>(a.page_size)) in_page = 0;
                     }
-                    __syncwarp();
-                    in_page += box_rows;
-                    if (in_page == a.page_size) in_page = 0;
                 }
+                __syncwarp();
             };
 
             // ---- by all loaders: lanes 0 .. 15 and 16 .. 31 have the tokens of the warp's first two groups, ----
@@ -632,8 +635,10 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     }
                 }
             };
-            constexpr int Q_WARP = S::E4M3 ? 0 : 1;
+            constexpr int Q_WARP = 1;
             auto load_queries = [&]() {
+                // by the second warp's copies, or by all loaders but an 8-bit cache's copying one
+                const int parts = S::E4M3 && box_rows > 0 ? LW - 1 : LW, part = lw - (LW - parts);
                 // f = |scale k_scale|; a negative or zero product is folded into the queries
                 const float f = a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f);
                 const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu, flip = f < 0.0f ? 0x80008000u : 0u;
@@ -641,8 +646,9 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 constexpr int RPI = 32 / CH;
                 const int c = lane % CH, sub = lane / CH;
                 const bool by_copy = q_box > 0 && f > 0.0f;
-                if (!by_copy || lw == Q_WARP) wait(q_empty, q_phase ^ 1u);
+                if (by_copy ? lw == Q_WARP : part >= 0) wait(q_empty, q_phase ^ 1u);
                 q_phase ^= 1u;
+                if (part < 0) return;
                 if (by_copy) {
                     // Tokens of G heads are G rows, one after another.  Rows behind the sequence's are another's,
                     // or zeros: nobody reads what they give.
@@ -658,11 +664,11 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 }
                 constexpr int AT = 16;  // loads at a time
 #pragma unroll 1
-                for (int n0 = lw * RPI + sub; n0 < padded; n0 += AT * LW * RPI) {
+                for (int n0 = part * RPI + sub; n0 < padded; n0 += AT * parts * RPI) {
                     uint4 v[AT];
 #pragma unroll
                     for (int x = 0; x < AT; ++x) {
-                        const int n = n0 + x * LW * RPI, row = row0 + n, i = token_of_row(row);
+                        const int n = n0 + x * parts * RPI, row = row0 + n, i = token_of_row(row);
                         v[x] = make_uint4(0, 0, 0, 0);
                         if (n < rows && c < row_chunks)
                             v[x] = *(reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(sq.first + i) * a.ldq +
@@ -670,7 +676,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     }
 #pragma unroll
                     for (int x = 0; x < AT; ++x) {
-                        const int n = n0 + x * LW * RPI, t = n / kTreeRows, r = n % kTreeRows;
+                        const int n = n0 + x * parts * RPI, t = n / kTreeRows, r = n % kTreeRows;
                         uint32_t* w = &v[x].x;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ flip;
@@ -693,7 +699,13 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         if (n < padded && c < row_chunks) tree_store16(q_smem + t * S::QTILE + at_smem(kTreeRows, r, c), v[x]);
                     }
                 }
-                all_there(q_full);
+                if (parts == LW) {
+                    all_there(q_full);
+                } else {
+                    fence_proxy_async_smem();
+                    asm volatile("bar.sync 3, %0;" ::"n"(32 * (LW - 1)) : "memory");
+                    if (part == 0 && lane == 0) mbar_arrive(q_full);
+                }
             };
             auto fill_step = [&](int st) {
                 look(st);
@@ -712,41 +724,46 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (st == seg.step) load_queries();
                 }
             } else if constexpr (S::E4M3) {
-                constexpr int NRAW = S::NRAW;
+                // The first warp copies 8-bit tiles; the others convert them into the ring.
+                constexpr int NRAW = S::NRAW, CW = LW - 1;
                 const uint32_t raw = ring + NSLOT * S::SLOT;
-                // tensor copies run ahead of the conversions: 2 st + side of the next one to issue
-                int ahead = 2 * seg.step, pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
-                auto issue_next = [&]() {
-                    if (ahead >= 2 * seg.step_end) return;
-                    if (lw == 0) {
-                        issue(raw + raw_in * S::RAW, raw_full + 8 * raw_in, S::RAW, ahead & 1 ? &vmap : &kmap, ahead >> 1, pid);
-                        if (ahead & 1) pid = pid1, pid1 = box_page((ahead + 3) >> 1);
-                    }
-                    ++ahead;
-                    if (++raw_in == NRAW) raw_in = 0;
-                };
-                for (int x = 0; x < NRAW; ++x) issue_next();
-                load_queries();
+                if (lw == 0) {
+                    int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
 #pragma unroll 1
-                for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
-                    wait(empty + 8 * slot, phase ^ 1u);
-                    wait(raw_full + 8 * raw_out, raw_phase);
-                    const uint32_t from = raw + raw_out * S::RAW, dst = ring + slot * S::SLOT;
-                    const int tok0 = tile_of(sq, half >> 1) * STEP;
-                    const bool care = (half & 1) && !clean(half >> 1);
-#pragma unroll 4
-                    for (int r = lw * LR + fsub; r < STEP; r += LW * LR) {
-                        uint4 v = lds_v4(from + r * DP + 16 * fc);
-                        if (care) {
-                            if (!wanted(tok0 + r)) v = make_uint4(0, 0, 0, 0);
-                            else if (some_not(tok0 + r)) finite(v);
-                        }
-                        put(dst, v, r);
+                    for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
+                        wait(raw_empty + 8 * raw_at, raw_phase ^ 1u);
+                        issue(raw + raw_at * S::RAW, raw_full + 8 * raw_at, S::RAW, half & 1 ? &vmap : &kmap, half >> 1, pid);
+                        if (half & 1) pid = pid1, pid1 = box_page((half + 3) >> 1);
+                        if (++raw_at == NRAW) raw_at = 0, raw_phase ^= 1u;
                     }
-                    all_there(full + 8 * slot);
-                    next_slot();
-                    if (++raw_out == NRAW) raw_out = 0, raw_phase ^= 1u;
-                    issue_next();
+                    load_queries();   // (no more than its place in their order)
+                } else {
+                    load_queries();
+#pragma unroll 1
+                    for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
+                        wait(empty + 8 * slot, phase ^ 1u);
+                        wait(raw_full + 8 * raw_at, raw_phase);
+                        const uint32_t from = raw + raw_at * S::RAW, dst = ring + slot * S::SLOT;
+                        const int tok0 = tile_of(sq, half >> 1) * STEP;
+                        const bool care = (half & 1) && !clean(half >> 1);
+#pragma unroll 4
+                        for (int r = (lw - 1) * LR + fsub; r < STEP; r += CW * LR) {
+                            uint4 v = lds_v4(from + r * DP + 16 * fc);
+                            if (care) {
+                                if (!wanted(tok0 + r)) v = make_uint4(0, 0, 0, 0);
+                                else if (some_not(tok0 + r)) finite(v);
+                            }
+                            put(dst, v, r);
+                        }
+                        fence_proxy_async_smem();
+                        asm volatile("bar.sync 3, %0;" ::"n"(32 * CW) : "memory");
+                        if (lw == 1 && lane == 0) {
+                            mbar_arrive(full + 8 * slot);
+                            mbar_arrive(raw_empty + 8 * raw_at);
+                        }
+                        next_slot();
+                        if (++raw_at == NRAW) raw_at = 0, raw_phase ^= 1u;
+                    }
                 }
             } else {
                 // Keys by the first warp, queries and values by the second (or the queries by both, behind the
