@@ -52,6 +52,11 @@ __device__ __forceinline__ uint32_t order_value(float v) {
 __device__ __forceinline__ uint64_t order_key(float v, int i) {
     return static_cast<uint64_t>(order_value(v)) << 32 | (0x7FFFFFFFu - static_cast<uint32_t>(i));
 }
+// The logit of a key (0 for -0, which makes no difference to its log probability).
+__device__ __forceinline__ float key_logit(uint64_t k) {
+    const uint32_t v = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float(v == 0xFFFFFFFFu ? 0x7FFFFFFFu : v >> 31 ? v & 0x7FFFFFFFu : ~v);
+}
 __device__ __forceinline__ int key_index(uint64_t k) {
     return static_cast<int>(0x7FFFFFFFu - static_cast<uint32_t>(k));
 }
@@ -128,6 +133,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
     const int p_lo = min(row.pieces, rank * per_cta), p_hi = min(row.pieces, p_lo + per_cta);
     const int tail0 = row.head + row.pieces * PER;
 
+    // the given token of this thread and its logit, under way from the start
+    const bool has_id = rank == 0 && tid < a.n_ids;
+    const int my_id = has_id ? a.ids[t * a.n_ids + tid] : -1;
+    const float my_logit = my_id >= 0 && my_id < a.V ? logit<DT>(base, my_id) : 0.0f;
+
     // ---- one pass: this thread's sums and its largest logit ----
     LpSums sum{-INFINITY, 0.0f, 0.0f};
     float bv = -INFINITY;   // NaN once there was one
@@ -200,32 +210,45 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
     if (rank == cluster - 1 && tid < row.tail) single(tail0 + tid);
 
     // ---- the CTA's sums, in warp 0 ----
-#pragma unroll
+    // (From here on loops stay loops: code that runs once per row is fetched as it runs, at some 20
+    // cycles an instruction: 60 rows of 32000 with 20 alternatives 16.0 us with them unrolled.)
+#pragma unroll 1
     for (int d = 16; d > 0; d >>= 1)
         sum.join({__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.s, d),
                   __shfl_xor_sync(0xFFFFFFFFu, sum.w, d)}, c);
     if (lane == 0) sh.part[warp] = sum;
     if (tid == 0) sh.n_chosen = sh.n_cand = 0, sh.least = 0xFFFFFFFFu;
 
+    auto cta_sums = [&]() {   // by one warp, beside what the others do
+        if (warp != kLpWarps - 1) return;
+        sum = sh.part[lane & (kLpWarps - 1)];
+#pragma unroll 1
+        for (int d = kLpWarps / 2; d > 0; d >>= 1)
+            sum.join({__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.s, d),
+                      __shfl_xor_sync(0xFFFFFFFFu, sum.w, d)}, c);
+        if (lane == 0) sh.part[0] = sum;
+    };
+
     // ---- the CTA's largest logits ----
     if (TOP) {
         const int k = a.top;
         const uint32_t mine = at == -1 ? 0u : order_value(bv);
         uint32_t key = mine;   // bitonic sort of the warp's, the largest in lane 0
-#pragma unroll
+#pragma unroll 1
         for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
+#pragma unroll 1
             for (int d = size >> 1; d > 0; d >>= 1) {
                 const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, key, d);
                 key = ((lane & d) == 0) == ((lane & size) == 0) ? max(key, o) : min(key, o);
             }
         sh.sorted[lane][warp] = key;
         __syncthreads();
+        cta_sums();
         // how many maxima are larger than this thread's: a binary search in every warp's list
         int lo[kLpWarps];
 #pragma unroll
         for (int w = 0; w < kLpWarps; ++w) lo[w] = 0;
-#pragma unroll
+#pragma unroll 1
         for (int step = 16; step > 0; step >>= 1)
 #pragma unroll
             for (int w = 0; w < kLpWarps; ++w)
@@ -264,6 +287,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
             __syncthreads();
             int larger = 0;
             if (in)
+#pragma unroll 2
                 for (int j = 0; j < kLpThreads; ++j) larger += sh.cand[j] > exact;
             if (in && larger < k) sh.chosen[larger] = tid;
             if (in && larger == k - 1) sh.least_key = exact;
@@ -288,13 +312,51 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
                 for (int e = 0; e < PER; ++e) use(x[e], row.head + p * PER + e);
             }
         };
-        each([&](float x, int i) {
-            const uint64_t key_of = order_key(x, i);
-            if (key_of >= least) {
-                const int slot = atomicAdd(&sh.n_cand, 1);
-                if (slot < kLpCandidates) sh.cand[slot] = key_of;
+        auto keep = [&](bool some, uint64_t key_of) {   // by whole warps: one addition for all lanes
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, some);
+            if (who == 0) return;
+            int at0 = 0;
+            if (lane == 0) at0 = atomicAdd(&sh.n_cand, __popc(who));
+            at0 = __shfl_sync(0xFFFFFFFFu, at0, 0) + __popc(who & ((1u << lane) - 1));
+            if (some && at0 < kLpCandidates) sh.cand[at0] = key_of;
+        };
+        if (row.head + row.tail > 0) {   // single logits of chosen threads
+            const int who = tid < chosen ? sh.chosen[tid] : kLpThreads;
+            const bool head = rank == 0 && who < row.head, tail = rank == cluster - 1 && who < row.tail;
+            uint64_t key_of = head ? order_key(logit<DT>(base, who), who) : 0;
+            keep(head && key_of >= least, key_of);
+            key_of = tail ? order_key(logit<DT>(base, tail0 + who), tail0 + who) : 0;
+            keep(tail && key_of >= least, key_of);
+        }
+        const uint32_t least_value = static_cast<uint32_t>(least >> 32);
+#pragma unroll 1
+        for (int n0 = tid - lane; n0 < chosen * each_has; n0 += kLpThreads) {
+            const int n = n0 + lane, nth = n / each_has;
+            const int p = n < chosen * each_has ? p_lo + sh.chosen[nth] + (n - nth * each_has) * kLpThreads : p_hi;
+            uint4 piece = make_uint4(0, 0, 0, 0);
+            uint32_t hits = 0;
+            if (p < p_hi) {
+                float x[PER];
+                piece = body[p];
+                unpack_logits<DT>(piece, x);
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    if (order_value(x[e]) >= least_value) hits |= 1u << e;
             }
-        });
+            while (__any_sync(0xFFFFFFFFu, hits != 0)) {   // one of each lane's at a time: few have any
+                const int e = __ffs(hits) - 1;
+                uint64_t key_of = 0;
+                if (hits) {
+                    const int word = DT == 2 ? e : e >> 1;
+                    const uint32_t w = word == 0 ? piece.x : word == 1 ? piece.y : word == 2 ? piece.z : piece.w;
+                    const float x = DT == 2 ? __uint_as_float(w)
+                                            : dec_to_f32<DT == 2 ? 0 : DT>(static_cast<uint16_t>(e & 1 ? w >> 16 : w & 0xFFFFu));
+                    key_of = order_key(x, row.head + p * PER + e);
+                }
+                keep(hits != 0 && key_of >= least, key_of);
+                hits &= hits - 1;
+            }
+        }
         __syncthreads();
         int n = sh.n_cand;
         if (n > kLpCandidates) {
@@ -306,13 +368,13 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
                     const uint64_t key_of = order_key(x, i);
                     if (key_of < below && key_of > most) most = key_of;
                 });
-#pragma unroll
+#pragma unroll 1
                 for (int d = 16; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
                 __syncthreads();
                 if (lane == 0) sh.red[warp] = most;
                 __syncthreads();
                 most = sh.red[lane & (kLpWarps - 1)];
-#pragma unroll
+#pragma unroll 1
                 for (int d = 16; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
                 if (tid == 0) sh.cand[n] = most;
                 below = most;
@@ -330,29 +392,26 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
         for (int i = tid; i < n; i += kLpThreads) {
             const uint64_t own = sh.cand[i];
             int larger = 0;
+#pragma unroll 8
             for (int j = 0; j < n; ++j) larger += sh.cand[j] > own;
             if (larger < k) put(larger, own);
         }
         if (tid >= n && tid < k) put(tid, 0);
     } else {
-        if (cluster > 1) cluster_wait_acquire();
         __syncthreads();
+        cta_sums();
+        if (cluster > 1) cluster_wait_acquire();
     }
 
     // ---- the row's ----
-    if (warp == 0) {
-        sum = sh.part[lane & (kLpWarps - 1)];
-        if (lane >= kLpWarps) sum = LpSums{-INFINITY, 0.0f, 0.0f};
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            sum.join({__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.s, d),
-                      __shfl_xor_sync(0xFFFFFFFFu, sum.w, d)}, c);
-        if (cluster > 1 && lane == 0) {
+    if (warp == kLpWarps - 1 && lane == 0) {
+        sum = sh.part[0];
+        if (cluster > 1) {
             const uint32_t dst = map_to_rank(smem_addr(&sh.ranks[rank]), 0);
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(sum.m) : "memory");
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 4), "f"(sum.s) : "memory");
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 8), "f"(sum.w) : "memory");
-        } else if (lane == 0) {
+        } else {
             sh.ranks[0] = sum;
         }
     }
@@ -363,35 +422,54 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
         __syncthreads();
     }
     sum = sh.ranks[0];
+#pragma unroll 1
     for (int r = 1; r < cluster; ++r) sum.join(sh.ranks[r], c);
-    // ln S by its exponent, in fp64, and its mantissa: within 2^-24 of the result's last bits however
-    // large S is, without a logarithm in fp64
+    // ln S = a_s + b_s: its exponent times 355 / 512, ln 2's leading bits, exact, and the rest (the reduction
+    // of Cody and Waite, Software Manual for the Elementary Functions, 1980); and sums with the error of
+    // each rounding, so that a result is within little more than its own last rounding however large m
+    // is.  (In fp64 these few operations took 6000 cycles, a third of a single row's time.)
     const float m = sum.m;
     const int s_bits = __float_as_int(sum.s);
-    const double log_s = ((s_bits >> 23) - 127) * 0.69314718055994530942 +
-                         logf(__int_as_float((s_bits & 0x007FFFFF) | 0x3F800000));
-    auto logprob = [&](float x) {
+    const float s_exp = static_cast<float>((s_bits >> 23) - 127);
+    const float a_s = s_exp * 0.693359375f;
+    const float b_s = fmaf(s_exp, -2.12194440054690583e-4f, logf(__int_as_float((s_bits & 0x007FFFFF) | 0x3F800000)));
+    auto two_sum = [](float x, float y, float& err) {
+        const float s = x + y, z = s - x;
+        err = (x - (s - z)) + (y - z);
+        return s;
+    };
+    auto logprob = [&](float x) {   // (x - m) f - ln S
         if (!fine || m != m) return NAN;
         if (m == -INFINITY) return -INFINITY;
         if (m == INFINITY) return x == INFINITY ? NAN : -INFINITY;
-        return static_cast<float>((static_cast<double>(x) - m) * f - log_s);
+        if (x == -INFINITY) return x;
+        float d_err, s_err;
+        const float d = two_sum(x, -m, d_err), p = d * f;
+        const float s = two_sum(p, -a_s, s_err);
+        return fabsf(p) < 1e30f ? s + (s_err + (fmaf(d, f, -p) + d_err * f - b_s)) : p;
     };
     if (tid == 0) {
         float lse = NAN, entropy = NAN;
         if (fine && m == m) {
             lse = m, entropy = m == INFINITY ? NAN : 0.0f;
             if (fabsf(m) < INFINITY) {
-                lse = static_cast<float>(static_cast<double>(m) * f + log_s);
-                entropy = static_cast<float>(log_s - 0.69314718055994530942 * static_cast<double>(sum.w) / sum.s);
+                float err;
+                const float p = m * f, s = two_sum(p, a_s, err);
+                lse = fabsf(p) < 1e30f ? s + (err + (fmaf(m, f, -p) + b_s)) : p;
+                entropy = a_s + fmaf(-0.69314718055994531f, sum.w / sum.s, b_s);
             }
         }
         if (a.lse) a.lse[t] = lse;
         if (a.entropy) a.entropy[t] = entropy;
     }
-    for (int i = tid; i < a.n_ids; i += kLpThreads) {
-        const int id = a.ids[t * a.n_ids + i];
+    auto given = [&](int i, int id, float x) {
         if (id >= a.V) record_status(a.status, kDecInvalidArg);
-        a.logprobs[t * a.n_ids + i] = id < 0 ? 0.0f : id >= a.V ? NAN : logprob(logit<DT>(base, id));
+        a.logprobs[t * a.n_ids + i] = id < 0 ? 0.0f : id >= a.V ? NAN : logprob(x);
+    };
+    if (has_id) given(tid, my_id, my_logit);
+    for (int i = tid + kLpThreads; i < a.n_ids; i += kLpThreads) {
+        const int id = a.ids[t * a.n_ids + i];
+        given(i, id, id >= 0 && id < a.V ? logit<DT>(base, id) : 0.0f);
     }
     if (TOP) {
         // the CTAs' largest, each CTA's in order: a thread per key counts the larger ones
@@ -399,20 +477,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
         static_assert(kLpThreads == kLpCluster * kLpTop, "a thread for each key");
         const uint64_t mine = r < cluster && n < a.top ? sh.best[r][n] : 0;
         int larger = n;
-        for (int o = 0; o < cluster; ++o) {
-            int lo = 0;  // of CTA o's: a binary search
-            if (o != r && mine != 0) {
-#pragma unroll
-                for (int step = kLpTop / 2; step > 0; step >>= 1)
-                    if (lo + step <= a.top && sh.best[o][lo + step - 1] > mine) lo += step;
-                if (lo < a.top && sh.best[o][lo] > mine) ++lo;
-            }
-            larger += lo;
+        if (cluster > 1) {
+            larger = 0;
+            if (mine != 0)
+#pragma unroll 1
+                for (int o = 0; o < cluster; ++o)
+#pragma unroll 8
+                    for (int j = 0; j < a.top; ++j) larger += sh.best[o][j] > mine;
         }
         if (mine != 0 && larger < a.top) {
             const int id = key_index(mine);
             a.top_ids[t * a.top + larger] = id;
-            if (a.top_logprobs) a.top_logprobs[t * a.top + larger] = logprob(logit<DT>(base, id));
+            if (a.top_logprobs) a.top_logprobs[t * a.top + larger] = logprob(key_logit(mine));
         }
     }
 }
