@@ -1212,69 +1212,60 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
 }
 
 // Joins the parts of items that several CTAs hold.  blockIdx.x: the CTA that began the item; blockIdx.y: 32 of its
-// rows, a lane each; a warp has every eighth piece of four columns.
+// rows, a lane each, and 32 columns, four for each warp.
 constexpr int kTreeJoinThreads = 256;
 template <int DT, int DP, bool SHIFT>
 __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(TreeArgs a, int ctas) {
     constexpr float kShift = SHIFT ? 7.0f : 0.0f;
-    constexpr int ROWS = kTreeRows * tree_streams(DP), WARPS = kTreeJoinThreads / 32, V = DP / 4 / WARPS;
-    constexpr int PITCH = DP + 4;   // of a staged row, so that lanes' 8 bytes fall in different banks
+    constexpr int ROWS = kTreeRows * tree_streams(DP), PIECES = DP / 32;
+    constexpr int PITCH = 36;   // of a staged row, so that lanes' 8 bytes fall in different banks
     __shared__ __align__(16) uint16_t staged[32 * PITCH];
     grid_dep_wait();
     const TreePart* heads = static_cast<const TreePart*>(a.workspace);
     const TreePart h = heads[blockIdx.x];
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-    const int row0 = 32 * static_cast<int>(blockIdx.y), row = row0 + lane;
-    if (h.n <= 0 || row0 >= h.rows) return;
-    const float* parts = reinterpret_cast<const float*>(heads + ctas);
+    const int row0 = 32 * static_cast<int>(blockIdx.y / PIECES), col0 = 32 * static_cast<int>(blockIdx.y % PIECES);
+    const int row = row0 + lane;
+    if (h.n <= 0 || row0 >= h.rows || col0 >= a.head_dim) return;
     const int G = a.q_heads / a.kv_heads;
-    // (rows behind the last hold whatever they held: they are not stored)
-    auto part_of = [&](int k) {
-        return parts + (2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0)) * tree_part_floats(ROWS, DP);
-    };
-    float top = -INFINITY, sum = 0.0f;
+    // Part k: the item's first stands second in its CTA's place, the others first in theirs.  (Rows behind the
+    // last hold whatever they held: they are not stored.)
+    constexpr size_t PART = tree_part_floats(ROWS, DP);
+    const float* parts = reinterpret_cast<const float*>(heads + ctas) + 2 * blockIdx.x * PART + row;
+    auto part_of = [&](int k) { return parts + (k == 0 ? PART : 2 * k * PART); };
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < h.n; ++k) top = tree_max(top, *part_of(k));
+    float sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int k = 0; k < h.n; ++k) top = tree_max(top, part_of(k)[row]);
-    float4 acc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
     for (int k = 0; k < h.n; ++k) {
         const float* p = part_of(k);
-        const float m = p[row], l = p[ROWS + row];
-        const float4* o = reinterpret_cast<const float4*>(p + 2 * ROWS) + warp * ROWS + row;
-        float4 x[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[v] = o[v * WARPS * ROWS];
+        const float m = p[0], l = p[ROWS];
+        const float4 x = *(reinterpret_cast<const float4*>(p - row + 2 * ROWS) + (col0 / 4 + warp) * ROWS + row);
         const float f = m == -INFINITY ? 0.0f : tree_exp2(m - top);
         sum += l * f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (f == 0.0f) continue;
-            acc[v].x = fmaf(x[v].x, f, acc[v].x), acc[v].y = fmaf(x[v].y, f, acc[v].y);
-            acc[v].z = fmaf(x[v].z, f, acc[v].z), acc[v].w = fmaf(x[v].w, f, acc[v].w);
+        if (f != 0.0f) {
+            acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
+            acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
         }
     }
     const float inv = sum == 0.0f ? 0.0f : h.vs / sum;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        *reinterpret_cast<uint2*>(staged + lane * PITCH + 4 * (warp + v * WARPS)) =
-            make_uint2(dec_pack2<DT>(acc[v].x * inv, acc[v].y * inv), dec_pack2<DT>(acc[v].z * inv, acc[v].w * inv));
-    if (warp == 0 && row < h.rows && a.lse) {
+    *reinterpret_cast<uint2*>(staged + lane * PITCH + 4 * warp) =
+        make_uint2(dec_pack2<DT>(acc.x * inv, acc.y * inv), dec_pack2<DT>(acc.z * inv, acc.w * inv));
+    if (warp == 0 && col0 == 0 && row < h.rows && a.lse) {
         const int r = h.row0 + row, i = r / G, head = h.head0 + r - i * G;
         a.lse[static_cast<int64_t>(h.first + i) * a.q_heads + head] =
             sum > 0.0f ? (top - kShift) * 0.69314718055994531f + logf(sum) : sum == 0.0f ? -INFINITY : top;
     }
     __syncthreads();
-    const int chunks = a.head_dim / 8;
-    for (int e = tid; e < 32 * chunks; e += kTreeJoinThreads) {
-        const int in = e / chunks, c = e - in * chunks;
-        if (row0 + in >= h.rows) break;
+    const int in = tid >> 2, c = tid & 3;   // four 16-byte chunks of a row
+    if (in < 32 && row0 + in < h.rows && col0 + 8 * c < a.head_dim) {
         const int r = h.row0 + row0 + in, i = r / G, head = h.head0 + r - i * G;
         const uint16_t* from = staged + in * PITCH + 8 * c;
         const uint2 lo = *reinterpret_cast<const uint2*>(from), hi = *reinterpret_cast<const uint2*>(from + 4);
         *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(h.first + i) * a.ldo +
-                                  static_cast<int64_t>(head) * a.head_dim + 8 * c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                                  static_cast<int64_t>(head) * a.head_dim + col0 + 8 * c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
 }
 
@@ -1296,7 +1287,7 @@ int launch_tree_shape(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stre
     const int rc = launch_dependent(tree_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), dim3(S::THREADS),
                                     S::SMEM, stream, a, power_of_two(a.page_size), box, q_box, maps[0], maps[1], maps[2]);
     if (rc != 0) return rc;
-    return launch_dependent(tree_join_kernel<S::DT, S::DP, !S::BF>, dim3(static_cast<unsigned>(ctx.num_sms), S::ROWS / 32),
+    return launch_dependent(tree_join_kernel<S::DT, S::DP, !S::BF>, dim3(static_cast<unsigned>(ctx.num_sms), S::ROWS / 32 * (S::DP / 32)),
                             dim3(kTreeJoinThreads), 0, stream, a, ctx.num_sms);
 }
 
