@@ -787,8 +787,10 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         loaders_sync();
                         const uint32_t tile = ring + (slot + 1) * S::SLOT;
                         const int tok0 = tile_of(sq, st) * STEP;
-#pragma unroll 4
-                        for (int r = lw * LR + fsub; r < STEP; r += LW * LR) {
+                        // (behind the window's edges only the drafted tokens and those past the end)
+                        const int r_lo = tok0 >= edge ? max(ctx - tok0, 0) & ~(LW * LR - 1) : 0;
+#pragma unroll 2
+                        for (int r = r_lo + lw * LR + fsub; r < STEP; r += LW * LR) {
                             const uint32_t at = tile + at_smem(STEP, r, fc);
                             if (!wanted(tok0 + r)) {
                                 tree_store16(at, make_uint4(0, 0, 0, 0));
@@ -1131,7 +1133,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             const bool patch = *static_cast<volatile int*>(&ctl.dirty) != 0;
             // (in short pieces, as code that runs once per item comes from beyond the SM)
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 16) {
+            for (int c = any_live ? c0 : c1; c < c1; c += 16) {
                 uint32_t x[STREAMS][16];
                 float o[16];
 #pragma unroll
