@@ -79,6 +79,16 @@ __device__ __forceinline__ float tree_max(float a, float b) {  // NaN if either 
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
+// 16 bytes global -> shared, asynchronously; zeros where `bytes` is 0.
+__device__ __forceinline__ void tree_copy16(uint32_t dst, const char* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void tree_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void tree_wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void tree_store16(uint32_t dst, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
@@ -347,7 +357,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         for (uint32_t e = tid; e < (STREAMS * S::QTILE + NSLOT * S::SLOT) / 16; e += S::THREADS)
             tree_store16(base + 16 * e, make_uint4(0, 0, 0, 0));
     if (tid < NSLOT) {
-        mbar_init(full + 8 * tid, 1);
+        mbar_init(full + 8 * tid, box_rows > 0 ? 1 : LW);  // a copying thread, or every loader warp
         mbar_init(empty + 8 * tid, STREAMS);
     }
     if (tid == 0) {
@@ -613,25 +623,31 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 return any;
             };
             auto fill = [&](uint32_t dst, const void* from, const int64_t (&at)[SETS], bool values) {
-                constexpr int LN = 16 / LR;   // loads of a group; all groups' are under way together
-                uint4 v[MINE][LN];
+                // Loads of a group; with 8 bits those of all groups go together (16 sequences of 8192, 4 heads, pages
+                // of 5: 87 us, 117 one group after another), with 16 bits they would not fit in registers.
+                constexpr int LN = 16 / LR, TOGETHER = S::E4M3 ? MINE : 1;
 #pragma unroll
-                for (int n = 0; n < MINE; ++n)
+                for (int n0 = 0; n0 < MINE; n0 += TOGETHER) {
+                    uint4 v[TOGETHER][LN];
 #pragma unroll
-                    for (int x = 0; x < LN; ++x) {
-                        const int64_t off = __shfl_sync(0xFFFFFFFFu, at[n / 2], n % 2 * 16 + x * LR + fsub);
-                        v[n][x] = make_uint4(0, 0, 0, 0);
-                        if (off >= 0 && 16 * fc < a.head_dim * S::ES)
-                            v[n][x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(from) + off) + fc);
-                    }
+                    for (int k = 0; k < TOGETHER; ++k)
 #pragma unroll
-                for (int n = 0; n < MINE; ++n) {
-                    const int group = lw + LW * n;
-                    if (group >= S::GROUPS) break;
+                        for (int x = 0; x < LN; ++x) {
+                            const int n = n0 + k;
+                            const int64_t off = __shfl_sync(0xFFFFFFFFu, at[n / 2], n % 2 * 16 + x * LR + fsub);
+                            v[k][x] = make_uint4(0, 0, 0, 0);
+                            if (off >= 0 && 16 * fc < a.head_dim * S::ES)
+                                v[k][x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(from) + off) + fc);
+                        }
 #pragma unroll
-                    for (int x = 0; x < LN; ++x) {
-                        if (values && (mixed[n / 2] >> (n % 2 * 16 + x * LR + fsub) & 1u)) finite(v[n][x]);
-                        put(dst, v[n][x], group * 16 + x * LR + fsub);
+                    for (int k = 0; k < TOGETHER; ++k) {
+                        const int n = n0 + k, group = lw + LW * n;
+                        if (group >= S::GROUPS) break;
+#pragma unroll
+                        for (int x = 0; x < LN; ++x) {
+                            if (values && (mixed[n / 2] >> (n % 2 * 16 + x * LR + fsub) & 1u)) finite(v[k][x]);
+                            put(dst, v[k][x], group * 16 + x * LR + fsub);
+                        }
                     }
                 }
             };
@@ -707,22 +723,77 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (part == 0 && lane == 0) mbar_arrive(q_full);
                 }
             };
-            auto fill_step = [&](int st) {
-                look(st);
-                wait(empty + 8 * slot, phase ^ 1u);
-                fill(ring + slot * S::SLOT, a.kc.p, kat, false);
-                all_there(full + 8 * slot);
-                next_slot();
-                wait(empty + 8 * slot, phase ^ 1u);
-                fill(ring + slot * S::SLOT, a.vc.p, vat, true);
-                all_there(full + 8 * slot);
-                next_slot();
-            };
-            if (box_rows == 0) {  // pages that no tensor map describes
+            if (box_rows == 0) {
+                // Pages that no tensor map describes: every warp copies its groups of tokens, 16-bit ones
+                // asynchronously, and arrives by itself.
+                auto there = [&](uint32_t bar) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                uint32_t under_way[2] = {0, 0};   // barriers of slots whose copies are, the older one first
+                auto settle = [&]() {
+                    if (under_way[0]) {
+                        tree_wait_copies<1>();
+                        there(under_way[0]);
+                    }
+                    if (under_way[1]) {
+                        tree_wait_copies<0>();
+                        there(under_way[1]);
+                    }
+                    under_way[0] = under_way[1] = 0;
+                };
+#pragma unroll 1
                 for (int st = seg.step; st < seg.step_end; ++st) {
-                    fill_step(st);
-                    if (st == seg.step) load_queries();
+                    look(st);
+                    uint32_t some = 0;
+#pragma unroll
+                    for (int s = 0; s < SETS; ++s) some |= mixed[s];
+#pragma unroll(S::E4M3 ? 2 : 1)
+                    for (int side = 0; side < 2; ++side) {
+                        const uint32_t dst = ring + slot * S::SLOT, bar = full + 8 * slot;
+                        if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(empty + 8 * slot, phase ^ 1u))) {
+                            settle();   // what is under way may be what the slot's readers wait for
+                            wait(empty + 8 * slot, phase ^ 1u);
+                        }
+                        if (S::E4M3 || (side && some)) {
+                            if (side)
+                                fill(dst, a.vc.p, vat, true);
+                            else
+                                fill(dst, a.kc.p, kat, false);
+                            there(bar);
+                        } else {
+                            constexpr int RPI = 32 / CH;
+                            const int c = lane % CH, sub = lane / CH;
+                            const char* from = static_cast<const char*>(side ? a.vc.p : a.kc.p);
+#pragma unroll
+                            for (int n = 0; n < MINE; ++n) {
+                                const int group = lw + LW * n;
+                                if (group >= S::GROUPS) break;
+                                const int64_t mine = side ? vat[n / 2] : kat[n / 2];
+#pragma unroll
+                                for (int r0 = 0; r0 < 16; r0 += RPI) {
+                                    const int64_t off = __shfl_sync(0xFFFFFFFFu, mine, n % 2 * 16 + r0 + sub);
+                                    if (c < row_chunks)
+                                        tree_copy16(dst + at_smem(STEP, group * 16 + r0 + sub, c), off >= 0 ? from + off + 16 * c : from,
+                                                    off >= 0 ? 16 : 0);
+                                }
+                            }
+                            tree_commit();
+                            if (under_way[0]) {
+                                tree_wait_copies<2>();
+                                there(under_way[0]);
+                            }
+                            under_way[0] = under_way[1], under_way[1] = bar;
+                        }
+                        next_slot();
+                    }
+                    if (st == seg.step) {
+                        settle();
+                        load_queries();
+                    }
                 }
+                settle();
             } else if constexpr (S::E4M3) {
                 // The first warp copies 8-bit tiles; the others convert them into the ring.
                 constexpr int NRAW = S::NRAW, CW = LW - 1;
