@@ -364,8 +364,8 @@ typedef struct dec_logprob_config {
  *   cfg           host struct, read during the call.
  *   logits        device, T rows, aligned to their element.  Any stride and length; rows whose
  *                 first elements are 16-byte aligned alike take no slow beginning.
- *   factor        device, float [T], 1 / temperature, or NULL (all 1).  One that is not positive and finite
- *                 gives NaN in the row's lse, entropy and log probabilities.
+ *   factor        device, float [T], 1 / temperature, or NULL (all 1).  One that is not positive, or
+ *                 above 2^127, gives NaN in the row's lse, entropy and log probabilities.
  *   ids           device, int32 [T][n_ids]; NULL only if n_ids is 0.  A negative one stands for no
  *                 token: its log probability is written as 0.  One of vocab or more gives NaN and
  *                 records W4A16_ERR_INVALID_ARG in the status word.
@@ -388,7 +388,8 @@ int dec_token_logprobs(const dec_logprob_config* cfg, const void* logits, const 
  * is read as written, and of two moves to one slot the later stands.  Groups (one per sequence)
  * run at the same time and may not touch one another's slots.  To keep the path i0 < i1 < ... of
  * a tree cached from slot(ctx) on, move slot(ctx + ij) to slot(ctx + j) for every j.
- *   cache     host struct, read during the call.
+ *   cache     host struct, read during the call.  No two pages, slots or heads of it, nor keys and
+ *             values, may share memory; a stride of 0 where there are several is INVALID_ARG.
  *   src, dst  device, int64 [N].  A negative one stands for no move; one outside the cache moves
  *             nothing and records W4A16_ERR_INVALID_ARG in the status word.
  *   starts    device, int32 [B + 1], ascending, 0 .. N; a group that is out of range moves nothing

@@ -99,6 +99,15 @@ def test_move_cache_refusals(L, change, want):
     assert L.dec_kv_move(_cache(**change), F, F, F, 2, 3, None) == want
 
 
+@pytest.mark.parametrize("stride", ["k_page_stride", "v_page_stride", "k_slot_stride", "v_slot_stride", "k_head_stride",
+                                    "v_head_stride"])
+def test_move_of_places_that_share_memory(L, stride):
+    """Refused where there are several pages, slots or heads; of one, the stride does not matter."""
+    assert L.dec_kv_move(_cache(**{stride: 0}), F, F, F, 2, 0, None) == BAD
+    one = {"page": "num_pages", "slot": "page_size", "head": "kv_heads"}[stride.split("_")[1]]
+    assert L.dec_kv_move(_cache(**{stride: 0, one: 1}), F, F, F, 2, 0, None) == OK
+
+
 def test_move_argument_refusals(L):
     call = lambda src=F, dst=F, starts=F, B=2, N=3: L.dec_kv_move(_cache(), src, dst, starts, B, N, None)  # noqa: E731
     assert call(B=0) == OK and call(N=0) == OK and call(B=-1) == BAD and call(N=-1) == BAD

@@ -174,6 +174,18 @@ def test_factors():
     check(x, f, ids, 5, call(x, "bf16", f, ids, 5))
 
 
+def test_largest_factors():
+    """Up to 2^127, the largest logit's neighbours included; above it NaN."""
+    x = logits(3, 3000, "fp32", 14)
+    f = torch.tensor([2.0 ** 127, 2.0 ** 127 * 1.5, 2.0 ** 126], device="cuda")
+    ids = x.argmax(1, keepdim=True).int()
+    lp, lse, ent, tid, tlp = call(x * 1e-3, "fp32", f, ids, 3)
+    assert bool((lp[[0, 2]] == 0).all()) and bool((ent[[0, 2]] == 0).all()) and bool((tlp[[0, 2], 0] == 0).all())
+    assert bool((lse[[0, 2]].double() == (x * 1e-3).max(1).values[[0, 2]].double() * f[[0, 2]].double()).all())
+    assert all(bool(torch.isnan(r[1]).all()) for r in (lp, lse, ent, tlp))
+    assert torch.equal(tid[:, 0], ids[:, 0])
+
+
 @pytest.mark.parametrize("shift", [-1000.0, 1000.0, 60000.0])
 def test_far_from_zero(shift):
     x = logits(3, 4000, "fp32", 5) + shift

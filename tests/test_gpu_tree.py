@@ -289,6 +289,78 @@ def test_infinite_scores():
         assert bool(((out[row, 1] - want[1]).abs() <= want[1].abs() * 2.0 ** -11 + mag[1] * 2.0 ** -12).all())
 
 
+@pytest.mark.parametrize("dtype,kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3")])
+def test_scale_of_zero(dtype, kv):
+    """All weights are alike; 0 times a query that is infinite or NaN is NaN, in its own row and head alone."""
+    c = Case([(200, 6), (30, 3)], 4, 2, 64, dtype, kv, scale=0.0, seed=24)
+    c.run().check()
+    c.q[1, 5], c.q[7, 64 * 3 + 2] = math.inf, math.nan
+    out, lse = c.out.clone(), c.lse.clone()
+    c.run()
+    hit = torch.zeros(c.T, 4, dtype=torch.bool, device="cuda")
+    hit[1, 0] = hit[7, 3] = True
+    got = c.out.view(c.T, 4, 64)
+    assert bool(torch.isnan(got[hit]).all()) and bool(torch.isnan(c.lse[hit]).all())
+    assert torch.equal(got[~hit], out.view(c.T, 4, 64)[~hit]) and torch.equal(c.lse[~hit], lse[~hit])
+
+
+def test_largest_scale():
+    """Scores of 0 stay 0 under a scale whose product with log2 e is past fp32."""
+    c = Case([(200, 6)], 4, 2, 64, "bf16", scale=3.0e38, seed=25)
+    c.q.zero_()
+    c.run().check()
+
+
+def test_infinities_in_a_long_context():
+    """Hidden and seen infinite values beside many tokens that all rows see."""
+    c = Case([(40000, 5), (3000, 4)], 2, 1, 64, "bf16", mask=lambda n, r: [1 << i for i in range(n)], seed=26)
+    want = [c.run().out.clone(), c.lse.clone()]
+    for b, (ctx, n) in enumerate(c.seqs):
+        c.v[int(c.pages[b][ctx // 16]), ctx % 16, 0, 9] = math.inf       # drafted token 0, seen by row 0 alone
+    c.run()
+    first = torch.tensor(c.starts[:-1], device="cuda")
+    rest = [i for i in range(c.T) if i not in c.starts[:-1]]
+    got = c.out.view(c.T, 2, 64)
+    assert bool((~torch.isfinite(got[first, :, 9])).all()) and torch.equal(c.lse, want[1])
+    assert torch.equal(got[rest], want[0].view(c.T, 2, 64)[rest])
+    others = [d for d in range(64) if d != 9]
+    assert torch.equal(got[first][..., others], want[0].view(c.T, 2, 64)[first][..., others])
+
+
+@pytest.mark.parametrize("stride", ["slots", "heads"])
+def test_places_that_share_memory(stride):
+    """A cache whose slots, or heads, are one place in memory is read as it stands."""
+    c = Case([(300, 7)], 4, 2, 64, "bf16", seed=27)
+    c.k, c.v = (torch.randn(x.shape, generator=torch.Generator(device="cuda").manual_seed(s), device="cuda").to(x.dtype)
+                for s, x in enumerate((c.k, c.v)))
+    if stride == "slots":
+        c.k, c.v = (x[:, :1].expand(-1, 16, -1, -1) for x in (c.k, c.v))
+    else:
+        c.k, c.v = (x[:, :, :1].expand(-1, -1, 2, -1) for x in (c.k, c.v))
+    c.run().check()
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls on one workspace, replayed in turn on one stream, and an eager one between them."""
+    cases = [Case([(2000, 12), (50, 3)], 8, 2, 128, "bf16", seed=28), Case([(700, 30)], 16, 2, 128, "bf16", seed=29)]
+    args = [list(c.args()) for c in cases]
+    args[1][-1] = args[0][-1]
+    graphs = []
+    for a in args:
+        w4.dec_attn_tree(*a)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            w4.dec_attn_tree(*a)
+    for order in ((0, 1, 0), (1, 0, 1)):
+        for c in cases:
+            c.out.fill_(MARK)
+        for i in order:
+            graphs[i].replay()
+            w4.dec_attn_tree(*args[1 - i])
+        for c in cases:
+            c.check()
+
+
 # ---- streams, graphs, determinism ----
 
 def test_graph_replays_with_new_lengths():

@@ -899,6 +899,11 @@ int dec_kv_move(const dec_kv_cache* cache, const int64_t* src, const int64_t* ds
     int rc = check_cache(cache);
     if (rc != W4A16_OK) return rc;
     if (cache->kv_heads > (1 << 20)) return W4A16_ERR_UNSUPPORTED;
+    // places that share memory would be moved by several threads, in no order
+    if ((cache->num_pages > 1 && (cache->k_page_stride == 0 || cache->v_page_stride == 0)) ||
+        (cache->page_size > 1 && (cache->k_slot_stride == 0 || cache->v_slot_stride == 0)) ||
+        (cache->kv_heads > 1 && (cache->k_head_stride == 0 || cache->v_head_stride == 0)))
+        return W4A16_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return W4A16_OK;
     if (!src || !dst || !starts || !aligned(src, 8) || !aligned(dst, 8) || !aligned(starts, 4))
         return W4A16_ERR_INVALID_ARG;

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
     if (cluster > 1) cluster_arrive_relaxed();
     grid_dep_wait();
     const float f = a.factor ? a.factor[t] : 1.0f;
-    const bool fine = f > 0.0f && f < INFINITY;
+    const bool fine = f > 0.0f && f <= 0x1p127f;   // (f log2 e is finite)
     const float c = f * kLog2e;
     const char* base = static_cast<const char*>(a.x) + t * a.ld * (DT == 2 ? 4 : 2);
     LpRow row;

@@ -8,22 +8,31 @@
 //   O += P V    P in TMEM, in the place of S; V in shared memory, its rows as they come from the
 //               cache: the MN-major operand.
 // (mma.sync, which dec_attn_paged uses for its few rows, would be short from some 40 rows on.)
-// Padding rows cost nothing while the cache streams from HBM: a step's S and P V take 1600 cycles of
-// the tensor pipe per tile, its 64 KB 2800 of the memory.
-//
 // P is carried as two 16-bit parts, each multiplied with V (a single rounding to bf16, 2^-9, would
 // show in the result as much as the result's own); a block of 16 tokens' S, 16 columns, holds both
-// parts of its P.  The softmax's state and all sums are fp32.
+// parts of its P.  The softmax's state and all sums are fp32.  So a step of 128 tokens and 128 rows is some 1600
+// cycles of the tensor pipe (512 for S, 1024 for P V at the peak), against the 2800 that an SM's share of the
+// memory takes for its 64 KB: padding rows cost nothing while the cache streams.
 //
-// Roles: two softmax warpgroups (a thread per row), one warp that issues the MMAs, eight
-// producer warps.  There are two streams of (S, O) in TMEM, one per warpgroup.  An item of more
-// than 128 rows has a stream per tile of 128; one of fewer gives its steps to the streams in
-// turn, whose sums are joined at its end.  While one stream's softmax runs the tensor pipe works on
-// the other's products.  (Heads of more than 128 values: one stream, whose S alternates between two
-// places; O alone takes half of TMEM.)
+// Roles: two warps issue the MMAs, one for each of two streams of (S, O) in TMEM; two softmax warpgroups, one
+// for each stream, a thread per row; loaders.  An item of more than 128 rows has a stream per tile of
+// 128; one of fewer gives its steps to the streams in turn, whose sums are joined at its end.  While one
+// stream's softmax runs the tensor pipe works on the other's products; streams at work together take turns,
+// a stream's P V and next S as one, which keeps them half a round apart (a step of both 5.0 thousand cycles
+// instead of 5.7).  (Heads of more than 128 values: one stream, whose S alternates between two places; O
+// alone takes half of TMEM.)
+// All copies and MMAs of a warp are issued by one thread with operands that are known to be the same in all
+// lanes; issued by several lanes, or from registers that might differ, each takes several times as long.
+//
+// Loaders, 16-bit cache: two warps, one has the keys, the other queries and values, as tensor copies (a box is
+// up to 128 tokens of a page, one head) into a ring of 128 KB, keys and values in turn.  8-bit cache: a warp
+// copies the raw tiles, five convert them to fp16, exactly, into the ring.  Pages that no tensor map
+// describes (sizes that no 8 divides, strides of 0) are copied 16 bytes at a time by all loaders: 16 sequences of 8192,
+// 4 heads of 128, 8 drafted, pages of 64, of 24, of 5 and of 1 tokens take 45, 45, 72 and 73 us.
 //
 // Softmax.  A running reference m per row: weights are exp2(s - m); only when a score passes m by
-// more than 2^8 is O, in TMEM, scaled to a new reference.  Maxima carry NaN.
+// more than 2^8 is O, in TMEM, scaled to a new reference.  Maxima carry NaN, and come with the loads from TMEM.
+// Its loops stay loops: the roles' code together has to fit in the instruction cache.
 //
 // Masks are applied to S by index (words of 32 tokens per row) in the steps that need them: the
 // drafted tokens' and those at the window's edges.  Values of such tokens that are infinite or NaN are
@@ -32,7 +41,12 @@
 //
 // Work split.  All items of the batch stand in one line, each as long as its steps and
 // kTreeItemCost, cut in equal shares, one per CTA.  An item that is cut leaves (m, l, O) of each
-// part in fp32 in the workspace, and a second kernel joins the parts in their order.
+// part in fp32 in the workspace, and a second kernel joins the parts in their order, 32 rows and columns a
+// block (one sequence of 131072, 8 drafted: 106 us; 112 with 32 rows and all columns a block).
+//
+// What bounds it.  16 of 32 heads' rows over 256 to 4096 tokens each: memory, 546 MB in 122 us, 4.5 TB/s.
+// 32 drafted tokens of 32 sequences, 8192 tokens, 32 heads on 8: the softmax's exponentials and
+// conversions, which take the four schedulers as long as the products take the tensor pipe.
 #pragma once
 #include "decode.cuh"
 
@@ -234,7 +248,7 @@ struct TreeShape {
     static constexpr int TM_O = 2 * STEP;                    // TMEM columns: S twice, then O of each stream
     // Shared memory: TreeControl, the queries' tiles, the ring.  The tiles' 1024-byte alignment follows
     // from the declared alignment of the dynamic part.
-    static constexpr int CONTROL = 3072;
+    static constexpr int CONTROL = 3 * 1024;
     static constexpr int SMEM = CONTROL + STREAMS * QTILE + NSLOT * SLOT + NRAW * RAW;
     static_assert(TM_O + STREAMS * DP <= 512, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -486,9 +500,9 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
 
     if (warp >= S::LOADERS && warp < S::SOFTMAX) {
         // ================= loaders =================
-        // Keys and values come by tensor copies, a box per lane.  In steps that not all rows see in full, at the ends of what is visible, all three
-        // look through the values: zeros for tokens that no row sees, and finite ones where some row does not
-        // see a token.  (Keys need no such care: their scores are masked.)
+        // In steps that not all rows see in full, at the ends of what is visible, the values are looked
+        // through: zeros for tokens that no row sees, and finite ones where some row does not see a
+        // token.  (Keys need no such care: their scores are masked.)
         const int lw = warp - S::LOADERS;
         constexpr int CH = S::CH;
         const int row_chunks = a.head_dim / 8;        // of 16-bit values
@@ -560,7 +574,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 const uint32_t to = tree_uniform(dst), done = tree_uniform(bar), head = tree_uniform(kvh);
                 uint32_t in_page = tree_uniform(tok0 - page_of(tok0) * a.page_size);
                 __syncwarp();
-                if (tree_elect()) {
+                if (tree_elect() && *static_cast<volatile int*>(&ctl.abort_flag) == 0) {
                     mbar_arrive_expect_tx(done, bytes);
 #pragma unroll 2
                     for (int g = 0; g < boxes; ++g) {
@@ -657,7 +671,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 const int parts = S::E4M3 && box_rows > 0 ? LW - 1 : LW, part = lw - (LW - parts);
                 // f = |scale k_scale|; a negative or zero product is folded into the queries
                 const float f = a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f);
-                const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu, flip = f < 0.0f ? 0x80008000u : 0u;
+                const uint32_t flip = f < 0.0f ? 0x80008000u : 0u;
                 const int row0 = row0_of(seg), rows = rows_of(seg), padded = rows > kTreeRows ? 2 * kTreeRows : kTreeRows;
                 constexpr int RPI = 32 / CH;
                 const int c = lane % CH, sub = lane / CH;
@@ -695,7 +709,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         const int n = n0 + x * parts * RPI, t = n / kTreeRows, r = n % kTreeRows;
                         uint32_t* w = &v[x].x;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep) ^ flip;
+                        for (int e = 0; e < 4; ++e) w[e] ^= flip;
                         // bf16 queries against an 8-bit cache, whose MMA is fp16: scaled by a power of two
                         // that brings the row's largest to 2^8 .. 2^9
                         if constexpr (S::E4M3 && S::DT == 1) {
@@ -713,6 +727,19 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                             if (c == 0 && n < padded) ctl.qe[t][r] = static_cast<int8_t>(exponent);
                         }
                         if (n < padded && c < row_chunks) tree_store16(q_smem + t * S::QTILE + at_smem(kTreeRows, r, c), v[x]);
+                    }
+                }
+                if (f == 0.0f && c < row_chunks) {   // 0 times what this thread has stored: NaN of infinite values and NaN
+                    constexpr uint32_t kExp = S::BF ? 0x7F80u : 0x7C00u;
+#pragma unroll 1
+                    for (int n = part * RPI + sub; n < padded; n += parts * RPI) {
+                        const uint32_t at = q_smem + n / kTreeRows * S::QTILE + at_smem(kTreeRows, n % kTreeRows, c);
+                        uint4 v = lds_v4(at);
+                        uint32_t* w = &v.x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = ((w[e] & kExp) == kExp ? 0x7FFFu : 0u) | ((w[e] >> 16 & kExp) == kExp ? 0x7FFF0000u : 0u);
+                        tree_store16(at, v);
                     }
                 }
                 if (parts == LW) {
@@ -1012,6 +1039,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             const int32_t* table = a.block_table + seg.b * a.ld_table;
             const float fabs_scale = fabsf(a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f));
             float f = (fabs_scale == 0.0f ? 1.0f : fabs_scale) * 1.4426950408889634f;
+            if (fabs_scale < INFINITY) f = fminf(f, 3.4028235e38f);   // so that scores of 0 stay 0
             float m = -INFINITY, ref = 0.0f, l = 0.0f;
             bool first = true;
             const bool alone = STREAMS == 2 && !dual;
@@ -1221,7 +1249,8 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     for (int st = seg.step; st < seg.step_end; ++st) {
                         const int tok0 = tile_of(sq, st) * STEP;
 #pragma unroll 1
-                        for (int t0 = tok0; t0 < tok0 + STEP; t0 += 32)
+                        for (int t0 = tok0; t0 < tok0 + STEP; t0 += 32) {
+                            if (t0 + 32 <= ctx && (t0 >= edge || t0 + 32 <= a.sinks)) continue;   // seen by all rows
 #pragma unroll 1
                             for (uint32_t left = see.seen(t0); left; left &= left - 1) {
                                 const int tok = t0 + __ffs(left) - 1;
@@ -1242,6 +1271,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                                     if (!(fabsf(v) < INFINITY)) o[e] += v;
                                 }
                             }
+                        }
                     }
                 }
                 if (!live) continue;
@@ -1277,7 +1307,10 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             more = after(seg);
         }
     }
-    // every MMA is done before TMEM is given back: the last ones were waited for by the softmax warps
+    // every MMA is done before TMEM is given back: the last ones were waited for by the softmax warps;
+    // after a wait that ran out a millisecond lets what is under way come to its end
+    if (*static_cast<volatile int*>(&ctl.abort_flag) != 0)
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) __nanosleep(1000);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
