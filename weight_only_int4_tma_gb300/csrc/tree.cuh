@@ -26,9 +26,11 @@
 //
 // Loaders, 16-bit cache: two warps, one has the keys, the other queries and values, as tensor copies (a box is
 // up to 128 tokens of a page, one head) into a ring of 128 KB, keys and values in turn.  8-bit cache: a warp
-// copies the raw tiles, five convert them to fp16, exactly, into the ring.  Pages that no tensor map
-// describes (sizes that no 8 divides, strides of 0) are copied 16 bytes at a time by all loaders: 16 sequences of 8192,
-// 4 heads of 128, 8 drafted, pages of 64, of 24, of 5 and of 1 tokens take 45, 45, 72 and 73 us.
+// copies the raw tiles, five convert them to fp16, exactly, into the ring, which takes them some 900 cycles a
+// tile and bounds this form (16 sequences of up to 4096, 64 heads on 8, 8 drafted: 51 us, and 45 with the bf16 cache of
+// twice the bytes; with the rows' conversions one after another it was 66).  Pages that no tensor map
+// describes (sizes that no 8 divides, strides of 0) are copied 16 bytes at a time: the same batch takes 45 us
+// with bf16 pages of 64 and of 24 tokens, 76 with pages of 5 and of 1; 103 with 8-bit pages of 5.
 //
 // Softmax.  A running reference m per row: weights are exp2(s - m); only when a score passes m by
 // more than 2^8 is O, in TMEM, scaled to a new reference.  Maxima carry NaN, and come with the loads from TMEM.
@@ -263,7 +265,7 @@ struct TreeLine {
 
 template <class S>
 struct TreeControl {
-    uint64_t bars[2 * S::NSLOT + 12 + 2 * S::NRAW];
+    uint64_t bars[2 * S::NSLOT + 13 + 2 * S::NRAW];
     TreeLine line;
     long long scan[S::THREADS / 32];
     uint32_t tmem_base;
@@ -362,7 +364,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     const uint32_t full = bar0, empty = full + 8 * NSLOT, q_full = empty + 8 * NSLOT, q_empty = q_full + 8;
     const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_full = p_full + 16, o_free = o_full + 8;
     const uint32_t pv_done = o_free + 8, fix_full = pv_done + 8, turn = fix_full + 8;
-    const uint32_t raw_full = turn + 16, raw_empty = raw_full + 8 * S::NRAW;
+    const uint32_t raw_full = turn + 16, raw_empty = raw_full + 8 * S::NRAW, q_raw = raw_empty + 8 * S::NRAW;
     TreePart* heads = static_cast<TreePart*>(a.workspace);
     float* parts = reinterpret_cast<float*>(heads + ctas);
 
@@ -371,11 +373,12 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         for (uint32_t e = tid; e < (STREAMS * S::QTILE + NSLOT * S::SLOT) / 16; e += S::THREADS)
             tree_store16(base + 16 * e, make_uint4(0, 0, 0, 0));
     if (tid < NSLOT) {
-        mbar_init(full + 8 * tid, box_rows > 0 ? 1 : LW);  // a copying thread, or every loader warp
+        mbar_init(full + 8 * tid, S::E4M3 || box_rows > 0 ? 1 : LW);  // one thread, or every loader warp
         mbar_init(empty + 8 * tid, STREAMS);
     }
     if (tid == 0) {
         mbar_init(q_full, 1);
+        mbar_init(q_raw, 1);
         for (int s = 0; s < 2 * S::NRAW; ++s) mbar_init(raw_full + 8 * s, 1);
         mbar_init(q_empty, STREAMS + SW);
         for (int s = 0; s < 2; ++s) {
@@ -623,8 +626,11 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         h[2 * e] = dec_e4m3x2_to_f16x2(w[e]);
                         h[2 * e + 1] = dec_e4m3x2_to_f16x2(w[e] >> 16);
                     }
-                    tree_store16(dst + at_smem(STEP, r, 2 * fc), make_uint4(h[0], h[1], h[2], h[3]));
-                    tree_store16(dst + at_smem(STEP, r, 2 * fc + 1), make_uint4(h[4], h[5], h[6], h[7]));
+                    // (eight lanes have a row of 128: half of them store their second chunk first, all banks at once)
+                    const int swap = DP > 64 ? (fc >> 2) & 1 : 0;
+                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                    tree_store16(dst + at_smem(STEP, r, 2 * fc + swap), swap ? hi : lo);
+                    tree_store16(dst + at_smem(STEP, r, 2 * fc + 1 - swap), swap ? lo : hi);
                 } else {
                     if (fc < row_chunks) tree_store16(dst + at_smem(STEP, r, fc), v);
                 }
@@ -636,100 +642,99 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 if (any) *static_cast<volatile int*>(&ctl.dirty) = 1;
                 return any;
             };
-            auto fill = [&](uint32_t dst, const void* from, const int64_t (&at)[SETS], bool values) {
-                // Loads of a group; with 8 bits those of all groups go together (16 sequences of 8192, 4 heads, pages
-                // of 5: 87 us, 117 one group after another), with 16 bits they would not fit in registers.
-                constexpr int LN = 16 / LR, TOGETHER = S::E4M3 ? MINE : 1;
+            auto fill = [&](uint32_t dst, const void* from, const int64_t (&at)[SETS]) {   // values, looked through
+                constexpr int LN = 16 / LR;   // loads of a group
 #pragma unroll
-                for (int n0 = 0; n0 < MINE; n0 += TOGETHER) {
-                    uint4 v[TOGETHER][LN];
+                for (int n = 0; n < MINE; ++n) {
+                    const int group = lw + LW * n;
+                    if (group >= S::GROUPS) break;
+                    uint4 v[LN];
 #pragma unroll
-                    for (int k = 0; k < TOGETHER; ++k)
+                    for (int x = 0; x < LN; ++x) {
+                        const int64_t off = __shfl_sync(0xFFFFFFFFu, at[n / 2], n % 2 * 16 + x * LR + fsub);
+                        v[x] = make_uint4(0, 0, 0, 0);
+                        if (off >= 0 && fc < row_chunks)
+                            v[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(from) + off) + fc);
+                    }
 #pragma unroll
-                        for (int x = 0; x < LN; ++x) {
-                            const int n = n0 + k;
-                            const int64_t off = __shfl_sync(0xFFFFFFFFu, at[n / 2], n % 2 * 16 + x * LR + fsub);
-                            v[k][x] = make_uint4(0, 0, 0, 0);
-                            if (off >= 0 && 16 * fc < a.head_dim * S::ES)
-                                v[k][x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(from) + off) + fc);
-                        }
-#pragma unroll
-                    for (int k = 0; k < TOGETHER; ++k) {
-                        const int n = n0 + k, group = lw + LW * n;
-                        if (group >= S::GROUPS) break;
-#pragma unroll
-                        for (int x = 0; x < LN; ++x) {
-                            if (values && (mixed[n / 2] >> (n % 2 * 16 + x * LR + fsub) & 1u)) finite(v[k][x]);
-                            put(dst, v[k][x], group * 16 + x * LR + fsub);
-                        }
+                    for (int x = 0; x < LN; ++x) {
+                        if (mixed[n / 2] >> (n % 2 * 16 + x * LR + fsub) & 1u) finite(v[x]);
+                        put(dst, v[x], group * 16 + x * LR + fsub);
                     }
                 }
             };
+            // Queries: by tensor copies where a tile of rows is whole tokens, else 16 bytes at a time by all loaders but an
+            // 8-bit cache's copying one.  Tokens of G heads are G rows, one after another.  Rows behind the
+            // sequence's are another's, or zeros: nobody reads what they give.
             constexpr int Q_WARP = 1;
-            auto load_queries = [&]() {
-                // by the second warp's copies, or by all loaders but an 8-bit cache's copying one
-                const int parts = S::E4M3 && box_rows > 0 ? LW - 1 : LW, part = lw - (LW - parts);
-                // f = |scale k_scale|; a negative or zero product is folded into the queries
-                const float f = a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f);
-                const uint32_t flip = f < 0.0f ? 0x80008000u : 0u;
-                const int row0 = row0_of(seg), rows = rows_of(seg), padded = rows > kTreeRows ? 2 * kTreeRows : kTreeRows;
+            constexpr bool Q_CONVERT = S::E4M3 && S::DT == 1;
+            // |q_scale| belongs to the softmax; a negative or zero one is folded into the queries
+            const float q_scale = a.scale * (S::E4M3 && a.kc.scale ? a.kc.scale[kvh] : 1.0f);
+            const bool by_copy = q_box > 0 && (Q_CONVERT || q_scale > 0.0f);
+            const int q_rows = rows_of(seg), padded = q_rows > kTreeRows ? 2 * kTreeRows : kTreeRows;
+            auto ask_queries = [&]() {
+                if (!by_copy || lw != Q_WARP) return;
+                const uint32_t bar = Q_CONVERT ? q_raw : q_full;
+                wait(q_empty, q_phase ^ 1u);
+                if (lane == 0) mbar_arrive_expect_tx(bar, padded * DP * 2);
+                __syncwarp();
+                const int tile = lane / S::BLOCKS, block = lane % S::BLOCKS;
+                if (tile * kTreeRows < padded)
+                    tma_tensor_4d_g2s(q_smem + tile * S::QTILE + block * kTreeRows * 128, &qmap, 64 * block, kvh * G,
+                                      sq.first + token_of_row(row0_of(seg)) + tile * q_box, 0, bar);
+                __syncwarp();
+            };
+            auto finish_queries = [&]() {
+                constexpr int parts = S::E4M3 ? LW - 1 : LW;
+                const int part = lw - (LW - parts);
+                const uint32_t phase_now = q_phase;
+                q_phase ^= 1u;
+                if (part < 0 || (by_copy && !Q_CONVERT)) return;
                 constexpr int RPI = 32 / CH;
                 const int c = lane % CH, sub = lane / CH;
-                const bool by_copy = q_box > 0 && f > 0.0f;
-                if (by_copy ? lw == Q_WARP : part >= 0) wait(q_empty, q_phase ^ 1u);
-                q_phase ^= 1u;
-                if (part < 0) return;
                 if (by_copy) {
-                    // Tokens of G heads are G rows, one after another.  Rows behind the sequence's are another's,
-                    // or zeros: nobody reads what they give.
-                    if (lw != Q_WARP) return;
-                    if (lane == 0) mbar_arrive_expect_tx(q_full, padded * DP * 2);
-                    __syncwarp();
-                    const int tile = lane / S::BLOCKS, block = lane % S::BLOCKS;
-                    if (tile * kTreeRows < padded)
-                        tma_tensor_4d_g2s(q_smem + tile * S::QTILE + block * kTreeRows * 128, &qmap, 64 * block, kvh * G,
-                                          sq.first + token_of_row(row0) + tile * q_box, 0, q_full);
-                    __syncwarp();
-                    return;
-                }
-                constexpr int AT = 16;  // loads at a time
+                    wait(q_raw, phase_now);
+                } else {
+                    wait(q_empty, phase_now ^ 1u);
+                    const int row0 = row0_of(seg);
+                    // (a short loop: it runs once per item, as code that comes from beyond the SM)
 #pragma unroll 1
-                for (int n0 = part * RPI + sub; n0 < padded; n0 += AT * parts * RPI) {
-                    uint4 v[AT];
-#pragma unroll
-                    for (int x = 0; x < AT; ++x) {
-                        const int n = n0 + x * parts * RPI, row = row0 + n, i = token_of_row(row);
-                        v[x] = make_uint4(0, 0, 0, 0);
-                        if (n < rows && c < row_chunks)
-                            v[x] = *(reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(sq.first + i) * a.ldq +
-                                                                    static_cast<int64_t>(kvh * G + row - i * G) * a.head_dim) + c);
+                    for (int n = part * RPI + sub; n < padded; n += parts * RPI) {
+                        const int row = row0 + n, i = token_of_row(row);
+                        const uint16_t* from = a.q + static_cast<int64_t>(sq.first + i) * a.ldq +
+                                               static_cast<int64_t>(kvh * G + row - i * G) * a.head_dim + 8 * c;
+                        if (c < row_chunks)
+                            tree_copy16(q_smem + n / kTreeRows * S::QTILE + at_smem(kTreeRows, n % kTreeRows, c),
+                                        reinterpret_cast<const char*>(n < q_rows ? from : a.q), n < q_rows ? 16 : 0);
                     }
+                    tree_commit();
+                    tree_wait_copies<0>();
+                }
+                // bf16 queries against an 8-bit cache, whose MMA is fp16: scaled by a power of two that brings the
+                // row's largest to 2^8 .. 2^9.  (The threads go through the chunks that they would have copied.)
+                if constexpr (Q_CONVERT) {
+#pragma unroll 1
+                    for (int n = part * RPI + sub; n < padded; n += parts * RPI) {
+                        const int t = n / kTreeRows, r = n % kTreeRows;
+                        const uint32_t at = q_smem + t * S::QTILE + at_smem(kTreeRows, r, c);
+                        uint4 v = lds_v4(at);
+                        uint32_t* w = &v.x;
+                        uint32_t top = 0;
 #pragma unroll
-                    for (int x = 0; x < AT; ++x) {
-                        const int n = n0 + x * parts * RPI, t = n / kTreeRows, r = n % kTreeRows;
-                        uint32_t* w = &v[x].x;
+                        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] ^= flip;
-                        // bf16 queries against an 8-bit cache, whose MMA is fp16: scaled by a power of two
-                        // that brings the row's largest to 2^8 .. 2^9
-                        if constexpr (S::E4M3 && S::DT == 1) {
-                            uint32_t top = 0;
+                        for (int d = CH / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        const int e2 = min(static_cast<int>(top >> 7) - 127, 127);
+                        const int exponent = e2 > -119 ? e2 - 8 : 0;
+                        const float up = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
-#pragma unroll
-                            for (int d = CH / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                            const int e2 = min(static_cast<int>(top >> 7) - 127, 127);
-                            const int exponent = e2 > -119 ? e2 - 8 : 0;
-                            const float up = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = dec_pack2<0>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-                            if (c == 0 && n < padded) ctl.qe[t][r] = static_cast<int8_t>(exponent);
-                        }
-                        if (n < padded && c < row_chunks) tree_store16(q_smem + t * S::QTILE + at_smem(kTreeRows, r, c), v[x]);
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = dec_pack2<0>(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+                        if (c == 0) ctl.qe[t][r] = static_cast<int8_t>(exponent);
+                        if (c < row_chunks) tree_store16(at, v);
                     }
                 }
-                if (f == 0.0f && c < row_chunks) {   // 0 times what this thread has stored: NaN of infinite values and NaN
+                if (!(q_scale > 0.0f) && c < row_chunks) {   // times -1, or 0, which makes NaN of infinite values and NaN
                     constexpr uint32_t kExp = S::BF ? 0x7F80u : 0x7C00u;
 #pragma unroll 1
                     for (int n = part * RPI + sub; n < padded; n += parts * RPI) {
@@ -738,7 +743,8 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         uint32_t* w = &v.x;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            w[e] = ((w[e] & kExp) == kExp ? 0x7FFFu : 0u) | ((w[e] >> 16 & kExp) == kExp ? 0x7FFF0000u : 0u);
+                            w[e] = q_scale == 0.0f ? ((w[e] & kExp) == kExp ? 0x7FFFu : 0u) | ((w[e] >> 16 & kExp) == kExp ? 0x7FFF0000u : 0u)
+                                 : q_scale < 0.0f ? w[e] ^ 0x80008000u : w[e];
                         tree_store16(at, v);
                     }
                 }
@@ -750,9 +756,114 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     if (part == 0 && lane == 0) mbar_arrive(q_full);
                 }
             };
-            if (box_rows == 0) {
-                // Pages that no tensor map describes: every warp copies its groups of tokens, 16-bit ones
-                // asynchronously, and arrives by itself.
+            if constexpr (S::E4M3) {
+                // The first warp copies 8-bit tiles; the others convert them into the ring.
+                constexpr int NRAW = S::NRAW, CW = LW - 1;
+                const uint32_t raw = ring + NSLOT * S::SLOT;
+                if (lw == 0 && box_rows == 0) {
+                    // pages that no tensor map describes, 16 bytes at a time; a tile is announced when the next
+                    // one's copies are under way
+                    int before = -1, page[STEP / 32], ahead[STEP / 32];
+                    auto pages_of = [&](int step, int (&to)[STEP / 32]) {   // of tokens 32 x + lane; -1: not wanted
+#pragma unroll
+                        for (int x = 0; x < STEP / 32; ++x) {
+                            const int tok = tile_of(sq, step) * STEP + 32 * x + lane;
+                            to[x] = -1;
+                            if (step < seg.step_end && wanted(tok)) {
+                                to[x] = table[page_of(tok)];
+                                if (to[x] == -1) to[x] = a.num_pages;   // (as bad as it)
+                            }
+                        }
+                    };
+                    pages_of(seg.step, ahead);
+#pragma unroll 1
+                    for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
+                        wait(raw_empty + 8 * raw_at, raw_phase ^ 1u);
+                        if (!(half & 1)) {
+#pragma unroll
+                            for (int x = 0; x < STEP / 32; ++x) page[x] = ahead[x];
+                            pages_of((half >> 1) + 1, ahead);
+                        }
+                        const KvView& kv = half & 1 ? a.vc : a.kc;
+                        const char* from = static_cast<const char*>(kv.p);
+#pragma unroll
+                        for (int x = 0; x < STEP / 32; ++x) {
+                            const int tok = tile_of(sq, half >> 1) * STEP + 32 * x + lane;
+                            const bool ok = static_cast<unsigned>(page[x]) < static_cast<unsigned>(a.num_pages);
+                            if (page[x] != -1 && !ok) bad();
+                            const int64_t at = ok ? page[x] * kv.page_stride +
+                                                    (tok - static_cast<int64_t>(page_of(tok)) * a.page_size) * kv.slot_stride +
+                                                    kvh * kv.head_stride : -1;
+#pragma unroll 4
+                            for (int r = fsub; r < 32; r += LR) {
+                                const int64_t off = __shfl_sync(0xFFFFFFFFu, at, r);
+                                if (16 * fc < a.head_dim)
+                                    tree_copy16(raw + raw_at * S::RAW + (32 * x + r) * DP + 16 * fc, off >= 0 ? from + off + 16 * fc : from,
+                                                off >= 0 ? 16 : 0);
+                            }
+                        }
+                        tree_commit();
+                        if (before >= 0) {
+                            tree_wait_copies<1>();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(raw_full + 8 * before);
+                        }
+                        before = raw_at;
+                        if (++raw_at == NRAW) raw_at = 0, raw_phase ^= 1u;
+                    }
+                    tree_wait_copies<0>();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(raw_full + 8 * before);
+                } else if (lw == 0) {
+                    int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
+#pragma unroll 1
+                    for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
+                        wait(raw_empty + 8 * raw_at, raw_phase ^ 1u);
+                        issue(raw + raw_at * S::RAW, raw_full + 8 * raw_at, S::RAW, half & 1 ? &vmap : &kmap, half >> 1, pid);
+                        if (half & 1) pid = pid1, pid1 = box_page((half + 3) >> 1);
+                        if (++raw_at == NRAW) raw_at = 0, raw_phase ^= 1u;
+                    }
+                } else {
+                    ask_queries();
+#pragma unroll 1
+                    for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
+                        wait(empty + 8 * slot, phase ^ 1u);
+                        wait(raw_full + 8 * raw_at, raw_phase);
+                        const uint32_t from = raw + raw_at * S::RAW, dst = ring + slot * S::SLOT;
+                        const int tok0 = tile_of(sq, half >> 1) * STEP;
+                        const bool care = (half & 1) && !clean(half >> 1);
+                        if (!care) {   // all rows' loads together
+                            constexpr int ROWS = (STEP + CW * LR - 1) / (CW * LR);
+                            const int r0 = (lw - 1) * LR + fsub;
+                            uint4 v[ROWS];
+#pragma unroll
+                            for (int x = 0; x < ROWS; ++x)
+                                if (r0 + x * CW * LR < STEP) v[x] = lds_v4(from + (r0 + x * CW * LR) * DP + 16 * fc);
+#pragma unroll
+                            for (int x = 0; x < ROWS; ++x)
+                                if (r0 + x * CW * LR < STEP) put(dst, v[x], r0 + x * CW * LR);
+                        } else {
+#pragma unroll 1
+                            for (int r = (lw - 1) * LR + fsub; r < STEP; r += CW * LR) {
+                                uint4 v = lds_v4(from + r * DP + 16 * fc);
+                                if (!wanted(tok0 + r)) v = make_uint4(0, 0, 0, 0);
+                                else if (some_not(tok0 + r)) finite(v);
+                                put(dst, v, r);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        asm volatile("bar.sync 3, %0;" ::"n"(32 * CW) : "memory");
+                        if (lw == 1 && lane == 0) {
+                            mbar_arrive(full + 8 * slot);
+                            mbar_arrive(raw_empty + 8 * raw_at);
+                        }
+                        next_slot();
+                        if (++raw_at == NRAW) raw_at = 0, raw_phase ^= 1u;
+                        if (half == 2 * seg.step) finish_queries();   // behind the first keys
+                    }
+                }
+            } else if (box_rows == 0) {
+                // Pages that no tensor map describes: every warp copies its groups of tokens and arrives by itself.
                 auto there = [&](uint32_t bar) {
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -776,18 +887,15 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     uint32_t some = 0;
 #pragma unroll
                     for (int s = 0; s < SETS; ++s) some |= mixed[s];
-#pragma unroll(S::E4M3 ? 2 : 1)
+#pragma unroll 1
                     for (int side = 0; side < 2; ++side) {
                         const uint32_t dst = ring + slot * S::SLOT, bar = full + 8 * slot;
                         if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(empty + 8 * slot, phase ^ 1u))) {
                             settle();   // what is under way may be what the slot's readers wait for
                             wait(empty + 8 * slot, phase ^ 1u);
                         }
-                        if (S::E4M3 || (side && some)) {
-                            if (side)
-                                fill(dst, a.vc.p, vat, true);
-                            else
-                                fill(dst, a.kc.p, kat, false);
+                        if (side && some) {
+                            fill(dst, a.vc.p, vat);
                             there(bar);
                         } else {
                             constexpr int RPI = 32 / CH;
@@ -817,57 +925,19 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     }
                     if (st == seg.step) {
                         settle();
-                        load_queries();
+                        ask_queries();
+                        finish_queries();
                     }
                 }
                 settle();
-            } else if constexpr (S::E4M3) {
-                // The first warp copies 8-bit tiles; the others convert them into the ring.
-                constexpr int NRAW = S::NRAW, CW = LW - 1;
-                const uint32_t raw = ring + NSLOT * S::SLOT;
-                if (lw == 0) {
-                    int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
-#pragma unroll 1
-                    for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
-                        wait(raw_empty + 8 * raw_at, raw_phase ^ 1u);
-                        issue(raw + raw_at * S::RAW, raw_full + 8 * raw_at, S::RAW, half & 1 ? &vmap : &kmap, half >> 1, pid);
-                        if (half & 1) pid = pid1, pid1 = box_page((half + 3) >> 1);
-                        if (++raw_at == NRAW) raw_at = 0, raw_phase ^= 1u;
-                    }
-                    load_queries();   // (no more than its place in their order)
-                } else {
-                    load_queries();
-#pragma unroll 1
-                    for (int half = 2 * seg.step; half < 2 * seg.step_end; ++half) {
-                        wait(empty + 8 * slot, phase ^ 1u);
-                        wait(raw_full + 8 * raw_at, raw_phase);
-                        const uint32_t from = raw + raw_at * S::RAW, dst = ring + slot * S::SLOT;
-                        const int tok0 = tile_of(sq, half >> 1) * STEP;
-                        const bool care = (half & 1) && !clean(half >> 1);
-#pragma unroll 4
-                        for (int r = (lw - 1) * LR + fsub; r < STEP; r += CW * LR) {
-                            uint4 v = lds_v4(from + r * DP + 16 * fc);
-                            if (care) {
-                                if (!wanted(tok0 + r)) v = make_uint4(0, 0, 0, 0);
-                                else if (some_not(tok0 + r)) finite(v);
-                            }
-                            put(dst, v, r);
-                        }
-                        fence_proxy_async_smem();
-                        asm volatile("bar.sync 3, %0;" ::"n"(32 * CW) : "memory");
-                        if (lw == 1 && lane == 0) {
-                            mbar_arrive(full + 8 * slot);
-                            mbar_arrive(raw_empty + 8 * raw_at);
-                        }
-                        next_slot();
-                        if (++raw_at == NRAW) raw_at = 0, raw_phase ^= 1u;
-                    }
-                }
             } else {
                 // Keys by the first warp, queries and values by the second (or the queries by both, behind the
                 // first step, as their place is taken until the item before has its last scores).  Each waits
                 // for slots of its own alone.
-                if (q_box > 0) load_queries();
+                if (q_box > 0) {
+                    ask_queries();
+                    finish_queries();
+                }
                 int pid = box_page(seg.step), pid1 = box_page(seg.step + 1);
 #pragma unroll 1
                 for (int st = seg.step; st < seg.step_end; ++st) {
@@ -901,7 +971,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     }
                     next_slot();
                     next_slot();
-                    if (st == seg.step && q_box == 0) load_queries();
+                    if (st == seg.step && q_box == 0) finish_queries();
                 }
             }
             more = after(seg);
@@ -1386,9 +1456,9 @@ int launch_tree_shape(const DeviceCtx& ctx, const TreeArgs& a, cudaStream_t stre
     CUtensorMap maps[3] = {};
     if (box < 8 || !tree_map(&maps[0], a, a.kc, S::E4M3, S::DP, box) || !tree_map(&maps[1], a, a.vc, S::E4M3, S::DP, box))
         box = 0;
-    // Queries by tensor copies where a tile of rows is whole tokens and the MMA takes them as they are.
+    // Queries by tensor copies where a tile of rows is whole tokens.
     const int G = a.q_heads / a.kv_heads;
-    int q_box = kTreeRows % G == 0 && !(S::E4M3 && S::DT == 1) ? kTreeRows / G : 0;
+    int q_box = kTreeRows % G == 0 ? kTreeRows / G : 0;
     if (q_box > 0 && !tree_query_map(&maps[2], a, q_box)) q_box = 0;
     const int rc = launch_dependent(tree_kernel<S>, dim3(static_cast<unsigned>(ctx.num_sms)), dim3(S::THREADS),
                                     S::SMEM, stream, a, power_of_two(a.page_size), box, q_box, maps[0], maps[1], maps[2]);
