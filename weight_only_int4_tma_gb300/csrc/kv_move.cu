@@ -1,6 +1,10 @@
 // Cached tokens to other slots (include/decode.h).  A thread has one 16-byte piece of the keys or
 // values of a slot and takes it through all moves of a group, one after another: no other
 // thread touches that piece, so the order holds without any synchronisation.
+//
+// Up to eight moves' loads go together, as a path's moves are a chain of latencies otherwise: 256 groups of up to
+// 12 moves of 4 KB 5.7 us (9.5 one after another in a CUDA graph, 7.2 together; 1.4 for the bytes), one
+// group of 4 moves 4.3 us, the call itself.
 #include "decode.cuh"
 
 namespace w4g {

@@ -11,6 +11,11 @@
 // maximum is not below it either.  So only these threads' pieces, `top` in 256 and a few more
 // where maxima are equal, are read again, from L2, whatever the order of the logits is.  Where many
 // are equal, the index of each thread's first decides.
+//
+// What bounds it: many rows without largest logits memory (2048 of 128000 bf16: 525 MB in 85 us, 6.1 TB/s of
+// the 6.8 that a plain copy reaches); with the largest their search, which runs once per row at cold
+// instructions' speed (301 of 50001 fp32 with 20: 18 us, 9 for the bytes; 2048 of 128000 with 20: 139 us); one row
+// the chain of launch, loads, joins of threads, CTAs and cluster (128000 with 5: 7.9 us, of which 0.04 for the bytes).
 #include "decode.cuh"
 
 namespace w4g {
