@@ -174,6 +174,17 @@ def test_factors():
     check(x, f, ids, 5, call(x, "bf16", f, ids, 5))
 
 
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("top", [0, 20])
+def test_odd_rows_of_many_blocks(kind, top):
+    """Long rows that begin and end off 16 bytes; equal logits in all of one."""
+    x = logits(5, 100003, kind, 16)
+    x[3] = x[3, 7]
+    x[4, 1000:] = -math.inf
+    ids = torch.randint(0, 100003, (5, 3), device="cuda").int()
+    check(x, None, ids, top, call(x, kind, None, ids, top))
+
+
 def test_largest_factors():
     """Up to 2^127, the largest logit's neighbours included; above it NaN."""
     x = logits(3, 3000, "fp32", 14)

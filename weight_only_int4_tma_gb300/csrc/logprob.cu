@@ -1,8 +1,8 @@
 // Log probabilities of given tokens, entropy and largest logits (include/decode.h):
 //   lse = f m + ln S,  S = sum 2^t,  t = (x - m) f log2 e,  entropy = ln 2 (log2 S - sum 2^t t / S).
 //
-// A row is read once, in 16-byte pieces, by a cluster of 1, 2, 4 or 8 CTAs (as many as keep all SMs
-// busy); a thread carries its own reference m, S and sum of 2^t t in fp32, rescaled only when a
+// A row is read once, in 16-byte pieces, by a cluster of 1, 2, 4 or 8 CTAs (the fewer the
+// more rows there are); a thread carries its own reference m, S and sum of 2^t t in fp32, rescaled only when a
 // value passes m by more than 2^10, and they are joined at the end.  Differences x - m are taken before
 // they are scaled, so that logits of any size are right.
 //
@@ -500,11 +500,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
 
 template <int DT, bool TOP>
 int launch_logprob_as(const DeviceCtx& ctx, const LogprobArgs& a, cudaStream_t stream) {
-    // CTAs for a row: as many as fit on the device together (four on an SM), each with at least a
-    // few pieces for every thread
+    // CTAs for a row: up to two on an SM, each with at least 32 logits for every thread.  More of them share the
+    // code that runs once per row badly: 60 rows of 32000 with 20 largest take 9.4 us with 2 CTAs a
+    // row, 10.9 with 4, 17.8 with 8; 64 of 128000 16.0 with 2, 14.5 with 4; one of 32000 7.8 with 2, 7.6 with 8.
     int cluster = 1;
-    while (cluster < kLpCluster && 2ll * cluster * a.T <= 4ll * ctx.num_sms &&
-           a.V / (2 * cluster) >= kLpThreads * 8)
+    while (cluster < kLpCluster && 2ll * cluster * a.T <= 2ll * ctx.num_sms &&
+           a.V / (2 * cluster) >= kLpThreads * 32)
         cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.T) * static_cast<unsigned>(cluster));
