@@ -304,6 +304,18 @@ def test_scale_of_zero(dtype, kv):
     assert torch.equal(got[~hit], out.view(c.T, 4, 64)[~hit]) and torch.equal(c.lse[~hit], lse[~hit])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,d,page", [(8, 128, 16), (12, 64, 16), (8, 64, 5), (4, 256, 64)])
+def test_signs_of_key_scales(dtype, hq, d, page):
+    """Positive, negative and zero scales of neighbouring heads, in many items of one step and some of several."""
+    rng = random.Random(hq + d)
+    c = Case([(rng.choice([0, 3, 60, 127, 300]), rng.randrange(9)) for _ in range(180)], hq, 4, d, dtype, "e4m3", page=page,
+             seed=30)
+    c.ks = torch.tensor([0.05, -0.03, 0.0, 0.04], device="cuda")
+    c.vs = torch.tensor([-0.05, 0.03, 0.02, 0.0], device="cuda")
+    c.run().check()
+
+
 def test_largest_scale():
     """Scores of 0 stay 0 under a scale whose product with log2 e is past fp32."""
     c = Case([(200, 6)], 4, 2, 64, "bf16", scale=3.0e38, seed=25)
