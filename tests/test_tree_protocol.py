@@ -70,6 +70,9 @@ class Kernel:
     def after(self, action):
         self.later.append((self.time + self.rng.randrange(1, 60), action))
 
+    def loading(self):
+        return [self.loader(0), self.loader(1)]
+
     # ---- the loaders: keys by the first, queries and values by the second ----
     def loader(self, lw):
         slot, phase, q_phase, fix_phase, g = 0, 0, 0, 0, 0
@@ -237,7 +240,7 @@ class Kernel:
         self.results.append(step0)
 
     def run(self):
-        agents = [self.loader(0), self.loader(1)] + [self.mma(s) for s in range(self.streams)]
+        agents = self.loading() + [self.mma(s) for s in range(self.streams)]
         agents += [self.softmax(s) for s in range(self.streams) for _ in range(4)]
         state = [(a, None) for a in agents]       # what each waits for
         favour = [self.rng.random() ** 3 for _ in agents]
@@ -271,6 +274,104 @@ class Kernel:
             idle = 0 if moved else idle + 1
             assert idle < 2000, "nobody moves"
         assert len(self.results) == 4 * self.streams
+
+
+class Converting(Kernel):
+    """With an 8-bit cache: a warp copies raw tiles, the others convert them into the ring.  queries: for each
+    item how they come: "raw" (copied, then converted by all), "copied", or "pieces" (by all).  late: a
+    tile is announced when the next one's copies are under way (pages without tensor maps)."""
+    CONVERTERS = 3
+
+    def __init__(self, segs, streams, nslot, nraw, queries, late, rng):
+        super().__init__(segs, streams, nslot, rng)
+        self.nraw, self.queries, self.late = nraw, queries, late
+        self.raw, self.q_raw, self.converters = [None] * nraw, Bar(1), Sync(self.CONVERTERS)
+        self.raw_full, self.raw_empty, self.landed = ([Bar(1) for _ in range(nraw)] for _ in range(3))
+
+    def loading(self):
+        return [self.copier()] + [self.converter(c) for c in range(self.CONVERTERS)]
+
+    def copier(self):
+        at, phase, g = 0, 0, 0
+        for steps, _, _ in self.segs:
+            before = None
+            for half in range(2 * steps):
+                yield self.raw_empty[at], phase ^ 1
+                assert self.raw[at] in (None, "read")
+                self.raw[at] = "loading"
+
+                def put(at=at, what=("KV"[half & 1], g + half // 2)):
+                    self.raw[at] = what
+                    if self.late:
+                        self.landed[at].arrive()
+                    else:
+                        self.raw_full[at].complete(1)
+                if not self.late:
+                    self.raw_full[at].arrive(1)
+                self.after(put)
+                if self.late and before:
+                    yield self.landed[before[0]], before[1]
+                    self.raw_full[before[0]].arrive()
+                before = (at, phase)
+                at, phase = (at + 1) % self.nraw, phase ^ (at + 1 == self.nraw)
+            if self.late:
+                yield self.landed[before[0]], before[1]
+                self.raw_full[before[0]].arrive()
+            g += steps
+
+    def converter(self, c):
+        slot, phase, at, raw_phase, q_phase, g = 0, 0, 0, 0, 0, 0
+        for n, (steps, _, _) in enumerate(self.segs):
+            how = self.queries[n]
+            if how != "pieces" and c == 0:
+                yield self.q_empty, q_phase ^ 1
+                bar = self.q_raw if how == "raw" else self.q_full
+
+                def put_q(what=("raw", n) if how == "raw" else n, bar=bar):
+                    self.q = what
+                    bar.complete(1)
+                self.q = "loading"
+                bar.arrive(1)
+                self.after(put_q)
+            for half in range(2 * steps):
+                yield self.empty[slot], phase ^ 1
+                yield self.raw_full[at], raw_phase
+                assert self.raw[at] == ("KV"[half & 1], g + half // 2)
+                self.slots[slot] = "loading"
+                yield self.converters
+                if c == 0:
+                    self.slots[slot], self.raw[at] = (*self.raw[at], True), "read"
+                    self.full[slot].arrive()
+                    self.raw_empty[at].arrive()
+                slot, phase = (slot + 1) % self.nslot, phase ^ (slot + 1 == self.nslot)
+                at, raw_phase = (at + 1) % self.nraw, raw_phase ^ (at + 1 == self.nraw)
+                if half == 0:   # behind the first keys
+                    if how == "raw":
+                        yield self.q_raw, q_phase
+                        assert self.q == ("raw", n)
+                    if how == "pieces":
+                        yield self.q_empty, q_phase ^ 1
+                        self.q = "loading"
+                    q_phase ^= 1
+                    if how != "copied":
+                        yield self.converters
+                        if c == 0:
+                            self.q = n
+                            self.q_full.arrive()
+            g += steps
+
+
+@pytest.mark.parametrize("late", [False, True])
+@pytest.mark.parametrize("streams,nslot,nraw", [(2, 4, 2), (2, 8, 4), (1, 4, 2)])
+def test_hand_overs_with_conversion(streams, nslot, nraw, late):
+    for seed in range(90):
+        rng = random.Random(seed)
+        segs = []
+        for _ in range(rng.randrange(1, 9)):
+            steps = rng.choice([1, 1, 1, 2, 3, rng.randrange(1, 12)])
+            segs.append((steps, streams == 2 and rng.random() < 0.5, set()))
+        ways = rng.choice([["raw"], ["pieces"], ["copied", "pieces"]])
+        Converting(segs, streams, nslot, nraw, [rng.choice(ways) for _ in segs], late, rng).run()
 
 
 @pytest.mark.parametrize("streams,nslot", [(2, 4), (2, 8), (1, 4)])
