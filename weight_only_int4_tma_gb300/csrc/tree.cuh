@@ -41,12 +41,12 @@
 // replaced by 0 in shared memory, as 0 times them would reach the rows that do not see them, and
 // added at the end to the rows that do.
 //
-// Work split.  All items of the batch stand in one line, each as long as its steps and
+// Work split.  All items of the batch stand in one line, each as long as its steps, weighted, and
 // kTreeItemCost, cut in equal shares, one per CTA.  An item that is cut leaves (m, l, O) of each
 // part in fp32 in the workspace, and a second kernel joins the parts in their order, 32 rows and columns a
 // block (one sequence of 131072, 8 drafted: 106 us; 112 with 32 rows and all columns a block).
 //
-// What bounds it.  16 sequences of up to 4096 tokens, 16 drafted, 32 heads on 32, fp16: memory, 546 MB in 116 us, 4.7
+// What bounds it.  16 sequences of up to 4096 tokens, 16 drafted, 32 heads on 32, fp16: memory, 546 MB in 106 us, 5.2
 // TB/s, and the ends of 512 short items.  32 sequences of up to 8192, 32 drafted, 64 heads on 8: the tensor pipe, 57 %
 // busy, 174 us (480 TFLOP/s, 720 with P's two parts), and between its turns the softmax's chain from S to P.
 // One tree of 8 over 777 tokens: 16 us of code that runs once.
@@ -55,7 +55,10 @@
 
 namespace w4g {
 
-constexpr int kTreeItemCost = 1;   // of an item by itself, in steps
+// The line's units: a step of an item of one tile, of one of two, and an item by itself.  (32 ragged sequences, trees of
+// up to 32: 152 us; 162 with equal steps, and 176 with an item as one of them.  16 sequences with 32 of 32
+// heads: 110 us; 114 with an item as two steps, 121 as one.)
+constexpr int kTreeStep = 2, kTreeDualStep = 3, kTreeItemCost = 6;
 constexpr float kTreeLag = 8.0f;   // scores may pass the reference by 2^8
 constexpr int kTreeRows = 128;     // of a tile: the MMA's M
 
@@ -283,6 +286,7 @@ struct TreeSeq {
     int first, n, len;     // rows first .. first + n - 1
     int sink_tiles, tile0; // steps: tiles 0 .. sink_tiles - 1, then from tile0 on
     int steps, row_tiles;  // row_tiles: items of a key-value head
+    int weight;            // of a step, in units of the line
 };
 template <class S>
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool report) {
@@ -300,7 +304,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool repor
     s.tile0 = lo / S::STEP;
     if (s.sink_tiles >= s.tile0) s.sink_tiles = s.tile0 = 0;
     s.steps = s.sink_tiles + (len + S::STEP - 1) / S::STEP - s.tile0;
-    s.row_tiles = (n * (a.q_heads / a.kv_heads) + S::ROWS - 1) / S::ROWS;
+    const int rows = n * (a.q_heads / a.kv_heads);
+    s.row_tiles = (rows + S::ROWS - 1) / S::ROWS;
+    s.weight = S::STREAMS == 2 && rows > kTreeRows ? kTreeDualStep : kTreeStep;
     return s;
 }
 
@@ -314,6 +320,9 @@ struct TreeSeg {
 template <class S>
 __device__ __forceinline__ long long tree_items(const TreeArgs& a, const TreeSeq& s) {
     return static_cast<long long>(s.row_tiles) * a.kv_heads;
+}
+__device__ __forceinline__ long long tree_units(const TreeSeq& s) {  // of an item
+    return static_cast<long long>(s.steps) * s.weight + kTreeItemCost;
 }
 
 // a / b for numbers >= 0; the long division, out of line, only where 32 bits do not hold them.
@@ -412,9 +421,11 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     {
         const int b_lo = min(a.B, tid * per_thread), b_hi = min(a.B, b_lo + per_thread);
         long long mine = 0;
+        int dual = 0;
         for (int b = b_lo; b < b_hi; ++b) {
             const TreeSeq s = tree_seq<S>(a, b, cta == 0);
-            mine += tree_items<S>(a, s) * (s.steps + kTreeItemCost);
+            mine += tree_items<S>(a, s) * tree_units(s);
+            dual |= s.weight == kTreeDualStep;
         }
         long long incl = mine;
 #pragma unroll
@@ -423,14 +434,16 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
             if (lane >= d) incl += o;
         }
         if (lane == 31) ctl.scan[warp] = incl;
-        __syncthreads();
+        dual = __syncthreads_or(dual);
         long long total = 0;
         for (int w = 0; w < S::THREADS / 32; ++w) {
             if (w < warp) incl += ctl.scan[w];
             total += ctl.scan[w];
         }
         prefix[tid] = incl - mine;
-        if (tid == 0) line = TreeLine{total, max(tree_quotient(total + ctas - 1, ctas), 1ll)};
+        // no share is shorter than a step: each between an item's first and last has one of its steps
+        const long long least = dual ? kTreeDualStep : kTreeStep;
+        if (tid == 0) line = TreeLine{total, max(tree_quotient(total + ctas - 1, ctas), least)};
     }
     if (tid == 32 * S::SOFTMAX) heads[cta] = TreePart{};
     tc_fence_before();
@@ -441,9 +454,14 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
 
     auto open_item = [&](TreeSeg& s, long long begin, long long from) {  // its steps at or after `from`
         const long long at0 = begin + kTreeItemCost;
-        s.step = static_cast<int>(max(from - at0, 0ll));
-        s.step_end = static_cast<int>(min(static_cast<long long>(s.seq.steps), share_end - at0));
-        s.rest = share_end - at0 - s.seq.steps;
+        const long long units = static_cast<long long>(s.seq.steps) * s.seq.weight;
+        auto steps_before = [&](long long to) {   // a step is whose share its first unit lies in
+            const unsigned n = static_cast<unsigned>(min(max(to - at0, 0ll), units));   // (below 2^27)
+            return static_cast<int>(s.seq.weight == kTreeStep ? (n + kTreeStep - 1) / kTreeStep : (n + kTreeDualStep - 1) / kTreeDualStep);
+        };
+        s.step = steps_before(from);
+        s.step_end = steps_before(share_end);
+        s.rest = share_end - at0 - units;
     };
     // The segment after s; false: there is none.
     auto after = [&](TreeSeg& s) {
@@ -468,11 +486,11 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
         long long at = prefix[t];
         s.b = t * per_thread;
         s.seq = tree_seq<S>(a, s.b, false);
-        while (at + tree_items<S>(a, s.seq) * (s.seq.steps + kTreeItemCost) <= u && s.b + 1 < a.B) {
-            at += tree_items<S>(a, s.seq) * (s.seq.steps + kTreeItemCost);
+        while (at + tree_items<S>(a, s.seq) * tree_units(s.seq) <= u && s.b + 1 < a.B) {
+            at += tree_items<S>(a, s.seq) * tree_units(s.seq);
             s.seq = tree_seq<S>(a, ++s.b, false);
         }
-        const long long per = s.seq.steps + kTreeItemCost;
+        const long long per = tree_units(s.seq);
         s.item = static_cast<int>(tree_quotient(u - at, per));
         open_item(s, at + s.item * per, u);
         return s.step < s.step_end || after(s);
@@ -1370,8 +1388,8 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                         l > 0.0f ? (m - kShift) * 0.69314718055994531f + logf(l) : l == 0.0f ? -INFINITY : m;
             }
             if (begins && !ends && tid == 32 * S::SOFTMAX) {
-                const long long at0 = share_end - seg.rest - sq.steps;  // of the item's first step in the line
-                heads[cta] = TreePart{static_cast<int>(tree_quotient(at0 + sq.steps - 1, line.share)) - cta + 1, row0, rows, kvh * G,
+                const long long last = share_end - seg.rest - sq.weight;  // its last step's place in the line
+                heads[cta] = TreePart{static_cast<int>(tree_quotient(last, line.share)) - cta + 1, row0, rows, kvh * G,
                                       sq.first, vs, {0, 0}};
             }
             step0 += steps;
