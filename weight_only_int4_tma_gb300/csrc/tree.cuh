@@ -511,14 +511,15 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
 
     TreeSeg seg{};
     bool more = locate(seg);
-    // the prefix sums have been read; where they stood may be zeros that the queries need
-    __syncthreads();
+    // The prefix sums have been read; where they stood may be zeros that the queries need.  The queries come by
+    // copies of the async proxy, which nothing but a fence by every thread orders behind its ordinary accesses.
     if (a.head_dim < DP) {
+        __syncthreads();
         for (uint32_t e = tid; e < (S::THREADS * 8 + 15) / 16; e += S::THREADS)
             tree_store16(base + 16 * e, make_uint4(0, 0, 0, 0));
-        fence_proxy_async_smem();
-        __syncthreads();
     }
+    fence_proxy_async_smem();
+    __syncthreads();
 
     if (warp >= S::LOADERS && warp < S::SOFTMAX) {
         // ================= loaders =================
