@@ -4,7 +4,9 @@
 // A row is read once, in 16-byte pieces, by a cluster of 1, 2, 4 or 8 CTAs (the fewer the
 // more rows there are); a thread carries its own reference m, S and sum of 2^t t in fp32, rescaled only when a
 // value passes m by more than 2^10, and they are joined at the end.  Differences x - m are taken before
-// they are scaled, so that logits of any size are right.
+// they are scaled, and where f is at most 1 of halves, with 2 f, so that logits of any size are right: a difference
+// that fp32 does not reach then is one whose product with f it does not reach either.  (Halves are
+// exact but for the last bit of subnormal numbers, so the results are the same bits wherever x - m is finite.)
 //
 // The largest logits need no second pass over the row either: every thread keeps the largest of its own
 // pieces.  Every logit that is not below the top-th largest of those maxima belongs to a thread whose
@@ -76,7 +78,7 @@ __device__ __forceinline__ float lp_max(float a, float b) {  // NaN if either is
     return y;
 }
 
-// m: the largest logit or a little less; s = sum 2^t, w = sum 2^t t, t = (x - m) c.
+// m: the largest x or a little less; s = sum 2^t, w = sum 2^t t, t = (x - m) c; x: logits or their halves.
 struct LpSums {
     float m, s, w;
     __device__ __forceinline__ void shift(float to, float c) {  // to a larger m
@@ -126,7 +128,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
     grid_dep_wait();
     const float f = a.factor ? a.factor[t] : 1.0f;
     const bool fine = f > 0.0f && f <= 0x1p127f;   // (f log2 e is finite)
-    const float c = f * kLog2e;
+    // what the sums have are logits times `half`, whose factor then is `ff`; fp16's differences are always finite
+    const bool halved = DT != 0 && f <= 1.0f;
+    const float half = halved ? 0.5f : 1.0f, ff = halved ? f + f : f, c = ff * kLog2e;
     const char* base = static_cast<const char*>(a.x) + t * a.ld * (DT == 2 ? 4 : 2);
     LpRow row;
     row.head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / (DT == 2 ? 4 : 2);
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
     };
     auto single = [&](int i) {
         const float x = logit<DT>(base, i);
-        add(x);
+        add(x * half);
         if (TOP) {
             if (at == -1 || (!(x <= bv) && bv == bv)) at = -2 - i;
             bv = lp_max(bv, x);
@@ -187,16 +191,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
             bv = lp_max(bv, top);
             at = p0;
         }
+        top *= half;
         if (!((top - sum.m) * c <= kLpLag)) sum.shift(lp_max(sum.m, top), c);
         const float m = sum.m == -INFINITY ? 0.0f : sum.m;
-        const uint64_t m2 = pack_f2(-m, -m), c2 = pack_f2(c, c);
+        const uint64_t m2 = pack_f2(-m, -m), c2 = pack_f2(c, c), half2 = pack_f2(half, half);
         uint64_t s2 = 0, w2 = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < PER; e += 2) {
                 float d0, d1;
-                unpack_f2(mul_f2(add_f2(pack_f2(x[u][e], x[u][e + 1]), m2), c2), d0, d1);
+                const uint64_t pair = pack_f2(x[u][e], x[u][e + 1]);
+                unpack_f2(mul_f2(DT == 0 ? add_f2(pair, m2) : fma_f2(pair, half2, m2), c2), d0, d1);
                 // 2^-200 is 0; a product of 0 and -infinity would be NaN
                 const uint64_t d = pack_f2(fmaxf(d0, -200.0f), fmaxf(d1, -200.0f));
                 unpack_f2(d, d0, d1);
@@ -443,24 +449,24 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(LogprobArgs a, i
         err = (x - (s - z)) + (y - z);
         return s;
     };
-    auto logprob = [&](float x) {   // (x - m) f - ln S
+    auto logprob = [&](float x) {   // (x half - m) ff - ln S
         if (!fine || m != m) return NAN;
         if (m == -INFINITY) return -INFINITY;
         if (m == INFINITY) return x == INFINITY ? NAN : -INFINITY;
         if (x == -INFINITY) return x;
         float d_err, s_err;
-        const float d = two_sum(x, -m, d_err), p = d * f;
+        const float d = two_sum(x * half, -m, d_err), p = d * ff;
         const float s = two_sum(p, -a_s, s_err);
-        return fabsf(p) < 1e30f ? s + (s_err + (fmaf(d, f, -p) + d_err * f - b_s)) : p;
+        return fabsf(p) < 1e30f ? s + (s_err + (fmaf(d, ff, -p) + d_err * ff - b_s)) : p;
     };
     if (tid == 0) {
         float lse = NAN, entropy = NAN;
         if (fine && m == m) {
-            lse = m, entropy = m == INFINITY ? NAN : 0.0f;
+            lse = m, entropy = m == INFINITY ? NAN : 0.0f;   // (where m is infinite)
             if (fabsf(m) < INFINITY) {
                 float err;
-                const float p = m * f, s = two_sum(p, a_s, err);
-                lse = fabsf(p) < 1e30f ? s + (err + (fmaf(m, f, -p) + b_s)) : p;
+                const float p = m * ff, s = two_sum(p, a_s, err);
+                lse = fabsf(p) < 1e30f ? s + (err + (fmaf(m, ff, -p) + b_s)) : p;
                 entropy = a_s + fmaf(-0.69314718055994531f, sum.w / sum.s, b_s);
             }
         }
