@@ -1147,7 +1147,12 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 s_phase ^= 1u << buf;
                 tc_fence_after();
                 if (first) {
-                    if constexpr (S::E4M3 && S::DT == 1) f *= __uint_as_float(static_cast<uint32_t>(ctl.qe[tile][r] + 127) << 23);
+                    if constexpr (S::E4M3 && S::DT == 1) {
+                        f *= __uint_as_float(static_cast<uint32_t>(ctl.qe[tile][r] + 127) << 23);
+                        // neither 0, which would make NaN of hidden tokens' -infinity, nor infinite: scores are below
+                        // 2^26 here, so that next to 0 they stay there
+                        if (fabs_scale < INFINITY) f = fminf(fmaxf(f, 0x1p-126f), 3.4028235e38f);
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(q_empty);
                 }
