@@ -1317,9 +1317,10 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 fx[0] = s0.x == -INFINITY ? 0.0f : tree_exp2(s0.x - m);
                 fx[1] = s1.x == -INFINITY ? 0.0f : tree_exp2(s1.x - m);
                 l = s0.y * fx[0] + s1.y * fx[1];
-                // a stream that had no job has nothing in its place
-                use[0] = fx[0] != 0.0f && (steps > 1 || (step0 & 1) == 0);
-                use[1] = fx[1] != 0.0f && (steps > 1 || (step0 & 1) == 1);
+                // A stream that had no job has nothing in its place.  (One whose weights vanish beside the other's has: its
+                // sums are finite, or infinite and NaN from such values, which 0 times them hands on as NaN.)
+                use[0] = steps > 1 || (step0 & 1) == 0;
+                use[1] = steps > 1 || (step0 & 1) == 1;
                 c0 = stream * (DP / 2), c1 = c0 + DP / 2;
             }
             const int64_t out_row = sq.first + i;
@@ -1339,7 +1340,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                     o[e] = use[0] ? __uint_as_float(x[0][e]) * fx[0] : 0.0f;
                     if (STREAMS == 2 && use[1]) o[e] = fmaf(__uint_as_float(x[STREAMS - 1][e]), fx[1], o[e]);
                 }
-                if (patch && live && l != 0.0f) {  // infinite values and NaN of tokens that this row sees
+                if (patch && live) {  // infinite values and NaN of tokens that this row sees
 #pragma unroll 1
                     for (int st = seg.step; st < seg.step_end; ++st) {
                         const int tok0 = tile_of(sq, st) * STEP;
@@ -1446,10 +1447,9 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(TreeArgs a,
         const float4 x = *(reinterpret_cast<const float4*>(p - row + 2 * ROWS) + (col0 / 4 + warp) * ROWS + row);
         const float f = m == -INFINITY ? 0.0f : tree_exp2(m - top);
         sum += l * f;
-        if (f != 0.0f) {
-            acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
-            acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
-        }
+        // (a part whose weights vanish still hands on values that are infinite or NaN, as NaN)
+        acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
+        acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
     }
     const float inv = sum == 0.0f ? 0.0f : h.vs / sum;
     *reinterpret_cast<uint2*>(staged + lane * PITCH + 4 * warp) =
