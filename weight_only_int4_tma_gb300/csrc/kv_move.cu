@@ -33,13 +33,15 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(MoveArgs a, int page
             continue;
         }
         // Eight moves at a time: their loads go together, unless one reads what another of them writes.
-        for (int i0 = first; i0 < last; i0 += kMoveBatch) {
+        // (Unsigned: the last ones' numbers may pass 2^31 before they are found to be past the end.)
+        const unsigned end = static_cast<unsigned>(last);
+        for (unsigned i0 = static_cast<unsigned>(first); i0 < end; i0 += kMoveBatch) {
             int64_t src[kMoveBatch], dst[kMoveBatch];
             bool apart = true;
 #pragma unroll
             for (int j = 0; j < kMoveBatch; ++j) {
                 src[j] = dst[j] = -1;
-                if (i0 + j < last) src[j] = a.src[i0 + j], dst[j] = a.dst[i0 + j];
+                if (i0 + j < end) src[j] = a.src[i0 + j], dst[j] = a.dst[i0 + j];
             }
 #pragma unroll
             for (int j = 0; j < kMoveBatch; ++j) {
