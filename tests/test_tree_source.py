@@ -62,3 +62,16 @@ def test_the_check_of_order_finds_what_is_missing():
     for bad in (["access", "barrier"], ["access", "fence"], ["fence", "access", "barrier"],
                 ["access", "fence", "barrier", "access", "barrier"], ["access", "barrier", "fence"]):
         assert not ready(bad), bad
+
+
+def test_no_copy_is_issued_after_a_wait_that_ran_out():
+    """Every place that issues tensor copies looks at the flag of a wait that gave up between its last wait, or its
+    beginning, and the copies: what is under way when the kernel ends is what was issued before."""
+    text = source()
+    places = [m.start() for m in re.finditer(r"auto (issue|ask_queries) = ", text)]
+    copies = [m.start() for m in re.finditer(r"tma_tensor_4d_g2s\(", text)]
+    assert len(places) == len(copies) == 2
+    for place, copy in zip(places, copies):
+        assert place < copy
+        waited = max(place, text.rfind("wait(", place, copy))
+        assert "abort_flag" in text[waited: copy], text[place: copy]

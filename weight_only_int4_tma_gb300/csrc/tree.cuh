@@ -696,6 +696,7 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
                 if (!by_copy || lw != Q_WARP) return;
                 const uint32_t bar = Q_CONVERT ? q_raw : q_full;
                 wait(q_empty, q_phase ^ 1u);
+                if (__any_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&ctl.abort_flag) != 0)) return;
                 if (lane == 0) mbar_arrive_expect_tx(bar, padded * DP * 2);
                 __syncwarp();
                 const int tile = lane / S::BLOCKS, block = lane % S::BLOCKS;
