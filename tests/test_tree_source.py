@@ -75,3 +75,12 @@ def test_no_copy_is_issued_after_a_wait_that_ran_out():
         assert place < copy
         waited = max(place, text.rfind("wait(", place, copy))
         assert "abort_flag" in text[waited: copy], text[place: copy]
+
+
+def test_only_tensor_maps_that_were_made_are_prefetched():
+    """Without boxes the kernel is given zeros in a map's place."""
+    text = source()
+    for name, boxes in (("kmap", "box_rows"), ("vmap", "box_rows"), ("qmap", "q_box")):
+        at = text.index(f"prefetch_tensormap(&{name})")
+        begin = text.rindex(f"if ({boxes} > 0)", 0, at)
+        assert "}" not in text[begin: at], text[begin: at]

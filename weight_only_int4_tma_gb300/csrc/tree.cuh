@@ -405,9 +405,11 @@ tree_kernel(TreeArgs a, int page_shift, int box_rows, int q_box, const __grid_co
     }
     fence_proxy_async_smem();  // the zeros
     if (tid == 32) {
-        prefetch_tensormap(&kmap);
-        prefetch_tensormap(&vmap);
-        prefetch_tensormap(&qmap);
+        if (box_rows > 0) {
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+        }
+        if (q_box > 0) prefetch_tensormap(&qmap);
     }
     grid_dep_wait();
     grid_dep_launch();
