@@ -285,8 +285,13 @@ int dec_attn_paged(const dec_attn_config* cfg, const dec_kv_cache* cache, const 
  * changes its result, whatever it holds.  A score that is NaN gives NaN in the row's out and lse,
  * one of +infinity NaN in out and +infinity in lse; one of -infinity has the weight 0.  An
  * infinite value gives that infinity (NaN with one of the other sign) if its token's weight is at
- * least 2^-20 of the row's largest, else that or NaN; a value that is NaN gives NaN.  Otherwise the weights are
- * exact to 2^-15, and with fp16 or 8-bit caches to 2^-24 of the row's largest.
+ * least 2^-20 of the row's largest, else that or NaN; a value that is NaN gives NaN.
+ *
+ * Otherwise a token's weight is exact to 2^-15 of itself over a bf16 cache, 2^-19 over an fp16 one and
+ * 2^-20 over an 8-bit one (or to 2^-30 of the row's largest, where that is more); the products q k and all sums are
+ * fp32's, and what passes its range is infinite.  bf16 queries meet an 8-bit cache in fp16, each row and head scaled by
+ * a power of two: values are exact down to 2^-25 of its largest, smaller ones to 2^-33 of it, and a row
+ * whose largest is below 2^-118 counts as zeros.
  */
 typedef struct dec_tree_config {
     int q_heads;         /* a multiple of the cache's kv_heads                              */
