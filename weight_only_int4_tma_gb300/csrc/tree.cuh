@@ -30,7 +30,7 @@
 // tile and bounds this form (16 sequences of up to 4096, 64 heads on 8, 8 drafted: 48 us, and 43 with the bf16 cache of
 // twice the bytes; with the rows' conversions one after another 66 against 45).  Pages that no tensor map
 // describes (sizes that no 8 divides, strides of 0) are copied 16 bytes at a time: the same batch takes 43 us
-// with bf16 pages of 64, 76 with pages of 5 and of 1; 103 with 8-bit pages of 5.
+// with bf16 pages of 64, 69 with pages of 5 and of 1; 114 with 8-bit pages of 5.
 //
 // Softmax.  A running reference m per row: weights are exp2(s - m); only when a score passes m by
 // more than 2^8 is O, in TMEM, scaled to a new reference.  Maxima carry NaN, and come with the loads from TMEM.
@@ -47,8 +47,8 @@
 // block (one sequence of 131072, 8 drafted: 106 to 109 us; 112 with 32 rows and all columns a block).
 //
 // What bounds it.  16 sequences of up to 4096 tokens, 16 drafted, 32 heads on 32, fp16: memory, 546 MB in 106 us, 5.2
-// TB/s, and the ends of 512 short items.  32 sequences of up to 8192, 32 drafted, 64 heads on 8: the tensor pipe (57 %
-// busy at 176 us, before the split weighted its steps; 152 now: 550 TFLOP/s, 825 with P's two parts), and between its turns the softmax's chain from S to P.
+// TB/s, and the ends of 512 short items.  32 sequences of up to 8192, 32 drafted, 64 heads on 8: the tensor pipe (59 %
+// busy; 154 us: 540 TFLOP/s, 815 with P's two parts), and between its turns the softmax's chain from S to P.
 // One tree of 8 over 777 tokens: 16 us of code that runs once.
 #pragma once
 #include "decode.cuh"
